@@ -7,6 +7,7 @@
 // 2.5배 빨라지는 방법", §블록 단위 인과 어텐션 (bidirectional inside a block,
 // causal between blocks, finished blocks cached).
 #include "attn_common.cuh"
+#include "kv4.cuh"
 
 namespace d2f {
 namespace {
@@ -45,7 +46,26 @@ __device__ __forceinline__ void ld4(const uint16_t *p, int64_t i, float (&x)[4])
   x[3] = bf16_bits_to_float(v.y >> 16);
 }
 
-template <typename T, int D>
+// Four consecutive dims d .. d + 3 (d a multiple of 4) of token o of a 4-bit page.
+template <int D>
+__device__ __forceinline__ void ld4_kv4(const AttnArgs &a, const uint8_t *tile, int o, int d,
+                                        float (&k)[4], float (&v)[4]) {
+  const int B = a.block_size;
+  const Kv4Layout L{D, B};
+  const uint32_t kc =
+      *reinterpret_cast<const uint16_t *>(tile + ((d >> 5) * B + o) * 16 + ((d & 31) >> 1));
+  const float ks = e4m3_value(tile[L.k_scales() + o * (D / 16) + (d >> 4)]) * a.k_mul;
+  const float vs = e4m3_value(tile[L.v_scales() + (d >> 4) * B + o]) * a.v_mul;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k[j] = e2m1_value(kc >> (4 * j)) * ks;
+    v[j] = e2m1_value((uint32_t)tile[L.v_codes() + (d + j) * (B / 2) + (o >> 1)] >>
+                      (4 * (o & 1))) * vs;
+  }
+}
+
+// KV4: the cached tokens come from a 4-bit pool.
+template <typename T, int D, bool KV4>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a) {
   constexpr int DPL = D / 32;
   __shared__ float q_s[RPC][D];
@@ -163,8 +183,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a) {
           ks = Kw;
           vs = Vw;
         }
-        ld4(ks, off, kv);
-        ld4(vs, off, vv);
+        if (KV4 && t < Tc) {
+          const int kk = t * KT + c;
+          ld4_kv4<D>(a, a.kv4_pool + ((int64_t)kpage[c] * Hk + g) * Kv4Layout{D, B}.page_bytes(),
+                     kk % B, d, kv, vv);
+        } else {
+          ld4(ks, off, kv);
+          ld4(vs, off, vv);
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -218,6 +244,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a) {
 #pragma unroll
       for (int ri = 0; ri < kRowsPerWarp; ++ri) {
         const float pc = __shfl_sync(0xffffffffu, p[ri], cc);
+        // (a key hidden from the row must not reach it through 0 * infinity)
+        if (KV4 && kwin[cc] >= win_end[ri]) continue;
 #pragma unroll
         for (int j = 0; j < DPL; ++j) o[ri][j] = fmaf(pc, vv[j], o[ri][j]);
       }
@@ -343,10 +371,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a) {
 template <typename T>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
   dim3 grid(a.m_tiles, a.num_splits, a.batch * a.num_heads_kv), block(kThreads);
+  if (a.kv4_pool) {
+    if (a.head_dim == 64) attn_simt_kernel<T, 64, true><<<grid, block, 0, s>>>(a);
+    else if (a.head_dim == 128) attn_simt_kernel<T, 128, true><<<grid, block, 0, s>>>(a);
+    else return cudaErrorInvalidValue;
+    return cudaGetLastError();
+  }
   switch (a.head_dim) {
-    case 32: attn_simt_kernel<T, 32><<<grid, block, 0, s>>>(a); break;
-    case 64: attn_simt_kernel<T, 64><<<grid, block, 0, s>>>(a); break;
-    case 128: attn_simt_kernel<T, 128><<<grid, block, 0, s>>>(a); break;
+    case 32: attn_simt_kernel<T, 32, false><<<grid, block, 0, s>>>(a); break;
+    case 64: attn_simt_kernel<T, 64, false><<<grid, block, 0, s>>>(a); break;
+    case 128: attn_simt_kernel<T, 128, false><<<grid, block, 0, s>>>(a); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

@@ -113,7 +113,7 @@ int force_deep() {
 }
 
 int plan_attn(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, int D, int B,
-              int dtype, int num_splits, AttnPlan *p) {
+              int dtype, int num_splits, AttnPlan *p, bool allow_tc = true) {
   if (batch < 0 || total_q < 0 || max_q < 0 || max_ctx < 0)
     return fail(D2F_ERR_INVALID_ARG, "negative size (batch %d, total_q %d, max_q %d, max_ctx %d)",
                 batch, total_q, max_q, max_ctx);
@@ -129,7 +129,7 @@ int plan_attn(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, i
   if ((long long)batch * Hkv > 65535)
     return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_kv must be <= 65535");
   const bool tc = dtype == D2F_BF16 && (D == 64 || D == 128) && (B == 8 || B == 16 || B == 32) &&
-                  !force_simt();
+                  allow_tc && !force_simt();
   if (!tc) {
     if (!(D == 32 || D == 64 || D == 128))
       return fail(D2F_ERR_UNSUPPORTED, "head_dim %d: supported are 64, 128 (bf16, B in {8,16,32}) "
@@ -421,7 +421,7 @@ int attn_entry(const void *q, const void *k_win, const void *v_win, const void *
     return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
                 workspace ? workspace_bytes : (size_t)0);
 
-  AttnArgs a;
+  AttnArgs a{};
   a.q = q;
   a.k_win = k_win;
   a.v_win = v_win;
@@ -778,6 +778,331 @@ int d2f_window_step(int batch, int block_size, int max_blocks, int capacity,
   a.err = err_word;
   const cudaError_t e = d2f::launch_window(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "window step launch");
+  return D2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit paged cache
+// ---------------------------------------------------------------------------
+namespace {
+// Sizes every entry point of the 4-bit cache shares.
+int kv4_sizes(int num_heads_kv, int head_dim, int block_size, int num_pages, int dtype, int k_exp,
+              int v_exp) {
+  if (num_heads_kv <= 0 || num_pages < 0)
+    return fail(D2F_ERR_INVALID_ARG, "num_heads_kv %d / num_pages %d out of range", num_heads_kv,
+                num_pages);
+  if (dtype != D2F_BF16 && dtype != D2F_F32)
+    return fail(D2F_ERR_INVALID_ARG, "dtype must be D2F_BF16 or D2F_F32");
+  if (k_exp < -D2F_KV4_MAX_EXP || k_exp > D2F_KV4_MAX_EXP || v_exp < -D2F_KV4_MAX_EXP ||
+      v_exp > D2F_KV4_MAX_EXP)
+    return fail(D2F_ERR_INVALID_ARG, "k_exp %d / v_exp %d outside +-%d", k_exp, v_exp,
+                D2F_KV4_MAX_EXP);
+  if ((head_dim != 64 && head_dim != 128) ||
+      (block_size != 8 && block_size != 16 && block_size != 32))
+    return fail(D2F_ERR_UNSUPPORTED, "the 4-bit cache takes head_dim 64 or 128 and block_size 8, "
+                "16 or 32 (got %d, %d)", head_dim, block_size);
+  return D2F_OK;
+}
+
+// 2^e, exact for the exponents kv4_sizes lets through.
+float exp2_int(int e) {
+  float f = 1.f;
+  for (; e > 0; --e) f *= 2.f;
+  for (; e < 0; ++e) f *= 0.5f;
+  return f;
+}
+
+int kv4_plan(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, int D, int B,
+             int dtype, AttnPlan *p) {
+  const int st = kv4_sizes(Hkv, D, B, 0, dtype, 0, 0);
+  if (st != D2F_OK) return st;
+  return plan_attn(batch, total_q, max_q, max_ctx, Hq, Hkv, D, B, dtype, 0, p, false);
+}
+}  // namespace
+
+int d2f_kv4_page_bytes(int head_dim, int block_size, size_t *bytes) {
+  if (!bytes) return fail(D2F_ERR_INVALID_ARG, "bytes is NULL");
+  const int st = kv4_sizes(1, head_dim, block_size, 0, D2F_BF16, 0, 0);
+  if (st != D2F_OK) return st;
+  *bytes = (size_t)block_size * head_dim * 9 / 8;
+  return D2F_OK;
+}
+
+int d2f_kv4_append(const void *k_win, const void *v_win, const int32_t *src_row,
+                   const int32_t *dst_page, const int32_t *n_rows, const int32_t *n_append_dev,
+                   int max_append, int total_q, void *kv_pool, int num_heads_kv, int head_dim,
+                   int block_size, int num_pages, int k_exp, int v_exp, int dtype,
+                   int32_t *err_word, void *stream) {
+  const int st = kv4_sizes(num_heads_kv, head_dim, block_size, num_pages, dtype, k_exp, v_exp);
+  if (st != D2F_OK) return st;
+  if (max_append < 0 || total_q < 0)
+    return fail(D2F_ERR_INVALID_ARG, "max_append %d / total_q %d negative", max_append, total_q);
+  if ((long long)max_append * num_heads_kv > 0x7fffffffLL)
+    return fail(D2F_ERR_UNSUPPORTED, "max_append * num_heads_kv too large");
+  if (max_append == 0) return D2F_OK;
+  if (!k_win || !v_win || !src_row || !dst_page || !kv_pool)
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(k_win) || !aligned16(v_win) || !aligned16(kv_pool))
+    return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  Kv4AppendArgs a{};
+  a.k_win = k_win;
+  a.v_win = v_win;
+  a.src_row = src_row;
+  a.dst_page = dst_page;
+  a.n_rows = n_rows;
+  a.n_dev = n_append_dev;
+  a.n_append = max_append;
+  a.total_q = total_q;
+  a.num_heads_kv = num_heads_kv;
+  a.block_size = block_size;
+  a.num_pages = num_pages;
+  a.k_mul = exp2_int(-k_exp);
+  a.v_mul = exp2_int(-v_exp);
+  a.pool = static_cast<uint8_t *>(kv_pool);
+  a.err = err_word;
+  const cudaError_t e =
+      launch_kv4_append(a, dtype, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_append launch");
+  return D2F_OK;
+}
+
+int d2f_kv4_read(const void *kv_pool, const int64_t *slot, int n, void *k_out, void *v_out,
+                 int num_heads_kv, int head_dim, int block_size, int num_pages, int k_exp,
+                 int v_exp, int dtype, int32_t *err_word, void *stream) {
+  const int st = kv4_sizes(num_heads_kv, head_dim, block_size, num_pages, dtype, k_exp, v_exp);
+  if (st != D2F_OK) return st;
+  if (n < 0) return fail(D2F_ERR_INVALID_ARG, "n %d < 0", n);
+  if (((long long)n * num_heads_kv * (head_dim / 16)) / 256 >= 0x7fffffffLL)
+    return fail(D2F_ERR_UNSUPPORTED, "n * num_heads_kv too large");
+  if (n == 0) return D2F_OK;
+  if (!slot || !k_out || !v_out || (!kv_pool && num_pages > 0))
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(kv_pool) || !aligned16(k_out) || !aligned16(v_out))
+    return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  Kv4ReadArgs a{};
+  a.pool = static_cast<const uint8_t *>(kv_pool);
+  a.slot = slot;
+  a.n = n;
+  a.num_heads_kv = num_heads_kv;
+  a.block_size = block_size;
+  a.num_pages = num_pages;
+  a.k_mul = exp2_int(k_exp);
+  a.v_mul = exp2_int(v_exp);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.err = err_word;
+  const cudaError_t e = launch_kv4_read(a, dtype, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_read launch");
+  return D2F_OK;
+}
+
+int d2f_block_attn_kv4_workspace_size(int batch, int total_q, int max_q_per_seq, int max_ctx,
+                                      int num_heads_q, int num_heads_kv, int head_dim,
+                                      int block_size, int dtype, size_t *bytes) {
+  if (!bytes) return fail(D2F_ERR_INVALID_ARG, "bytes is NULL");
+  AttnPlan p{};
+  const int st = kv4_plan(batch, total_q, max_q_per_seq, max_ctx, num_heads_q, num_heads_kv,
+                          head_dim, block_size, dtype, &p);
+  if (st != D2F_OK) return st;
+  *bytes = p.bytes;
+  return D2F_OK;
+}
+
+int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, const void *kv_pool,
+                       const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,
+                       const int32_t *q_start, void *out, float *lse_out, int batch, int total_q,
+                       int max_q_per_seq, int max_ctx, int num_heads_q, int num_heads_kv,
+                       int head_dim, int block_size, int num_pages, int k_exp, int v_exp,
+                       int dtype, float softmax_scale, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, void *stream) {
+  AttnPlan p{};
+  int st = kv4_plan(batch, total_q, max_q_per_seq, max_ctx, num_heads_q, num_heads_kv, head_dim,
+                    block_size, dtype, &p);
+  if (st != D2F_OK) return st;
+  st = kv4_sizes(num_heads_kv, head_dim, block_size, num_pages, dtype, k_exp, v_exp);
+  if (st != D2F_OK) return st;
+  if (batch == 0 || total_q == 0) return D2F_OK;
+  if (!q || !k_win || !v_win || !out || !ctx_len || !q_start)
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (max_pages_per_seq < 0) return fail(D2F_ERR_INVALID_ARG, "max_pages_per_seq negative");
+  if ((long long)max_pages_per_seq * block_size < max_ctx)
+    return fail(D2F_ERR_INVALID_ARG, "max_ctx %d exceeds max_pages_per_seq * block_size", max_ctx);
+  if (max_pages_per_seq > 0 && (!kv_pool || !page_table))
+    return fail(D2F_ERR_INVALID_ARG, "a cached context needs kv_pool and page_table");
+  if (!(softmax_scale > 0.f)) return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0");
+  const void *ptrs[] = {q, k_win, v_win, kv_pool, out};
+  for (const void *x : ptrs)
+    if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  AttnArgs a{};
+  a.q = q;
+  a.k_win = k_win;
+  a.v_win = v_win;
+  // (without a pool every ctx_len must be 0, and no cached token is read)
+  a.kv4_pool = static_cast<const uint8_t *>(kv_pool ? kv_pool : k_win);
+  a.k_mul = exp2_int(k_exp);
+  a.v_mul = exp2_int(v_exp);
+  a.page_table = page_table;
+  a.max_pages_per_seq = max_pages_per_seq;
+  a.ctx_len = ctx_len;
+  a.q_start = q_start;
+  a.out = out;
+  a.lse_out = lse_out;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.max_q_per_seq = max_q_per_seq;
+  a.num_heads_q = num_heads_q;
+  a.num_heads_kv = num_heads_kv;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_pages = kv_pool ? num_pages : 0;
+  a.group = num_heads_q / num_heads_kv;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.num_splits = p.splits;
+  a.tiles_per_split = p.tiles_per_split;
+  a.m_tiles = p.m_tiles;
+  a.wait_cycles = kWaitCycles;
+  a.counters = reinterpret_cast<int32_t *>(workspace);
+  a.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.off_ml);
+  a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
+  a.err = err_word;
+  const cudaError_t e = launch_attn_simt(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "CUDA-core kv4 attention launch");
+  return D2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Page map
+// ---------------------------------------------------------------------------
+int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
+                 const int32_t *num_new, const int32_t *ctx_len, const int32_t *free_pages,
+                 const int32_t *free_count, int32_t *page_table, int32_t *ctx_len_out,
+                 int32_t *free_count_out, int32_t *row_start, uint8_t *admitted,
+                 int64_t *slot_map, int32_t *app_src, int32_t *app_dst, int32_t *app_rows,
+                 int32_t *n_append, int32_t *err_word, void *stream) {
+  if (batch < 0 || block_size < 1 || max_pages_per_seq < 0 || capacity < 0 || max_append < 0)
+    return fail(D2F_ERR_INVALID_ARG, "size out of range");
+  if (batch > kPageMapMaxBatch)
+    return fail(D2F_ERR_UNSUPPORTED, "batch %d > %d", batch, kPageMapMaxBatch);
+  if (!free_count || !free_count_out || !row_start || !n_append ||
+      (batch > 0 && (!num_new || !ctx_len || !ctx_len_out || !admitted)) ||
+      (!free_pages && max_append > 0) || (!page_table && batch > 0 && max_pages_per_seq > 0) ||
+      (!slot_map && capacity > 0) || ((!app_src || !app_dst || !app_rows) && max_append > 0))
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  PageMapArgs a{};
+  a.batch = batch;
+  a.block_size = block_size;
+  a.max_pages_per_seq = max_pages_per_seq;
+  a.capacity = capacity;
+  a.max_append = max_append;
+  a.num_new = num_new;
+  a.ctx_len = ctx_len;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.page_table = page_table;
+  a.ctx_out = ctx_len_out;
+  a.free_out = free_count_out;
+  a.row_start = row_start;
+  a.admitted = admitted;
+  a.slot = slot_map;
+  a.app_src = app_src;
+  a.app_dst = app_dst;
+  a.app_rows = app_rows;
+  a.n_append = n_append;
+  a.err = err_word;
+  const cudaError_t e = launch_page_map(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page map launch");
+  return D2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Token log probabilities
+// ---------------------------------------------------------------------------
+namespace {
+struct LogprobsPlan {
+  int splits, chunk;
+  size_t off_partial, off_top, bytes;
+};
+
+int plan_logprobs(int n, int vocab, int top_k, int dtype, LogprobsPlan *p) {
+  if (n < 0 || vocab <= 0)
+    return fail(D2F_ERR_INVALID_ARG, "n %d / vocab %d out of range", n, vocab);
+  if (top_k < 0 || top_k > vocab)
+    return fail(D2F_ERR_INVALID_ARG, "top_k %d outside [0, vocab]", top_k);
+  if (dtype != D2F_BF16 && dtype != D2F_F32)
+    return fail(D2F_ERR_INVALID_ARG, "dtype must be D2F_BF16 or D2F_F32");
+  if (top_k > kLogprobsMaxTop)
+    return fail(D2F_ERR_UNSUPPORTED, "top_k %d > %d", top_k, kLogprobsMaxTop);
+  if (n > 65535) return fail(D2F_ERR_UNSUPPORTED, "n must be <= 65535");
+  if (vocab > (1 << 30)) return fail(D2F_ERR_UNSUPPORTED, "vocab must be <= 2^30");
+  const int vec = dtype == D2F_BF16 ? 8 : 4;
+  const int sms = max(1, num_sms_current_device());
+  int splits = (int)((4LL * sms) / max(n, 1));
+  splits = max(1, min(splits, 64));
+  splits = max(1, min(splits, vocab / 2048));
+  const int chunk = cdiv(cdiv(vocab, splits), vec) * vec;
+  splits = cdiv(vocab, chunk);
+  p->splits = splits;
+  p->chunk = chunk;
+  // the counters come first: their place does not depend on the split count
+  p->off_partial = align_up((size_t)n * sizeof(int32_t));
+  p->off_top = p->off_partial + align_up((size_t)n * splits * sizeof(float4));
+  p->bytes = splits > 1 ? p->off_top + align_up((size_t)n * splits * top_k * sizeof(uint64_t)) : 0;
+  return D2F_OK;
+}
+}  // namespace
+
+int d2f_token_logprobs_workspace_size(int n, int vocab, int top_k, int dtype, size_t *bytes) {
+  if (!bytes) return fail(D2F_ERR_INVALID_ARG, "bytes is NULL");
+  LogprobsPlan p{};
+  const int st = plan_logprobs(n, vocab, top_k, dtype, &p);
+  if (st != D2F_OK) return st;
+  *bytes = p.bytes;
+  return D2F_OK;
+}
+
+int d2f_token_logprobs(const void *logits, int64_t row_stride, int dtype, int vocab,
+                       int num_logit_rows, const int32_t *logit_row, const int32_t *tokens, int n,
+                       int top_k, float *logprob, float *entropy, int32_t *top_id,
+                       float *top_logprob, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, void *stream) {
+  LogprobsPlan p{};
+  const int st = plan_logprobs(n, vocab, top_k, dtype, &p);
+  if (st != D2F_OK) return st;
+  if (n == 0) return D2F_OK;
+  if (!logits || !tokens || !logprob || (top_k > 0 && (!top_id || !top_logprob)))
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (row_stride < vocab) return fail(D2F_ERR_INVALID_ARG, "row_stride < vocab");
+  if (num_logit_rows <= 0) return fail(D2F_ERR_INVALID_ARG, "num_logit_rows must be > 0");
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  const int elt = dtype == D2F_BF16 ? 2 : 4;
+  const int path = aligned16(logits) && (row_stride * elt) % 16 == 0 ? 1 : 0;
+  LogprobsArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.vocab = vocab;
+  a.num_logit_rows = num_logit_rows;
+  a.logit_row = logit_row;
+  a.tokens = tokens;
+  a.n = n;
+  a.top_k = top_k;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_id = top_id;
+  a.top_logprob = top_logprob;
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  char *ws = static_cast<char *>(workspace);
+  a.row_cnt = reinterpret_cast<int32_t *>(ws);
+  a.partial = reinterpret_cast<float4 *>(ws + p.off_partial);
+  a.top_part = reinterpret_cast<uint64_t *>(ws + p.off_top);
+  a.err = err_word;
+  const cudaError_t e = launch_logprobs(a, dtype, path, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "token logprobs launch");
   return D2F_OK;
 }
 

@@ -70,6 +70,8 @@ struct AttnArgs {
   int sk;                // tensor-core path: stream-K form (see attn_tc.cu), else 0
   int32_t *sk_cnt;       // stream-K: [batch * Hkv] arrival counters (zero at rest)
   uint8_t *sk_slots;     // stream-K: [2 * grid] partial slots of kSkSlotBytes
+  const uint8_t *kv4_pool;  // non-null: the cache is the 4-bit pool (kv4.cuh), k_pool / v_pool unused
+  float k_mul, v_mul;       // ... and 2^k_exp, 2^v_exp
   int32_t *counters;     // [batch * Hkv * m_tiles] merge arrival counters (zero at rest)
   float2 *ws_ml;         // [num_splits][total_q * Hq] (max in log2 units, sum)
   float *ws_o;           // [num_splits][total_q * Hq][head_dim] unnormalised partial output
@@ -129,11 +131,67 @@ struct WindowArgs {
   int32_t *err;
 };
 
+// A batch of requests larger than this does not fit the page map's shared memory
+// (three ints a request).
+constexpr int kPageMapMaxBatch = 16384;
+struct PageMapArgs {
+  int batch, block_size, max_pages_per_seq, capacity, max_append;
+  const int32_t *num_new, *ctx_len, *free_pages, *free_count;
+  int32_t *page_table, *ctx_out, *free_out, *row_start;
+  uint8_t *admitted;
+  int64_t *slot;
+  int32_t *app_src, *app_dst, *app_rows, *n_append;
+  int32_t *err;
+};
+
+struct Kv4AppendArgs {
+  const void *k_win, *v_win;
+  const int32_t *src_row, *dst_page;
+  const int32_t *n_rows;   // rows of each entry, or NULL: block_size
+  const int32_t *n_dev;    // non-null: the list's length, read on the device
+  int n_append, total_q, num_heads_kv, block_size, num_pages;
+  float k_mul, v_mul;      // 2^-k_exp, 2^-v_exp
+  uint8_t *pool;
+  int32_t *err;
+};
+
+struct Kv4ReadArgs {
+  const uint8_t *pool;
+  const int64_t *slot;
+  int64_t n;
+  int num_heads_kv, block_size, num_pages;
+  float k_mul, v_mul;      // 2^k_exp, 2^v_exp
+  void *k_out, *v_out;
+  int32_t *err;
+};
+
+constexpr int kLogprobsMaxTop = 32;  // alternatives of a row: one per lane of a warp
+struct LogprobsArgs {
+  const void *logits;
+  int64_t row_stride;
+  int vocab, num_logit_rows;
+  const int32_t *logit_row, *tokens;
+  int n, top_k;
+  float *logprob, *entropy;
+  int32_t *top_id;
+  float *top_logprob;
+  int splits, chunk;       // CTAs per row, vocabulary entries per CTA
+  int32_t *row_cnt;        // [n] arrivals per row (zero at rest)
+  float4 *partial;         // [n][splits] (max, sum of exp, sum of exp * (l - max), -)
+  uint64_t *top_part;      // [n][splits][top_k] ordered keys of the largest logits
+  int32_t *err;
+};
+
 // Launchers (one per translation unit). Return cudaSuccess or the launch error.
 // path: 0 scalar loads, 1 128-bit loads (see commit.cu)
 cudaError_t launch_commit(const CommitArgs &a, int dtype, int path, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs &a, bool vec_ok, cudaStream_t s);
 cudaError_t launch_window(const WindowArgs &a, cudaStream_t s);
+cudaError_t launch_page_map(const PageMapArgs &a, cudaStream_t s);
+cudaError_t launch_kv4_append(const Kv4AppendArgs &a, int dtype, int D, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4ReadArgs &a, int dtype, int D, cudaStream_t s);
+// path: 0 scalar loads, 1 128-bit loads
+cudaError_t launch_logprobs(const LogprobsArgs &a, int dtype, int path, cudaStream_t s);
 size_t window_smem_bytes(int batch, int capacity, int block_size);
 cudaError_t launch_attn_simt(const AttnArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s, char *why, size_t why_len);

@@ -36,7 +36,10 @@ EXPORTS = ("d2f_version", "d2f_status_string", "d2f_last_error_string",
            "d2f_block_attn_append", "d2f_block_attn_part",
            "d2f_commit_workspace_size",
            "d2f_commit", "d2f_commit_metric", "d2f_commit_noalloc", "d2f_kv_append",
-           "d2f_kv_append_dev", "d2f_block_attn_append_dev", "d2f_window_step")
+           "d2f_kv_append_dev", "d2f_block_attn_append_dev", "d2f_window_step",
+           "d2f_kv4_page_bytes", "d2f_kv4_append", "d2f_kv4_read",
+           "d2f_block_attn_kv4_workspace_size", "d2f_block_attn_kv4", "d2f_page_map",
+           "d2f_token_logprobs_workspace_size", "d2f_token_logprobs")
 
 # attention parts of block_attn(part=...) (include/d2f.h D2F_ATTN_*)
 ATTN_ALL, ATTN_CACHED, ATTN_WINDOW = 0, 1, 2
@@ -108,6 +111,24 @@ def load(path=LIB_PATH):
     lib.d2f_window_step.restype = _I
     lib.d2f_window_step.argtypes = ([_I] * 5 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float] +
                                     [_P] * 18)
+    lib.d2f_kv4_page_bytes.restype = _I
+    lib.d2f_kv4_page_bytes.argtypes = [_I, _I, ctypes.POINTER(_SZ)]
+    lib.d2f_kv4_append.restype = _I
+    lib.d2f_kv4_append.argtypes = [_P] * 6 + [_I, _I, _P] + [_I] * 7 + [_P, _P]
+    lib.d2f_kv4_read.restype = _I
+    lib.d2f_kv4_read.argtypes = [_P, _P, _I, _P, _P] + [_I] * 7 + [_P, _P]
+    lib.d2f_block_attn_kv4_workspace_size.restype = _I
+    lib.d2f_block_attn_kv4_workspace_size.argtypes = [_I] * 9 + [ctypes.POINTER(_SZ)]
+    lib.d2f_block_attn_kv4.restype = _I
+    lib.d2f_block_attn_kv4.argtypes = ([_P] * 5 + [_I] + [_P] * 4 + [_I] * 12 +
+                                       [ctypes.c_float, _P, _SZ, _P, _P])
+    lib.d2f_page_map.restype = _I
+    lib.d2f_page_map.argtypes = [_I] * 5 + [_P] * 16
+    lib.d2f_token_logprobs_workspace_size.restype = _I
+    lib.d2f_token_logprobs_workspace_size.argtypes = [_I] * 4 + [ctypes.POINTER(_SZ)]
+    lib.d2f_token_logprobs.restype = _I
+    lib.d2f_token_logprobs.argtypes = ([_P, ctypes.c_int64, _I, _I, _I, _P, _P, _I, _I] +
+                                       [_P] * 4 + [_P, _SZ, _P, _P])
     _lib = lib
     return lib
 
@@ -144,6 +165,37 @@ def _dev(t, name, dtype=None):
         raise ValueError("%s must be contiguous" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+class _On:
+    """Checks that the given tensors are contiguous CUDA tensors of one device and makes
+    it the current one: the stream (that device's current one unless given) and the
+    launch belong to it. Entries are (name, tensor or None, dtype or None)."""
+
+    def __init__(self, stream, *tensors):
+        dev = None
+        for name, t, dtype in tensors:
+            if t is None:
+                continue
+            _dev(t, name, dtype)
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("%s is on %s, the others on %s" % (name, t.device, dev))
+        self._guard = torch.cuda.device(dev)
+        self._given = stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return _stream(self._given)
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _shape(t, name, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def status_string(status):
@@ -408,3 +460,248 @@ def window_step(st, *, tau_add, tau_act, err=None, stream=None, use_stopped=True
         _ptr(st.page_table), _ptr(st.next_block), _ptr(st.gen_blocks), _ptr(st.n_leaving),
         _ptr(st.stopped) if use_stopped else None, _ptr(st.free_pages), _ptr(st.free_count),
         _ptr(st.app_src), _ptr(st.app_dst), _ptr(st.n_append), _ptr(err), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 4-bit paged cache
+# ---------------------------------------------------------------------------
+def kv4_page_bytes(head_dim, block_size):
+    """Bytes of one page of one KV head in a 4-bit pool."""
+    lib = load()
+    n = _SZ(0)
+    _check(lib.d2f_kv4_page_bytes(head_dim, block_size, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_pool(device, *, num_pages, num_heads_kv, head_dim, block_size):
+    """A zero-filled 4-bit pool: uint8 [num_pages, num_heads_kv, page bytes]."""
+    return torch.zeros((num_pages, num_heads_kv, kv4_page_bytes(head_dim, block_size)),
+                       dtype=torch.uint8, device=device)
+
+
+def _kv4_pool_shape(pool, num_heads_kv, head_dim, block_size):
+    if pool.dim() != 3:
+        raise ValueError("the 4-bit pool is [num_pages, num_heads_kv, page bytes]")
+    _shape(pool, "pool", (pool.shape[0], num_heads_kv, kv4_page_bytes(head_dim, block_size)))
+
+
+def kv4_append(k_win, v_win, src_row, dst_page, pool, *, block_size, n_rows=None, k_exp=0,
+               v_exp=0, n_append_dev=None, err=None, stream=None):
+    """Quantise blocks (rows src_row[a] .. + n_rows[a] of K/V [rows, Hkv, D]; n_rows None:
+    block_size each) into pages dst_page[a] of a 4-bit pool. With n_append_dev (int32 [1]
+    on the device) the list's length is read there, at most len(src_row)."""
+    lib = load()
+    total_q, hkv, d = k_win.shape
+    _shape(v_win, "v_win", k_win.shape)
+    _kv4_pool_shape(pool, hkv, d, block_size)
+    n = src_row.shape[0]
+    _shape(src_row, "src_row", (n,))
+    _shape(dst_page, "dst_page", (n,))
+    _shape(n_rows, "n_rows", (n,))
+    _shape(n_append_dev, "n_append_dev", (1,))
+    with _On(stream, ("k_win", k_win, k_win.dtype), ("v_win", v_win, k_win.dtype),
+             ("src_row", src_row, torch.int32), ("dst_page", dst_page, torch.int32),
+             ("pool", pool, torch.uint8), ("n_rows", n_rows, torch.int32),
+             ("n_append_dev", n_append_dev, torch.int32), ("err", err, torch.int32)) as s:
+        _check(lib.d2f_kv4_append(
+            _ptr(k_win), _ptr(v_win), _ptr(src_row), _ptr(dst_page), _ptr(n_rows),
+            _ptr(n_append_dev), n, total_q, _ptr(pool), hkv, d, block_size, pool.shape[0],
+            int(k_exp), int(v_exp), _dtype_code(k_win), _ptr(err), s))
+
+
+def kv4_read(pool, slot, *, head_dim, block_size, dtype=torch.bfloat16, k_exp=0, v_exp=0,
+             k=None, v=None, err=None, stream=None):
+    """Tokens at int64 slots (page * block_size + offset; -1 gives zeros) of a 4-bit pool.
+
+    Returns (k, v) [len(slot), Hkv, D] of `dtype`, exact."""
+    lib = load()
+    hkv = pool.shape[1]
+    _kv4_pool_shape(pool, hkv, head_dim, block_size)
+    n = slot.shape[0]
+    _shape(slot, "slot", (n,))
+    shape = (n, hkv, head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=pool.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=pool.device)
+    _shape(k, "k", shape)
+    _shape(v, "v", shape)
+    with _On(stream, ("pool", pool, torch.uint8), ("slot", slot, torch.int64), ("k", k, dtype),
+             ("v", v, dtype), ("err", err, torch.int32)) as s:
+        _check(lib.d2f_kv4_read(_ptr(pool), _ptr(slot), n, _ptr(k), _ptr(v), hkv, head_dim,
+                                block_size, pool.shape[0], int(k_exp), int(v_exp), _dtype_code(k),
+                                _ptr(err), s))
+    return k, v
+
+
+def attn_kv4_workspace_size(batch, total_q, max_q_per_seq, max_ctx, num_heads_q, num_heads_kv,
+                            head_dim, block_size, dtype=BF16):
+    lib = load()
+    n = _SZ(0)
+    _check(lib.d2f_block_attn_kv4_workspace_size(batch, total_q, max_q_per_seq, max_ctx,
+                                                 num_heads_q, num_heads_kv, head_dim, block_size,
+                                                 dtype, ctypes.byref(n)))
+    return n.value
+
+
+def attn_kv4_workspace(device, **kw):
+    """A zero-filled workspace of the size attn_kv4_workspace_size(**kw) returns."""
+    with torch.cuda.device(device):
+        return torch.zeros(max(attn_kv4_workspace_size(**kw), 1), dtype=torch.uint8, device=device)
+
+
+def block_attn_kv4(q, k_win, v_win, pool, page_table, ctx_len, q_start, *, block_size,
+                   max_q_per_seq, max_ctx, k_exp=0, v_exp=0, softmax_scale=None, out=None,
+                   lse=None, want_lse=True, workspace=None, err=None, stream=None):
+    """Block-causal attention of the window over [4-bit paged cache ; window] (one layer):
+    block_attn with one 4-bit pool in place of k_pool and v_pool.
+
+    Returns (out [total_q, Hq, D] like q, lse [total_q, Hq] float32 or None)."""
+    lib = load()
+    total_q, hq, d = q.shape
+    hkv = k_win.shape[1]
+    batch = ctx_len.shape[0]
+    _shape(k_win, "k_win", (total_q, hkv, d))
+    _shape(v_win, "v_win", (total_q, hkv, d))
+    _kv4_pool_shape(pool, hkv, d, block_size)
+    _shape(ctx_len, "ctx_len", (batch,))
+    _shape(q_start, "q_start", (batch + 1,))
+    _shape(page_table, "page_table", (batch, page_table.shape[-1]))
+    dt = _dtype_code(q)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    _shape(out, "out", q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
+    _shape(lse, "lse", (total_q, hq))
+    if workspace is None:
+        workspace = attn_kv4_workspace(q.device, batch=batch, total_q=total_q,
+                                       max_q_per_seq=max_q_per_seq, max_ctx=max_ctx,
+                                       num_heads_q=hq, num_heads_kv=hkv, head_dim=d,
+                                       block_size=block_size, dtype=dt)
+    with _On(stream, ("q", q, q.dtype), ("k_win", k_win, q.dtype), ("v_win", v_win, q.dtype),
+             ("pool", pool, torch.uint8), ("page_table", page_table, torch.int32),
+             ("ctx_len", ctx_len, torch.int32), ("q_start", q_start, torch.int32),
+             ("out", out, q.dtype), ("lse", lse, torch.float32), ("workspace", workspace, None),
+             ("err", err, torch.int32)) as s:
+        _check(lib.d2f_block_attn_kv4(
+            _ptr(q), _ptr(k_win), _ptr(v_win), _ptr(pool), _ptr(page_table), page_table.shape[1],
+            _ptr(ctx_len), _ptr(q_start), _ptr(out), _ptr(lse), batch, total_q, max_q_per_seq,
+            max_ctx, hq, hkv, d, block_size, pool.shape[0], int(k_exp), int(v_exp), dt,
+            float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _ptr(err), s))
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# page map of a batch of requests
+# ---------------------------------------------------------------------------
+def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size, capacity,
+             max_append, ctx_len_out=None, free_count_out=None, err=None, stream=None):
+    """Lay out num_new[b] new tokens of each request behind its ctx_len[b] cached ones, with
+    pages off the free list (d2f_page_map). page_table is written in place; ctx_len_out and
+    free_count_out are new tensors unless given (ctx_len and free_count themselves update
+    in place).
+
+    Returns a dict: page_table, ctx_len, row_start [batch + 1], admitted uint8 [batch], slot
+    int64 [capacity], app_src / app_dst / app_rows [max_append] and n_append [1] (the list
+    kv4_append takes), free_count [1]."""
+    lib = load()
+    batch = num_new.shape[0]
+    dev = num_new.device
+    _shape(num_new, "num_new", (batch,))
+    _shape(ctx_len, "ctx_len", (batch,))
+    _shape(page_table, "page_table", (batch, page_table.shape[-1]))
+    _shape(free_count, "free_count", (1,))
+    i32 = dict(dtype=torch.int32, device=dev)
+    if ctx_len_out is None:
+        ctx_len_out = torch.empty(batch, **i32)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, **i32)
+    _shape(ctx_len_out, "ctx_len_out", (batch,))
+    _shape(free_count_out, "free_count_out", (1,))
+    if capacity < 0 or max_append < 0:
+        raise ValueError("capacity and max_append must not be negative")
+    row_start = torch.empty(batch + 1, **i32)
+    admitted = torch.empty(batch, dtype=torch.uint8, device=dev)
+    slot = torch.empty(capacity, dtype=torch.int64, device=dev)
+    app = torch.empty((3, max_append), **i32)
+    n_append = torch.empty(1, **i32)
+    with _On(stream, ("num_new", num_new, torch.int32), ("ctx_len", ctx_len, torch.int32),
+             ("page_table", page_table, torch.int32), ("free_pages", free_pages, torch.int32),
+             ("free_count", free_count, torch.int32), ("ctx_len_out", ctx_len_out, torch.int32),
+             ("free_count_out", free_count_out, torch.int32), ("err", err, torch.int32)) as s:
+        _check(lib.d2f_page_map(
+            batch, block_size, page_table.shape[1], capacity, max_append, _ptr(num_new),
+            _ptr(ctx_len), _ptr(free_pages), _ptr(free_count), _ptr(page_table),
+            _ptr(ctx_len_out), _ptr(free_count_out), _ptr(row_start), _ptr(admitted), _ptr(slot),
+            _ptr(app[0]), _ptr(app[1]), _ptr(app[2]), _ptr(n_append), _ptr(err), s))
+    return {"page_table": page_table, "ctx_len": ctx_len_out, "row_start": row_start,
+            "admitted": admitted, "slot": slot, "app_src": app[0], "app_dst": app[1],
+            "app_rows": app[2], "n_append": n_append, "free_count": free_count_out}
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens
+# ---------------------------------------------------------------------------
+def logprobs_workspace_size(n, vocab, top_k, dtype=BF16):
+    lib = load()
+    b = _SZ(0)
+    _check(lib.d2f_token_logprobs_workspace_size(n, vocab, top_k, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def logprobs_workspace(device, **kw):
+    """A zero-filled workspace of the size logprobs_workspace_size(**kw) returns."""
+    with torch.cuda.device(device):
+        return torch.zeros(max(logprobs_workspace_size(**kw), 1), dtype=torch.uint8, device=device)
+
+
+def token_logprobs(logits, tokens, *, logit_row=None, top_k=0, want_entropy=True, logprob=None,
+                   entropy=None, top_id=None, top_logprob=None, workspace=None, err=None,
+                   stream=None):
+    """Log probability of tokens[r] (int32; < 0: no token, the row is not read) in each row's
+    distribution, its entropy and its top_k alternatives (d2f_token_logprobs).
+
+    logits may be a row-strided view ([rows, vocab] with stride(1) == 1). Returns
+    dict(logprob [n], entropy [n] or None, top_id [n, top_k], top_logprob [n, top_k])."""
+    lib = load()
+    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor with unit stride along the vocabulary")
+    n = tokens.shape[0]
+    rows, vocab = logits.shape
+    if logit_row is None and rows < n:
+        raise ValueError("%d tokens for %d logit rows" % (n, rows))
+    _shape(tokens, "tokens", (n,))
+    _shape(logit_row, "logit_row", (n,))
+    dt = _dtype_code(logits)
+    dev = logits.device
+    if tokens.device != dev:
+        raise ValueError("tokens is on %s, logits on %s" % (tokens.device, dev))
+    f32 = dict(dtype=torch.float32, device=dev)
+    if logprob is None:
+        logprob = torch.empty(n, **f32)
+    if entropy is None and want_entropy:
+        entropy = torch.empty(n, **f32)
+    if top_id is None:
+        top_id = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+    if top_logprob is None:
+        top_logprob = torch.empty((n, top_k), **f32)
+    _shape(logprob, "logprob", (n,))
+    _shape(entropy, "entropy", (n,))
+    _shape(top_id, "top_id", (n, top_k))
+    _shape(top_logprob, "top_logprob", (n, top_k))
+    if workspace is None:
+        workspace = logprobs_workspace(dev, n=n, vocab=vocab, top_k=top_k, dtype=dt)
+    stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
+    with _On(stream, ("tokens", tokens, torch.int32), ("logit_row", logit_row, torch.int32),
+             ("logprob", logprob, torch.float32), ("entropy", entropy, torch.float32),
+             ("top_id", top_id, torch.int32), ("top_logprob", top_logprob, torch.float32),
+             ("workspace", workspace, None), ("err", err, torch.int32)) as s:
+        _check(lib.d2f_token_logprobs(
+            _ptr(logits), stride, dt, vocab, rows, _ptr(logit_row), _ptr(tokens), n, top_k,
+            _ptr(logprob), _ptr(entropy), _ptr(top_id), _ptr(top_logprob), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(err), s))
+    return {"logprob": logprob, "entropy": entropy, "top_id": top_id, "top_logprob": top_logprob}

@@ -513,6 +513,190 @@ int d2f_window_step(int batch, int block_size, int max_blocks, int capacity,
                     const int32_t *free_pages, int32_t *free_count, int32_t *app_src,
                     int32_t *app_dst, int32_t *n_append, int32_t *err_word, void *stream);
 
+/* ------------------------------------------------------------------------- */
+/* The 4-bit paged cache                                                     */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * A page pool whose elements take 4.5 bits ([P1] §운영 관점: a page holds exactly
+ * one finished block, whose K/V never change, so they are quantised once). One
+ * buffer holds K and V:
+ *   kv_pool  device uint8 [num_pages][num_heads_kv][page_bytes],
+ *            page_bytes = block_size * head_dim * 9 / 8 (d2f_kv4_page_bytes)
+ * Sixteen consecutive elements of a token's head row share a scale. With
+ * y = x * 2^-e in float (e = k_exp for K, v_exp for V: host constants of a pool,
+ * the power of two that centres its values; the same for every call on it),
+ *   scale = e4m3(max |y| / 6), code = e2m1(y / scale), value = code * scale * 2^e:
+ * float divisions, conversions to nearest with ties to even, saturating (e4m3 at
+ * 448, e2m1 at 6). Values of e2m1 are 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives. A group whose scale rounds to 0 (max |y| <= 6 * 2^-10) is all zeros,
+ * an infinity saturates, a NaN makes its group of sixteen NaN. Stored values are
+ * exact in bf16 and float (|e| <= D2F_KV4_MAX_EXP). With B = block_size and D =
+ * head_dim, the bytes of one page and head are, one after another,
+ *   K codes   [D / 32][B][16]  byte i of chunk c, token t: dims 32c + 2i (low nibble), + 1
+ *   V codes   [D][B / 2]       byte i of dim d: tokens 2i (low nibble), 2i + 1
+ *   K scales  [B][D / 16]      e4m3
+ *   V scales  [D / 16][B]      e4m3
+ * head_dim is 64 or 128 and block_size 8, 16 or 32 (else D2F_ERR_UNSUPPORTED); the
+ * pool is 16-byte aligned.
+ */
+#define D2F_KV4_MAX_EXP 64
+
+/* Bytes of one page of one KV head. */
+int d2f_kv4_page_bytes(int head_dim, int block_size, size_t *bytes);
+
+/*
+ * d2f_kv4_append -- quantise blocks of the window (or of a prompt's packed rows)
+ * into their pages: d2f_kv_append for a 4-bit pool.
+ *
+ *   k_win,v_win   device [total_q][num_heads_kv][head_dim], dtype, 16-byte aligned
+ *   src_row,
+ *   dst_page      device int32 [max_append]: entry a writes rows src_row[a] ..
+ *                 + n_rows[a] - 1 to page dst_page[a]. src_row need not be a
+ *                 multiple of block_size. Destination pages must be distinct.
+ *   n_rows        device int32 [max_append] or NULL (block_size rows each): rows of
+ *                 an entry, 0..block_size. The whole page is written: its slots past
+ *                 n_rows[a] hold zeros.
+ *   n_append_dev  device int32 [1] or NULL: entries to apply, read on the device (as
+ *                 d2f_kv_append_dev); NULL applies max_append
+ * Entries whose rows or page are out of range set err_word = D2F_ERR_BAD_INDEX and
+ * are skipped. d2f_window_step's and d2f_page_map's lists go in as they are.
+ */
+int d2f_kv4_append(const void *k_win, const void *v_win, const int32_t *src_row,
+                   const int32_t *dst_page, const int32_t *n_rows, const int32_t *n_append_dev,
+                   int max_append, int total_q, void *kv_pool, int num_heads_kv, int head_dim,
+                   int block_size, int num_pages, int k_exp, int v_exp, int dtype,
+                   int32_t *err_word, void *stream);
+
+/*
+ * d2f_kv4_read -- tokens of a 4-bit pool as dtype values (exact).
+ *
+ *   slot          device int64 [n]: page * block_size + offset of each token, or -1
+ *                 (d2f_page_map's slot map); a -1 gives zeros, another slot outside
+ *                 the pool zeros and err_word = D2F_ERR_BAD_INDEX
+ *   k_out, v_out  device [n][num_heads_kv][head_dim], dtype, 16-byte aligned
+ */
+int d2f_kv4_read(const void *kv_pool, const int64_t *slot, int n, void *k_out, void *v_out,
+                 int num_heads_kv, int head_dim, int block_size, int num_pages, int k_exp,
+                 int v_exp, int dtype, int32_t *err_word, void *stream);
+
+/* Workspace bytes for d2f_block_attn_kv4 with the same sizes, on the current device. */
+int d2f_block_attn_kv4_workspace_size(int batch, int total_q, int max_q_per_seq, int max_ctx,
+                                      int num_heads_q, int num_heads_kv, int head_dim,
+                                      int block_size, int dtype, size_t *bytes);
+
+/*
+ * d2f_block_attn_kv4 -- d2f_block_attn with the cached tokens in a 4-bit pool; the
+ * window's K/V are this step's, in dtype, unquantised.
+ *
+ * Arguments as d2f_block_attn, with kv_pool, k_exp and v_exp in place of k_pool and
+ * v_pool. The result is the attention over the stored values (code * scale * 2^e).
+ * D2F_BF16 runs on tensor cores, D2F_F32 on CUDA cores. A cached page whose id is
+ * out of range is left out of the softmax (err_word = D2F_ERR_BAD_INDEX). A key
+ * that a row does not see never reaches it, not even with infinite or NaN K or V;
+ * slots of a page past ctx_len may hold anything. ctx_len need not be a multiple of
+ * block_size. The workspace is the caller's, zeroed once (and again after a device
+ * error); captured graphs that may run at the same time need one each.
+ */
+int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, const void *kv_pool,
+                       const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,
+                       const int32_t *q_start, void *out, float *lse_out, int batch, int total_q,
+                       int max_q_per_seq, int max_ctx, int num_heads_q, int num_heads_kv,
+                       int head_dim, int block_size, int num_pages, int k_exp, int v_exp,
+                       int dtype, float softmax_scale, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, void *stream);
+
+/* ------------------------------------------------------------------------- */
+/* Page map of a batch of requests                                           */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * d2f_page_map -- block table, slot map and append list of a batch of requests,
+ * from their lengths, with pages off the device free list that d2f_window_step
+ * uses. It lays a batch's prompts out before their K/V exist, so a request enters
+ * the cache without a host readback.
+ *
+ * Request b brings num_new[b] >= 0 tokens behind its ctx_len[b] cached ones (a
+ * multiple of block_size: pages hold whole blocks). The tokens of all requests are
+ * packed rows: those of request b are row_start[b] .. row_start[b+1] - 1. Request b
+ * needs ceil(num_new[b] / block_size) pages. Requests are admitted in order while
+ * the pages of all so far fit both *free_count and max_append (those behind the
+ * first that does not fit are refused too); one whose page-table row is too short
+ * for it is refused alone and takes none. Pages are handed out in (request, block)
+ * order from the top of the list, free_pages[*free_count - 1] first.
+ *
+ *   num_new, ctx_len    device int32 [batch]
+ *   free_pages          device int32 [>= *free_count]; free_count device int32 [1]
+ *   page_table          device int32 [batch][max_pages_per_seq] in/out: the new
+ *                       blocks' entries are written, the others left
+ *   ctx_len_out         device int32 [batch]: ctx_len + num_new where admitted, else
+ *                       ctx_len; may be ctx_len itself
+ *   free_count_out      device int32 [1]: pages left; may be free_count itself
+ *   row_start           device int32 [batch+1]
+ *   admitted            device uint8 [batch]
+ *   slot_map            device int64 [capacity]: page * block_size + offset of each
+ *                       packed row; -1 for a refused request's rows and for rows
+ *                       past row_start[batch]
+ *   app_src, app_dst,
+ *   app_rows            device int32 [max_append]: first packed row, page and rows
+ *                       of each new block (d2f_kv4_append's list); -1, -1, 0 past
+ *                       the list
+ *   n_append            device int32 [1]: entries of the list
+ *   capacity            rows of slot_map; the packed rows must not exceed it
+ *
+ * Errors in err_word: D2F_ERR_NO_PAGE when a request was refused (the others are
+ * laid out); D2F_ERR_INVALID_ARG when nothing was written: a negative num_new,
+ * ctx_len or *free_count, a ctx_len that is no multiple of block_size, more packed
+ * rows than capacity. Page ids of the free list are taken as they are.
+ * D2F_ERR_UNSUPPORTED for batch > 16384.
+ */
+int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
+                 const int32_t *num_new, const int32_t *ctx_len, const int32_t *free_pages,
+                 const int32_t *free_count, int32_t *page_table, int32_t *ctx_len_out,
+                 int32_t *free_count_out, int32_t *row_start, uint8_t *admitted,
+                 int64_t *slot_map, int32_t *app_src, int32_t *app_dst, int32_t *app_rows,
+                 int32_t *n_append, int32_t *err_word, void *stream);
+
+/* ------------------------------------------------------------------------- */
+/* Log probabilities of given tokens                                         */
+/* ------------------------------------------------------------------------- */
+
+/* Workspace bytes for d2f_token_logprobs with the same sizes, on the current device. */
+int d2f_token_logprobs_workspace_size(int n, int vocab, int top_k, int dtype, size_t *bytes);
+
+/*
+ * d2f_token_logprobs -- log probability of a given token per row (a committed one,
+ * or one to score), the entropy of the row's distribution and its top_k largest
+ * logits, in one pass over the logits ([P3] §토큰 순서의 이론: a position's largest
+ * probabilities and its entropy).
+ *
+ * For each row r with tokens[r] >= 0, with l = the logit row logit_row[r] (or r when
+ * logit_row is NULL), m = max l, S = sum_v exp(l_v - m):
+ *   logprob[r] = l[tokens[r]] - m - ln S
+ *   entropy[r] = ln S - (1/S) sum_v exp(l_v - m) (l_v - m)   (-sum p ln p)
+ *   top_id[r][i], top_logprob[r][i]: the i-th largest logit's index and log
+ *     probability; equal logits in order of index.
+ * in float. A logit of -inf has probability 0 and adds nothing. A NaN or +inf logit,
+ * or a row without any logit above -inf, makes the row's logprob and entropy NaN;
+ * NaN logits never enter top_id (-1 and 0 where fewer than top_k are left). Rows
+ * with tokens[r] < 0 are not read: logprob and entropy 0, top_id -1, top_logprob 0.
+ * The same for a token >= vocab or a logit_row out of range, with err_word =
+ * D2F_ERR_BAD_INDEX.
+ *
+ *   logits       device [num_logit_rows][row_stride] dtype; columns >= vocab are not read
+ *   tokens       device int32 [n]; logit_row device int32 [n] or NULL
+ *   logprob      device float [n]; entropy device float [n] or NULL
+ *   top_id       device int32 [n][top_k]; top_logprob device float [n][top_k]
+ *                (NULL with top_k 0)
+ *   top_k        0..32 (more: D2F_ERR_UNSUPPORTED), at most vocab
+ * Limits: n <= 65535, vocab <= 2^30.
+ */
+int d2f_token_logprobs(const void *logits, int64_t row_stride, int dtype, int vocab,
+                       int num_logit_rows, const int32_t *logit_row, const int32_t *tokens, int n,
+                       int top_k, float *logprob, float *entropy, int32_t *top_id,
+                       float *top_logprob, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
