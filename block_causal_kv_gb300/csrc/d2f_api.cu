@@ -929,7 +929,8 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
     return fail(D2F_ERR_INVALID_ARG, "max_ctx %d exceeds max_pages_per_seq * block_size", max_ctx);
   if (max_pages_per_seq > 0 && (!kv_pool || !page_table))
     return fail(D2F_ERR_INVALID_ARG, "a cached context needs kv_pool and page_table");
-  if (!(softmax_scale > 0.f)) return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0");
+  if (!(softmax_scale > 0.f && softmax_scale < 3e38f))
+    return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0 and finite");
   const void *ptrs[] = {q, k_win, v_win, kv_pool, out};
   for (const void *x : ptrs)
     if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
