@@ -1,0 +1,984 @@
+// Tensor-core path of d2f_block_attn_kv4 (bf16 queries and window, 4-bit cached
+// tokens; layout and conversions of the cache: kv4.cuh).
+//
+// Source of the computation: "D2F: 확산 언어 모델이 KV 캐시를 얻고 자기회귀
+// 모델보다 2.5배 빨라지는 방법", §블록 단위 인과 어텐션 (bidirectional inside a
+// block, causal between blocks, finished blocks in a KV cache) and §운영 관점
+// (paged cache, one block per page); "확산 언어 모델(Diffusion LLM)이란 무엇인가",
+// §FlashBlock (attention parts recombined in log space).
+//
+// Orientation. A window has few query rows and a cache many keys, so the products
+// put keys and head dims on the 128 rows of the MMA and the queries on its columns:
+//   S^T [128 keys x rows] = K [128 keys x D] Q^T,
+//   O^T [D x rows]       += V^T [D x 128 keys] P^T.
+// K and V^T are then the A operands, which tcgen05 reads from tensor memory: a
+// thread dequantises the codes of one key (or one dim) in registers and stores them
+// to its own TMEM lane. Dequantised tiles never pass through shared memory, whose
+// bandwidth would bound the kernel (4x the bytes that the cache read brings), and
+// the MMA's time follows the real number of rows in steps of 16.
+//
+// Types. Stored values are exact in fp16, so cached tiles multiply in fp16: Q is
+// scaled per row by a power of two so that its largest element is in [2^14, 2^15)
+// (8 significant bits stay exact down to 2^-28 of it), P is rounded to fp16 (2^-11).
+// Window tiles keep bf16 K, V and Q and round P to bf16. Sums, maxima and both
+// accumulators are float.
+//
+// Work. Row tile m of (sequence, KV head) holds up to NT = 64 or 128 of its
+// group * n query rows (row r = query r / group, head r % group); its key tiles (128
+// cached tokens each, then 128 window rows each) are units of work. All units of the
+// launch are one line, cut into equal shares, one CTA a share: every SM gets the
+// same number of tiles whatever the batch looks like. A row tile whose units lie in
+// several shares is put together by the CTA that arrives last at its counter, from
+// float partials in the workspace, in unit order (the result does not depend on who
+// is last). No CTA waits on another.
+//
+// Roles of a CTA's warps:
+//   0        producer: page ids -> one bulk copy per page (K and V of a head are one
+//            contiguous piece) into a ring of stages
+//   1, 2     MMA issuers of S^T and of O^T (one lane each)
+//   dequant  K warpgroup and V warpgroup (one warpgroup for both with NT = 128)
+//   softmax  a warpgroup per 32 columns, thread = key lane: online softmax whose
+//            per-column reference moves only when a score exceeds it by 2^8, so the
+//            columns' maxima are not reduced over the lanes tile by tile
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+
+#include "kv4.cuh"
+
+namespace d2f {
+namespace {
+
+constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K extent of O^T)
+constexpr float kRescale = 8.0f;           // a reference moves when a score exceeds it by 2^8
+constexpr int kMaxBatch = kKv4MaxBatch;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kDq = NT == 64 ? 2 : 1;        // dequantising warpgroups
+  static constexpr int kSw = NT / 32;                 // softmax warpgroups
+  static constexpr int kThreads = 128 * (1 + kDq + kSw);
+  static constexpr int kBuf = NT == 64 ? 2 : 1;       // K and V^T operand buffers in TMEM
+  static constexpr int kStages = NT == 64 ? 5 : 4;
+  static constexpr int kNh = NT / 64;                 // 64-column (128-byte) blocks of P
+  // TMEM columns: two S buffers, O, then the K and V^T operands (two halves a column)
+  static constexpr uint32_t kTmS = 0, kTmO = 2 * NT, kTmK = 3 * NT, kTmV = kTmK + kBuf * (D / 2);
+  static_assert(kTmV + kBuf * (kKeys / 2) <= 512, "TMEM columns");
+  // shared memory: Q in fp16 and in bf16, two P buffers, the ring, the small arrays
+  static constexpr int kQBytes = NT * D * 2;
+  static constexpr int kPBytes = kKeys * NT * 2;
+  static constexpr int kStage = kKeys * D * 9 / 8;
+  static constexpr int kQ16 = 0, kQbf = kQBytes, kP = 2 * kQBytes, kRing = kP + 2 * kPBytes;
+  static constexpr int kMisc = kRing + kStages * kStage;
+  static constexpr int kPSbo = kNh * 1024;            // bytes between 8-key groups of P
+};
+
+template <int D, int NT>
+struct Misc {
+  using C = Cfg<D, NT>;
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
+  uint32_t tmem_base;
+  int abort_flag, last;
+  alignas(16) float c[NT];        // cached tiles: factor of a score, log2 units
+  alignas(16) float nm[NT];       // minus the column's reference maximum (0: none yet)
+  alignas(16) float al[NT];       // rescale factors, then output factors
+  alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
+  float red[C::kSw][4][32];       // reductions over a warpgroup's warps
+  uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
+  uint8_t pvalid[C::kStages][16]; // valid tokens of a stage's pages
+  // Per dim: first window block whose V is not finite, the value, and the first block at
+  // which the sum of such values is NaN. By segment mod 4: V^T tiles run up to two
+  // segments ahead of the epilogue that reads them.
+  int nf_blk[4][128], nf_nan[4][128];
+  float nf_val[4][128];
+  alignas(8) long long pre[1];    // units before each sequence, [batch + 1] (runs on)
+};
+
+// ---- small device helpers ----------------------------------------------------
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1)
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ bool named_sync_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+// kind::f16 instruction descriptor: as idesc_bf16_f32, for fp16 (bf = 0) or bf16 operands.
+__device__ __forceinline__ uint32_t idesc(int bf, int n, int b_mn) {
+  return (1u << 4) | ((uint32_t)bf << 7) | ((uint32_t)bf << 10) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
+}
+
+// Largest (or sum) over the 32 lanes of each of 32 registers: lane j gets column j's.
+template <bool SUM>
+__device__ __forceinline__ float transpose_reduce(const float (&v)[32], int lane) {
+  float w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const bool up = lane & 16;
+    const float mine = up ? v[i + 16] : v[i], other = up ? v[i] : v[i + 16];
+    const float got = __shfl_xor_sync(0xffffffffu, other, 16);
+    w[i] = SUM ? mine + got : fmaxf(mine, got);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float mine = up ? w[i + o] : w[i], other = up ? w[i] : w[i + o];
+      const float got = __shfl_xor_sync(0xffffffffu, other, o);
+      w[i] = SUM ? mine + got : fmaxf(mine, got);
+    }
+  }
+  return w[0];
+}
+
+// ---- work line -----------------------------------------------------------------
+// Row tiles of a sequence: `tiles` of `rows` rows each (a multiple of 16, the last
+// one shorter), as equal as 16 rows allow.
+struct RowTiles {
+  int tiles, rows;
+};
+__device__ __forceinline__ RowTiles row_tiles(int total, int nt) {
+  RowTiles r;
+  r.tiles = (total + nt - 1) / nt;
+  if (r.tiles == 0) return {0, 16};
+  r.rows = ((total + r.tiles - 1) / r.tiles + 15) & ~15;
+  r.tiles = (total + r.rows - 1) / r.rows;
+  return r;
+}
+
+struct Seg {      // the part of one row tile that lies in a CTA's share
+  int q0, n, C;   // sequence: first window row, window rows, cached tokens
+  int b, g;
+  int r0, nrows;  // rows of the tile
+  int t0, len;    // key tiles [t0, t0 + len) of T; the first Tc are cached
+  int T, Tc;
+  long long w0;   // first unit of the row tile on the line
+  int item;       // its counter
+};
+
+// The segment that starts at unit w of the line (w < w1: end of the share).
+template <int NT>
+__device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, long long w,
+                                       long long w1) {
+  int lo = 0, hi = a.batch - 1;  // largest b with pre[b] <= w
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= w) lo = mid; else hi = mid - 1;
+  }
+  Seg s;
+  s.b = lo;
+  s.q0 = __ldg(a.q_start + lo);
+  s.n = __ldg(a.q_start + lo + 1) - s.q0;
+  s.C = __ldg(a.ctx_len + lo);
+  const RowTiles rt = row_tiles(a.group * s.n, NT);
+  s.Tc = (s.C + kKeys - 1) / kKeys;
+  s.T = s.Tc + (s.n + kKeys - 1) / kKeys;
+  const long long local = w - pre[lo];
+  const int it = (int)(local / s.T);
+  s.t0 = (int)(local - (long long)it * s.T);
+  s.w0 = w - s.t0;
+  s.len = (int)min((long long)(s.T - s.t0), w1 - w);
+  s.g = it / rt.tiles;
+  const int m = it - s.g * rt.tiles;
+  s.r0 = m * rt.rows;
+  s.nrows = min(rt.rows, a.group * s.n - s.r0);
+  s.item = (s.b * a.num_heads_kv + s.g) * a.m_tiles + m;
+  return s;
+}
+
+// ---- dequantisation ---------------------------------------------------------------
+// 8 codes (a word) times a scale (packed pair) -> 4 packed halves.
+__device__ __forceinline__ void dq8(uint32_t w, uint32_t s, uint32_t *out) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = hmul2(e2m1x2_to_half2((w >> (8 * i)) & 0xffu), s);
+}
+
+// 64 dims (half h) of token o of the page tile at `tile`.
+template <int D>
+__device__ __forceinline__ void dq_k(uint32_t tile, int B, int o, int h, uint32_t (&out)[32]) {
+  const uint32_t sc = lds32(tile + B * D + o * (D / 16) + h * 4);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint4 w = lds128(tile + ((h * 2 + c) * B + o) * 16);
+    const uint32_t s0 = e4m3x2_to_half2(__byte_perm(sc, 0, c ? 0x22 : 0x00));
+    const uint32_t s1 = e4m3x2_to_half2(__byte_perm(sc, 0, c ? 0x33 : 0x11));
+    dq8(w.x, s0, out + 16 * c);
+    dq8(w.y, s0, out + 16 * c + 4);
+    dq8(w.z, s1, out + 16 * c + 8);
+    dq8(w.w, s1, out + 16 * c + 12);
+  }
+}
+
+// 8 tokens of one dim: codes word w, scale bytes (s.x: tokens 0-3, s.y: 4-7), of which
+// the first `valid` tokens count (the others give 0 whatever their scale).
+__device__ __forceinline__ void dq_v8(uint32_t w, uint2 s, int valid, uint32_t *out) {
+  if (valid < 8) {
+    s.x &= valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1;
+    s.y &= valid <= 4 ? 0u : (1u << (8 * (valid - 4))) - 1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t sp = e4m3x2_to_half2(((i < 2 ? s.x : s.y) >> (16 * (i & 1))) & 0xffffu);
+    out[i] = hmul2(e2m1x2_to_half2((w >> (8 * i)) & 0xffu), sp);
+  }
+}
+
+// 64 keys (half h of the tile) of dim d.
+template <int D, int B>
+__device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, int d, int h,
+                                     uint32_t (&out)[32]) {
+  constexpr int kPage = B * D + B * D / 8;
+  constexpr int kPages = 64 / B;
+#pragma unroll
+  for (int p = 0; p < kPages; ++p) {
+    const int page = h * kPages + p;
+    const uint32_t tile = stage + page * kPage;
+    const int valid = pvalid[page];
+    const uint32_t ca = tile + B * D / 2 + d * (B / 2);
+    const uint32_t sa = tile + B * D + B * D / 16 + (d >> 4) * B;
+    uint32_t *o = out + p * (B / 2);
+    if constexpr (B == 8) {
+      dq_v8(lds32(ca), lds64(sa), valid, o);
+    } else {
+#pragma unroll
+      for (int q = 0; q < B / 16; ++q) {
+        const uint2 w = lds64(ca + 8 * q);
+        const uint4 s = lds128(sa + 16 * q);
+        dq_v8(w.x, make_uint2(s.x, s.y), valid - 16 * q, o + 8 * q);
+        dq_v8(w.y, make_uint2(s.z, s.w), valid - 16 * q - 8, o + 8 * q + 4);
+      }
+    }
+  }
+}
+
+// ---- the kernel ---------------------------------------------------------------------
+constexpr int kBarSoft = 1;  // named barriers 1 .. kSw: a softmax warpgroup; kSw + 1: all of them
+
+template <int D, int NT>
+__global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(const AttnArgs a) {
+  using C = Cfg<D, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  Misc<D, NT> *ms = reinterpret_cast<Misc<D, NT> *>(smem + C::kMisc);
+  volatile int *abort_flag = &ms->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_u32(&ms->full[i]), 1);
+      mbar_init(smem_u32(&ms->empty[i]), 4 * C::kDq);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ms->k_full[i]), 4);
+      mbar_init(smem_u32(&ms->v_full[i]), 4);
+      mbar_init(smem_u32(&ms->k_free[i]), 1);
+      mbar_init(smem_u32(&ms->v_free[i]), 1);
+      mbar_init(smem_u32(&ms->s_full[i]), 1);
+      mbar_init(smem_u32(&ms->s_free[i]), 4 * C::kSw);
+      mbar_init(smem_u32(&ms->p_full[i]), 4 * C::kSw);
+      mbar_init(smem_u32(&ms->pv_done[i]), 1);
+    }
+    mbar_init(smem_u32(&ms->q_full), 4 * C::kSw);
+    mbar_init(smem_u32(&ms->drain), 2);
+    ms->abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ms->tmem_base), 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- the line of work: units before each sequence -----------------------------
+  long long *pre = ms->pre;
+  if (warp == 0) {
+    long long run = 0;
+    for (int base = 0; base < a.batch; base += 32) {
+      const int b = base + lane;
+      long long u = 0;
+      if (b < a.batch) {
+        int q0, n, ctx;
+        if (load_seq_meta(a, b, q0, n, ctx)) {
+          const long long tiles = (ctx + kKeys - 1LL) / kKeys + (n + kKeys - 1) / kKeys;
+          u = tiles * a.num_heads_kv * row_tiles(a.group * n, NT).tiles;
+        } else if (blockIdx.x == 0) {
+          set_err(a.err, D2F_ERR_INVALID_ARG);
+        }
+      }
+      long long inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (b < a.batch) pre[b] = run + inc - u;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) pre[a.batch] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem_base;
+  const long long W = pre[a.batch];
+  // shares of at least one unit; the CTAs past the last share have none
+  const long long n_cta = min((long long)gridDim.x, W);
+  const bool has = blockIdx.x < n_cta;
+  const long long wb = has ? W * blockIdx.x / n_cta : 0, we = has ? W * (blockIdx.x + 1) / n_cta : 0;
+  const int B = a.block_size;
+  const int page_bytes = B * D + B * D / 8;
+  const long long wait = a.wait_cycles;
+
+  if (warp == 0) {
+    // ============================ producer =======================================
+    const int ppt = kKeys / B;
+    int cu = 0;  // cached tiles so far: stage cu % kStages
+    bool ok = true;
+    for (long long w = wb; w < we && ok;) {
+      const Seg s = segment<NT>(a, pre, w, we);
+      w += s.len;
+      const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
+      const int t1 = min(s.t0 + s.len, s.Tc);
+      auto fetch = [&](int t) -> int {  // page id of this lane's slot of tile t
+        return t < t1 && lane < ppt && (int64_t)t * kKeys + lane * B < s.C
+                   ? __ldg(pt + (int64_t)t * ppt + lane) : -1;
+      };
+      int id = fetch(s.t0);
+      for (int t = s.t0; t < t1; ++t, ++cu) {
+        const int next = fetch(t + 1);
+        const int st = cu % C::kStages;
+        if (cu >= C::kStages) {
+          ok = mbar_wait(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, wait);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        const int first = t * kKeys + lane * B;  // first token of the slot
+        int valid = lane < ppt ? min(max(s.C - first, 0), B) : 0;
+        if (valid > 0 && (id < 0 || id >= a.num_pages)) {
+          set_err(a.err, D2F_ERR_BAD_INDEX);
+          valid = 0;
+        }
+        if (lane < 16) ms->pvalid[st][lane] = (uint8_t)valid;
+        const unsigned have = __ballot_sync(0xffffffffu, valid > 0);
+        const uint32_t full = smem_u32(&ms->full[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * (uint32_t)page_bytes);
+        __syncwarp();
+        if (valid > 0)
+          bulk_load(sb + C::kRing + st * C::kStage + lane * page_bytes,
+                    a.kv4_pool + ((int64_t)id * a.num_heads_kv + s.g) * page_bytes, page_bytes, full);
+        id = next;
+      }
+    }
+    if (lane == 0) {  // every copy issued must have landed before the CTA ends
+      for (int i = max(0, cu - C::kStages); i < cu; ++i) {
+        volatile int no_abort = 0;
+        mbar_wait(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err,
+                  kDrainCycles);
+      }
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ============================ MMA issuers ======================================
+    if (lane == 0) {
+      bool ok = true;
+      int u = 0, sg = 0;
+      const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
+      const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
+      for (long long w = wb; w < we && ok; ++sg) {
+        const Seg s = segment<NT>(a, pre, w, we);
+        w += s.len;
+        const int ncols = (s.nrows + 15) & ~15;
+        if (warp == 1) ok = mbar_wait(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
+        for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
+          const int bf = t >= s.Tc;  // window tiles are bf16
+          const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
+          if (warp == 1) {
+            ok = mbar_wait(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, wait) &&
+                 (u < 2 || mbar_wait(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
+                                     a.err, wait));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t id = idesc(bf, ncols, 0);
+            const uint64_t qd = smem_desc_advance(q_desc, bf ? C::kQbf - C::kQ16 : 0);
+            const uint32_t sd = tmem + C::kTmS + (u & 1) * NT, ka = tmem + C::kTmK + kb * (D / 2);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              umma_bf16_tmem_a(sd, ka + k * 8,
+                               smem_desc_advance(qd, (k >> 2) * (NT * 128) + (k & 3) * 32), id, k > 0);
+            umma_commit(smem_u32(&ms->s_full[u & 1]));
+            umma_commit(smem_u32(&ms->k_free[kb]));
+          } else {
+            ok = mbar_wait(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, wait) &&
+                 mbar_wait(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, wait);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t id = idesc(bf, ncols, 1);
+            const uint64_t pd = smem_desc_advance(p_desc, (u & 1) * C::kPBytes);
+            const uint32_t va = tmem + C::kTmV + kb * (kKeys / 2);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
+                               id, t > s.t0 || k > 0);
+            umma_commit(smem_u32(&ms->pv_done[u & 1]));
+            umma_commit(smem_u32(&ms->v_free[kb]));
+          }
+        }
+      }
+      umma_commit(smem_u32(&ms->drain));
+      volatile int no_abort = 0;
+      mbar_wait(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
+    }
+  } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
+    // ============================ dequantisation =====================================
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;  // key of the K tile, dim of the V^T tile
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const bool do_k = C::kDq == 1 || warp < 8, do_v = C::kDq == 1 || warp >= 8;
+    int u = 0, cu = 0, sg = 0;
+    bool ok = true;
+    for (long long w = wb; w < we && ok; ++sg) {
+      const Seg s = segment<NT>(a, pre, w, we);
+      w += s.len;
+      int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
+      float nf_val = 0.f;
+      for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
+        const int kb = u % C::kBuf;
+        const bool reuse = u >= C::kBuf;  // the operand buffer held tile u - kBuf
+        const uint32_t free_ph = (u / C::kBuf - 1) & 1;
+        const bool win = t >= s.Tc;
+        const int st = cu % C::kStages;
+        const uint32_t stage = sb + C::kRing + st * C::kStage;
+        if (!win)
+          ok = mbar_wait(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+        if (do_k) {
+          uint32_t x[32];
+          const int wr = (t - s.Tc) * kKeys + row;  // window row, for a window tile
+          const int sh = B == 8 ? 3 : B == 16 ? 4 : 5;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            if (!win) {
+              if (h == 0) {
+                const unsigned m = __ballot_sync(
+                    0xffffffffu, (row & (B - 1)) < (int)ms->pvalid[st][row >> sh]);
+                if (lane == 0) ms->vmask[u & 3][quad] = m;
+              }
+              dq_k<D>(stage + (row >> sh) * page_bytes, B, row & (B - 1), h, x);
+            } else {
+              const uint4 *src = reinterpret_cast<const uint4 *>(
+                  static_cast<const uint16_t *>(a.k_win) +
+                  ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D + h * 64);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = wr < s.n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                x[4 * i] = v.x;
+                x[4 * i + 1] = v.y;
+                x[4 * i + 2] = v.z;
+                x[4 * i + 3] = v.w;
+              }
+            }
+            if (h == 0 && reuse) {
+              ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+            }
+            __syncwarp();
+            tmem_st32(lane_base + C::kTmK + kb * (D / 2) + h * 32, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ms->k_full[kb]));
+        }
+        if (do_v) {
+          if (D == 64 && row >= 64) {
+            // (lanes past the head dim: their output lanes are never read)
+          } else {
+            uint32_t x[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!win) {
+                if (B == 16) dq_v<D, 16>(stage, ms->pvalid[st], row, h, x);
+                else if (B == 32) dq_v<D, 32>(stage, ms->pvalid[st], row, h, x);
+                else dq_v<D, 8>(stage, ms->pvalid[st], row, h, x);
+              } else {
+                const int w0 = (t - s.Tc) * kKeys + h * 64;
+                const uint16_t *src = static_cast<const uint16_t *>(a.v_win) +
+                                      ((int64_t)(s.q0 + w0) * a.num_heads_kv + s.g) * D + row;
+                const int64_t step = (int64_t)a.num_heads_kv * D;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  uint32_t e[2];
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    const int k = 2 * i + j;
+                    e[j] = w0 + k < s.n ? (uint32_t)__ldg(src + k * step) : 0u;
+                    if ((e[j] & 0x7f80u) == 0x7f80u) {
+                      // infinite or NaN: out of the product (a hidden key's P is 0, and
+                      // 0 * infinity is not), into the sums of the rows that see it
+                      const float v = bf16_bits_to_float(e[j]);
+                      const int blk = (w0 + k) / B;
+                      if (nf_blk == 0x7fffffff) {
+                        nf_blk = blk;
+                        nf_val = v;
+                      } else {
+                        const float z = nf_val + v;
+                        if (z != z && nf_nan == 0x7fffffff) nf_nan = blk;
+                      }
+                      e[j] = 0;
+                    }
+                  }
+                  x[i] = e[0] | (e[1] << 16);
+                }
+              }
+              if (h == 0 && reuse) {
+                ok = ok && mbar_wait(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+              }
+              __syncwarp();
+              tmem_st32(lane_base + C::kTmV + kb * (kKeys / 2) + h * 32, x);
+            }
+            tmem_wait_st();
+          }
+          if (t == s.t0 + s.len - 1) {  // read by the epilogue, which follows this tile's product
+            ms->nf_blk[sg & 3][row] = nf_blk;
+            ms->nf_nan[sg & 3][row] = nf_nan;
+            ms->nf_val[sg & 3][row] = nf_val;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ms->v_full[kb]));
+        }
+        if (!win) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ms->empty[st]));
+          ++cu;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+  } else if (warp >= 4 + 4 * C::kDq) {
+    // ============================ softmax ============================================
+    const int wg = (warp - 4 - 4 * C::kDq) >> 2;  // columns 32 wg .. 32 wg + 31
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;             // key of the tile, later dim of O^T
+    const int bar = kBarSoft + wg, bar_all = kBarSoft + C::kSw;
+    const int stid = tid - 128 * (1 + C::kDq);    // thread among the softmax threads
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t o_addr = lane_base + C::kTmO + 32 * wg;
+    const int G = a.group, H = a.num_heads_q;
+    const float win_unit = 1.0f / a.v_mul;        // O is in units of 2^v_exp
+    int u = 0, sg = -1;
+    bool ok = true;
+    for (long long w = wb; w < we && ok;) {
+      ++sg;
+      const Seg s = segment<NT>(a, pre, w, we);
+      const bool starts_share = w == wb;
+      w += s.len;
+      const int ncols = (s.nrows + 15) & ~15;
+      const int cols = max(0, min(32, ncols - 32 * wg));  // 0, 16 or 32 of this warpgroup
+
+      // ---- Q: four threads per row; bf16 as it is, fp16 scaled by a power of two ------
+      {
+        const int qr = stid >> 2, part = stid & 3;
+        constexpr int kV = D / 32;  // 16-byte pieces of a thread
+        uint4 v[kV];
+        const int r = s.r0 + qr;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const uint16_t *>(a.q) +
+            ((int64_t)(s.q0 + r / G) * H + s.g * G + r % G) * D) + part * kV;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] = qr < s.nrows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;  // largest magnitude's bits
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const uint32_t wv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max(top, max(wv[j] & 0x7fffu, (wv[j] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = top ? min(max((int)(top >> 7) - 127 - 14, -126), 112) : 0;
+        const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const uint32_t wv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t hv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            hv[j] = pack_half2(__uint_as_float(wv[j] << 16) * down,
+                               __uint_as_float(wv[j] & 0xffff0000u) * down);
+          const int c = part * kV + i;
+          const uint32_t off = (c >> 3) * (NT * 128) + (qr >> 3) * 1024 + (qr & 7) * 128 +
+                               (((c & 7) ^ (qr & 7)) << 4);
+          sts128(sb + C::kQ16 + off, make_uint4(hv[0], hv[1], hv[2], hv[3]));
+          sts128(sb + C::kQbf + off, v[i]);
+        }
+        // (the other warpgroups are done with the previous segment's arrays)
+        named_sync(bar_all, 128 * C::kSw);
+        if (part == 0) {
+          const float up = __int_as_float((127 + e) << 23);
+          ms->c[qr] = a.scale_log2 * a.k_mul * up;
+          ms->nm[qr] = 0.f;
+          ms->blk[qr] = qr < s.nrows ? (r / G) / B : 0x7fffffff;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+        named_sync(bar_all, 128 * C::kSw);  // c, nm and blk of every column
+      }
+
+      float l[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+      float m_lane = -INFINITY;  // reference of column `lane`
+      bool unset = true;         // a column may have no reference yet
+      for (int t = s.t0; t < s.t0 + s.len; ++t, ++u) {
+        const bool win = t >= s.Tc;
+        const int sbuf = u & 1;
+        ok = mbar_wait(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
+        if (u >= 2)  // P of tile u - 2 has been read
+          ok = mbar_wait(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
+        __syncwarp();
+        tc_fence_after();
+        if (cols == 0) {
+          ok = named_sync_and(bar, 128, ok);
+          if (!ok) break;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&ms->s_free[sbuf]));
+            mbar_arrive(smem_u32(&ms->p_full[sbuf]));
+          }
+          continue;
+        }
+        const int kw = (t - s.Tc) * kKeys + row;  // window key
+        const bool valid = win ? kw < s.n : (ms->vmask[u & 3][quad] >> lane) & 1;
+        const int kblk = win ? kw / B : 0;
+        float x[32];
+        // scores in log2 units, keys that a column does not see at -inf; minus the
+        // columns' references if `sub`
+        auto scores = [&](bool sub) {
+          uint32_t sv[32];
+          tmem_ld32(lane_base + C::kTmS + sbuf * NT + 32 * wg, sv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (q >= 4 && cols == 16) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[4 * q + j] = -INFINITY;
+              continue;
+            }
+            float4 c4 = *reinterpret_cast<const float4 *>(&ms->c[32 * wg + 4 * q]);
+            float4 n4 = *reinterpret_cast<const float4 *>(&ms->nm[32 * wg + 4 * q]);
+            if (win) c4 = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+            if (!sub) n4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            fma2(x[4 * q], x[4 * q + 1], __uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1]),
+                 c4.x, c4.y, n4.x, n4.y);
+            fma2(x[4 * q + 2], x[4 * q + 3], __uint_as_float(sv[4 * q + 2]),
+                 __uint_as_float(sv[4 * q + 3]), c4.z, c4.w, n4.z, n4.w);
+          }
+          if (!__all_sync(0xffffffffu, valid)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!valid) x[j] = -INFINITY;
+          }
+          if (win) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int4 b4 = *reinterpret_cast<const int4 *>(&ms->blk[32 * wg + 4 * q]);
+              if (b4.x < kblk) x[4 * q] = -INFINITY;
+              if (b4.y < kblk) x[4 * q + 1] = -INFINITY;
+              if (b4.z < kblk) x[4 * q + 2] = -INFINITY;
+              if (b4.w < kblk) x[4 * q + 3] = -INFINITY;
+            }
+          }
+        };
+        scores(true);
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j + 1 < 32; j += 2) top = fmax3(top, x[j], x[j + 1]);
+        top = fmaxf(top, x[31]);
+        if (named_sync_or(bar, 128, unset || top > kRescale || !ok)) {
+          // ---- move references: the columns' maxima over the tile ------------------
+          // every P.V product so far must have landed in O before O is rescaled
+          if (t > s.t0)
+            ok = mbar_wait(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a.err,
+                           wait) && ok;
+          __syncwarp();
+          tc_fence_after();
+          scores(false);
+          const float wm = transpose_reduce<false>(x, lane);
+          ms->red[wg][quad][lane] = wm;
+          ok = named_sync_and(bar, 128, ok);
+          if (!ok) break;
+          const float m_tile = fmaxf(fmaxf(ms->red[wg][0][lane], ms->red[wg][1][lane]),
+                                     fmaxf(ms->red[wg][2][lane], ms->red[wg][3][lane]));
+          const bool move = m_tile > m_lane + kRescale || (m_lane == -INFINITY && m_tile > -INFINITY);
+          const float m_new = move ? m_tile : m_lane;
+          const float alpha = !move ? 1.f : m_lane == -INFINITY ? 0.f : fast_exp2(m_lane - m_new);
+          m_lane = m_new;
+          unset = __any_sync(0xffffffffu, m_new == -INFINITY && lane < cols);
+          if (quad == 0) {
+            ms->nm[32 * wg + lane] = m_new == -INFINITY ? 0.f : -m_new;
+            ms->al[32 * wg + lane] = alpha;
+          }
+          named_sync(bar, 128);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) l[j] *= ms->al[32 * wg + j];
+          if (t > s.t0) {
+            uint32_t o[32];
+            tmem_ld32(o_addr, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * ms->al[32 * wg + j]);
+            tmem_st32(o_addr, o);
+            tmem_wait_st();
+          }
+          scores(true);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sbuf]));
+        // ---- P = 2^x; the row sums take the unrounded values ------------------------
+        const uint32_t pb = sb + C::kP + sbuf * C::kPBytes + (row >> 3) * C::kPSbo +
+                            (wg >> 1) * 1024 + (row & 7) * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // 8 columns, 16 bytes
+          if (q >= 2 && cols == 16) break;
+          float p[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = fast_exp2(x[8 * q + j]);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            add2(l[8 * q + j], l[8 * q + j + 1], l[8 * q + j], l[8 * q + j + 1], p[j], p[j + 1]);
+          uint4 v;
+          if (win)
+            v = make_uint4(pack_bf16x2(p[0] * win_unit, p[1] * win_unit),
+                           pack_bf16x2(p[2] * win_unit, p[3] * win_unit),
+                           pack_bf16x2(p[4] * win_unit, p[5] * win_unit),
+                           pack_bf16x2(p[6] * win_unit, p[7] * win_unit));
+          else
+            v = make_uint4(pack_half2(p[0], p[1]), pack_half2(p[2], p[3]), pack_half2(p[4], p[5]),
+                           pack_half2(p[6], p[7]));
+          sts128(pb + ((((wg & 1) * 4 + q) ^ (row & 7)) << 4), v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[sbuf]));
+      }
+
+      // ---- epilogue of the segment (a warpgroup that gave up joins the vote) ----------
+      const int last = u - 1;
+      ok = ok && mbar_wait(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, wait);
+      __syncwarp();
+      const float ws = transpose_reduce<true>(l, lane);
+      ms->red[wg][quad][lane] = ws;
+      ok = named_sync_and(bar_all, 128 * C::kSw, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // sum of column `lane` (the same in the four warps)
+      const float L = (ms->red[wg][0][lane] + ms->red[wg][1][lane]) +
+                      (ms->red[wg][2][lane] + ms->red[wg][3][lane]);
+      const bool col_on = 32 * wg + lane < s.nrows;
+      uint32_t o[32];
+      tmem_ld32(o_addr, o);
+      tc_fence_before();
+      // infinite or NaN window values of this dim, for the rows that see them
+      if (s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff) {
+        const int nb = ms->nf_blk[sg & 3][row], nn = ms->nf_nan[sg & 3][row];
+        const float nv = ms->nf_val[sg & 3][row];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int bj = ms->blk[32 * wg + j];
+          if (bj >= nb) o[j] = __float_as_uint(__uint_as_float(o[j]) + (bj >= nn ? NAN : nv));
+        }
+      }
+      const bool dim_on = row < D;
+      uint16_t *outp = static_cast<uint16_t *>(a.out);
+      // output row of column j of this warpgroup
+      auto head_row = [&](int j) -> int64_t {
+        const int r = s.r0 + 32 * wg + j;
+        return (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
+      };
+      if (s.len == s.T) {
+        const float f = a.v_mul / L;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float fj = __shfl_sync(0xffffffffu, f, j);
+          if (32 * wg + j < s.nrows && dim_on)
+            outp[head_row(j) * D + row] = float_to_bf16_bits(__uint_as_float(o[j]) * fj);
+        }
+        if (quad == 0 && col_on && a.lse_out)
+          a.lse_out[head_row(lane)] = (m_lane + __log2f(L)) * 0.6931471805599453f;
+        continue;
+      }
+      // ---- a part of the row tile: to the workspace; the last to arrive composes --------
+      constexpr int kSlotFloats = NT * D + 2 * NT;
+      {
+        float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (starts_share ? 0 : 1)) * kSlotFloats;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (32 * wg + j < s.nrows && dim_on)
+            __stcg(slot + (32 * wg + j) * D + row, __uint_as_float(o[j]));
+        if (quad == 0 && col_on)
+          __stcg(reinterpret_cast<float2 *>(slot + NT * D) + 32 * wg + lane, make_float2(m_lane, L));
+      }
+      __threadfence();
+      named_sync(bar_all, 128 * C::kSw);
+      // shares that hold units of this row tile: share of unit w is ((w + 1) n - 1) / W
+      const int c0 = (int)(((s.w0 + 1) * n_cta - 1) / W);
+      const int c1 = (int)(((s.w0 + s.T) * n_cta - 1) / W);
+      if (stid == 0) {
+        const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == c1 - c0;
+        if (is_last) a.counters[s.item] = 0;
+        ms->last = is_last;
+      }
+      named_sync(bar_all, 128 * C::kSw);
+      const bool compose = ms->last != 0;
+      named_sync(bar_all, 128 * C::kSw);  // ms->last may be written again
+      if (!compose || cols == 0) continue;
+      __threadfence();
+      auto part = [&](int c) -> const float * {
+        // the first share's part is its first segment only if the row tile starts there
+        const bool second = c == c0 && W * c / n_cta != s.w0;
+        return a.ws_o + ((int64_t)2 * c + (second ? 1 : 0)) * kSlotFloats;
+      };
+      float Mx = -INFINITY;
+      for (int c = c0; c <= c1; ++c)
+        if (col_on)
+          Mx = fmaxf(Mx, __ldcg(reinterpret_cast<const float2 *>(part(c) + NT * D) + 32 * wg + lane).x);
+      float Lx = 0.f, acc[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float *p = part(c);
+        float wt = 0.f;
+        if (col_on) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + 32 * wg + lane);
+          wt = ml.x == -INFINITY && Mx != -INFINITY ? 0.f : ml.x == Mx ? 1.f : fast_exp2(ml.x - Mx);
+          Lx += wt * ml.y;
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = 32 * wg + j < s.nrows && dim_on ? __ldcg(p + (32 * wg + j) * D + row) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[j] = fmaf(__shfl_sync(0xffffffffu, wt, j), v[j], acc[j]);
+      }
+      const float f = a.v_mul / Lx;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        if (32 * wg + j < s.nrows && dim_on)
+          outp[head_row(j) * D + row] = float_to_bf16_bits(acc[j] * fj);
+      }
+      if (quad == 0 && col_on && a.lse_out)
+        a.lse_out[head_row(lane)] = (Mx + __log2f(Lx)) * 0.6931471805599453f;
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();  // every role is done, every copy and MMA complete
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, int NT>
+constexpr int smem_bytes(int batch) {
+  return Cfg<D, NT>::kMisc + (int)sizeof(Misc<D, NT>) + 8 * batch + 1024;
+}
+
+template <int D, int NT>
+cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+  static_assert(smem_bytes<D, NT>(kMaxBatch) <= 232448, "shared memory of a CTA");
+  static std::mutex mu;
+  static bool opted[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !opted[dev]) {
+    std::lock_guard<std::mutex> g(mu);
+    e = cudaFuncSetAttribute(attn_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes<D, NT>(kMaxBatch));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) opted[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_splits);
+  cfg.blockDim = dim3(Cfg<D, NT>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D, NT>(a.batch);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, NT>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_kv4(const AttnArgs &a, cudaStream_t s) {
+  if (a.head_dim == 64)
+    return a.tc_rows == 64 ? launch<64, 64>(a, s) : launch<64, 128>(a, s);
+  return a.tc_rows == 64 ? launch<128, 64>(a, s) : launch<128, 128>(a, s);
+}
+
+}  // namespace d2f

@@ -812,11 +812,30 @@ float exp2_int(int e) {
   return f;
 }
 
+// Attention over the 4-bit cache: bf16 on tensor cores, float on CUDA cores
+// (D2F_ATTN_PATH=simt forces the latter, as for d2f_block_attn).
 int kv4_plan(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, int D, int B,
              int dtype, AttnPlan *p) {
-  const int st = kv4_sizes(Hkv, D, B, 0, dtype, 0, 0);
+  int st = kv4_sizes(Hkv, D, B, 0, dtype, 0, 0);
   if (st != D2F_OK) return st;
-  return plan_attn(batch, total_q, max_q, max_ctx, Hq, Hkv, D, B, dtype, 0, p, false);
+  st = plan_attn(batch, total_q, max_q, max_ctx, Hq, Hkv, D, B, dtype, 0, p, false);
+  if (st != D2F_OK || dtype != D2F_BF16 || force_simt()) return st;
+  if (batch > kKv4MaxBatch)
+    return fail(D2F_ERR_UNSUPPORTED, "batch %d > %d", batch, kKv4MaxBatch);
+  const long long rows = (long long)(Hq / Hkv) * max_q;
+  p->tc = true;
+  p->rows = rows <= 64 ? 64 : 128;
+  p->m_tiles = max(1, cdiv(rows, p->rows));
+  const long long units = (long long)max(batch, 1) * Hkv * p->m_tiles *
+                          max(1, cdiv(max_ctx, 128) + cdiv(max_q, 128));
+  const int sms = max(1, num_sms_current_device());
+  p->splits = (int)min((long long)sms, max(1LL, units));
+  p->n_counters = max(batch, 1) * Hkv * p->m_tiles;
+  p->off_ml = 0;
+  p->off_o = align_up((size_t)p->n_counters * sizeof(int32_t));
+  const size_t slot = ((size_t)p->rows * D + 2 * p->rows) * sizeof(float);
+  p->bytes = p->off_o + 2 * slot * p->splits;  // two partial row tiles a CTA
+  return D2F_OK;
 }
 }  // namespace
 
@@ -969,6 +988,12 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
   a.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.off_ml);
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
   a.err = err_word;
+  if (p.tc) {
+    a.tc_rows = p.rows;
+    const cudaError_t e = launch_attn_kv4(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tensor-core kv4 attention launch");
+    return D2F_OK;
+  }
   const cudaError_t e = launch_attn_simt(a, dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "CUDA-core kv4 attention launch");
   return D2F_OK;

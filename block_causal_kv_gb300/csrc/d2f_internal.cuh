@@ -131,6 +131,8 @@ struct WindowArgs {
   int32_t *err;
 };
 
+constexpr int kKv4MaxBatch = 1024;  // sequences of one attention call over the 4-bit cache
+
 // A batch of requests larger than this does not fit the page map's shared memory
 // (three ints a request).
 constexpr int kPageMapMaxBatch = 16384;
@@ -187,6 +189,8 @@ struct LogprobsArgs {
 cudaError_t launch_commit(const CommitArgs &a, int dtype, int path, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs &a, bool vec_ok, cudaStream_t s);
 cudaError_t launch_window(const WindowArgs &a, cudaStream_t s);
+// tensor-core attention over the 4-bit cache: num_splits CTAs, tc_rows 64 or 128 rows a tile
+cudaError_t launch_attn_kv4(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_page_map(const PageMapArgs &a, cudaStream_t s);
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, int dtype, int D, cudaStream_t s);
 cudaError_t launch_kv4_read(const Kv4ReadArgs &a, int dtype, int D, cudaStream_t s);
