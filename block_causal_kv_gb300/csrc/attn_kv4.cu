@@ -58,6 +58,10 @@ struct Cfg {
   static constexpr int kDq = NT == 64 ? 2 : 1;        // dequantising warpgroups
   static constexpr int kSw = NT / 32;                 // softmax warpgroups
   static constexpr int kThreads = 128 * (1 + kDq + kSw);
+  static constexpr int kRegLaunch = NT == 64 ? 96 : 80;  // per thread at launch
+  static constexpr int kRegCtl = 40, kRegDq = NT == 64 ? 88 : 72, kRegSoft = NT == 64 ? 128 : 88;
+  static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
+                "register split within the launch's allocation");
   static constexpr int kBuf = NT == 64 ? 2 : 1;       // K and V^T operand buffers in TMEM
   static constexpr int kStages = NT == 64 ? 5 : 4;
   static constexpr int kNh = NT / 64;                 // 64-column (128-byte) blocks of P
@@ -85,9 +89,11 @@ struct Misc {
   alignas(16) float nm[NT];       // minus the column's reference maximum (0: none yet)
   alignas(16) float al[NT];       // rescale factors, then output factors
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
+  alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
   float red[C::kSw][4][32];       // reductions over a warpgroup's warps
   uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
   uint8_t pvalid[C::kStages][16]; // valid tokens of a stage's pages
+  bool ragged[C::kStages];        // ... some page has fewer than a full one
   // Per dim: first window block whose V is not finite, the value, and the first block at
   // which the sum of such values is NaN. By segment mod 4: V^T tiles run up to two
   // segments ahead of the epilogue that reads them.
@@ -97,6 +103,14 @@ struct Misc {
 };
 
 // ---- small device helpers ----------------------------------------------------
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
                                           uint32_t bar) {
   asm volatile(
@@ -153,6 +167,24 @@ __device__ __forceinline__ bool named_sync_or(int id, int count, bool v) {
       : "r"((uint32_t)v), "r"(id), "r"(count)
       : "memory");
   return r != 0;
+}
+// One lane of a converged warp. (The compiler knows that elect.sync picks a single
+// thread: an MMA issued under it takes its operands from uniform registers and issues
+// at the tensor pipe's rate, 24 cycles for 48 columns, where `lane == 0` takes 45.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 // kind::f16 instruction descriptor: as idesc_bf16_f32, for fp16 (bf = 0) or bf16 operands.
 __device__ __forceinline__ uint32_t idesc(int bf, int n, int b_mn) {
@@ -240,66 +272,265 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
 }
 
 // ---- dequantisation ---------------------------------------------------------------
-// 8 codes (a word) times a scale (packed pair) -> 4 packed halves.
-__device__ __forceinline__ void dq8(uint32_t w, uint32_t s, uint32_t *out) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = hmul2(e2m1x2_to_half2((w >> (8 * i)) & 0xffu), s);
+// The eight codes of a word as packed halves. (Byte-wise conversions straight from the
+// word: one ALU instruction per pair of codes, no shifts or masks.)
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t *out) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(w));
+}
+// The four e4m3 scales of a word as two packed pairs of halves.
+__device__ __forceinline__ void scales_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-// 64 dims (half h) of token o of the page tile at `tile`.
-template <int D>
-__device__ __forceinline__ void dq_k(uint32_t tile, int B, int o, int h, uint32_t (&out)[32]) {
-  const uint32_t sc = lds32(tile + B * D + o * (D / 16) + h * 4);
+// The 32 dims of one 16-byte piece of a K row, scales s0 (first 16) and s1.
+__device__ __forceinline__ void dq_k32(uint4 w, uint32_t s0, uint32_t s1, uint32_t *out) {
+  codes_to_half(w.x, out);
+  codes_to_half(w.y, out + 4);
+  codes_to_half(w.z, out + 8);
+  codes_to_half(w.w, out + 12);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint4 w = lds128(tile + ((h * 2 + c) * B + o) * 16);
-    const uint32_t s0 = e4m3x2_to_half2(__byte_perm(sc, 0, c ? 0x22 : 0x00));
-    const uint32_t s1 = e4m3x2_to_half2(__byte_perm(sc, 0, c ? 0x33 : 0x11));
-    dq8(w.x, s0, out + 16 * c);
-    dq8(w.y, s0, out + 16 * c + 4);
-    dq8(w.z, s1, out + 16 * c + 8);
-    dq8(w.w, s1, out + 16 * c + 12);
-  }
+  for (int i = 0; i < 8; ++i) out[i] = hmul2(out[i], s0);
+#pragma unroll
+  for (int i = 8; i < 16; ++i) out[i] = hmul2(out[i], s1);
 }
 
-// 8 tokens of one dim: codes word w, scale bytes (s.x: tokens 0-3, s.y: 4-7), of which
-// the first `valid` tokens count (the others give 0 whatever their scale).
-__device__ __forceinline__ void dq_v8(uint32_t w, uint2 s, int valid, uint32_t *out) {
-  if (valid < 8) {
-    s.x &= valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1;
-    s.y &= valid <= 4 ? 0u : (1u << (8 * (valid - 4))) - 1;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t sp = e4m3x2_to_half2(((i < 2 ? s.x : s.y) >> (16 * (i & 1))) & 0xffffu);
-    out[i] = hmul2(e2m1x2_to_half2((w >> (8 * i)) & 0xffu), sp);
-  }
+// Scale bytes of tokens 0-3 / 4-7 of which the first `valid` count: the others become 0.
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int valid) {
+  return valid >= 4 ? w : valid <= 0 ? 0u : w & ((1u << (8 * valid)) - 1);
 }
 
-// 64 keys (half h of the tile) of dim d.
+// 64 keys (half h of the tile) of dim d: out[i] holds keys 2i and 2i + 1. `ragged`:
+// some page holds fewer than B valid tokens (the others give 0 whatever their bytes).
 template <int D, int B>
-__device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, int d, int h,
-                                     uint32_t (&out)[32]) {
-  constexpr int kPage = B * D + B * D / 8;
-  constexpr int kPages = 64 / B;
+__device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool ragged, int d,
+                                     int h, uint32_t (&out)[32]) {
+  constexpr int kPage = B * D + B * D / 8, kPages = 64 / B;
+  uint32_t w[8], sc[16];  // the half's codes and scale bytes, every load before any use
+  const uint32_t ca = stage + h * kPages * kPage + B * D / 2 + d * (B / 2);
+  const uint32_t sa = stage + h * kPages * kPage + B * D + B * D / 16 + (d >> 4) * B;
 #pragma unroll
   for (int p = 0; p < kPages; ++p) {
-    const int page = h * kPages + p;
-    const uint32_t tile = stage + page * kPage;
-    const int valid = pvalid[page];
-    const uint32_t ca = tile + B * D / 2 + d * (B / 2);
-    const uint32_t sa = tile + B * D + B * D / 16 + (d >> 4) * B;
-    uint32_t *o = out + p * (B / 2);
     if constexpr (B == 8) {
-      dq_v8(lds32(ca), lds64(sa), valid, o);
+      w[p] = lds32(ca + p * kPage);
+      const uint2 v = lds64(sa + p * kPage);
+      sc[2 * p] = v.x;
+      sc[2 * p + 1] = v.y;
     } else {
+      if constexpr (B == 16) {
+        const uint2 v = lds64(ca + p * kPage);
+        w[2 * p] = v.x;
+        w[2 * p + 1] = v.y;
+      } else {
+        const uint4 v = lds128(ca + p * kPage);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+        w[4 * p + 2] = v.z;
+        w[4 * p + 3] = v.w;
+      }
 #pragma unroll
       for (int q = 0; q < B / 16; ++q) {
-        const uint2 w = lds64(ca + 8 * q);
-        const uint4 s = lds128(sa + 16 * q);
-        dq_v8(w.x, make_uint2(s.x, s.y), valid - 16 * q, o + 8 * q);
-        dq_v8(w.y, make_uint2(s.z, s.w), valid - 16 * q - 8, o + 8 * q + 4);
+        const uint4 v = lds128(sa + p * kPage + 16 * q);
+        const int i = p * (B / 4) + 4 * q;
+        sc[i] = v.x;
+        sc[i + 1] = v.y;
+        sc[i + 2] = v.z;
+        sc[i + 3] = v.w;
       }
+    }
+  }
+  if (ragged) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      sc[i] = keep_bytes(sc[i], (int)pvalid[h * kPages + 4 * i / B] - (4 * i) % B);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t s0, s1, s2, s3;
+    scales_to_half(sc[2 * i], s0, s1);
+    scales_to_half(sc[2 * i + 1], s2, s3);
+    codes_to_half(w[i], out + 4 * i);
+    out[4 * i] = hmul2(out[4 * i], s0);
+    out[4 * i + 1] = hmul2(out[4 * i + 1], s1);
+    out[4 * i + 2] = hmul2(out[4 * i + 2], s2);
+    out[4 * i + 3] = hmul2(out[4 * i + 3], s3);
+  }
+}
+
+// The warps that fill the K and V^T operands: thread = key of the K tile, dim of the
+// V^T tile.
+template <int D, int NT, int B>
+__device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D, NT> *ms, uint32_t sb,
+                                             uint32_t tmem, long long wb, long long we) {
+  using C = Cfg<D, NT>;
+  constexpr int kPage = B * D + B * D / 8;
+  volatile int *abort_flag = &ms->abort_flag;
+  const long long wait = a.wait_cycles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
+  const int row = quad * 32 + lane;
+  const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+  const bool do_k = C::kDq == 1 || warp < 8, do_v = C::kDq == 1 || warp >= 8;
+  int u = 0, cu = 0, sg = 0;
+  bool ok = true;
+  for (long long w = wb; w < we && ok; ++sg) {
+    const Seg s = segment<NT>(a, ms->pre, w, we);
+    w += s.len;
+    int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
+    float nf_val = 0.f;
+    for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
+      const int kb = u % C::kBuf;
+      const bool reuse = u >= C::kBuf;  // the operand buffer held tile u - kBuf
+      const uint32_t free_ph = (u / C::kBuf - 1) & 1;
+      const bool win = t >= s.Tc;
+      const int st = cu % C::kStages;
+      const uint32_t stage = sb + C::kRing + st * C::kStage;
+      if (!win)
+        ok = mbar_wait(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+      const bool ragged = !win && ms->ragged[st];
+      if (do_k) {
+        uint32_t x[32];
+        const uint32_t ka = lane_base + C::kTmK + kb * (D / 2);
+        if (!win) {
+          const uint32_t tile = stage + (row / B) * kPage;
+          const int o = row % B;
+          uint4 c[D / 32];
+          uint32_t sc[D / 64];
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) sc[i] = lds32(tile + B * D + o * (D / 16) + 4 * i);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) c[i] = lds128(tile + (i * B + o) * 16);
+          unsigned m = 0xffffffffu;
+          if (ragged) m = __ballot_sync(0xffffffffu, o < (int)ms->pvalid[st][row / B]);
+          if (lane == 0) ms->vmask[u & 3][quad] = m;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            uint32_t s01[2], s23[2];  // every scale in both halves of its pair
+            scales_to_half(__byte_perm(sc[h], 0, 0x1100), s01[0], s01[1]);
+            scales_to_half(__byte_perm(sc[h], 0, 0x3322), s23[0], s23[1]);
+            dq_k32(c[2 * h], s01[0], s01[1], x);
+            dq_k32(c[2 * h + 1], s23[0], s23[1], x + 16);
+            if (h == 0 && reuse) {
+              ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+            }
+            __syncwarp();
+            tmem_st32(ka + h * 32, x);
+          }
+        } else {
+          const int wr = (t - s.Tc) * kKeys + row;  // window row
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              static_cast<const uint16_t *>(a.k_win) +
+              ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D);
+          if (reuse) {
+            ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = wr < s.n ? __ldg(src + 8 * h + i) : make_uint4(0, 0, 0, 0);
+              x[4 * i] = v.x;
+              x[4 * i + 1] = v.y;
+              x[4 * i + 2] = v.z;
+              x[4 * i + 3] = v.w;
+            }
+            __syncwarp();
+            tmem_st32(ka + h * 32, x);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->k_full[kb]));
+      }
+      if (do_v) {
+        if (D == 128 || row < 64) {  // (lanes past the head dim: their output is never read)
+          const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
+          auto wait_free = [&] {
+            ok = ok && mbar_wait(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+          };
+          if (!win) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t x[32];
+              dq_v<D, B>(stage, ms->pvalid[st], ragged, row, h, x);
+              if (h == 0 && reuse) wait_free();
+              __syncwarp();
+              tmem_st32(va + h * 32, x);
+            }
+          } else {
+            if (reuse) wait_free();
+            const int64_t step = (int64_t)a.num_heads_kv * D;
+#pragma unroll 1
+            for (int w0 = 0; w0 < kKeys; w0 += 32) {  // 32 keys at a time
+              const int k0 = (t - s.Tc) * kKeys + w0;
+              const int left = s.n - k0;  // window rows from here on
+              const uint16_t *src = static_cast<const uint16_t *>(a.v_win) +
+                                    ((int64_t)(s.q0 + k0) * a.num_heads_kv + s.g) * D + row;
+              uint32_t x[16];
+              bool odd = false;  // a value is not finite
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {  // every load before any use
+                const uint32_t e0 = 2 * i < left ? (uint32_t)__ldg(src + 2 * i * step) : 0u;
+                const uint32_t e1 = 2 * i + 1 < left ? (uint32_t)__ldg(src + (2 * i + 1) * step) : 0u;
+                x[i] = e0 | (e1 << 16);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+              if (odd) {
+                // infinite or NaN: out of the product (a hidden key's P is 0, and
+                // 0 * infinity is not), into the sums of the rows that see it
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    const uint32_t e = (x[i] >> (16 * j)) & 0xffffu;
+                    if ((e & 0x7f80u) != 0x7f80u) continue;
+                    const float v = bf16_bits_to_float(e);
+                    const int blk = (k0 + 2 * i + j) / B;
+                    if (nf_blk == 0x7fffffff) {
+                      nf_blk = blk;
+                      nf_val = v;
+                    } else {
+                      const float z = nf_val + v;
+                      if (z != z && nf_nan == 0x7fffffff) nf_nan = blk;
+                    }
+                    x[i] &= j ? 0x0000ffffu : 0xffff0000u;
+                  }
+              }
+              __syncwarp();
+              tmem_st16(va + w0 / 2, x);
+            }
+          }
+          tmem_wait_st();
+        }
+        if (t == s.t0 + s.len - 1) {  // read by the epilogue, which follows this tile's product
+          ms->nf_blk[sg & 3][row] = nf_blk;
+          ms->nf_nan[sg & 3][row] = nf_nan;
+          ms->nf_val[sg & 3][row] = nf_val;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->v_full[kb]));
+      }
+      if (!win) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->empty[st]));
+        ++cu;
+      }
+      ok = __all_sync(0xffffffffu, ok);
     }
   }
 }
@@ -385,7 +616,11 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
   const int page_bytes = B * D + B * D / 8;
   const long long wait = a.wait_cycles;
 
-  if (warp == 0) {
+  // Registers: what the control and dequantising warps do not need goes to the softmax
+  // warps (the sum over the warpgroups stays under the launch's allocation).
+  if (warp < 4) {
+    set_regs_dec<C::kRegCtl>();
+    if (warp == 0) {
     // ============================ producer =======================================
     const int ppt = kKeys / B;
     int cu = 0;  // cached tiles so far: stage cu % kStages
@@ -416,6 +651,8 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
         }
         if (lane < 16) ms->pvalid[st][lane] = (uint8_t)valid;
         const unsigned have = __ballot_sync(0xffffffffu, valid > 0);
+        const bool whole = __all_sync(0xffffffffu, lane >= ppt || valid == B);
+        if (lane == 0) ms->ragged[st] = !whole;
         const uint32_t full = smem_u32(&ms->full[st]);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * (uint32_t)page_bytes);
@@ -435,7 +672,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
     }
   } else if (warp == 1 || warp == 2) {
     // ============================ MMA issuers ======================================
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       int u = 0, sg = 0;
       const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
@@ -484,136 +721,14 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       volatile int no_abort = 0;
       mbar_wait(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
     }
-  } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
-    // ============================ dequantisation =====================================
-    const int quad = warp & 3;
-    const int row = quad * 32 + lane;  // key of the K tile, dim of the V^T tile
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const bool do_k = C::kDq == 1 || warp < 8, do_v = C::kDq == 1 || warp >= 8;
-    int u = 0, cu = 0, sg = 0;
-    bool ok = true;
-    for (long long w = wb; w < we && ok; ++sg) {
-      const Seg s = segment<NT>(a, pre, w, we);
-      w += s.len;
-      int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
-      float nf_val = 0.f;
-      for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
-        const int kb = u % C::kBuf;
-        const bool reuse = u >= C::kBuf;  // the operand buffer held tile u - kBuf
-        const uint32_t free_ph = (u / C::kBuf - 1) & 1;
-        const bool win = t >= s.Tc;
-        const int st = cu % C::kStages;
-        const uint32_t stage = sb + C::kRing + st * C::kStage;
-        if (!win)
-          ok = mbar_wait(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
-        if (do_k) {
-          uint32_t x[32];
-          const int wr = (t - s.Tc) * kKeys + row;  // window row, for a window tile
-          const int sh = B == 8 ? 3 : B == 16 ? 4 : 5;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            if (!win) {
-              if (h == 0) {
-                const unsigned m = __ballot_sync(
-                    0xffffffffu, (row & (B - 1)) < (int)ms->pvalid[st][row >> sh]);
-                if (lane == 0) ms->vmask[u & 3][quad] = m;
-              }
-              dq_k<D>(stage + (row >> sh) * page_bytes, B, row & (B - 1), h, x);
-            } else {
-              const uint4 *src = reinterpret_cast<const uint4 *>(
-                  static_cast<const uint16_t *>(a.k_win) +
-                  ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D + h * 64);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = wr < s.n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                x[4 * i] = v.x;
-                x[4 * i + 1] = v.y;
-                x[4 * i + 2] = v.z;
-                x[4 * i + 3] = v.w;
-              }
-            }
-            if (h == 0 && reuse) {
-              ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
-              ok = __all_sync(0xffffffffu, ok);
-              tc_fence_after();
-            }
-            __syncwarp();
-            tmem_st32(lane_base + C::kTmK + kb * (D / 2) + h * 32, x);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ms->k_full[kb]));
-        }
-        if (do_v) {
-          if (D == 64 && row >= 64) {
-            // (lanes past the head dim: their output lanes are never read)
-          } else {
-            uint32_t x[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!win) {
-                if (B == 16) dq_v<D, 16>(stage, ms->pvalid[st], row, h, x);
-                else if (B == 32) dq_v<D, 32>(stage, ms->pvalid[st], row, h, x);
-                else dq_v<D, 8>(stage, ms->pvalid[st], row, h, x);
-              } else {
-                const int w0 = (t - s.Tc) * kKeys + h * 64;
-                const uint16_t *src = static_cast<const uint16_t *>(a.v_win) +
-                                      ((int64_t)(s.q0 + w0) * a.num_heads_kv + s.g) * D + row;
-                const int64_t step = (int64_t)a.num_heads_kv * D;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  uint32_t e[2];
-#pragma unroll
-                  for (int j = 0; j < 2; ++j) {
-                    const int k = 2 * i + j;
-                    e[j] = w0 + k < s.n ? (uint32_t)__ldg(src + k * step) : 0u;
-                    if ((e[j] & 0x7f80u) == 0x7f80u) {
-                      // infinite or NaN: out of the product (a hidden key's P is 0, and
-                      // 0 * infinity is not), into the sums of the rows that see it
-                      const float v = bf16_bits_to_float(e[j]);
-                      const int blk = (w0 + k) / B;
-                      if (nf_blk == 0x7fffffff) {
-                        nf_blk = blk;
-                        nf_val = v;
-                      } else {
-                        const float z = nf_val + v;
-                        if (z != z && nf_nan == 0x7fffffff) nf_nan = blk;
-                      }
-                      e[j] = 0;
-                    }
-                  }
-                  x[i] = e[0] | (e[1] << 16);
-                }
-              }
-              if (h == 0 && reuse) {
-                ok = ok && mbar_wait(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-              }
-              __syncwarp();
-              tmem_st32(lane_base + C::kTmV + kb * (kKeys / 2) + h * 32, x);
-            }
-            tmem_wait_st();
-          }
-          if (t == s.t0 + s.len - 1) {  // read by the epilogue, which follows this tile's product
-            ms->nf_blk[sg & 3][row] = nf_blk;
-            ms->nf_nan[sg & 3][row] = nf_nan;
-            ms->nf_val[sg & 3][row] = nf_val;
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ms->v_full[kb]));
-        }
-        if (!win) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ms->empty[st]));
-          ++cu;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-      }
     }
-  } else if (warp >= 4 + 4 * C::kDq) {
+  } else if (warp < 4 + 4 * C::kDq) {
+    set_regs_dec<C::kRegDq>();
+    if (B == 16) dequant_role<D, NT, 16>(a, ms, sb, tmem, wb, we);
+    else if (B == 32) dequant_role<D, NT, 32>(a, ms, sb, tmem, wb, we);
+    else dequant_role<D, NT, 8>(a, ms, sb, tmem, wb, we);
+  } else {
+    set_regs_inc<C::kRegSoft>();
     // ============================ softmax ============================================
     const int wg = (warp - 4 - 4 * C::kDq) >> 2;  // columns 32 wg .. 32 wg + 31
     const int quad = warp & 3;
@@ -676,6 +791,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
           const float up = __int_as_float((127 + e) << 23);
           ms->c[qr] = a.scale_log2 * a.k_mul * up;
           ms->nm[qr] = 0.f;
+          ms->hr[qr] = (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
           ms->blk[qr] = qr < s.nrows ? (r / G) / B : 0x7fffffff;
         }
         fence_proxy_async_smem();
@@ -724,10 +840,10 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
               for (int j = 0; j < 4; ++j) x[4 * q + j] = -INFINITY;
               continue;
             }
-            float4 c4 = *reinterpret_cast<const float4 *>(&ms->c[32 * wg + 4 * q]);
-            float4 n4 = *reinterpret_cast<const float4 *>(&ms->nm[32 * wg + 4 * q]);
-            if (win) c4 = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
-            if (!sub) n4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 n4 = sub ? *reinterpret_cast<const float4 *>(&ms->nm[32 * wg + 4 * q])
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 c4 = win ? make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2)
+                                  : *reinterpret_cast<const float4 *>(&ms->c[32 * wg + 4 * q]);
             fma2(x[4 * q], x[4 * q + 1], __uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1]),
                  c4.x, c4.y, n4.x, n4.y);
             fma2(x[4 * q + 2], x[4 * q + 3], __uint_as_float(sv[4 * q + 2]),
@@ -852,10 +968,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       const bool dim_on = row < D;
       uint16_t *outp = static_cast<uint16_t *>(a.out);
       // output row of column j of this warpgroup
-      auto head_row = [&](int j) -> int64_t {
-        const int r = s.r0 + 32 * wg + j;
-        return (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
-      };
+      auto head_row = [&](int j) -> int64_t { return ms->hr[32 * wg + j]; };
       if (s.len == s.T) {
         const float f = a.v_mul / L;
 #pragma unroll
