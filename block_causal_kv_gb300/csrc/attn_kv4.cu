@@ -40,9 +40,7 @@
 //   softmax  a warpgroup per 32 columns, thread = key lane: online softmax whose
 //            per-column reference moves only when a score exceeds it by 2^8, so the
 //            columns' maxima are not reduced over the lanes tile by tile
-#include <cstdio>
-#include <cstring>
-#include <mutex>
+#include <atomic>
 
 #include "kv4.cuh"
 
@@ -53,18 +51,19 @@ constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K ex
 constexpr float kRescale = 8.0f;           // a reference moves when a score exceeds it by 2^8
 constexpr int kMaxBatch = kKv4MaxBatch;
 
-template <int D, int NT>
+constexpr int NT = 64;                     // rows (columns of S^T and O^T) per row tile
+
+template <int D>
 struct Cfg {
-  static constexpr int kDq = NT == 64 ? 2 : 1;        // dequantising warpgroups
-  static constexpr int kSw = NT / 32;                 // softmax warpgroups
+  static constexpr int kDq = 2;                       // dequantising warpgroups: K, V^T
+  static constexpr int kSw = NT / 16;                 // softmax warpgroups, 16 columns each
   static constexpr int kThreads = 128 * (1 + kDq + kSw);
-  static constexpr int kRegLaunch = NT == 64 ? 96 : 80;  // per thread at launch
-  static constexpr int kRegCtl = 40, kRegDq = NT == 64 ? 88 : 72, kRegSoft = NT == 64 ? 128 : 88;
+  static constexpr int kRegLaunch = 72;               // registers per thread at launch
+  static constexpr int kRegCtl = 40, kRegDq = 96, kRegSoft = 64;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");
-  static constexpr int kBuf = NT == 64 ? 2 : 1;       // K and V^T operand buffers in TMEM
-  static constexpr int kStages = NT == 64 ? 5 : 4;
-  static constexpr int kNh = NT / 64;                 // 64-column (128-byte) blocks of P
+  static constexpr int kBuf = 2;                      // K and V^T operand buffers in TMEM
+  static constexpr int kStages = 5;
   // TMEM columns: two S buffers, O, then the K and V^T operands (two halves a column)
   static constexpr uint32_t kTmS = 0, kTmO = 2 * NT, kTmK = 3 * NT, kTmV = kTmK + kBuf * (D / 2);
   static_assert(kTmV + kBuf * (kKeys / 2) <= 512, "TMEM columns");
@@ -74,23 +73,24 @@ struct Cfg {
   static constexpr int kStage = kKeys * D * 9 / 8;
   static constexpr int kQ16 = 0, kQbf = kQBytes, kP = 2 * kQBytes, kRing = kP + 2 * kPBytes;
   static constexpr int kMisc = kRing + kStages * kStage;
-  static constexpr int kPSbo = kNh * 1024;            // bytes between 8-key groups of P
+  static constexpr int kPSbo = 1024;                  // bytes between 8-key groups of P
 };
 
-template <int D, int NT>
+template <int D>
 struct Misc {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_base;
-  int abort_flag, last;
+  int abort_flag;
+  int last, c0, c1, second;       // composition: the last to arrive; the row tile's shares
+  long long W, wb, we;            // units of the line, and this CTA's share of them
   alignas(16) float c[NT];        // cached tiles: factor of a score, log2 units
-  alignas(16) float nm[NT];       // minus the column's reference maximum (0: none yet)
-  alignas(16) float al[NT];       // rescale factors, then output factors
+  alignas(16) float nm[NT];       // minus the column's reference (0: none yet)
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
   alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
-  float red[C::kSw][4][32];       // reductions over a warpgroup's warps
+  float red[C::kSw][4][16];       // reductions over a warpgroup's warps
   uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
   uint8_t pvalid[C::kStages][16]; // valid tokens of a stage's pages
   bool ragged[C::kStages];        // ... some page has fewer than a full one
@@ -99,7 +99,7 @@ struct Misc {
   // segments ahead of the epilogue that reads them.
   int nf_blk[4][128], nf_nan[4][128];
   float nf_val[4][128];
-  alignas(8) long long pre[1];    // units before each sequence, [batch + 1] (runs on)
+  alignas(8) long long pre[1];    // units before each sequence, [batch] (runs on)
 };
 
 // ---- small device helpers ----------------------------------------------------
@@ -178,6 +178,26 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
+// 16 consecutive 32-bit TMEM columns of this thread's lane as floats, waited for.
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+      "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -192,28 +212,30 @@ __device__ __forceinline__ uint32_t idesc(int bf, int n, int b_mn) {
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
 }
 
-// Largest (or sum) over the 32 lanes of each of 32 registers: lane j gets column j's.
+// Largest (or sum) over the 32 lanes of each of 16 registers: lanes j and j + 16 get
+// column j's.
 template <bool SUM>
-__device__ __forceinline__ float transpose_reduce(const float (&v)[32], int lane) {
-  float w[16];
+__device__ __forceinline__ float transpose_reduce(const float (&v)[16], int lane) {
+  float w[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const bool up = lane & 16;
-    const float mine = up ? v[i + 16] : v[i], other = up ? v[i] : v[i + 16];
-    const float got = __shfl_xor_sync(0xffffffffu, other, 16);
+  for (int i = 0; i < 8; ++i) {
+    const bool up = lane & 8;
+    const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 8], 8);
+    const float mine = up ? v[i + 8] : v[i];
     w[i] = SUM ? mine + got : fmaxf(mine, got);
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = 4; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = lane & o;
-      const float mine = up ? w[i + o] : w[i], other = up ? w[i] : w[i + o];
-      const float got = __shfl_xor_sync(0xffffffffu, other, o);
+      const float got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + o], o);
+      const float mine = up ? w[i + o] : w[i];
       w[i] = SUM ? mine + got : fmaxf(mine, got);
     }
   }
-  return w[0];
+  const float got = __shfl_xor_sync(0xffffffffu, w[0], 16);
+  return SUM ? w[0] + got : fmaxf(w[0], got);
 }
 
 // ---- work line -----------------------------------------------------------------
@@ -222,9 +244,9 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[32], int lane
 struct RowTiles {
   int tiles, rows;
 };
-__device__ __forceinline__ RowTiles row_tiles(int total, int nt) {
+__device__ __forceinline__ RowTiles row_tiles(int total) {
   RowTiles r;
-  r.tiles = (total + nt - 1) / nt;
+  r.tiles = (total + NT - 1) / NT;
   if (r.tiles == 0) return {0, 16};
   r.rows = ((total + r.tiles - 1) / r.tiles + 15) & ~15;
   r.tiles = (total + r.rows - 1) / r.rows;
@@ -242,7 +264,6 @@ struct Seg {      // the part of one row tile that lies in a CTA's share
 };
 
 // The segment that starts at unit w of the line (w < w1: end of the share).
-template <int NT>
 __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, long long w,
                                        long long w1) {
   int lo = 0, hi = a.batch - 1;  // largest b with pre[b] <= w
@@ -255,11 +276,11 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   s.q0 = __ldg(a.q_start + lo);
   s.n = __ldg(a.q_start + lo + 1) - s.q0;
   s.C = __ldg(a.ctx_len + lo);
-  const RowTiles rt = row_tiles(a.group * s.n, NT);
+  const RowTiles rt = row_tiles(a.group * s.n);
   s.Tc = (s.C + kKeys - 1) / kKeys;
   s.T = s.Tc + (s.n + kKeys - 1) / kKeys;
   const long long local = w - pre[lo];
-  const int it = (int)(local / s.T);
+  const int it = (int)((uint32_t)local / (uint32_t)s.T);  // (a sequence has < 2^31 units)
   s.t0 = (int)(local - (long long)it * s.T);
   s.w0 = w - s.t0;
   s.len = (int)min((long long)(s.T - s.t0), w1 - w);
@@ -365,24 +386,26 @@ __device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool
 
 // The warps that fill the K and V^T operands: thread = key of the K tile, dim of the
 // V^T tile.
-template <int D, int NT, int B>
-__device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D, NT> *ms, uint32_t sb,
+template <int D, int B>
+__device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uint32_t sb,
                                              uint32_t tmem, long long wb, long long we) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   constexpr int kPage = B * D + B * D / 8;
   volatile int *abort_flag = &ms->abort_flag;
   const long long wait = a.wait_cycles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
   const int row = quad * 32 + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  const bool do_k = C::kDq == 1 || warp < 8, do_v = C::kDq == 1 || warp >= 8;
+  const bool do_k = warp < 8;
   int u = 0, cu = 0, sg = 0;
   bool ok = true;
+#pragma unroll 1
   for (long long w = wb; w < we && ok; ++sg) {
-    const Seg s = segment<NT>(a, ms->pre, w, we);
+    const Seg s = segment(a, ms->pre, w, we);
     w += s.len;
     int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
     float nf_val = 0.f;
+#pragma unroll 1
     for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
       const int kb = u % C::kBuf;
       const bool reuse = u >= C::kBuf;  // the operand buffer held tile u - kBuf
@@ -452,7 +475,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D, NT> *ms,
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->k_full[kb]));
       }
-      if (do_v) {
+      if (!do_k) {
         if (D == 128 || row < 64) {  // (lanes past the head dim: their output is never read)
           const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
           auto wait_free = [&] {
@@ -461,7 +484,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D, NT> *ms,
             tc_fence_after();
           };
           if (!win) {
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint32_t x[32];
               dq_v<D, B>(stage, ms->pvalid[st], ragged, row, h, x);
@@ -538,14 +561,14 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D, NT> *ms,
 // ---- the kernel ---------------------------------------------------------------------
 constexpr int kBarSoft = 1;  // named barriers 1 .. kSw: a softmax warpgroup; kSw + 1: all of them
 
-template <int D, int NT>
-__global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(const AttnArgs a) {
-  using C = Cfg<D, NT>;
+template <int D, int B>
+__global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const AttnArgs a) {
+  using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
-  Misc<D, NT> *ms = reinterpret_cast<Misc<D, NT> *>(smem + C::kMisc);
+  Misc<D> *ms = reinterpret_cast<Misc<D> *>(smem + C::kMisc);
   volatile int *abort_flag = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -580,6 +603,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
   long long *pre = ms->pre;
   if (warp == 0) {
     long long run = 0;
+#pragma unroll 1
     for (int base = 0; base < a.batch; base += 32) {
       const int b = base + lane;
       long long u = 0;
@@ -587,7 +611,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
         int q0, n, ctx;
         if (load_seq_meta(a, b, q0, n, ctx)) {
           const long long tiles = (ctx + kKeys - 1LL) / kKeys + (n + kKeys - 1) / kKeys;
-          u = tiles * a.num_heads_kv * row_tiles(a.group * n, NT).tiles;
+          u = tiles * a.num_heads_kv * row_tiles(a.group * n).tiles;
         } else if (blockIdx.x == 0) {
           set_err(a.err, D2F_ERR_INVALID_ARG);
         }
@@ -601,19 +625,20 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       if (b < a.batch) pre[b] = run + inc - u;
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) pre[a.batch] = run;
+    if (lane == 0) {
+      // shares of at least one unit; the CTAs past the last share have none
+      const long long n = min((long long)gridDim.x, run), c = blockIdx.x;
+      ms->W = run;
+      ms->wb = c < n ? run * c / n : 0;
+      ms->we = c < n ? run * (c + 1) / n : 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
-  const long long W = pre[a.batch];
-  // shares of at least one unit; the CTAs past the last share have none
-  const long long n_cta = min((long long)gridDim.x, W);
-  const bool has = blockIdx.x < n_cta;
-  const long long wb = has ? W * blockIdx.x / n_cta : 0, we = has ? W * (blockIdx.x + 1) / n_cta : 0;
-  const int B = a.block_size;
-  const int page_bytes = B * D + B * D / 8;
+  const long long wb = ms->wb, we = ms->we;  // this CTA's share of the line
+  constexpr int page_bytes = B * D + B * D / 8;
   const long long wait = a.wait_cycles;
 
   // Registers: what the control and dequantising warps do not need goes to the softmax
@@ -622,11 +647,12 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
     set_regs_dec<C::kRegCtl>();
     if (warp == 0) {
     // ============================ producer =======================================
-    const int ppt = kKeys / B;
+    constexpr int ppt = kKeys / B;
     int cu = 0;  // cached tiles so far: stage cu % kStages
     bool ok = true;
+#pragma unroll 1
     for (long long w = wb; w < we && ok;) {
-      const Seg s = segment<NT>(a, pre, w, we);
+      const Seg s = segment(a, pre, w, we);
       w += s.len;
       const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
       const int t1 = min(s.t0 + s.len, s.Tc);
@@ -635,6 +661,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
                    ? __ldg(pt + (int64_t)t * ppt + lane) : -1;
       };
       int id = fetch(s.t0);
+#pragma unroll 1
       for (int t = s.t0; t < t1; ++t, ++cu) {
         const int next = fetch(t + 1);
         const int st = cu % C::kStages;
@@ -664,6 +691,7 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       }
     }
     if (lane == 0) {  // every copy issued must have landed before the CTA ends
+#pragma unroll 1
       for (int i = max(0, cu - C::kStages); i < cu; ++i) {
         volatile int no_abort = 0;
         mbar_wait(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err,
@@ -677,11 +705,13 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       int u = 0, sg = 0;
       const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
       const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
+#pragma unroll 1
       for (long long w = wb; w < we && ok; ++sg) {
-        const Seg s = segment<NT>(a, pre, w, we);
+        const Seg s = segment(a, pre, w, we);
         w += s.len;
         const int ncols = (s.nrows + 15) & ~15;
         if (warp == 1) ok = mbar_wait(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
+#pragma unroll 1
         for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
           const int bf = t >= s.Tc;  // window tiles are bf16
           const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
@@ -723,41 +753,40 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
     }
     }
   } else if (warp < 4 + 4 * C::kDq) {
-    set_regs_dec<C::kRegDq>();
-    if (B == 16) dequant_role<D, NT, 16>(a, ms, sb, tmem, wb, we);
-    else if (B == 32) dequant_role<D, NT, 32>(a, ms, sb, tmem, wb, we);
-    else dequant_role<D, NT, 8>(a, ms, sb, tmem, wb, we);
+    set_regs_inc<C::kRegDq>();
+    dequant_role<D, B>(a, ms, sb, tmem, wb, we);
   } else {
-    set_regs_inc<C::kRegSoft>();
+    set_regs_dec<C::kRegSoft>();
     // ============================ softmax ============================================
-    const int wg = (warp - 4 - 4 * C::kDq) >> 2;  // columns 32 wg .. 32 wg + 31
-    const int quad = warp & 3;
+    const int wg = (warp - 4 - 4 * C::kDq) >> 2;  // columns col0 .. col0 + 15
+    const int col0 = 16 * wg;
+    const int quad = warp & 3, col = lane & 15;
     const int row = quad * 32 + lane;             // key of the tile, later dim of O^T
     const int bar = kBarSoft + wg, bar_all = kBarSoft + C::kSw;
     const int stid = tid - 128 * (1 + C::kDq);    // thread among the softmax threads
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t o_addr = lane_base + C::kTmO + 32 * wg;
+    const uint32_t o_addr = lane_base + C::kTmO + col0;
     const int G = a.group, H = a.num_heads_q;
     const float win_unit = 1.0f / a.v_mul;        // O is in units of 2^v_exp
     int u = 0, sg = -1;
     bool ok = true;
+#pragma unroll 1
     for (long long w = wb; w < we && ok;) {
       ++sg;
-      const Seg s = segment<NT>(a, pre, w, we);
+      const Seg s = segment(a, pre, w, we);
       const bool starts_share = w == wb;
       w += s.len;
-      const int ncols = (s.nrows + 15) & ~15;
-      const int cols = max(0, min(32, ncols - 32 * wg));  // 0, 16 or 32 of this warpgroup
+      const bool idle = col0 >= s.nrows;  // (warpgroup-uniform) no row in these columns
 
-      // ---- Q: four threads per row; bf16 as it is, fp16 scaled by a power of two ------
+      // ---- Q: eight threads per row; bf16 as it is, fp16 scaled by a power of two -----
       {
-        const int qr = stid >> 2, part = stid & 3;
-        constexpr int kV = D / 32;  // 16-byte pieces of a thread
+        const int qr = stid >> 3, part = stid & 7;
+        constexpr int kV = D / 64;  // 16-byte pieces of a thread
         uint4 v[kV];
         const int r = s.r0 + qr;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            static_cast<const uint16_t *>(a.q) +
-            ((int64_t)(s.q0 + r / G) * H + s.g * G + r % G) * D) + part * kV;
+        const int64_t hr = (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + hr * D) + part * kV;
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] = qr < s.nrows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
         uint32_t top = 0;  // largest magnitude's bits
@@ -767,8 +796,8 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
 #pragma unroll
           for (int j = 0; j < 4; ++j) top = max(top, max(wv[j] & 0x7fffu, (wv[j] >> 16) & 0x7fffu));
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int e = top ? min(max((int)(top >> 7) - 127 - 14, -126), 112) : 0;
         const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
@@ -791,29 +820,29 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
           const float up = __int_as_float((127 + e) << 23);
           ms->c[qr] = a.scale_log2 * a.k_mul * up;
           ms->nm[qr] = 0.f;
-          ms->hr[qr] = (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
+          ms->hr[qr] = hr;
           ms->blk[qr] = qr < s.nrows ? (r / G) / B : 0x7fffffff;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
-        named_sync(bar_all, 128 * C::kSw);  // c, nm and blk of every column
+        named_sync(bar_all, 128 * C::kSw);  // c, nm, hr and blk of every column
       }
 
-      float l[32];
+      float l[16];  // this key lane's share of the columns' sums
 #pragma unroll
-      for (int j = 0; j < 32; ++j) l[j] = 0.f;
-      float m_lane = -INFINITY;  // reference of column `lane`
-      bool unset = true;         // a column may have no reference yet
+      for (int j = 0; j < 16; ++j) l[j] = 0.f;
+      float m_col = -INFINITY;  // reference of column `col`
+      bool unset = true;        // a column may have no reference yet
+#pragma unroll 1
       for (int t = s.t0; t < s.t0 + s.len; ++t, ++u) {
-        const bool win = t >= s.Tc;
         const int sbuf = u & 1;
         ok = mbar_wait(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
         if (u >= 2)  // P of tile u - 2 has been read
           ok = mbar_wait(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
         __syncwarp();
         tc_fence_after();
-        if (cols == 0) {
+        if (idle) {
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
           tc_fence_before();
@@ -824,52 +853,32 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
           }
           continue;
         }
-        const int kw = (t - s.Tc) * kKeys + row;  // window key
-        const bool valid = win ? kw < s.n : (ms->vmask[u & 3][quad] >> lane) & 1;
-        const int kblk = win ? kw / B : 0;
-        float x[32];
-        // scores in log2 units, keys that a column does not see at -inf; minus the
-        // columns' references if `sub`
-        auto scores = [&](bool sub) {
-          uint32_t sv[32];
-          tmem_ld32(lane_base + C::kTmS + sbuf * NT + 32 * wg, sv);
+        const bool win = t >= s.Tc;
+        // scores in log2 units against the columns' references
+        float x[16];
+        const unsigned keys = win ? 0u : ms->vmask[u & 3][quad];
+        tmem_ld16f(lane_base + C::kTmS + sbuf * NT + col0, x);
+        if (keys == 0xffffffffu) {  // a cached tile of whole pages: every column sees every key
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (q >= 4 && cols == 16) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x[4 * q + j] = -INFINITY;
-              continue;
-            }
-            const float4 n4 = sub ? *reinterpret_cast<const float4 *>(&ms->nm[32 * wg + 4 * q])
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 c4 = win ? make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2)
-                                  : *reinterpret_cast<const float4 *>(&ms->c[32 * wg + 4 * q]);
-            fma2(x[4 * q], x[4 * q + 1], __uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1]),
-                 c4.x, c4.y, n4.x, n4.y);
-            fma2(x[4 * q + 2], x[4 * q + 3], __uint_as_float(sv[4 * q + 2]),
-                 __uint_as_float(sv[4 * q + 3]), c4.z, c4.w, n4.z, n4.w);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(&ms->c[col0 + j]);
+            const float4 n = *reinterpret_cast<const float4 *>(&ms->nm[col0 + j]);
+            fma2(x[j], x[j + 1], x[j], x[j + 1], c.x, c.y, n.x, n.y);
+            fma2(x[j + 2], x[j + 3], x[j + 2], x[j + 3], c.z, c.w, n.z, n.w);
           }
-          if (!__all_sync(0xffffffffu, valid)) {
+        } else {
+          const int kw = (t - s.Tc) * kKeys + row;  // window key
+          const bool none = win ? kw >= s.n : !((keys >> lane) & 1);
+          const int kblk = win ? kw / B : -1;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!valid) x[j] = -INFINITY;
+          for (int j = 0; j < 16; ++j) {
+            x[j] = fmaf(x[j], win ? a.scale_log2 : ms->c[col0 + j], ms->nm[col0 + j]);
+            if (none || ms->blk[col0 + j] < kblk) x[j] = -INFINITY;
           }
-          if (win) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int4 b4 = *reinterpret_cast<const int4 *>(&ms->blk[32 * wg + 4 * q]);
-              if (b4.x < kblk) x[4 * q] = -INFINITY;
-              if (b4.y < kblk) x[4 * q + 1] = -INFINITY;
-              if (b4.z < kblk) x[4 * q + 2] = -INFINITY;
-              if (b4.w < kblk) x[4 * q + 3] = -INFINITY;
-            }
-          }
-        };
-        scores(true);
-        float top = x[0];
-#pragma unroll
-        for (int j = 1; j + 1 < 32; j += 2) top = fmax3(top, x[j], x[j + 1]);
-        top = fmaxf(top, x[31]);
+        }
+        const float top =
+            fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
+                  fmax3(fmax3(x[9], x[10], x[11]), x[12], x[13]), fmaxf(x[14], x[15]));
         if (named_sync_or(bar, 128, unset || top > kRescale || !ok)) {
           // ---- move references: the columns' maxima over the tile ------------------
           // every P.V product so far must have landed in O before O is rescaled
@@ -878,62 +887,54 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
                            wait) && ok;
           __syncwarp();
           tc_fence_after();
-          scores(false);
-          const float wm = transpose_reduce<false>(x, lane);
-          ms->red[wg][quad][lane] = wm;
+          ms->red[wg][quad][col] = transpose_reduce<false>(x, lane);
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
-          const float m_tile = fmaxf(fmaxf(ms->red[wg][0][lane], ms->red[wg][1][lane]),
-                                     fmaxf(ms->red[wg][2][lane], ms->red[wg][3][lane]));
-          const bool move = m_tile > m_lane + kRescale || (m_lane == -INFINITY && m_tile > -INFINITY);
-          const float m_new = move ? m_tile : m_lane;
-          const float alpha = !move ? 1.f : m_lane == -INFINITY ? 0.f : fast_exp2(m_lane - m_new);
-          m_lane = m_new;
-          unset = __any_sync(0xffffffffu, m_new == -INFINITY && lane < cols);
-          if (quad == 0) {
-            ms->nm[32 * wg + lane] = m_new == -INFINITY ? 0.f : -m_new;
-            ms->al[32 * wg + lane] = alpha;
+          // column `col`: its largest score against the reference (0 before it has one)
+          const float rise = fmaxf(fmaxf(ms->red[wg][0][col], ms->red[wg][1][col]),
+                                   fmaxf(ms->red[wg][2][col], ms->red[wg][3][col]));
+          const bool fresh = m_col == -INFINITY;
+          const bool move = fresh ? rise > -INFINITY : rise > kRescale;
+          const float d_col = move ? rise : 0.f;
+          const float a_col = !move ? 1.f : fresh ? 0.f : fast_exp2(-rise);
+          if (move) m_col = (fresh ? 0.f : m_col) + rise;
+          unset = __any_sync(0xffffffffu, m_col == -INFINITY);
+          if (quad == 0 && lane < 16) ms->nm[col0 + lane] -= d_col;
+          float o[16];
+          if (t > s.t0) tmem_ld16f(o_addr, o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float al = __shfl_sync(0xffffffffu, a_col, j);
+            x[j] -= __shfl_sync(0xffffffffu, d_col, j);
+            l[j] *= al;
+            o[j] *= al;
           }
-          named_sync(bar, 128);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) l[j] *= ms->al[32 * wg + j];
           if (t > s.t0) {
-            uint32_t o[32];
-            tmem_ld32(o_addr, o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * ms->al[32 * wg + j]);
-            tmem_st32(o_addr, o);
+            tmem_st16f(o_addr, o);
             tmem_wait_st();
           }
-          scores(true);
+          named_sync(bar, 128);  // nm is written, and red may be written again
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sbuf]));
         // ---- P = 2^x; the row sums take the unrounded values ------------------------
-        const uint32_t pb = sb + C::kP + sbuf * C::kPBytes + (row >> 3) * C::kPSbo +
-                            (wg >> 1) * 1024 + (row & 7) * 128;
+        const uint32_t pb = sb + C::kP + sbuf * C::kPBytes + row * 128;
+        float p[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // 8 columns, 16 bytes
-          if (q >= 2 && cols == 16) break;
-          float p[8];
+        for (int j = 0; j < 16; ++j) p[j] = fast_exp2(x[j]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = fast_exp2(x[8 * q + j]);
+        for (int j = 0; j < 16; j += 2) add2(l[j], l[j + 1], l[j], l[j + 1], p[j], p[j + 1]);
+        uint32_t h[8];
+        if (win) {
 #pragma unroll
-          for (int j = 0; j < 8; j += 2)
-            add2(l[8 * q + j], l[8 * q + j + 1], l[8 * q + j], l[8 * q + j + 1], p[j], p[j + 1]);
-          uint4 v;
-          if (win)
-            v = make_uint4(pack_bf16x2(p[0] * win_unit, p[1] * win_unit),
-                           pack_bf16x2(p[2] * win_unit, p[3] * win_unit),
-                           pack_bf16x2(p[4] * win_unit, p[5] * win_unit),
-                           pack_bf16x2(p[6] * win_unit, p[7] * win_unit));
-          else
-            v = make_uint4(pack_half2(p[0], p[1]), pack_half2(p[2], p[3]), pack_half2(p[4], p[5]),
-                           pack_half2(p[6], p[7]));
-          sts128(pb + ((((wg & 1) * 4 + q) ^ (row & 7)) << 4), v);
+          for (int j = 0; j < 8; ++j) h[j] = pack_bf16x2(p[2 * j] * win_unit, p[2 * j + 1] * win_unit);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[j] = pack_half2(p[2 * j], p[2 * j + 1]);
         }
+        sts128(pb + (((2 * wg) ^ (row & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(pb + (((2 * wg + 1) ^ (row & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[sbuf]));
@@ -943,42 +944,38 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       const int last = u - 1;
       ok = ok && mbar_wait(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, wait);
       __syncwarp();
-      const float ws = transpose_reduce<true>(l, lane);
-      ms->red[wg][quad][lane] = ws;
+      ms->red[wg][quad][col] = transpose_reduce<true>(l, lane);
       ok = named_sync_and(bar_all, 128 * C::kSw, ok);
       if (!ok) break;
       tc_fence_after();
-      // sum of column `lane` (the same in the four warps)
-      const float L = (ms->red[wg][0][lane] + ms->red[wg][1][lane]) +
-                      (ms->red[wg][2][lane] + ms->red[wg][3][lane]);
-      const bool col_on = 32 * wg + lane < s.nrows;
-      uint32_t o[32];
-      tmem_ld32(o_addr, o);
+      // sum of column `col` (the same in the four warps)
+      const float L = (ms->red[wg][0][col] + ms->red[wg][1][col]) +
+                      (ms->red[wg][2][col] + ms->red[wg][3][col]);
+      const int live = min(16, s.nrows - col0);  // columns with a row (none or fewer: idle)
+      float o[16];
+      tmem_ld16f(o_addr, o);
       tc_fence_before();
       // infinite or NaN window values of this dim, for the rows that see them
       if (s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff) {
         const int nb = ms->nf_blk[sg & 3][row], nn = ms->nf_nan[sg & 3][row];
         const float nv = ms->nf_val[sg & 3][row];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int bj = ms->blk[32 * wg + j];
-          if (bj >= nb) o[j] = __float_as_uint(__uint_as_float(o[j]) + (bj >= nn ? NAN : nv));
+        for (int j = 0; j < 16; ++j) {
+          const int bj = ms->blk[col0 + j];
+          if (bj >= nb) o[j] += bj >= nn ? NAN : nv;
         }
       }
-      const bool dim_on = row < D;
-      uint16_t *outp = static_cast<uint16_t *>(a.out);
-      // output row of column j of this warpgroup
-      auto head_row = [&](int j) -> int64_t { return ms->hr[32 * wg + j]; };
+      const bool dim_on = D == 128 || row < D;
+      uint16_t *outp = static_cast<uint16_t *>(a.out) + row;
       if (s.len == s.T) {
         const float f = a.v_mul / L;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float fj = __shfl_sync(0xffffffffu, f, j);
-          if (32 * wg + j < s.nrows && dim_on)
-            outp[head_row(j) * D + row] = float_to_bf16_bits(__uint_as_float(o[j]) * fj);
+        for (int j = 0; j < 16; ++j) {
+          const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
+          if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
         }
-        if (quad == 0 && col_on && a.lse_out)
-          a.lse_out[head_row(lane)] = (m_lane + __log2f(L)) * 0.6931471805599453f;
+        if (quad == 0 && lane < live && a.lse_out)
+          a.lse_out[ms->hr[col0 + lane]] = (m_col + __log2f(L)) * 0.6931471805599453f;
         continue;
       }
       // ---- a part of the row tile: to the workspace; the last to arrive composes --------
@@ -986,63 +983,67 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
       {
         float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (starts_share ? 0 : 1)) * kSlotFloats;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (32 * wg + j < s.nrows && dim_on)
-            __stcg(slot + (32 * wg + j) * D + row, __uint_as_float(o[j]));
-        if (quad == 0 && col_on)
-          __stcg(reinterpret_cast<float2 *>(slot + NT * D) + 32 * wg + lane, make_float2(m_lane, L));
+        for (int j = 0; j < 16; ++j)
+          if (j < live && dim_on) __stcg(slot + (col0 + j) * D + row, o[j]);
+        if (quad == 0 && lane < live)
+          __stcg(reinterpret_cast<float2 *>(slot + NT * D) + col0 + lane, make_float2(m_col, L));
       }
       __threadfence();
       named_sync(bar_all, 128 * C::kSw);
-      // shares that hold units of this row tile: share of unit w is ((w + 1) n - 1) / W
-      const int c0 = (int)(((s.w0 + 1) * n_cta - 1) / W);
-      const int c1 = (int)(((s.w0 + s.T) * n_cta - 1) / W);
       if (stid == 0) {
+        // shares that hold units of this row tile: share of unit w is ((w + 1) n - 1) / W;
+        // the first one's part is in its first slot only if the share starts with the tile
+        const long long W = ms->W, n = min((long long)gridDim.x, W);
+        const int c0 = (int)(((s.w0 + 1) * n - 1) / W), c1 = (int)(((s.w0 + s.T) * n - 1) / W);
         const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == c1 - c0;
         if (is_last) a.counters[s.item] = 0;
         ms->last = is_last;
+        ms->c0 = c0;
+        ms->c1 = c1;
+        ms->second = W * c0 / n != s.w0;
       }
       named_sync(bar_all, 128 * C::kSw);
       const bool compose = ms->last != 0;
+      const int c0 = ms->c0, c1 = ms->c1, second = ms->second;
       named_sync(bar_all, 128 * C::kSw);  // ms->last may be written again
-      if (!compose || cols == 0) continue;
+      if (!compose || idle) continue;
       __threadfence();
       auto part = [&](int c) -> const float * {
-        // the first share's part is its first segment only if the row tile starts there
-        const bool second = c == c0 && W * c / n_cta != s.w0;
-        return a.ws_o + ((int64_t)2 * c + (second ? 1 : 0)) * kSlotFloats;
+        return a.ws_o + ((int64_t)2 * c + (c == c0 ? second : 0)) * kSlotFloats;
       };
-      float Mx = -INFINITY;
-      for (int c = c0; c <= c1; ++c)
-        if (col_on)
-          Mx = fmaxf(Mx, __ldcg(reinterpret_cast<const float2 *>(part(c) + NT * D) + 32 * wg + lane).x);
-      float Lx = 0.f, acc[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+      // (largest reference, sum) of column `col` over the parts
+      float Mx = -INFINITY, Lx = 0.f;
+#pragma unroll 1
       for (int c = c0; c <= c1; ++c) {
-        const float *p = part(c);
-        float wt = 0.f;
-        if (col_on) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + 32 * wg + lane);
-          wt = ml.x == -INFINITY && Mx != -INFINITY ? 0.f : ml.x == Mx ? 1.f : fast_exp2(ml.x - Mx);
-          Lx += wt * ml.y;
-        }
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = 32 * wg + j < s.nrows && dim_on ? __ldcg(p + (32 * wg + j) * D + row) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[j] = fmaf(__shfl_sync(0xffffffffu, wt, j), v[j], acc[j]);
+        if (col >= live) continue;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(c) + NT * D) + col0 + col);
+        const float m_new = fmaxf(Mx, ml.x);
+        if (m_new == -INFINITY) continue;  // no key of these parts is visible to the row
+        Lx = (Mx == m_new ? Lx : Lx * fast_exp2(Mx - m_new)) +
+             (ml.x == m_new ? ml.y : ml.y * fast_exp2(ml.x - m_new));
+        Mx = m_new;
       }
       const float f = a.v_mul / Lx;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float fj = __shfl_sync(0xffffffffu, f, j);
-        if (32 * wg + j < s.nrows && dim_on)
-          outp[head_row(j) * D + row] = float_to_bf16_bits(acc[j] * fj);
+      for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll 1
+      for (int c = c0; c <= c1; ++c) {
+        const float *p = part(c) + col0 * D + row;
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = j < live && dim_on ? __ldcg(p + j * D) : 0.f;
+        const float m = col < live ? __ldcg(part(c) + NT * D + 2 * (col0 + col)) : -INFINITY;
+        const float wt = m == Mx ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - Mx);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = fmaf(__shfl_sync(0xffffffffu, wt, j), v[j], o[j]);
       }
-      if (quad == 0 && col_on && a.lse_out)
-        a.lse_out[head_row(lane)] = (Mx + __log2f(Lx)) * 0.6931471805599453f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
+        if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
+      }
+      if (quad == 0 && lane < live && a.lse_out)
+        a.lse_out[ms->hr[col0 + lane]] = (Mx + __log2f(Lx)) * 0.6931471805599453f;
     }
   }
 
@@ -1053,45 +1054,50 @@ __global__ void __launch_bounds__((Cfg<D, NT>::kThreads), 1) attn_kv4_kernel(con
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D, int NT>
+template <int D>
 constexpr int smem_bytes(int batch) {
-  return Cfg<D, NT>::kMisc + (int)sizeof(Misc<D, NT>) + 8 * batch + 1024;
+  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * batch + 1024;
 }
 
-template <int D, int NT>
+template <int D, int B>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
-  static_assert(smem_bytes<D, NT>(kMaxBatch) <= 232448, "shared memory of a CTA");
-  static std::mutex mu;
-  static bool opted[64] = {};
+  static_assert(smem_bytes<D>(kMaxBatch) <= 232448, "shared memory of a CTA");
+  static std::atomic<bool> opted[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !opted[dev]) {
-    std::lock_guard<std::mutex> g(mu);
-    e = cudaFuncSetAttribute(attn_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_bytes<D, NT>(kMaxBatch));
+    e = cudaFuncSetAttribute(attn_kv4_kernel<D, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes<D>(kMaxBatch));
     if (e != cudaSuccess) return e;
     if (dev < 64) opted[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_splits);
-  cfg.blockDim = dim3(Cfg<D, NT>::kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<D, NT>(a.batch);
+  cfg.blockDim = dim3(Cfg<D>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D>(a.batch);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, B>, a);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
+  switch (a.block_size) {
+    case 8: return launch<D, 8>(a, s);
+    case 16: return launch<D, 16>(a, s);
+    default: return launch<D, 32>(a, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_attn_kv4(const AttnArgs &a, cudaStream_t s) {
-  if (a.head_dim == 64)
-    return a.tc_rows == 64 ? launch<64, 64>(a, s) : launch<64, 128>(a, s);
-  return a.tc_rows == 64 ? launch<128, 64>(a, s) : launch<128, 128>(a, s);
+  return a.head_dim == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
 }
 
 }  // namespace d2f

@@ -824,7 +824,7 @@ int kv4_plan(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, in
     return fail(D2F_ERR_UNSUPPORTED, "batch %d > %d", batch, kKv4MaxBatch);
   const long long rows = (long long)(Hq / Hkv) * max_q;
   p->tc = true;
-  p->rows = rows <= 64 ? 64 : 128;
+  p->rows = 64;
   p->m_tiles = max(1, cdiv(rows, p->rows));
   const long long units = (long long)max(batch, 1) * Hkv * p->m_tiles *
                           max(1, cdiv(max_ctx, 128) + cdiv(max_q, 128));
@@ -989,7 +989,6 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
   a.err = err_word;
   if (p.tc) {
-    a.tc_rows = p.rows;
     const cudaError_t e = launch_attn_kv4(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tensor-core kv4 attention launch");
     return D2F_OK;

@@ -189,7 +189,7 @@ struct LogprobsArgs {
 cudaError_t launch_commit(const CommitArgs &a, int dtype, int path, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs &a, bool vec_ok, cudaStream_t s);
 cudaError_t launch_window(const WindowArgs &a, cudaStream_t s);
-// tensor-core attention over the 4-bit cache: num_splits CTAs, tc_rows 64 or 128 rows a tile
+// tensor-core attention over the 4-bit cache: num_splits CTAs, 64 rows a tile
 cudaError_t launch_attn_kv4(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_page_map(const PageMapArgs &a, cudaStream_t s);
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, int dtype, int D, cudaStream_t s);
