@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kSw = NT / 16;                 // softmax warpgroups, 16 columns each
   static constexpr int kThreads = 128 * (1 + kDq + kSw);
   static constexpr int kRegLaunch = 72;               // registers per thread at launch
-  static constexpr int kRegCtl = 40, kRegDq = 96, kRegSoft = 64;
+  static constexpr int kRegCtl = 40, kRegDq = 72, kRegSoft = 80;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");
   static constexpr int kBuf = 2;                      // K and V^T operand buffers in TMEM
@@ -76,6 +76,16 @@ struct Cfg {
   static constexpr int kPSbo = 1024;                  // bytes between 8-key groups of P
 };
 
+struct Seg {      // the part of one row tile that lies in a CTA's share
+  int q0, n, C;   // sequence: first window row, window rows, cached tokens
+  int b, g;
+  int r0, nrows;  // rows of the tile
+  int t0, len;    // key tiles [t0, t0 + len) of T; the first Tc are cached
+  int T, Tc;
+  long long w0;   // first unit of the row tile on the line
+  int item;       // its counter
+};
+
 template <int D>
 struct Misc {
   using C = Cfg<D>;
@@ -90,6 +100,7 @@ struct Misc {
   alignas(16) float nm[NT];       // minus the column's reference (0: none yet)
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
   alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
+  Seg seg;                        // the softmax warps' current segment
   float red[C::kSw][4][16];       // reductions over a warpgroup's warps
   uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
   uint8_t pvalid[C::kStages][16]; // valid tokens of a stage's pages
@@ -238,6 +249,35 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[16], int lane
   return SUM ? w[0] + got : fmaxf(w[0], got);
 }
 
+// Wait for a phase of an mbarrier. Every 64 polls it looks whether another thread of
+// the CTA gave up, and gives up itself after `budget` SM cycles.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                           int32_t *err, long long budget) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > budget) {
+      *abort_flag = 1;
+      set_err(err, D2F_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+// Arrive on an mbarrier from the warp's first lane (the warp's earlier accesses ordered
+// before it), without a branch.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(lane)
+      : "memory");
+}
+
 // ---- work line -----------------------------------------------------------------
 // Row tiles of a sequence: `tiles` of `rows` rows each (a multiple of 16, the last
 // one shorter), as equal as 16 rows allow.
@@ -252,16 +292,6 @@ __device__ __forceinline__ RowTiles row_tiles(int total) {
   r.tiles = (total + r.rows - 1) / r.rows;
   return r;
 }
-
-struct Seg {      // the part of one row tile that lies in a CTA's share
-  int q0, n, C;   // sequence: first window row, window rows, cached tokens
-  int b, g;
-  int r0, nrows;  // rows of the tile
-  int t0, len;    // key tiles [t0, t0 + len) of T; the first Tc are cached
-  int T, Tc;
-  long long w0;   // first unit of the row tile on the line
-  int item;       // its counter
-};
 
 // The segment that starts at unit w of the line (w < w1: end of the share).
 __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, long long w,
@@ -414,7 +444,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       const int st = cu % C::kStages;
       const uint32_t stage = sb + C::kRing + st * C::kStage;
       if (!win)
-        ok = mbar_wait(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+        ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
       const bool ragged = !win && ms->ragged[st];
       if (do_k) {
         uint32_t x[32];
@@ -439,7 +469,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
             dq_k32(c[2 * h], s01[0], s01[1], x);
             dq_k32(c[2 * h + 1], s23[0], s23[1], x + 16);
             if (h == 0 && reuse) {
-              ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
+              ok = ok && wait_phase(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
             }
@@ -452,7 +482,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
               static_cast<const uint16_t *>(a.k_win) +
               ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D);
           if (reuse) {
-            ok = ok && mbar_wait(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
+            ok = ok && wait_phase(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
           }
@@ -472,14 +502,13 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->k_full[kb]));
+        warp_arrive(smem_u32(&ms->k_full[kb]), lane);
       }
       if (!do_k) {
         if (D == 128 || row < 64) {  // (lanes past the head dim: their output is never read)
           const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
           auto wait_free = [&] {
-            ok = ok && mbar_wait(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
+            ok = ok && wait_phase(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
           };
@@ -545,12 +574,10 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
           ms->nf_val[sg & 3][row] = nf_val;
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->v_full[kb]));
+        warp_arrive(smem_u32(&ms->v_full[kb]), lane);
       }
       if (!win) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->empty[st]));
+        warp_arrive(smem_u32(&ms->empty[st]), lane);
         ++cu;
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -564,13 +591,15 @@ constexpr int kBarSoft = 1;  // named barriers 1 .. kSw: a softmax warpgroup; kS
 template <int D, int B>
 __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const AttnArgs a) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   Misc<D> *ms = reinterpret_cast<Misc<D> *>(smem + C::kMisc);
   volatile int *abort_flag = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sb & 1023) {  // the swizzled tiles need the alignment that the declaration asks for
+    if (tid == 0) set_err(a.err, D2F_ERR_UNSUPPORTED);
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -666,7 +695,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const int next = fetch(t + 1);
         const int st = cu % C::kStages;
         if (cu >= C::kStages) {
-          ok = mbar_wait(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, wait);
+          ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, wait);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
@@ -694,7 +723,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 #pragma unroll 1
       for (int i = max(0, cu - C::kStages); i < cu; ++i) {
         volatile int no_abort = 0;
-        mbar_wait(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err,
+        wait_phase(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err,
                   kDrainCycles);
       }
     }
@@ -710,14 +739,14 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const Seg s = segment(a, pre, w, we);
         w += s.len;
         const int ncols = (s.nrows + 15) & ~15;
-        if (warp == 1) ok = mbar_wait(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
+        if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
 #pragma unroll 1
         for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
           const int bf = t >= s.Tc;  // window tiles are bf16
           const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
           if (warp == 1) {
-            ok = mbar_wait(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, wait) &&
-                 (u < 2 || mbar_wait(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
+            ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, wait) &&
+                 (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
                                      a.err, wait));
             if (!ok) break;
             tc_fence_after();
@@ -731,8 +760,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
             umma_commit(smem_u32(&ms->s_full[u & 1]));
             umma_commit(smem_u32(&ms->k_free[kb]));
           } else {
-            ok = mbar_wait(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, wait) &&
-                 mbar_wait(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, wait);
+            ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, wait) &&
+                 wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, wait);
             if (!ok) break;
             tc_fence_after();
             const uint32_t id = idesc(bf, ncols, 1);
@@ -749,14 +778,14 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       }
       umma_commit(smem_u32(&ms->drain));
       volatile int no_abort = 0;
-      mbar_wait(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
+      wait_phase(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
     }
     }
   } else if (warp < 4 + 4 * C::kDq) {
-    set_regs_inc<C::kRegDq>();
+    // (the dequantising warps keep theirs)
     dequant_role<D, B>(a, ms, sb, tmem, wb, we);
   } else {
-    set_regs_dec<C::kRegSoft>();
+    set_regs_inc<C::kRegSoft>();
     // ============================ softmax ============================================
     const int wg = (warp - 4 - 4 * C::kDq) >> 2;  // columns col0 .. col0 + 15
     const int col0 = 16 * wg;
@@ -773,13 +802,18 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 #pragma unroll 1
     for (long long w = wb; w < we && ok;) {
       ++sg;
-      const Seg s = segment(a, pre, w, we);
-      const bool starts_share = w == wb;
-      w += s.len;
-      const bool idle = col0 >= s.nrows;  // (warpgroup-uniform) no row in these columns
+      int t, t_end, Tc, n;  // what the tile loop needs of the segment
+      bool idle;            // (warpgroup-uniform) no row in these columns
 
       // ---- Q: eight threads per row; bf16 as it is, fp16 scaled by a power of two -----
       {
+        const Seg s = segment(a, pre, w, we);
+        w += s.len;
+        t = s.t0;
+        t_end = s.t0 + s.len;
+        Tc = s.Tc;
+        n = s.n;
+        idle = col0 >= s.nrows;
         const int qr = stid >> 3, part = stid & 7;
         constexpr int kV = D / 64;  // 16-byte pieces of a thread
         uint4 v[kV];
@@ -816,6 +850,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         }
         // (the other warpgroups are done with the previous segment's arrays)
         named_sync(bar_all, 128 * C::kSw);
+        if (stid == 0) ms->seg = s;  // (read back by the epilogue)
         if (part == 0) {
           const float up = __int_as_float((127 + e) << 23);
           ms->c[qr] = a.scale_log2 * a.k_mul * up;
@@ -824,8 +859,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           ms->blk[qr] = qr < s.nrows ? (r / G) / B : 0x7fffffff;
         }
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+        warp_arrive(smem_u32(&ms->q_full), lane);
         named_sync(bar_all, 128 * C::kSw);  // c, nm, hr and blk of every column
       }
 
@@ -834,26 +868,24 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       for (int j = 0; j < 16; ++j) l[j] = 0.f;
       float m_col = -INFINITY;  // reference of column `col`
       bool unset = true;        // a column may have no reference yet
+      const int t_first = t;
 #pragma unroll 1
-      for (int t = s.t0; t < s.t0 + s.len; ++t, ++u) {
+      for (; t < t_end; ++t, ++u) {
         const int sbuf = u & 1;
-        ok = mbar_wait(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
+        ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
         if (u >= 2)  // P of tile u - 2 has been read
-          ok = mbar_wait(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
+          ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
         __syncwarp();
         tc_fence_after();
         if (idle) {
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&ms->s_free[sbuf]));
-            mbar_arrive(smem_u32(&ms->p_full[sbuf]));
-          }
+          warp_arrive(smem_u32(&ms->s_free[sbuf]), lane);
+          warp_arrive(smem_u32(&ms->p_full[sbuf]), lane);
           continue;
         }
-        const bool win = t >= s.Tc;
+        const bool win = t >= Tc;
         // scores in log2 units against the columns' references
         float x[16];
         const unsigned keys = win ? 0u : ms->vmask[u & 3][quad];
@@ -867,8 +899,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
             fma2(x[j + 2], x[j + 3], x[j + 2], x[j + 3], c.z, c.w, n.z, n.w);
           }
         } else {
-          const int kw = (t - s.Tc) * kKeys + row;  // window key
-          const bool none = win ? kw >= s.n : !((keys >> lane) & 1);
+          const int kw = (t - Tc) * kKeys + row;  // window key
+          const bool none = win ? kw >= n : !((keys >> lane) & 1);
           const int kblk = win ? kw / B : -1;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -882,8 +914,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         if (named_sync_or(bar, 128, unset || top > kRescale || !ok)) {
           // ---- move references: the columns' maxima over the tile ------------------
           // every P.V product so far must have landed in O before O is rescaled
-          if (t > s.t0)
-            ok = mbar_wait(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a.err,
+          if (t > t_first)
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a.err,
                            wait) && ok;
           __syncwarp();
           tc_fence_after();
@@ -901,7 +933,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           unset = __any_sync(0xffffffffu, m_col == -INFINITY);
           if (quad == 0 && lane < 16) ms->nm[col0 + lane] -= d_col;
           float o[16];
-          if (t > s.t0) tmem_ld16f(o_addr, o);
+          if (t > t_first) tmem_ld16f(o_addr, o);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float al = __shfl_sync(0xffffffffu, a_col, j);
@@ -909,15 +941,14 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
             l[j] *= al;
             o[j] *= al;
           }
-          if (t > s.t0) {
+          if (t > t_first) {
             tmem_st16f(o_addr, o);
             tmem_wait_st();
           }
           named_sync(bar, 128);  // nm is written, and red may be written again
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[sbuf]));
+        warp_arrive(smem_u32(&ms->s_free[sbuf]), lane);
         // ---- P = 2^x; the row sums take the unrounded values ------------------------
         const uint32_t pb = sb + C::kP + sbuf * C::kPBytes + row * 128;
         float p[16];
@@ -936,13 +967,12 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         sts128(pb + (((2 * wg) ^ (row & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(pb + (((2 * wg + 1) ^ (row & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[sbuf]));
+        warp_arrive(smem_u32(&ms->p_full[sbuf]), lane);
       }
 
       // ---- epilogue of the segment (a warpgroup that gave up joins the vote) ----------
       const int last = u - 1;
-      ok = ok && mbar_wait(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, wait);
+      ok = ok && wait_phase(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, wait);
       __syncwarp();
       ms->red[wg][quad][col] = transpose_reduce<true>(l, lane);
       ok = named_sync_and(bar_all, 128 * C::kSw, ok);
@@ -951,6 +981,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       // sum of column `col` (the same in the four warps)
       const float L = (ms->red[wg][0][col] + ms->red[wg][1][col]) +
                       (ms->red[wg][2][col] + ms->red[wg][3][col]);
+      const Seg s = ms->seg;
       const int live = min(16, s.nrows - col0);  // columns with a row (none or fewer: idle)
       float o[16];
       tmem_ld16f(o_addr, o);
@@ -981,7 +1012,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       // ---- a part of the row tile: to the workspace; the last to arrive composes --------
       constexpr int kSlotFloats = NT * D + 2 * NT;
       {
-        float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (starts_share ? 0 : 1)) * kSlotFloats;
+        float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (s.w0 + s.t0 == wb ? 0 : 1)) * kSlotFloats;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (j < live && dim_on) __stcg(slot + (col0 + j) * D + row, o[j]);
@@ -1056,7 +1087,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
 template <int D>
 constexpr int smem_bytes(int batch) {
-  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * batch + 1024;
+  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * batch;
 }
 
 template <int D, int B>
