@@ -58,6 +58,8 @@ struct Cfg {
   static constexpr int kDq = 2;                       // dequantising warpgroups: K, V^T
   static constexpr int kSw = NT / 16;                 // softmax warpgroups, 16 columns each
   static constexpr int kThreads = 128 * (1 + kDq + kSw);
+  // named barriers: 1 .. kSw a softmax warpgroup each, then all of them, then K, V^T
+  static constexpr int kBarSoft = 1, kBarAll = kBarSoft + kSw, kBarK = kBarAll + 1;
   static constexpr int kRegLaunch = 72;               // registers per thread at launch
   static constexpr int kRegCtl = 40, kRegDq = 72, kRegSoft = 80;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
@@ -443,8 +445,18 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       const bool win = t >= s.Tc;
       const int st = cu % C::kStages;
       const uint32_t stage = sb + C::kRing + st * C::kStage;
-      if (!win)
-        ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+      // One warp of the warpgroup polls, for the tile's bytes and for the operand buffer;
+      // the others wait in the named barrier, which takes no issue slots.
+      if (quad == 0) {
+        if (!win)
+          ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+        if (reuse)
+          ok = wait_phase(smem_u32(do_k ? &ms->k_free[kb] : &ms->v_free[kb]), free_ph, abort_flag,
+                          a.err, wait) && ok;
+      }
+      ok = named_sync_and(do_k ? C::kBarK : C::kBarK + 1, 128, ok);
+      if (!ok) break;
+      tc_fence_after();
       const bool ragged = !win && ms->ragged[st];
       if (do_k) {
         uint32_t x[32];
@@ -468,11 +480,6 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
             scales_to_half(__byte_perm(sc[h], 0, 0x3322), s23[0], s23[1]);
             dq_k32(c[2 * h], s01[0], s01[1], x);
             dq_k32(c[2 * h + 1], s23[0], s23[1], x + 16);
-            if (h == 0 && reuse) {
-              ok = ok && wait_phase(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
-              ok = __all_sync(0xffffffffu, ok);
-              tc_fence_after();
-            }
             __syncwarp();
             tmem_st32(ka + h * 32, x);
           }
@@ -481,11 +488,6 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
           const uint4 *src = reinterpret_cast<const uint4 *>(
               static_cast<const uint16_t *>(a.k_win) +
               ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D);
-          if (reuse) {
-            ok = ok && wait_phase(smem_u32(&ms->k_free[kb]), free_ph, abort_flag, a.err, wait);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-          }
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
@@ -507,22 +509,15 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       if (!do_k) {
         if (D == 128 || row < 64) {  // (lanes past the head dim: their output is never read)
           const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
-          auto wait_free = [&] {
-            ok = ok && wait_phase(smem_u32(&ms->v_free[kb]), free_ph, abort_flag, a.err, wait);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-          };
           if (!win) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint32_t x[32];
               dq_v<D, B>(stage, ms->pvalid[st], ragged, row, h, x);
-              if (h == 0 && reuse) wait_free();
               __syncwarp();
               tmem_st32(va + h * 32, x);
             }
           } else {
-            if (reuse) wait_free();
             const int64_t step = (int64_t)a.num_heads_kv * D;
 #pragma unroll 1
             for (int w0 = 0; w0 < kKeys; w0 += 32) {  // 32 keys at a time
@@ -580,14 +575,11 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
         warp_arrive(smem_u32(&ms->empty[st]), lane);
         ++cu;
       }
-      ok = __all_sync(0xffffffffu, ok);
     }
   }
 }
 
 // ---- the kernel ---------------------------------------------------------------------
-constexpr int kBarSoft = 1;  // named barriers 1 .. kSw: a softmax warpgroup; kSw + 1: all of them
-
 template <int D, int B>
 __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const AttnArgs a) {
   using C = Cfg<D>;
@@ -791,7 +783,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     const int col0 = 16 * wg;
     const int quad = warp & 3, col = lane & 15;
     const int row = quad * 32 + lane;             // key of the tile, later dim of O^T
-    const int bar = kBarSoft + wg, bar_all = kBarSoft + C::kSw;
+    const int bar = C::kBarSoft + wg, bar_all = C::kBarAll;
     const int stid = tid - 128 * (1 + C::kDq);    // thread among the softmax threads
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t o_addr = lane_base + C::kTmO + col0;
@@ -872,14 +864,17 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 #pragma unroll 1
       for (; t < t_end; ++t, ++u) {
         const int sbuf = u & 1;
-        ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
-        if (u >= 2)  // P of tile u - 2 has been read
-          ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
-        __syncwarp();
+        // One warp of the warpgroup polls; the others wait in the named barrier, which
+        // takes no issue slots.
+        if (quad == 0) {
+          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
+          if (u >= 2)  // P of tile u - 2 has been read
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
+        }
+        ok = named_sync_and(bar, 128, ok);
+        if (!ok) break;
         tc_fence_after();
         if (idle) {
-          ok = named_sync_and(bar, 128, ok);
-          if (!ok) break;
           tc_fence_before();
           warp_arrive(smem_u32(&ms->s_free[sbuf]), lane);
           warp_arrive(smem_u32(&ms->p_full[sbuf]), lane);
@@ -911,7 +906,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const float top =
             fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
                   fmax3(fmax3(x[9], x[10], x[11]), x[12], x[13]), fmaxf(x[14], x[15]));
-        if (named_sync_or(bar, 128, unset || top > kRescale || !ok)) {
+        if (named_sync_or(bar, 128, unset || top > kRescale)) {
           // ---- move references: the columns' maxima over the tile ------------------
           // every P.V product so far must have landed in O before O is rescaled
           if (t > t_first)
