@@ -1064,9 +1064,10 @@ int plan_logprobs(int n, int vocab, int top_k, int dtype, LogprobsPlan *p) {
   if (vocab > (1 << 30)) return fail(D2F_ERR_UNSUPPORTED, "vocab must be <= 2^30");
   const int vec = dtype == D2F_BF16 ? 8 : 4;
   const int sms = max(1, num_sms_current_device());
-  int splits = (int)((4LL * sms) / max(n, 1));
+  int splits = cdiv(8LL * sms, max(n, 1));
+  if (const char *e = getenv("D2F_LP_SPLITS")) splits = atoi(e);
   splits = max(1, min(splits, 64));
-  splits = max(1, min(splits, vocab / 2048));
+  splits = max(1, min(splits, vocab / 4096));
   const int chunk = cdiv(cdiv(vocab, splits), vec) * vec;
   splits = cdiv(vocab, chunk);
   p->splits = splits;

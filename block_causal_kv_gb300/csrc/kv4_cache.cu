@@ -40,6 +40,13 @@ __device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
 }
 
 // Scale bits and the sixteen codes (two words, element 0 in the lowest nibble) of one group.
+//
+// The definition's quotient is the float y / s. With bf16 elements the code can be had
+// from y * (1 / s) instead: y has 8 significant bits and a midpoint between two codes
+// times s has at most 7, so a quotient that is not a midpoint is at least 2^-8 (relative)
+// away from it; rounded to fp16 (error 2^-11, the product's own error 2^-23 beside it)
+// it stays on its side, and an exact midpoint comes out as itself. Sixteen divisions a
+// group would make the kernel compute-bound (35,000 tokens x 32 heads: 440 us with them).
 template <typename T>
 __device__ __forceinline__ uint32_t encode16(const float (&x)[16], float mul, uint32_t (&code)[2]) {
   float y[16], amax = 0.f;
@@ -50,32 +57,45 @@ __device__ __forceinline__ uint32_t encode16(const float (&x)[16], float mul, ui
   }
   const uint32_t sb = e4m3_bits(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(sb);
+  const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     uint32_t c = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float a = y[8 * w + 2 * j], b = y[8 * w + 2 * j + 1];
-      const float qa = s == 0.f ? 0.f : __fdiv_rn(a, s), qb = s == 0.f ? 0.f : __fdiv_rn(b, s);
+      float qa, qb;
+      if constexpr (sizeof(T) == 2) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b * inv), "f"(a * inv));
+        qa = half_lo(h);
+        qb = half_hi(h);
+      } else {
+        qa = s == 0.f ? 0.f : __fdiv_rn(a, s);
+        qb = s == 0.f ? 0.f : __fdiv_rn(b, s);
+      }
       c |= e2m1x2_bits(qa, qb) << (8 * j);
     }
-    code[w] = c;
+    code[w] = s == 0.f ? 0u : c;  // (no negative zeros in a group without a scale)
   }
   return sb;
 }
 
-// One CTA per (append entry, KV head): the page is put together in shared memory and
-// stored 16 bytes at a time. A thread owns one group of 16 elements.
-template <typename T, int D>
+// One CTA per (append entry, KV head). A thread owns one group of 16 elements of one
+// token; K codes go straight to the page. The V codes of a page are transposed through
+// shared memory: there a thread owns a dim and collects its nibble of every token (one
+// 16-byte read brings two tokens' codes of its group, shared by the group's dims), so
+// the page is written in words and not in bytes.
+template <typename T, int D, int B>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a) {
   constexpr int NG = D / 16;
-  extern __shared__ uint4 tile4[];
-  uint8_t *tile = reinterpret_cast<uint8_t *>(tile4);
+  constexpr Kv4Layout L{D, B};
+  __shared__ uint2 v_s[NG][B];                // codes of a (group, token)
+  __shared__ __align__(16) uint8_t sc_s[2 * B * NG];  // K scales, V scales, in page order
   grid_dependency_wait();
   const int ap = blockIdx.x / a.num_heads_kv;
   const int g = blockIdx.x % a.num_heads_kv;
   if (a.n_dev != nullptr && ap >= min(max(*a.n_dev, 0), a.n_append)) return;
-  const int B = a.block_size;
   const int src = a.src_row[ap], dst = a.dst_page[ap];
   const int rows = a.n_rows ? a.n_rows[ap] : B;
   if (src < 0 || rows < 0 || rows > B || (int64_t)src + rows > a.total_q || dst < 0 ||
@@ -83,8 +103,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a)
     if (threadIdx.x == 0 && g == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
     return;
   }
-  const Kv4Layout L{D, B};
-  const int per = B * NG;  // groups of one tensor (a multiple of 32)
+  uint8_t *page = a.pool + ((int64_t)dst * a.num_heads_kv + g) * L.page_bytes();
+  constexpr int per = B * NG;  // groups of one tensor
+#pragma unroll
   for (int i = threadIdx.x; i < 2 * per; i += kThreads) {
     const int which = i / per, t = (i % per) / NG, grp = i % NG;
     float x[16];
@@ -98,30 +119,37 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a)
     uint32_t code[2];
     const uint32_t sb = encode16<T>(x, which ? a.v_mul : a.k_mul, code);
     if (which == 0) {
-      *reinterpret_cast<uint2 *>(tile + ((grp >> 1) * B + t) * 16 + (grp & 1) * 8) =
+      *reinterpret_cast<uint2 *>(page + ((grp >> 1) * B + t) * 16 + (grp & 1) * 8) =
           make_uint2(code[0], code[1]);
-      tile[L.k_scales() + t * NG + grp] = (uint8_t)sb;
+      sc_s[t * NG + grp] = (uint8_t)sb;
     } else {
-      // token t and its neighbour t ^ 1 (the lane NG away) share bytes: each of the
-      // two threads takes half of the dims and writes both tokens' nibbles
-      const uint32_t other0 = __shfl_xor_sync(0xffffffffu, code[0], NG);
-      const uint32_t other1 = __shfl_xor_sync(0xffffffffu, code[1], NG);
-      const bool odd = t & 1;
-      const uint32_t mine = odd ? code[1] : code[0], theirs = odd ? other1 : other0;
-      const uint32_t lo = odd ? theirs : mine, hi = odd ? mine : theirs;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int d = grp * 16 + odd * 8 + j;
-        tile[L.v_codes() + d * (B / 2) + (t >> 1)] =
-            (uint8_t)(((lo >> (4 * j)) & 15u) | (((hi >> (4 * j)) & 15u) << 4));
-      }
-      tile[L.v_scales() + grp * B + t] = (uint8_t)sb;
+      v_s[grp][t] = make_uint2(code[0], code[1]);
+      sc_s[per + grp * B + t] = (uint8_t)sb;
     }
   }
   __syncthreads();
-  uint4 *out = reinterpret_cast<uint4 *>(a.pool + ((int64_t)dst * a.num_heads_kv + g) *
-                                                      L.page_bytes());
-  for (int i = threadIdx.x; i < L.page_bytes() / 16; i += kThreads) out[i] = tile4[i];
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x, grp = d >> 4, sh = 4 * (d & 7);
+    uint32_t out[B / 8];
+#pragma unroll
+    for (int w = 0; w < B / 8; ++w) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int t = 0; t < 8; t += 2) {
+        const uint4 two = *reinterpret_cast<const uint4 *>(&v_s[grp][8 * w + t]);
+        const uint32_t w0 = d & 8 ? two.y : two.x, w1 = d & 8 ? two.w : two.z;
+        c |= (((w0 >> sh) & 15u) | (((w1 >> sh) & 15u) << 4)) << (4 * t);
+      }
+      out[w] = c;
+    }
+    uint8_t *p = page + L.v_codes() + d * (B / 2);
+    if constexpr (B == 8) *reinterpret_cast<uint32_t *>(p) = out[0];
+    if constexpr (B == 16) *reinterpret_cast<uint2 *>(p) = make_uint2(out[0], out[1]);
+    if constexpr (B == 32) *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+  } else {
+    for (int i = threadIdx.x - D; i < 2 * per / 16; i += kThreads - D)
+      reinterpret_cast<uint4 *>(page + L.k_scales())[i] = reinterpret_cast<const uint4 *>(sc_s)[i];
+  }
 }
 
 template <typename T>
@@ -142,50 +170,117 @@ __device__ __forceinline__ void store16<float>(float *p, const float (&x)[16]) {
         make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
 }
 
-// A thread owns one group of 16 elements of one (token, KV head), K and V.
-template <typename T, int D>
+// One CTA per (64 tokens of the list, KV head). K: a thread owns a group of 16 elements of
+// one token. V: the list is cut into runs of consecutive slots of one page; a warp owns
+// 64 dims of a run, a lane two of them, whose codes of the whole page are one coalesced
+// read, so a page of V is read once a run and written a token (128 bytes a warp) at a
+// time. (Gathering V element by element took twice as long: eight cache lines a load.)
+constexpr int kReadRows = 64;
+template <typename T, int D, int B>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
   constexpr int NG = D / 16;
+  constexpr Kv4Layout L{D, B};
+  __shared__ int64_t slot_s[kReadRows];  // -1: none
+  __shared__ uint8_t run_s[kReadRows + 1];
+  __shared__ int runs0_s, nruns_s;
   grid_dependency_wait();
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int grp = (int)(i % NG);
-  const int64_t th = i / NG;
-  const int g = (int)(th % a.num_heads_kv);
-  const int64_t t = th / a.num_heads_kv;
-  if (t >= a.n) return;
-  const int B = a.block_size;
-  const Kv4Layout L{D, B};
-  const int64_t slot = a.slot[t];
-  float k[16], v[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) k[j] = v[j] = 0.f;
-  if (slot >= 0 && slot < (int64_t)a.num_pages * B) {
-    const int64_t page = slot / B;
-    const int o = (int)(slot % B);
-    const uint8_t *tile = a.pool + (page * a.num_heads_kv + g) * L.page_bytes();
-    const uint2 kc = *reinterpret_cast<const uint2 *>(tile + ((grp >> 1) * B + o) * 16 + (grp & 1) * 8);
-    const float ks = e4m3_value(tile[L.k_scales() + o * NG + grp]) * a.k_mul;
-    const float vs = e4m3_value(tile[L.v_scales() + grp * B + o]) * a.v_mul;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      k[j] = e2m1_value((j < 8 ? kc.x : kc.y) >> (4 * (j & 7))) * ks;
-      const uint32_t vb = tile[L.v_codes() + (grp * 16 + j) * (B / 2) + (o >> 1)];
-      v[j] = e2m1_value(vb >> (4 * (o & 1))) * vs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = blockIdx.x % a.num_heads_kv;
+  const int64_t i0 = (int64_t)(blockIdx.x / a.num_heads_kv) * kReadRows;
+  const int n = (int)min((int64_t)kReadRows, a.n - i0);
+  if (warp < 2) {
+    int64_t slot = -1;
+    if (tid < n) {
+      slot = a.slot[i0 + tid];
+      if (slot < 0 || slot >= (int64_t)a.num_pages * B) {
+        if (slot != -1 && g == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
+        slot = -1;
+      }
     }
-  } else if (slot != -1 && grp == 0 && g == 0) {
-    set_err(a.err, D2F_ERR_BAD_INDEX);
+    slot_s[tid] = slot;
+    // a run starts where the slot does not follow its predecessor within a page
+    const int64_t prev = __shfl_up_sync(0xffffffffu, slot, 1);
+    const bool start = tid < n && (lane == 0 || slot < 0 || slot != prev + 1 || slot % B == 0);
+    const unsigned m = __ballot_sync(0xffffffffu, start);
+    if (warp == 0 && lane == 0) runs0_s = __popc(m);
+    if (warp == 0 && start) run_s[__popc(m & ((1u << lane) - 1))] = (uint8_t)tid;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (warp == 1) {
+      const int at = runs0_s;
+      if (start) run_s[at + __popc(m & ((1u << lane) - 1))] = (uint8_t)tid;
+      if (lane == 0) {
+        nruns_s = at + __popc(m);
+        run_s[at + __popc(m)] = (uint8_t)n;
+      }
+    }
   }
-  const int64_t off = (t * a.num_heads_kv + g) * D + grp * 16;
-  store16<T>(reinterpret_cast<T *>(a.k_out) + off, k);
-  store16<T>(reinterpret_cast<T *>(a.v_out) + off, v);
+  __syncthreads();
+  T *k_out = reinterpret_cast<T *>(a.k_out), *v_out = reinterpret_cast<T *>(a.v_out);
+  for (int i = tid; i < n * NG; i += kThreads) {
+    const int t = i / NG, grp = i % NG;
+    const int64_t slot = slot_s[t];
+    float k[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) k[j] = 0.f;
+    if (slot >= 0) {
+      const int o = (int)(slot % B);
+      const uint8_t *page = a.pool + (slot / B * a.num_heads_kv + g) * L.page_bytes();
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(page + ((grp >> 1) * B + o) * 16 + (grp & 1) * 8));
+      const float s = e4m3_value(__ldg(page + L.k_scales() + o * NG + grp)) * a.k_mul;
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const uint32_t h = e2m1x2_to_half2(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 0xffu);
+        k[j] = half_lo(h) * s;
+        k[j + 1] = half_hi(h) * s;
+      }
+    }
+    store16<T>(k_out + ((i0 + t) * a.num_heads_kv + g) * D + grp * 16, k);
+  }
+  constexpr int kHalves = D / 64;  // warps a run
+  const int d = 64 * (warp % kHalves) + 2 * lane;
+  for (int r = warp / kHalves; r < nruns_s; r += (kThreads / 32) / kHalves) {
+    const int t0 = run_s[r], t1 = run_s[r + 1];
+    const int64_t slot = slot_s[t0];
+    const int o0 = slot < 0 ? 0 : (int)(slot % B);  // (a run of no slot is one token long)
+    uint32_t w0[B / 8], w1[B / 8], sc[B / 4];  // both dims' codes, the group's scale bytes
+#pragma unroll
+    for (int i = 0; i < B / 8; ++i) w0[i] = w1[i] = 0;
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) sc[i] = 0;
+    if (slot >= 0) {
+      const uint8_t *page = a.pool + (slot / B * a.num_heads_kv + g) * L.page_bytes();
+      const uint32_t *c = reinterpret_cast<const uint32_t *>(page + L.v_codes() + d * (B / 2));
+      const uint32_t *s = reinterpret_cast<const uint32_t *>(page + L.v_scales() + (d >> 4) * B);
+#pragma unroll
+      for (int i = 0; i < B / 8; ++i) {
+        w0[i] = __ldg(c + i);
+        w1[i] = __ldg(c + B / 8 + i);
+      }
+#pragma unroll
+      for (int i = 0; i < B / 4; ++i) sc[i] = __ldg(s + i);
+    }
+    T *out = v_out + ((i0 + t0 - o0) * a.num_heads_kv + g) * D + d;  // of token 0 of the page
+    const int64_t step = (int64_t)a.num_heads_kv * D;
+#pragma unroll
+    for (int o = 0; o < B; ++o) {
+      if (o < o0 || o >= o0 + (t1 - t0)) continue;
+      const uint32_t c = ((w0[o / 8] >> (4 * (o % 8))) & 15u) | (((w1[o / 8] >> (4 * (o % 8))) & 15u) << 4);
+      const uint32_t h = e2m1x2_to_half2(c);
+      const float s = e4m3_value(sc[o / 4] >> (8 * (o % 4))) * a.v_mul;
+      const float x = half_lo(h) * s, y = half_hi(h) * s;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint32_t *>(out + o * step) = pack_bf16x2(x, y);
+      else
+        *reinterpret_cast<float2 *>(out + o * step) = make_float2(x, y);
+    }
+  }
 }
 
 template <typename Kernel, typename Args>
-cudaError_t launch(Kernel kernel, unsigned grid, size_t smem, const Args &a, cudaStream_t s) {
+cudaError_t launch(Kernel kernel, unsigned grid, const Args &a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -195,25 +290,41 @@ cudaError_t launch(Kernel kernel, unsigned grid, size_t smem, const Args &a, cud
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int D, int B>
+cudaError_t launch_append(const Kv4AppendArgs &a, int dtype, cudaStream_t s) {
+  const unsigned grid = (unsigned)a.n_append * a.num_heads_kv;
+  return dtype == D2F_BF16 ? launch(append_kernel<uint16_t, D, B>, grid, a, s)
+                           : launch(append_kernel<float, D, B>, grid, a, s);
+}
+template <int D, int B>
+cudaError_t launch_read(const Kv4ReadArgs &a, int dtype, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.n + kReadRows - 1) / kReadRows * a.num_heads_kv);
+  return dtype == D2F_BF16 ? launch(read_kernel<uint16_t, D, B>, grid, a, s)
+                           : launch(read_kernel<float, D, B>, grid, a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, int dtype, int D, cudaStream_t s) {
-  const unsigned grid = (unsigned)a.n_append * a.num_heads_kv;
-  const size_t smem = (size_t)Kv4Layout{D, a.block_size}.page_bytes();
-  if (dtype == D2F_BF16)
-    return D == 64 ? launch(append_kernel<uint16_t, 64>, grid, smem, a, s)
-                   : launch(append_kernel<uint16_t, 128>, grid, smem, a, s);
-  return D == 64 ? launch(append_kernel<float, 64>, grid, smem, a, s)
-                 : launch(append_kernel<float, 128>, grid, smem, a, s);
+  switch (a.block_size * 1000 + D) {
+    case 8064: return launch_append<64, 8>(a, dtype, s);
+    case 16064: return launch_append<64, 16>(a, dtype, s);
+    case 32064: return launch_append<64, 32>(a, dtype, s);
+    case 8128: return launch_append<128, 8>(a, dtype, s);
+    case 16128: return launch_append<128, 16>(a, dtype, s);
+    default: return launch_append<128, 32>(a, dtype, s);
+  }
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadArgs &a, int dtype, int D, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.n * a.num_heads_kv * (D / 16) + kThreads - 1) / kThreads);
-  if (dtype == D2F_BF16)
-    return D == 64 ? launch(read_kernel<uint16_t, 64>, grid, 0, a, s)
-                   : launch(read_kernel<uint16_t, 128>, grid, 0, a, s);
-  return D == 64 ? launch(read_kernel<float, 64>, grid, 0, a, s)
-                 : launch(read_kernel<float, 128>, grid, 0, a, s);
+  switch (a.block_size * 1000 + D) {
+    case 8064: return launch_read<64, 8>(a, dtype, s);
+    case 16064: return launch_read<64, 16>(a, dtype, s);
+    case 32064: return launch_read<64, 32>(a, dtype, s);
+    case 8128: return launch_read<128, 8>(a, dtype, s);
+    case 16128: return launch_read<128, 16>(a, dtype, s);
+    default: return launch_read<128, 32>(a, dtype, s);
+  }
 }
 
 }  // namespace d2f

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kOneCtaRows = 16384;  // slots + 4 per list entry
 
 // Exclusive running sum over the CTA's threads of (x, y), and the totals.
 __device__ longlong2 block_scan(longlong2 v, longlong2 *warp_sum, longlong2 &total) {
@@ -66,7 +67,10 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
   __shared__ longlong2 warp_sum[kWarps];
   __shared__ int bad_s;
   const int tid = threadIdx.x, B = a.block_size, batch = a.batch;
+  if (PHASE == kPlan) grid_launch_dependents();  // (the fill waits for this grid's end)
   grid_dependency_wait();
+  // a fill behind a plan that refused its inputs does nothing
+  if (PHASE == kFill && *a.n_append < 0) return;
   const int per = (batch + kThreads - 1) / kThreads;  // consecutive requests of a thread
   const int b0 = min(tid * per, batch), b1 = min(b0 + per, batch);
   int n_pages, n_rows, free0;
@@ -92,7 +96,10 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     longlong2 total;
     longlong2 at = block_scan(sum, warp_sum, total);
     if (bad_s || total.x > a.capacity) {  // an inconsistent state: nothing is written
-      if (tid == 0) set_err(a.err, D2F_ERR_INVALID_ARG);
+      if (tid == 0) {
+        set_err(a.err, D2F_ERR_INVALID_ARG);
+        if (PHASE == kPlan) *a.n_append = -1;
+      }
       return;
     }
     n_rows = (int)total.x;
@@ -163,16 +170,40 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     a.app_dst[p] = dst;
     a.app_rows[p] = rows;
   }
-  for (int64_t r = first; r < a.capacity; r += step) {
-    int64_t slot = -1;
-    if (r < n_rows) {
-      const int b = find(row0, batch, (int)r);
-      if (ctxp[b] >= 0) {
-        const int t = (int)r - row0[b];
-        slot = (int64_t)a.free_pages[free0 - 1 - (page0[b] + t / B)] * B + t % B;
+  // slots, four rows a thread: one search, then a walk (a row's request and page are
+  // mostly its predecessor's)
+  for (int64_t q = first; 4 * q < a.capacity; q += step) {
+    const int r0 = (int)(4 * q), r1 = min(r0 + 4, a.capacity);
+    int64_t slot[4];
+    int b = r0 < n_rows ? find(row0, batch, r0) : 0;
+    int next = 0, have = -1;
+    int64_t base = 0;  // page * B of page number `have`
+    if (r0 < n_rows) next = b + 1 < batch ? row0[b + 1] : n_rows;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + j;
+      slot[j] = -1;
+      if (r >= n_rows) continue;
+      while (r >= next) {
+        ++b;
+        next = b + 1 < batch ? row0[b + 1] : n_rows;
       }
+      if (ctxp[b] < 0) continue;
+      const int t = r - row0[b], p = page0[b] + t / B;
+      if (p != have) {
+        base = (int64_t)a.free_pages[free0 - 1 - p] * B;
+        have = p;
+      }
+      slot[j] = base + t % B;
     }
-    a.slot[r] = slot;
+    if (r1 - r0 == 4 && (reinterpret_cast<uintptr_t>(a.slot) & 15) == 0) {
+      reinterpret_cast<longlong2 *>(a.slot + r0)[0] = make_longlong2(slot[0], slot[1]);
+      reinterpret_cast<longlong2 *>(a.slot + r0)[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r0 + j < r1) a.slot[r0 + j] = slot[j];
+    }
   }
 }
 
@@ -200,7 +231,16 @@ cudaError_t launch_phase(const PageMapArgs &a, unsigned grid, size_t smem, cudaS
 
 cudaError_t launch_page_map(const PageMapArgs &a, cudaStream_t s) {
   const size_t smem = (size_t)a.batch * 3 * sizeof(int);
-  return launch_phase<kBoth>(a, 1, smem, s);
+  // One CTA does it all up to some ten thousand rows; beyond, a second launch fills the
+  // maps on every SM.
+  if ((long long)a.capacity + 4LL * a.max_append <= kOneCtaRows)
+    return launch_phase<kBoth>(a, 1, smem, s);
+  const cudaError_t e = launch_phase<kPlan>(a, 1, 0, s);
+  if (e != cudaSuccess) return e;
+  const long long work = max((long long)a.capacity / 4, (long long)a.max_append);
+  const unsigned grid = (unsigned)min(2LL * max(1, num_sms_current_device()),
+                                      (work + kThreads - 1) / kThreads);
+  return launch_phase<kFill>(a, grid, smem, s);
 }
 
 }  // namespace d2f
