@@ -1064,10 +1064,14 @@ int plan_logprobs(int n, int vocab, int top_k, int dtype, LogprobsPlan *p) {
   if (vocab > (1 << 30)) return fail(D2F_ERR_UNSUPPORTED, "vocab must be <= 2^30");
   const int vec = dtype == D2F_BF16 ? 8 : 4;
   const int sms = max(1, num_sms_current_device());
-  int splits = cdiv(8LL * sms, max(n, 1));
-  if (const char *e = getenv("D2F_LP_SPLITS")) splits = atoi(e);
+  // Eight CTAs an SM over the whole grid (rows without a token leave at once, so about
+  // four of them work), at least 16,384 logits a slice: every slice pays for its
+  // second look and its list. Measured on GB300 (us, bf16): 48 rows of 126,464, 5
+  // alternatives: 6 slices 14.8 (8: 16.1, 12: 16.2, 4: 16.2); 384 rows of 152,064, half
+  // of them with a token, 20 alternatives: 3 slices 32.8 (4: 39.6, 2: 41.1); all with a
+  // token: 1 slice 56.8 (3: 57.4, 2: 65.2).
+  int splits = (int)min(8LL * sms / max(n, 1), (long long)(vocab / 16384));
   splits = max(1, min(splits, 64));
-  splits = max(1, min(splits, vocab / 4096));
   const int chunk = cdiv(cdiv(vocab, splits), vec) * vec;
   splits = cdiv(vocab, chunk);
   p->splits = splits;

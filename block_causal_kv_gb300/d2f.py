@@ -172,29 +172,37 @@ class _On:
     it the current one: the stream (that device's current one unless given) and the
     launch belong to it. Entries are (name, tensor or None, dtype or None)."""
 
+    __slots__ = ("_guard", "_given", "_index")
+
     def __init__(self, stream, *tensors):
         dev = None
         for name, t, dtype in tensors:
             if t is None:
                 continue
-            _dev(t, name, dtype)
+            if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+                _dev(t, name, dtype)
             if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("%s is on %s, the others on %s" % (name, t.device, dev))
-        self._guard = torch.cuda.device(dev)
+                dev = t.get_device()
+            elif t.get_device() != dev:
+                raise ValueError("%s is on cuda:%d, the others on cuda:%d" %
+                                 (name, t.get_device(), dev))
+        self._index = dev
+        self._guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
         self._given = stream
 
     def __enter__(self):
-        self._guard.__enter__()
-        return _stream(self._given)
+        if self._guard is not None:
+            self._guard.__enter__()
+        if self._given is None:
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        return self._given.cuda_stream
 
     def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+        return None if self._guard is None else self._guard.__exit__(*exc)
 
 
 def _shape(t, name, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -615,20 +623,20 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
     _shape(ctx_len, "ctx_len", (batch,))
     _shape(page_table, "page_table", (batch, page_table.shape[-1]))
     _shape(free_count, "free_count", (1,))
-    i32 = dict(dtype=torch.int32, device=dev)
-    if ctx_len_out is None:
-        ctx_len_out = torch.empty(batch, **i32)
-    if free_count_out is None:
-        free_count_out = torch.empty(1, **i32)
-    _shape(ctx_len_out, "ctx_len_out", (batch,))
-    _shape(free_count_out, "free_count_out", (1,))
     if capacity < 0 or max_append < 0:
         raise ValueError("capacity and max_append must not be negative")
-    row_start = torch.empty(batch + 1, **i32)
+    # the int32 results, one allocation
+    ctx_new, free_new, row_start, n_append, src, dst, rows = torch.empty(
+        2 * batch + 3 + 3 * max_append, dtype=torch.int32, device=dev).split(
+            [batch, 1, batch + 1, 1, max_append, max_append, max_append])
+    if ctx_len_out is None:
+        ctx_len_out = ctx_new
+    if free_count_out is None:
+        free_count_out = free_new
+    _shape(ctx_len_out, "ctx_len_out", (batch,))
+    _shape(free_count_out, "free_count_out", (1,))
     admitted = torch.empty(batch, dtype=torch.uint8, device=dev)
     slot = torch.empty(capacity, dtype=torch.int64, device=dev)
-    app = torch.empty((3, max_append), **i32)
-    n_append = torch.empty(1, **i32)
     with _On(stream, ("num_new", num_new, torch.int32), ("ctx_len", ctx_len, torch.int32),
              ("page_table", page_table, torch.int32), ("free_pages", free_pages, torch.int32),
              ("free_count", free_count, torch.int32), ("ctx_len_out", ctx_len_out, torch.int32),
@@ -637,10 +645,10 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
             batch, block_size, page_table.shape[1], capacity, max_append, _ptr(num_new),
             _ptr(ctx_len), _ptr(free_pages), _ptr(free_count), _ptr(page_table),
             _ptr(ctx_len_out), _ptr(free_count_out), _ptr(row_start), _ptr(admitted), _ptr(slot),
-            _ptr(app[0]), _ptr(app[1]), _ptr(app[2]), _ptr(n_append), _ptr(err), s))
+            _ptr(src), _ptr(dst), _ptr(rows), _ptr(n_append), _ptr(err), s))
     return {"page_table": page_table, "ctx_len": ctx_len_out, "row_start": row_start,
-            "admitted": admitted, "slot": slot, "app_src": app[0], "app_dst": app[1],
-            "app_rows": app[2], "n_append": n_append, "free_count": free_count_out}
+            "admitted": admitted, "slot": slot, "app_src": src, "app_dst": dst,
+            "app_rows": rows, "n_append": n_append, "free_count": free_count_out}
 
 
 # ---------------------------------------------------------------------------
@@ -680,15 +688,14 @@ def token_logprobs(logits, tokens, *, logit_row=None, top_k=0, want_entropy=True
     dev = logits.device
     if tokens.device != dev:
         raise ValueError("tokens is on %s, logits on %s" % (tokens.device, dev))
-    f32 = dict(dtype=torch.float32, device=dev)
     if logprob is None:
-        logprob = torch.empty(n, **f32)
+        logprob = torch.empty(n, dtype=torch.float32, device=dev)
     if entropy is None and want_entropy:
-        entropy = torch.empty(n, **f32)
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
     if top_id is None:
         top_id = torch.empty((n, top_k), dtype=torch.int32, device=dev)
     if top_logprob is None:
-        top_logprob = torch.empty((n, top_k), **f32)
+        top_logprob = torch.empty((n, top_k), dtype=torch.float32, device=dev)
     _shape(logprob, "logprob", (n,))
     _shape(entropy, "entropy", (n,))
     _shape(top_id, "top_id", (n, top_k))
