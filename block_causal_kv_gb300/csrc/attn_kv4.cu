@@ -48,7 +48,13 @@ namespace d2f {
 namespace {
 
 constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K extent of O^T)
-constexpr float kRescale = 8.0f;           // a reference moves when a score exceeds it by 2^8
+// References. P is fp16, so a column's scores should lie around its reference: at most
+// 2^15 above it (then the reference moves), and the largest at least 2^-2 of it, so that
+// what falls into fp16's subnormals (below 2^-14, steps of 2^-24) is nothing beside the
+// column's sum. A column starts with the reference 0 (scores as they are) and keeps it
+// if its first tile has a score in that range, which saves most row tiles the search
+// for a maximum over the lanes.
+constexpr float kHigh = 15.0f, kLow = -2.0f;
 constexpr int kMaxBatch = kKv4MaxBatch;
 
 constexpr int NT = 64;                     // rows (columns of S^T and O^T) per row tile
@@ -103,7 +109,8 @@ struct Misc {
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
   alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
   Seg seg;                        // the softmax warps' current segment
-  float red[C::kSw][4][16];       // reductions over a warpgroup's warps
+  float red[C::kSw][4][16];
+  unsigned near[C::kSw][4];       // reductions over a warpgroup's warps
   uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
   uint8_t pvalid[C::kStages][16]; // valid tokens of a stage's pages
   bool ragged[C::kStages];        // ... some page has fewer than a full one
@@ -116,6 +123,9 @@ struct Misc {
 };
 
 // ---- small device helpers ----------------------------------------------------
+// Paths that a steady tile does not take, out of the way of its instructions.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
 template <int N>
 __device__ __forceinline__ void set_regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -200,6 +210,14 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
         "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
         "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld4f(uint32_t taddr, float (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
       : "r"(taddr)
       : "memory");
 }
@@ -455,7 +473,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
                           a.err, wait) && ok;
       }
       ok = named_sync_and(do_k ? C::kBarK : C::kBarK + 1, 128, ok);
-      if (!ok) break;
+      if (rare(!ok)) break;
       tc_fence_after();
       const bool ragged = !win && ms->ragged[st];
       if (do_k) {
@@ -689,7 +707,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         if (cu >= C::kStages) {
           ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, wait);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (rare(!ok)) break;
         }
         const int first = t * kKeys + lane * B;  // first token of the slot
         int valid = lane < ppt ? min(max(s.C - first, 0), B) : 0;
@@ -740,7 +758,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
             ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, wait) &&
                  (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
                                      a.err, wait));
-            if (!ok) break;
+            if (rare(!ok)) break;
             tc_fence_after();
             const uint32_t id = idesc(bf, ncols, 0);
             const uint64_t qd = smem_desc_advance(q_desc, bf ? C::kQbf - C::kQ16 : 0);
@@ -754,7 +772,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           } else {
             ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, wait) &&
                  wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, wait);
-            if (!ok) break;
+            if (rare(!ok)) break;
             tc_fence_after();
             const uint32_t id = idesc(bf, ncols, 1);
             const uint64_t pd = smem_desc_advance(p_desc, (u & 1) * C::kPBytes);
@@ -808,36 +826,36 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         idle = col0 >= s.nrows;
         const int qr = stid >> 3, part = stid & 7;
         constexpr int kV = D / 64;  // 16-byte pieces of a thread
-        uint4 v[kV];
         const int r = s.r0 + qr;
         const int64_t hr = (int64_t)(s.q0 + r / G) * H + s.g * G + r % G;
         const uint4 *src =
             reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + hr * D) + part * kV;
+        uint4 v[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] = qr < s.nrows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        uint32_t top = 0;  // largest magnitude's bits
+        uint32_t top = 0;  // largest magnitude's bits, of both halves of the words at once
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-          const uint32_t wv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(wv[j] & 0x7fffu, (wv[j] >> 16) & 0x7fffu));
+          const uint32_t t4 = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+          top = __vmaxu2(top, t4);
         }
+        top = max(top & 0xffffu, top >> 16);
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int e = top ? min(max((int)(top >> 7) - 127 - 14, -126), 112) : 0;
         const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-          const uint32_t wv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t hv[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            hv[j] = pack_half2(__uint_as_float(wv[j] << 16) * down,
-                               __uint_as_float(wv[j] & 0xffff0000u) * down);
+          uint4 h;
+          h.x = pack_half2(__uint_as_float(v[i].x << 16) * down, __uint_as_float(v[i].x & 0xffff0000u) * down);
+          h.y = pack_half2(__uint_as_float(v[i].y << 16) * down, __uint_as_float(v[i].y & 0xffff0000u) * down);
+          h.z = pack_half2(__uint_as_float(v[i].z << 16) * down, __uint_as_float(v[i].z & 0xffff0000u) * down);
+          h.w = pack_half2(__uint_as_float(v[i].w << 16) * down, __uint_as_float(v[i].w & 0xffff0000u) * down);
           const int c = part * kV + i;
           const uint32_t off = (c >> 3) * (NT * 128) + (qr >> 3) * 1024 + (qr & 7) * 128 +
                                (((c & 7) ^ (qr & 7)) << 4);
-          sts128(sb + C::kQ16 + off, make_uint4(hv[0], hv[1], hv[2], hv[3]));
+          sts128(sb + C::kQ16 + off, h);
           sts128(sb + C::kQbf + off, v[i]);
         }
         // (the other warpgroups are done with the previous segment's arrays)
@@ -858,8 +876,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       float l[16];  // this key lane's share of the columns' sums
 #pragma unroll
       for (int j = 0; j < 16; ++j) l[j] = 0.f;
-      float m_col = -INFINITY;  // reference of column `col`
-      bool unset = true;        // a column may have no reference yet
+      float m_col = 0.f;  // reference of column `col`
+      bool settled = false;  // every column has had a score near its reference
+      unsigned seen_mask = 0;  // columns that have seen a key (kept while not settled)
       const int t_first = t;
 #pragma unroll 1
       for (; t < t_end; ++t, ++u) {
@@ -872,7 +891,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
             ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
         }
         ok = named_sync_and(bar, 128, ok);
-        if (!ok) break;
+        if (rare(!ok)) break;
         tc_fence_after();
         if (idle) {
           tc_fence_before();
@@ -906,7 +925,20 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const float top =
             fmax3(fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8])),
                   fmax3(fmax3(x[9], x[10], x[11]), x[12], x[13]), fmaxf(x[14], x[15]));
-        if (named_sync_or(bar, 128, unset || top > kRescale)) {
+        bool move_any = top > kHigh;
+        if (!settled) {
+          // columns with a score above kLow, over the warpgroup's keys of this tile
+          unsigned near = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) near |= x[j] > kLow ? 1u << j : 0u;
+          near = __reduce_or_sync(0xffffffffu, near);
+          if (lane == 0) ms->near[wg][quad] = near;
+          named_sync(bar, 128);
+          settled = (ms->near[wg][0] | ms->near[wg][1] | ms->near[wg][2] | ms->near[wg][3]) == 0xffffu;
+          if (settled) seen_mask = 0xffffu;
+          move_any = move_any || !settled;
+        }
+        if (rare(named_sync_or(bar, 128, move_any))) {
           // ---- move references: the columns' maxima over the tile ------------------
           // every P.V product so far must have landed in O before O is rescaled
           if (t > t_first)
@@ -916,16 +948,19 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           tc_fence_after();
           ms->red[wg][quad][col] = transpose_reduce<false>(x, lane);
           ok = named_sync_and(bar, 128, ok);
-          if (!ok) break;
-          // column `col`: its largest score against the reference (0 before it has one)
+          if (rare(!ok)) break;
+          // column `col`: its largest score against the reference. Without a visible key
+          // (-inf) there is nothing to move to; the column settles with a later tile.
           const float rise = fmaxf(fmaxf(ms->red[wg][0][col], ms->red[wg][1][col]),
                                    fmaxf(ms->red[wg][2][col], ms->red[wg][3][col]));
-          const bool fresh = m_col == -INFINITY;
-          const bool move = fresh ? rise > -INFINITY : rise > kRescale;
+          const bool seen = rise > -INFINITY;
+          const bool move = seen && (rise > kHigh || (!settled && rise < kLow && !(seen_mask >> col & 1)));
           const float d_col = move ? rise : 0.f;
-          const float a_col = !move ? 1.f : fresh ? 0.f : fast_exp2(-rise);
-          if (move) m_col = (fresh ? 0.f : m_col) + rise;
-          unset = __any_sync(0xffffffffu, m_col == -INFINITY);
+          // (a column that has seen no key yet has nothing to rescale)
+          const float a_col = !move ? 1.f : !(seen_mask >> col & 1) ? 0.f : fast_exp2(-rise);
+          m_col += d_col;
+          seen_mask |= __ballot_sync(0xffffffffu, seen) & 0xffffu;
+          settled = seen_mask == 0xffffu;
           if (quad == 0 && lane < 16) ms->nm[col0 + lane] -= d_col;
           float o[16];
           if (t > t_first) tmem_ld16f(o_addr, o);
@@ -971,49 +1006,45 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       __syncwarp();
       ms->red[wg][quad][col] = transpose_reduce<true>(l, lane);
       ok = named_sync_and(bar_all, 128 * C::kSw, ok);
-      if (!ok) break;
+      if (rare(!ok)) break;
       tc_fence_after();
       // sum of column `col` (the same in the four warps)
-      const float L = (ms->red[wg][0][col] + ms->red[wg][1][col]) +
-                      (ms->red[wg][2][col] + ms->red[wg][3][col]);
+      float L = (ms->red[wg][0][col] + ms->red[wg][1][col]) +
+                (ms->red[wg][2][col] + ms->red[wg][3][col]);
+      float M = L > 0.f || L != L ? m_col : -INFINITY;  // (no key seen: no reference)
+      float f = a.v_mul / L;
       const Seg s = ms->seg;
       const int live = min(16, s.nrows - col0);  // columns with a row (none or fewer: idle)
-      float o[16];
-      tmem_ld16f(o_addr, o);
-      tc_fence_before();
-      // infinite or NaN window values of this dim, for the rows that see them
-      if (s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff) {
-        const int nb = ms->nf_blk[sg & 3][row], nn = ms->nf_nan[sg & 3][row];
-        const float nv = ms->nf_val[sg & 3][row];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int bj = ms->blk[col0 + j];
-          if (bj >= nb) o[j] += bj >= nn ? NAN : nv;
-        }
-      }
-      const bool dim_on = D == 128 || row < D;
+      const bool dim_on = D == 128 || row < D, whole = s.len == s.T;
+      const bool odd = s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff;
       uint16_t *outp = static_cast<uint16_t *>(a.out) + row;
-      if (s.len == s.T) {
-        const float f = a.v_mul / L;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
-          if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
-        }
-        if (quad == 0 && lane < live && a.lse_out)
-          a.lse_out[ms->hr[col0 + lane]] = (m_col + __log2f(L)) * 0.6931471805599453f;
-        continue;
-      }
-      // ---- a part of the row tile: to the workspace; the last to arrive composes --------
       constexpr int kSlotFloats = NT * D + 2 * NT;
-      {
-        float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (s.w0 + s.t0 == wb ? 0 : 1)) * kSlotFloats;
+      float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (s.w0 + s.t0 == wb ? 0 : 1)) * kSlotFloats;
+      // (loops of four columns: what runs once a row tile is kept short, since it comes
+      // from beyond the instruction cache every time)
+#pragma unroll 1
+      for (int c = 0; c < live; c += 4) {
+        float o[4];
+        tmem_ld4f(o_addr + c, o);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < live && dim_on) __stcg(slot + (col0 + j) * D + row, o[j]);
-        if (quad == 0 && lane < live)
-          __stcg(reinterpret_cast<float2 *>(slot + NT * D) + col0 + lane, make_float2(m_col, L));
+        for (int j = 0; j < 4; ++j) {
+          if (rare(odd)) {  // infinite or NaN window values of this dim, for the rows that see them
+            const int bj = ms->blk[col0 + c + j];
+            if (bj >= ms->nf_blk[sg & 3][row])
+              o[j] += bj >= ms->nf_nan[sg & 3][row] ? NAN : ms->nf_val[sg & 3][row];
+          }
+          const float y = o[j] * __shfl_sync(0xffffffffu, f, c + j);
+          if (c + j < live && dim_on) {
+            if (whole) outp[ms->hr[col0 + c + j] * D] = float_to_bf16_bits(y);
+            else __stcg(slot + (col0 + c + j) * D + row, o[j]);
+          }
+        }
       }
+      tc_fence_before();
+      if (!whole) {
+      // ---- a part of the row tile: to the workspace; the last to arrive composes --------
+      if (quad == 0 && lane < live)
+        __stcg(reinterpret_cast<float2 *>(slot + NT * D) + col0 + lane, make_float2(M, L));
       __threadfence();
       named_sync(bar_all, 128 * C::kSw);
       if (stid == 0) {
@@ -1032,24 +1063,26 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       const bool compose = ms->last != 0;
       const int c0 = ms->c0, c1 = ms->c1, second = ms->second;
       named_sync(bar_all, 128 * C::kSw);  // ms->last may be written again
-      if (!compose || idle) continue;
+      if (!compose) continue;
       __threadfence();
       auto part = [&](int c) -> const float * {
         return a.ws_o + ((int64_t)2 * c + (c == c0 ? second : 0)) * kSlotFloats;
       };
       // (largest reference, sum) of column `col` over the parts
-      float Mx = -INFINITY, Lx = 0.f;
+      M = -INFINITY;
+      L = 0.f;
 #pragma unroll 1
       for (int c = c0; c <= c1; ++c) {
         if (col >= live) continue;
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(c) + NT * D) + col0 + col);
-        const float m_new = fmaxf(Mx, ml.x);
+        const float m_new = fmaxf(M, ml.x);
         if (m_new == -INFINITY) continue;  // no key of these parts is visible to the row
-        Lx = (Mx == m_new ? Lx : Lx * fast_exp2(Mx - m_new)) +
-             (ml.x == m_new ? ml.y : ml.y * fast_exp2(ml.x - m_new));
-        Mx = m_new;
+        L = (M == m_new ? L : L * fast_exp2(M - m_new)) +
+            (ml.x == m_new ? ml.y : ml.y * fast_exp2(ml.x - m_new));
+        M = m_new;
       }
-      const float f = a.v_mul / Lx;
+      f = a.v_mul / L;
+      float o[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = 0.f;
 #pragma unroll 1
@@ -1059,7 +1092,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = j < live && dim_on ? __ldcg(p + j * D) : 0.f;
         const float m = col < live ? __ldcg(part(c) + NT * D + 2 * (col0 + col)) : -INFINITY;
-        const float wt = m == Mx ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - Mx);
+        const float wt = m == M ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - M);
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = fmaf(__shfl_sync(0xffffffffu, wt, j), v[j], o[j]);
       }
@@ -1068,8 +1101,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
         if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
       }
+      }
       if (quad == 0 && lane < live && a.lse_out)
-        a.lse_out[ms->hr[col0 + lane]] = (Mx + __log2f(Lx)) * 0.6931471805599453f;
+        a.lse_out[ms->hr[col0 + lane]] = (M + __log2f(L)) * 0.6931471805599453f;
     }
   }
 
