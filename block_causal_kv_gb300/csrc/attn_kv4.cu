@@ -84,6 +84,9 @@ struct Cfg {
   static constexpr int kPSbo = 1024;                  // bytes between 8-key groups of P
 };
 
+struct SeqMeta {
+  int q0, n, C, pad;
+};
 struct Seg {      // the part of one row tile that lies in a CTA's share
   int q0, n, C;   // sequence: first window row, window rows, cached tokens
   int b, g;
@@ -119,7 +122,9 @@ struct Misc {
   // segments ahead of the epilogue that reads them.
   int nf_blk[4][128], nf_nan[4][128];
   float nf_val[4][128];
-  alignas(8) long long pre[1];    // units before each sequence, [batch] (runs on)
+  // per sequence, [batch] (each array runs on behind the struct): units before it, then
+  // its first window row, window rows and cached tokens
+  alignas(16) long long pre[2];
 };
 
 // ---- small device helpers ----------------------------------------------------
@@ -299,6 +304,12 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
 }
 
 // ---- work line -----------------------------------------------------------------
+// x / n, by 32-bit division where that does (64-bit ones take hundreds of cycles).
+__device__ __forceinline__ long long share(long long x, long long n) {
+  if ((x | n) >> 32 == 0) return (uint32_t)x / (uint32_t)n;
+  return x / n;
+}
+
 // Row tiles of a sequence: `tiles` of `rows` rows each (a multiple of 16, the last
 // one shorter), as equal as 16 rows allow.
 struct RowTiles {
@@ -316,6 +327,7 @@ __device__ __forceinline__ RowTiles row_tiles(int total) {
 // The segment that starts at unit w of the line (w < w1: end of the share).
 __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, long long w,
                                        long long w1) {
+  const SeqMeta *meta = reinterpret_cast<const SeqMeta *>(pre + ((a.batch + 1) & ~1));
   int lo = 0, hi = a.batch - 1;  // largest b with pre[b] <= w
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -323,9 +335,9 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   }
   Seg s;
   s.b = lo;
-  s.q0 = __ldg(a.q_start + lo);
-  s.n = __ldg(a.q_start + lo + 1) - s.q0;
-  s.C = __ldg(a.ctx_len + lo);
+  s.q0 = meta[lo].q0;
+  s.n = meta[lo].n;
+  s.C = meta[lo].C;
   const RowTiles rt = row_tiles(a.group * s.n);
   s.Tc = (s.C + kKeys - 1) / kKeys;
   s.T = s.Tc + (s.n + kKeys - 1) / kKeys;
@@ -340,6 +352,26 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   s.nrows = min(rt.rows, a.group * s.n - s.r0);
   s.item = (s.b * a.num_heads_kv + s.g) * a.m_tiles + m;
   return s;
+}
+
+// Four parts of a column into the running composition: o, l in units of 2^-m. A part
+// without weight (reference -inf) may hold anything.
+__device__ __forceinline__ void fold_parts(float4 &o, float &m, float &l, const float4 (&v)[4],
+                                           const float2 (&ml)[4]) {
+  const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+  if (top == -INFINITY) return;
+  const float keep = m == -INFINITY ? 0.f : m == top ? 1.f : fast_exp2(m - top);
+  o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+  l *= keep;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (ml[k].x == -INFINITY) continue;
+    const float w = ml[k].x == top ? 1.f : fast_exp2(ml[k].x - top);
+    o = make_float4(fmaf(w, v[k].x, o.x), fmaf(w, v[k].y, o.y), fmaf(w, v[k].z, o.z),
+                    fmaf(w, v[k].w, o.w));
+    l = fmaf(w, ml[k].y, l);
+  }
+  m = top;
 }
 
 // ---- dequantisation ---------------------------------------------------------------
@@ -640,6 +672,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
   // ---- the line of work: units before each sequence -----------------------------
   long long *pre = ms->pre;
+  SeqMeta *meta = reinterpret_cast<SeqMeta *>(pre + ((a.batch + 1) & ~1));
   if (warp == 0) {
     long long run = 0;
 #pragma unroll 1
@@ -651,6 +684,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         if (load_seq_meta(a, b, q0, n, ctx)) {
           const long long tiles = (ctx + kKeys - 1LL) / kKeys + (n + kKeys - 1) / kKeys;
           u = tiles * a.num_heads_kv * row_tiles(a.group * n).tiles;
+          meta[b] = SeqMeta{q0, n, ctx, 0};
         } else if (blockIdx.x == 0) {
           set_err(a.err, D2F_ERR_INVALID_ARG);
         }
@@ -668,8 +702,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       // shares of at least one unit; the CTAs past the last share have none
       const long long n = min((long long)gridDim.x, run), c = blockIdx.x;
       ms->W = run;
-      ms->wb = c < n ? run * c / n : 0;
-      ms->we = c < n ? run * (c + 1) / n : 0;
+      ms->wb = c < n ? share(run * c, n) : 0;
+      ms->we = c < n ? share(run * (c + 1), n) : 0;
     }
   }
   tc_fence_before();
@@ -860,7 +894,15 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         }
         // (the other warpgroups are done with the previous segment's arrays)
         named_sync(bar_all, 128 * C::kSw);
-        if (stid == 0) ms->seg = s;  // (read back by the epilogue)
+        if (stid == 0) {  // (read back by the epilogue)
+          ms->seg = s;
+          // Shares that hold units of this row tile: unit w is in share ((w + 1) n - 1) / W;
+          // the first one's part is in its first slot only if the share starts with the tile.
+          const long long W = ms->W, nc = min((long long)gridDim.x, W);
+          ms->c0 = (int)share((s.w0 + 1) * nc - 1, W);
+          ms->c1 = (int)share((s.w0 + s.T) * nc - 1, W);
+          ms->second = share(W * ms->c0, nc) != s.w0;
+        }
         if (part == 0) {
           const float up = __int_as_float((127 + e) << 23);
           ms->c[qr] = a.scale_log2 * a.k_mul * up;
@@ -1020,90 +1062,91 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       uint16_t *outp = static_cast<uint16_t *>(a.out) + row;
       constexpr int kSlotFloats = NT * D + 2 * NT;
       float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (s.w0 + s.t0 == wb ? 0 : 1)) * kSlotFloats;
-      // (loops of four columns: what runs once a row tile is kept short, since it comes
-      // from beyond the instruction cache every time)
-#pragma unroll 1
-      for (int c = 0; c < live; c += 4) {
-        float o[4];
-        tmem_ld4f(o_addr + c, o);
+      float o[16];
+      tmem_ld16f(o_addr, o);
+      tc_fence_before();
+      if (rare(odd)) {  // infinite or NaN window values of this dim, for the rows that see them
+        const int nb = ms->nf_blk[sg & 3][row], nn = ms->nf_nan[sg & 3][row];
+        const float nv = ms->nf_val[sg & 3][row];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (rare(odd)) {  // infinite or NaN window values of this dim, for the rows that see them
-            const int bj = ms->blk[col0 + c + j];
-            if (bj >= ms->nf_blk[sg & 3][row])
-              o[j] += bj >= ms->nf_nan[sg & 3][row] ? NAN : ms->nf_val[sg & 3][row];
-          }
-          const float y = o[j] * __shfl_sync(0xffffffffu, f, c + j);
-          if (c + j < live && dim_on) {
-            if (whole) outp[ms->hr[col0 + c + j] * D] = float_to_bf16_bits(y);
-            else __stcg(slot + (col0 + c + j) * D + row, o[j]);
-          }
+        for (int j = 0; j < 16; ++j) {
+          const int bj = ms->blk[col0 + j];
+          if (bj >= nb) o[j] += bj >= nn ? NAN : nv;
         }
       }
-      tc_fence_before();
-      if (!whole) {
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
+          if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
+        }
+        if (quad == 0 && lane < live && a.lse_out)
+          a.lse_out[ms->hr[col0 + lane]] = (M + __log2f(L)) * 0.6931471805599453f;
+        continue;
+      }
       // ---- a part of the row tile: to the workspace; the last to arrive composes --------
-      if (quad == 0 && lane < live)
+      if (dim_on) {
+        float *so = slot + col0 * D + row;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) __stcg(so + j * D, o[j]);  // (columns without a row too)
+      }
+      if (quad == 0 && lane < 16)
         __stcg(reinterpret_cast<float2 *>(slot + NT * D) + col0 + lane, make_float2(M, L));
-      __threadfence();
       named_sync(bar_all, 128 * C::kSw);
       if (stid == 0) {
-        // shares that hold units of this row tile: share of unit w is ((w + 1) n - 1) / W;
-        // the first one's part is in its first slot only if the share starts with the tile
-        const long long W = ms->W, n = min((long long)gridDim.x, W);
-        const int c0 = (int)(((s.w0 + 1) * n - 1) / W), c1 = (int)(((s.w0 + s.T) * n - 1) / W);
-        const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == c1 - c0;
+        __threadfence();  // (the barrier ordered the others' stores before this)
+        const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == ms->c1 - ms->c0;
         if (is_last) a.counters[s.item] = 0;
+        __threadfence();
         ms->last = is_last;
-        ms->c0 = c0;
-        ms->c1 = c1;
-        ms->second = W * c0 / n != s.w0;
       }
       named_sync(bar_all, 128 * C::kSw);
-      const bool compose = ms->last != 0;
-      const int c0 = ms->c0, c1 = ms->c1, second = ms->second;
-      named_sync(bar_all, 128 * C::kSw);  // ms->last may be written again
-      if (!compose) continue;
-      __threadfence();
+      if (!ms->last) continue;  // (written again only after the next segment's first barrier)
+      const int c0 = ms->c0, parts = ms->c1 - c0 + 1;
       auto part = [&](int c) -> const float * {
-        return a.ws_o + ((int64_t)2 * c + (c == c0 ? second : 0)) * kSlotFloats;
+        return a.ws_o + ((int64_t)2 * (c0 + c) + (c == 0 ? ms->second : 0)) * kSlotFloats;
       };
-      // (largest reference, sum) of column `col` over the parts
-      M = -INFINITY;
-      L = 0.f;
+      // The composition, over the whole CTA's columns: a thread owns four dims of a few
+      // columns, reads four parts of two columns at a time and keeps the running
+      // (reference, sum) of its columns beside their outputs.
+      constexpr int kD4 = D / 4, kStep = 128 * C::kSw / kD4;  // threads a column, columns a pass
+      const int d4 = 4 * (stid % kD4);
 #pragma unroll 1
-      for (int c = c0; c <= c1; ++c) {
-        if (col >= live) continue;
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(c) + NT * D) + col0 + col);
-        const float m_new = fmaxf(M, ml.x);
-        if (m_new == -INFINITY) continue;  // no key of these parts is visible to the row
-        L = (M == m_new ? L : L * fast_exp2(M - m_new)) +
-            (ml.x == m_new ? ml.y : ml.y * fast_exp2(ml.x - m_new));
-        M = m_new;
-      }
-      f = a.v_mul / L;
-      float o[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = 0.f;
+      for (int cl = stid / kD4; cl < s.nrows; cl += 2 * kStep) {
+        const int cb = min(cl + kStep, NT - 1);  // second column (it may hold no row)
+        float4 oa = make_float4(0.f, 0.f, 0.f, 0.f), ob = oa;
+        float Ma = -INFINITY, La = 0.f, Mb = -INFINITY, Lb = 0.f;
 #pragma unroll 1
-      for (int c = c0; c <= c1; ++c) {
-        const float *p = part(c) + col0 * D + row;
-        float v[16];
+        for (int c = 0; c < parts; c += 4) {
+          float4 va[4], vb[4];
+          float2 ma[4], mb[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = j < live && dim_on ? __ldcg(p + j * D) : 0.f;
-        const float m = col < live ? __ldcg(part(c) + NT * D + 2 * (col0 + col)) : -INFINITY;
-        const float wt = m == M ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - M);
+          for (int k = 0; k < 4; ++k) {
+            const float *p = part(min(c + k, parts - 1));
+            va[k] = __ldcg(reinterpret_cast<const float4 *>(p + cl * D + d4));
+            vb[k] = __ldcg(reinterpret_cast<const float4 *>(p + cb * D + d4));
+            ma[k] = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + cl);
+            mb[k] = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + cb);
+          }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = fmaf(__shfl_sync(0xffffffffu, wt, j), v[j], o[j]);
-      }
+          for (int k = 0; k < 4; ++k)
+            if (c + k >= parts) ma[k].x = mb[k].x = -INFINITY;  // (no part: no weight)
+          fold_parts(oa, Ma, La, va, ma);
+          fold_parts(ob, Mb, Lb, vb, mb);
+        }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float y = o[j] * __shfl_sync(0xffffffffu, f, j);
-        if (j < live && dim_on) outp[ms->hr[col0 + j] * D] = float_to_bf16_bits(y);
+        for (int k = 0; k < 2; ++k) {
+          const int cc = k ? cl + kStep : cl;
+          if (cc >= s.nrows) continue;
+          const float4 v = k ? ob : oa;
+          const float g = a.v_mul / (k ? Lb : La);
+          const int64_t at = ms->hr[cc];
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at * D + d4) =
+              make_uint2(pack_bf16x2(v.x * g, v.y * g), pack_bf16x2(v.z * g, v.w * g));
+          if (d4 == 0 && a.lse_out)
+            a.lse_out[at] = ((k ? Mb : Ma) + __log2f(k ? Lb : La)) * 0.6931471805599453f;
+        }
       }
-      }
-      if (quad == 0 && lane < live && a.lse_out)
-        a.lse_out[ms->hr[col0 + lane]] = (M + __log2f(L)) * 0.6931471805599453f;
     }
   }
 
@@ -1116,7 +1159,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
 template <int D>
 constexpr int smem_bytes(int batch) {
-  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * batch;
+  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * (batch + 2) + 16 * batch;
 }
 
 template <int D, int B>
