@@ -56,6 +56,9 @@ constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K ex
 // for a maximum over the lanes.
 constexpr float kHigh = 15.0f, kLow = -2.0f;
 constexpr int kMaxBatch = kKv4MaxBatch;
+// What a row tile costs beside its key tiles (its queries, the pipeline's start, its
+// output: about 7 us, against 1.2 us a key tile), in key tiles.
+constexpr int kSegmentTiles = 6;
 
 constexpr int NT = 64;                     // rows (columns of S^T and O^T) per row tile
 
@@ -85,14 +88,15 @@ struct Cfg {
 };
 
 struct SeqMeta {
-  int q0, n, C, pad;
+  int q0, n, C, items;  // items: row tiles of the sequences before it
 };
 struct Seg {      // the part of one row tile that lies in a CTA's share
   int q0, n, C;   // sequence: first window row, window rows, cached tokens
   int b, g;
   int r0, nrows;  // rows of the tile
-  int t0, len;    // key tiles [t0, t0 + len) of T; the first Tc are cached
+  int t0, len;    // key tiles [t0, t0 + len) of T (may be none); the first Tc are cached
   int T, Tc;
+  int units;      // units of the line that the segment covers
   long long w0;   // first unit of the row tile on the line
   int item;       // its counter
 };
@@ -105,8 +109,9 @@ struct Misc {
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_base;
   int abort_flag;
-  int last, c0, c1, second;       // composition: the last to arrive; the row tile's shares
+  int last, slot, c0, c1, second; // composition: the last to arrive; the row tile's shares
   long long W, wb, we;            // units of the line, and this CTA's share of them
+  int n_cta, k0;                  // CTAs with a share; units of a row tile before its tiles
   alignas(16) float c[NT];        // cached tiles: factor of a score, log2 units
   alignas(16) float nm[NT];       // minus the column's reference (0: none yet)
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
@@ -324,8 +329,9 @@ __device__ __forceinline__ RowTiles row_tiles(int total) {
   return r;
 }
 
-// The segment that starts at unit w of the line (w < w1: end of the share).
-__device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, long long w,
+// The segment that starts at unit w of the line (w < w1: end of the share). A row tile
+// is k0 units without work, then one per key tile.
+__device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, int k0, long long w,
                                        long long w1) {
   const SeqMeta *meta = reinterpret_cast<const SeqMeta *>(pre + ((a.batch + 1) & ~1));
   int lo = 0, hi = a.batch - 1;  // largest b with pre[b] <= w
@@ -341,11 +347,13 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   const RowTiles rt = row_tiles(a.group * s.n);
   s.Tc = (s.C + kKeys - 1) / kKeys;
   s.T = s.Tc + (s.n + kKeys - 1) / kKeys;
-  const long long local = w - pre[lo];
-  const int it = (int)((uint32_t)local / (uint32_t)s.T);  // (a sequence has < 2^31 units)
-  s.t0 = (int)(local - (long long)it * s.T);
-  s.w0 = w - s.t0;
-  s.len = (int)min((long long)(s.T - s.t0), w1 - w);
+  const int units = s.T + k0;
+  const uint32_t local = (uint32_t)(w - pre[lo]);  // (the host checks: below 2^31 a sequence)
+  const int it = (int)(local / (uint32_t)units), off = (int)(local - (uint32_t)it * units);
+  s.w0 = w - off;
+  s.units = (int)min((long long)(units - off), w1 - w);
+  s.t0 = max(0, off - k0);
+  s.len = max(0, off + s.units - k0) - s.t0;
   s.g = it / rt.tiles;
   const int m = it - s.g * rt.tiles;
   s.r0 = m * rt.rows;
@@ -482,9 +490,10 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
   int u = 0, cu = 0, sg = 0;
   bool ok = true;
 #pragma unroll 1
-  for (long long w = wb; w < we && ok; ++sg) {
-    const Seg s = segment(a, ms->pre, w, we);
-    w += s.len;
+  for (long long w = wb; w < we && ok;) {
+    const Seg s = segment(a, ms->pre, ms->k0, w, we);
+    w += s.units;
+    if (s.len == 0) continue;
     int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
     float nf_val = 0.f;
 #pragma unroll 1
@@ -626,6 +635,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
         ++cu;
       }
     }
+    ++sg;
   }
 }
 
@@ -674,36 +684,67 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
   long long *pre = ms->pre;
   SeqMeta *meta = reinterpret_cast<SeqMeta *>(pre + ((a.batch + 1) & ~1));
   if (warp == 0) {
-    long long run = 0;
+    long long tiles = 0;  // key tiles and row tiles of the sequences so far
+    int items = 0, longest = 0;
 #pragma unroll 1
     for (int base = 0; base < a.batch; base += 32) {
       const int b = base + lane;
       long long u = 0;
+      int it = 0;
       if (b < a.batch) {
         int q0, n, ctx;
         if (load_seq_meta(a, b, q0, n, ctx)) {
-          const long long tiles = (ctx + kKeys - 1LL) / kKeys + (n + kKeys - 1) / kKeys;
-          u = tiles * a.num_heads_kv * row_tiles(a.group * n).tiles;
+          const int T = (int)((ctx + kKeys - 1LL) / kKeys) + (n + kKeys - 1) / kKeys;
+          it = a.num_heads_kv * row_tiles(a.group * n).tiles;
+          u = (long long)T * it;
+          if (it > 0) longest = max(longest, T);
           meta[b] = SeqMeta{q0, n, ctx, 0};
         } else if (blockIdx.x == 0) {
           set_err(a.err, D2F_ERR_INVALID_ARG);
         }
       }
       long long inc = u;
+      int inc_it = it;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const int y = __shfl_up_sync(0xffffffffu, inc_it, o);
+        if (lane >= o) {
+          inc += x;
+          inc_it += y;
+        }
       }
-      if (b < a.batch) pre[b] = run + inc - u;
-      run += __shfl_sync(0xffffffffu, inc, 31);
+      if (b < a.batch) {
+        pre[b] = tiles + inc - u;
+        meta[b].items = items + inc_it - it;
+      }
+      tiles += __shfl_sync(0xffffffffu, inc, 31);
+      items += __shfl_sync(0xffffffffu, inc_it, 31);
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    // At least two key tiles a share: a smaller one costs more than it saves. Where all
+    // row tiles are alike and there are no more of them than CTAs, each is cut into the
+    // same number of shares, unless that leaves a share more than kSegmentTiles longer
+    // than an even cut of the whole line (whose shares straddle row tiles, each a segment
+    // of its own).
+    long long n = max(1LL, min((long long)gridDim.x, max((long long)items, tiles / 2)));
+    int k0 = kSegmentTiles;
+    if (items > 0 && items <= n && (long long)longest * items == tiles) {
+      const int k = (int)n / items;
+      if ((longest + k - 1) / k <= tiles / n + kSegmentTiles) {
+        n = (long long)items * k;
+        k0 = 0;
+      }
+    }
+    __syncwarp();
+    for (int b = lane; b < a.batch; b += 32) pre[b] += (long long)k0 * meta[b].items;
     if (lane == 0) {
-      // shares of at least one unit; the CTAs past the last share have none
-      const long long n = min((long long)gridDim.x, run), c = blockIdx.x;
-      ms->W = run;
-      ms->wb = c < n ? share(run * c, n) : 0;
-      ms->we = c < n ? share(run * (c + 1), n) : 0;
+      const long long W = tiles + (long long)k0 * items, c = blockIdx.x;
+      ms->W = W;
+      ms->n_cta = (int)n;
+      ms->k0 = k0;
+      ms->wb = c < n ? share(W * c, n) : 0;
+      ms->we = c < n ? share(W * (c + 1), n) : 0;
     }
   }
   tc_fence_before();
@@ -725,8 +766,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     bool ok = true;
 #pragma unroll 1
     for (long long w = wb; w < we && ok;) {
-      const Seg s = segment(a, pre, w, we);
-      w += s.len;
+      const Seg s = segment(a, pre, ms->k0, w, we);
+      w += s.units;
       const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
       const int t1 = min(s.t0 + s.len, s.Tc);
       auto fetch = [&](int t) -> int {  // page id of this lane's slot of tile t
@@ -779,11 +820,13 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
       const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
 #pragma unroll 1
-      for (long long w = wb; w < we && ok; ++sg) {
-        const Seg s = segment(a, pre, w, we);
-        w += s.len;
+      for (long long w = wb; w < we && ok;) {
+        const Seg s = segment(a, pre, ms->k0, w, we);
+        w += s.units;
+        if (s.len == 0) continue;
         const int ncols = (s.nrows + 15) & ~15;
         if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
+        ++sg;
 #pragma unroll 1
         for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
           const int bf = t >= s.Tc;  // window tiles are bf16
@@ -845,14 +888,15 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     bool ok = true;
 #pragma unroll 1
     for (long long w = wb; w < we && ok;) {
-      ++sg;
       int t, t_end, Tc, n;  // what the tile loop needs of the segment
       bool idle;            // (warpgroup-uniform) no row in these columns
 
       // ---- Q: eight threads per row; bf16 as it is, fp16 scaled by a power of two -----
       {
-        const Seg s = segment(a, pre, w, we);
-        w += s.len;
+        const Seg s = segment(a, pre, ms->k0, w, we);
+        w += s.units;
+        if (s.len == 0) continue;
+        ++sg;
         t = s.t0;
         t_end = s.t0 + s.len;
         Tc = s.Tc;
@@ -896,12 +940,14 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         named_sync(bar_all, 128 * C::kSw);
         if (stid == 0) {  // (read back by the epilogue)
           ms->seg = s;
-          // Shares that hold units of this row tile: unit w is in share ((w + 1) n - 1) / W;
-          // the first one's part is in its first slot only if the share starts with the tile.
-          const long long W = ms->W, nc = min((long long)gridDim.x, W);
-          ms->c0 = (int)share((s.w0 + 1) * nc - 1, W);
-          ms->c1 = (int)share((s.w0 + s.T) * nc - 1, W);
-          ms->second = share(W * ms->c0, nc) != s.w0;
+          // Shares that hold key tiles of this row tile: unit w is in share ((w + 1) n - 1) / W.
+          // A share's first segment has the CTA's first slot, any other the second: the
+          // first share's part is in its second slot if the share starts before the row tile.
+          const long long W = ms->W, nc = ms->n_cta, first = s.w0 + ms->k0;
+          ms->c0 = (int)share((first + 1) * nc - 1, W);
+          ms->c1 = (int)share((first + s.T) * nc - 1, W);
+          ms->second = share(W * ms->c0, nc) < s.w0;
+          ms->slot = w - s.units == wb ? 0 : 1;
         }
         if (part == 0) {
           const float up = __int_as_float((127 + e) << 23);
@@ -1061,7 +1107,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       const bool odd = s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff;
       uint16_t *outp = static_cast<uint16_t *>(a.out) + row;
       constexpr int kSlotFloats = NT * D + 2 * NT;
-      float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + (s.w0 + s.t0 == wb ? 0 : 1)) * kSlotFloats;
+      float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + ms->slot) * kSlotFloats;
       float o[16];
       tmem_ld16f(o_addr, o);
       tc_fence_before();

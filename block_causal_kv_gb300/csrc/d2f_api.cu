@@ -989,6 +989,11 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
   a.err = err_word;
   if (p.tc) {
+    const long long key_tiles = ((long long)max_pages_per_seq * block_size + 127) / 128 +
+                                cdiv(max_q_per_seq, 128);
+    if ((long long)num_heads_kv * p.m_tiles * (key_tiles + 16) > 0x7fffffffLL)
+      return fail(D2F_ERR_UNSUPPORTED, "a sequence of %lld key tiles in %lld row tiles is too large",
+                  key_tiles, (long long)num_heads_kv * p.m_tiles);
     const cudaError_t e = launch_attn_kv4(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tensor-core kv4 attention launch");
     return D2F_OK;
