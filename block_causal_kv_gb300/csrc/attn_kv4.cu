@@ -70,7 +70,7 @@ struct Cfg {
   // named barriers: 1 .. kSw a softmax warpgroup each, then all of them, then K, V^T
   static constexpr int kBarSoft = 1, kBarAll = kBarSoft + kSw, kBarK = kBarAll + 1;
   static constexpr int kRegLaunch = 72;               // registers per thread at launch
-  static constexpr int kRegCtl = 40, kRegDq = 72, kRegSoft = 80;
+  static constexpr int kRegCtl = 40, kRegDq = 56, kRegSoft = 88;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");
   static constexpr int kBuf = 2;                      // K and V^T operand buffers in TMEM
@@ -105,7 +105,9 @@ template <int D>
 struct Misc {
   using C = Cfg<D>;
   uint64_t full[C::kStages], empty[C::kStages];
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t k_full[2], v_full[2];
+  // (s_full: S^T is there, and its K operand buffer free; pv_done: O^T is up to date, P
+  // and the V^T operand buffer free)
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -117,6 +119,7 @@ struct Misc {
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
   alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
   Seg seg;                        // the softmax warps' current segment
+  Seg dseg[4 * C::kDq];           // the dequantising warps' current segments
   float red[C::kSw][4][16];
   unsigned near[C::kSw][4];       // reductions over a warpgroup's warps
   uint32_t vmask[4][4];           // valid keys of a tile (by tile index mod 4, warp)
@@ -238,6 +241,12 @@ __device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&r)[16])
       "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
       "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -417,13 +426,13 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int valid) {
   return valid >= 4 ? w : valid <= 0 ? 0u : w & ((1u << (8 * valid)) - 1);
 }
 
-// 64 keys (half h of the tile) of dim d: out[i] holds keys 2i and 2i + 1. `ragged`:
+// 32 keys (quarter h of the tile) of dim d: out[i] holds keys 2i and 2i + 1. `ragged`:
 // some page holds fewer than B valid tokens (the others give 0 whatever their bytes).
 template <int D, int B>
 __device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool ragged, int d,
-                                     int h, uint32_t (&out)[32]) {
-  constexpr int kPage = B * D + B * D / 8, kPages = 64 / B;
-  uint32_t w[8], sc[16];  // the half's codes and scale bytes, every load before any use
+                                     int h, uint32_t (&out)[16]) {
+  constexpr int kPage = B * D + B * D / 8, kPages = 32 / B;
+  uint32_t w[4], sc[8];  // the quarter's codes and scale bytes, every load before any use
   const uint32_t ca = stage + h * kPages * kPage + B * D / 2 + d * (B / 2);
   const uint32_t sa = stage + h * kPages * kPage + B * D + B * D / 16 + (d >> 4) * B;
 #pragma unroll
@@ -440,10 +449,10 @@ __device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool
         w[2 * p + 1] = v.y;
       } else {
         const uint4 v = lds128(ca + p * kPage);
-        w[4 * p] = v.x;
-        w[4 * p + 1] = v.y;
-        w[4 * p + 2] = v.z;
-        w[4 * p + 3] = v.w;
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
       }
 #pragma unroll
       for (int q = 0; q < B / 16; ++q) {
@@ -458,11 +467,11 @@ __device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool
   }
   if (ragged) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       sc[i] = keep_bytes(sc[i], (int)pvalid[h * kPages + 4 * i / B] - (4 * i) % B);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t s0, s1, s2, s3;
     scales_to_half(sc[2 * i], s0, s1);
     scales_to_half(sc[2 * i + 1], s2, s3);
@@ -478,11 +487,10 @@ __device__ __forceinline__ void dq_v(uint32_t stage, const uint8_t *pvalid, bool
 // V^T tile.
 template <int D, int B>
 __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uint32_t sb,
-                                             uint32_t tmem, long long wb, long long we) {
+                                             uint32_t tmem) {
   using C = Cfg<D>;
   constexpr int kPage = B * D + B * D / 8;
   volatile int *abort_flag = &ms->abort_flag;
-  const long long wait = a.wait_cycles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
   const int row = quad * 32 + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -490,75 +498,80 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
   int u = 0, cu = 0, sg = 0;
   bool ok = true;
 #pragma unroll 1
-  for (long long w = wb; w < we && ok;) {
-    const Seg s = segment(a, ms->pre, ms->k0, w, we);
-    w += s.units;
-    if (s.len == 0) continue;
+  for (long long w = ms->wb; w < ms->we && ok;) {
+    int t, t_end, Tc;  // what the tile loop needs of the segment
+    {
+      const Seg s = segment(a, ms->pre, ms->k0, w, ms->we);
+      w += s.units;
+      if (s.len == 0) continue;
+      t = s.t0;
+      t_end = s.t0 + s.len;
+      Tc = s.Tc;
+      // (read back for window tiles)
+      Seg &keep = ms->dseg[warp - 4];
+      if (lane == 0) keep = s;
+      __syncwarp();
+    }
+    const Seg &s = ms->dseg[warp - 4];
     int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
     float nf_val = 0.f;
 #pragma unroll 1
-    for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
+    for (; t < t_end && ok; ++t, ++u) {
       const int kb = u % C::kBuf;
       const bool reuse = u >= C::kBuf;  // the operand buffer held tile u - kBuf
       const uint32_t free_ph = (u / C::kBuf - 1) & 1;
-      const bool win = t >= s.Tc;
+      const bool win = t >= Tc;
       const int st = cu % C::kStages;
       const uint32_t stage = sb + C::kRing + st * C::kStage;
       // One warp of the warpgroup polls, for the tile's bytes and for the operand buffer;
       // the others wait in the named barrier, which takes no issue slots.
       if (quad == 0) {
         if (!win)
-          ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, wait);
+          ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, a.wait_cycles);
         if (reuse)
-          ok = wait_phase(smem_u32(do_k ? &ms->k_free[kb] : &ms->v_free[kb]), free_ph, abort_flag,
-                          a.err, wait) && ok;
+          ok = wait_phase(smem_u32(do_k ? &ms->s_full[kb] : &ms->pv_done[kb]), free_ph, abort_flag,
+                          a.err, a.wait_cycles) && ok;
       }
       ok = named_sync_and(do_k ? C::kBarK : C::kBarK + 1, 128, ok);
       if (rare(!ok)) break;
       tc_fence_after();
       const bool ragged = !win && ms->ragged[st];
       if (do_k) {
-        uint32_t x[32];
         const uint32_t ka = lane_base + C::kTmK + kb * (D / 2);
-        if (!win) {
+        if (!rare(win)) {
           const uint32_t tile = stage + (row / B) * kPage;
           const int o = row % B;
-          uint4 c[D / 32];
-          uint32_t sc[D / 64];
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) sc[i] = lds32(tile + B * D + o * (D / 16) + 4 * i);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) c[i] = lds128(tile + (i * B + o) * 16);
           unsigned m = 0xffffffffu;
-          if (ragged) m = __ballot_sync(0xffffffffu, o < (int)ms->pvalid[st][row / B]);
+          if (rare(ragged)) m = __ballot_sync(0xffffffffu, o < (int)ms->pvalid[st][row / B]);
           if (lane == 0) ms->vmask[u & 3][quad] = m;
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            uint32_t s01[2], s23[2];  // every scale in both halves of its pair
-            scales_to_half(__byte_perm(sc[h], 0, 0x1100), s01[0], s01[1]);
-            scales_to_half(__byte_perm(sc[h], 0, 0x3322), s23[0], s23[1]);
-            dq_k32(c[2 * h], s01[0], s01[1], x);
-            dq_k32(c[2 * h + 1], s23[0], s23[1], x + 16);
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t x[16];
+            const uint32_t sc = lds32(tile + B * D + o * (D / 16) + 4 * (i >> 1));
+            uint32_t s0, s1;  // every scale in both halves of its pair
+            scales_to_half(__byte_perm(sc, 0, i & 1 ? 0x3322 : 0x1100), s0, s1);
+            dq_k32(lds128(tile + (i * B + o) * 16), s0, s1, x);
             __syncwarp();
-            tmem_st32(ka + h * 32, x);
+            tmem_st16(ka + i * 16, x);
           }
         } else {
-          const int wr = (t - s.Tc) * kKeys + row;  // window row
+          const int wr = (t - Tc) * kKeys + row, n = s.n;  // window row
           const uint4 *src = reinterpret_cast<const uint4 *>(
               static_cast<const uint16_t *>(a.k_win) +
               ((int64_t)(s.q0 + wr) * a.num_heads_kv + s.g) * D);
+#pragma unroll 1
+          for (int h = 0; h < D / 32; ++h) {
+            uint32_t x[16];
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = wr < s.n ? __ldg(src + 8 * h + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = wr < n ? __ldg(src + 4 * h + i) : make_uint4(0, 0, 0, 0);
               x[4 * i] = v.x;
               x[4 * i + 1] = v.y;
               x[4 * i + 2] = v.z;
               x[4 * i + 3] = v.w;
             }
             __syncwarp();
-            tmem_st32(ka + h * 32, x);
+            tmem_st16(ka + h * 16, x);
           }
         }
         tmem_wait_st();
@@ -570,36 +583,36 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
           const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
           if (!win) {
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              uint32_t x[32];
+            for (int h = 0; h < 4; ++h) {
+              uint32_t x[16];
               dq_v<D, B>(stage, ms->pvalid[st], ragged, row, h, x);
               __syncwarp();
-              tmem_st32(va + h * 32, x);
+              tmem_st16(va + h * 16, x);
             }
           } else {
             const int64_t step = (int64_t)a.num_heads_kv * D;
 #pragma unroll 1
-            for (int w0 = 0; w0 < kKeys; w0 += 32) {  // 32 keys at a time
-              const int k0 = (t - s.Tc) * kKeys + w0;
+            for (int w0 = 0; w0 < kKeys; w0 += 16) {  // 16 keys at a time
+              const int k0 = (t - Tc) * kKeys + w0;
               const int left = s.n - k0;  // window rows from here on
               const uint16_t *src = static_cast<const uint16_t *>(a.v_win) +
                                     ((int64_t)(s.q0 + k0) * a.num_heads_kv + s.g) * D + row;
-              uint32_t x[16];
+              uint32_t x[8];
               bool odd = false;  // a value is not finite
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {  // every load before any use
+              for (int i = 0; i < 8; ++i) {  // every load before any use
                 const uint32_t e0 = 2 * i < left ? (uint32_t)__ldg(src + 2 * i * step) : 0u;
                 const uint32_t e1 = 2 * i + 1 < left ? (uint32_t)__ldg(src + (2 * i + 1) * step) : 0u;
                 x[i] = e0 | (e1 << 16);
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
+              for (int i = 0; i < 8; ++i)
                 odd = odd || (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
               if (odd) {
                 // infinite or NaN: out of the product (a hidden key's P is 0, and
                 // 0 * infinity is not), into the sums of the rows that see it
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
                   for (int j = 0; j < 2; ++j) {
                     const uint32_t e = (x[i] >> (16 * j)) & 0xffffu;
@@ -617,12 +630,12 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
                   }
               }
               __syncwarp();
-              tmem_st16(va + w0 / 2, x);
+              tmem_st8(va + w0 / 2, x);
             }
           }
           tmem_wait_st();
         }
-        if (t == s.t0 + s.len - 1) {  // read by the epilogue, which follows this tile's product
+        if (t == t_end - 1) {  // read by the epilogue, which follows this tile's product
           ms->nf_blk[sg & 3][row] = nf_blk;
           ms->nf_nan[sg & 3][row] = nf_nan;
           ms->nf_val[sg & 3][row] = nf_val;
@@ -661,8 +674,6 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->k_full[i]), 4);
       mbar_init(smem_u32(&ms->v_full[i]), 4);
-      mbar_init(smem_u32(&ms->k_free[i]), 1);
-      mbar_init(smem_u32(&ms->v_free[i]), 1);
       mbar_init(smem_u32(&ms->s_full[i]), 1);
       mbar_init(smem_u32(&ms->s_free[i]), 4 * C::kSw);
       mbar_init(smem_u32(&ms->p_full[i]), 4 * C::kSw);
@@ -751,9 +762,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
-  const long long wb = ms->wb, we = ms->we;  // this CTA's share of the line
   constexpr int page_bytes = B * D + B * D / 8;
-  const long long wait = a.wait_cycles;
 
   // Registers: what the control and dequantising warps do not need goes to the softmax
   // warps (the sum over the warpgroups stays under the launch's allocation).
@@ -765,8 +774,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     int cu = 0;  // cached tiles so far: stage cu % kStages
     bool ok = true;
 #pragma unroll 1
-    for (long long w = wb; w < we && ok;) {
-      const Seg s = segment(a, pre, ms->k0, w, we);
+    for (long long w = ms->wb; w < ms->we && ok;) {
+      const Seg s = segment(a, pre, ms->k0, w, ms->we);
       w += s.units;
       const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
       const int t1 = min(s.t0 + s.len, s.Tc);
@@ -780,7 +789,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const int next = fetch(t + 1);
         const int st = cu % C::kStages;
         if (cu >= C::kStages) {
-          ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, wait);
+          ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, a.wait_cycles);
           ok = __all_sync(0xffffffffu, ok);
           if (rare(!ok)) break;
         }
@@ -820,21 +829,21 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
       const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
 #pragma unroll 1
-      for (long long w = wb; w < we && ok;) {
-        const Seg s = segment(a, pre, ms->k0, w, we);
+      for (long long w = ms->wb; w < ms->we && ok;) {
+        const Seg s = segment(a, pre, ms->k0, w, ms->we);
         w += s.units;
         if (s.len == 0) continue;
         const int ncols = (s.nrows + 15) & ~15;
-        if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, wait);
+        if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, a.wait_cycles);
         ++sg;
 #pragma unroll 1
         for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
           const int bf = t >= s.Tc;  // window tiles are bf16
           const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
           if (warp == 1) {
-            ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, wait) &&
+            ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, a.wait_cycles) &&
                  (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
-                                     a.err, wait));
+                                     a.err, a.wait_cycles));
             if (rare(!ok)) break;
             tc_fence_after();
             const uint32_t id = idesc(bf, ncols, 0);
@@ -845,10 +854,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
               umma_bf16_tmem_a(sd, ka + k * 8,
                                smem_desc_advance(qd, (k >> 2) * (NT * 128) + (k & 3) * 32), id, k > 0);
             umma_commit(smem_u32(&ms->s_full[u & 1]));
-            umma_commit(smem_u32(&ms->k_free[kb]));
           } else {
-            ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, wait) &&
-                 wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, wait);
+            ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, a.wait_cycles) &&
+                 wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, a.wait_cycles);
             if (rare(!ok)) break;
             tc_fence_after();
             const uint32_t id = idesc(bf, ncols, 1);
@@ -859,7 +867,6 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
               umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
                                id, t > s.t0 || k > 0);
             umma_commit(smem_u32(&ms->pv_done[u & 1]));
-            umma_commit(smem_u32(&ms->v_free[kb]));
           }
         }
       }
@@ -869,8 +876,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     }
     }
   } else if (warp < 4 + 4 * C::kDq) {
-    // (the dequantising warps keep theirs)
-    dequant_role<D, B>(a, ms, sb, tmem, wb, we);
+    set_regs_dec<C::kRegDq>();
+    dequant_role<D, B>(a, ms, sb, tmem);
   } else {
     set_regs_inc<C::kRegSoft>();
     // ============================ softmax ============================================
@@ -887,13 +894,13 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     int u = 0, sg = -1;
     bool ok = true;
 #pragma unroll 1
-    for (long long w = wb; w < we && ok;) {
+    for (long long w = ms->wb; w < ms->we && ok;) {
       int t, t_end, Tc, n;  // what the tile loop needs of the segment
       bool idle;            // (warpgroup-uniform) no row in these columns
 
       // ---- Q: eight threads per row; bf16 as it is, fp16 scaled by a power of two -----
       {
-        const Seg s = segment(a, pre, ms->k0, w, we);
+        const Seg s = segment(a, pre, ms->k0, w, ms->we);
         w += s.units;
         if (s.len == 0) continue;
         ++sg;
@@ -947,7 +954,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           ms->c0 = (int)share((first + 1) * nc - 1, W);
           ms->c1 = (int)share((first + s.T) * nc - 1, W);
           ms->second = share(W * ms->c0, nc) < s.w0;
-          ms->slot = w - s.units == wb ? 0 : 1;
+          ms->slot = w - s.units == ms->wb ? 0 : 1;
         }
         if (part == 0) {
           const float up = __int_as_float((127 + e) << 23);
@@ -974,9 +981,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         // One warp of the warpgroup polls; the others wait in the named barrier, which
         // takes no issue slots.
         if (quad == 0) {
-          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, wait);
+          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, a.wait_cycles);
           if (u >= 2)  // P of tile u - 2 has been read
-            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, wait) && ok;
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, a.wait_cycles) && ok;
         }
         ok = named_sync_and(bar, 128, ok);
         if (rare(!ok)) break;
@@ -1031,7 +1038,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           // every P.V product so far must have landed in O before O is rescaled
           if (t > t_first)
             ok = wait_phase(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a.err,
-                           wait) && ok;
+                           a.wait_cycles) && ok;
           __syncwarp();
           tc_fence_after();
           ms->red[wg][quad][col] = transpose_reduce<false>(x, lane);
@@ -1090,7 +1097,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
       // ---- epilogue of the segment (a warpgroup that gave up joins the vote) ----------
       const int last = u - 1;
-      ok = ok && wait_phase(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, wait);
+      ok = ok && wait_phase(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, a.wait_cycles);
       __syncwarp();
       ms->red[wg][quad][col] = transpose_reduce<true>(l, lane);
       ok = named_sync_and(bar_all, 128 * C::kSw, ok);
@@ -1152,46 +1159,35 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       auto part = [&](int c) -> const float * {
         return a.ws_o + ((int64_t)2 * (c0 + c) + (c == 0 ? ms->second : 0)) * kSlotFloats;
       };
-      // The composition, over the whole CTA's columns: a thread owns four dims of a few
-      // columns, reads four parts of two columns at a time and keeps the running
-      // (reference, sum) of its columns beside their outputs.
+      // The composition, over the whole CTA's columns: a thread owns four dims of a column
+      // at a time, reads four parts at once and keeps the running (reference, sum) of the
+      // column beside its outputs.
       constexpr int kD4 = D / 4, kStep = 128 * C::kSw / kD4;  // threads a column, columns a pass
       const int d4 = 4 * (stid % kD4);
 #pragma unroll 1
-      for (int cl = stid / kD4; cl < s.nrows; cl += 2 * kStep) {
-        const int cb = min(cl + kStep, NT - 1);  // second column (it may hold no row)
-        float4 oa = make_float4(0.f, 0.f, 0.f, 0.f), ob = oa;
-        float Ma = -INFINITY, La = 0.f, Mb = -INFINITY, Lb = 0.f;
+      for (int cl = stid / kD4; cl < s.nrows; cl += kStep) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        float My = -INFINITY, Ly = 0.f;
 #pragma unroll 1
         for (int c = 0; c < parts; c += 4) {
-          float4 va[4], vb[4];
-          float2 ma[4], mb[4];
+          float4 v[4];
+          float2 ml[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float *p = part(min(c + k, parts - 1));
-            va[k] = __ldcg(reinterpret_cast<const float4 *>(p + cl * D + d4));
-            vb[k] = __ldcg(reinterpret_cast<const float4 *>(p + cb * D + d4));
-            ma[k] = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + cl);
-            mb[k] = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + cb);
+            v[k] = __ldcg(reinterpret_cast<const float4 *>(p + cl * D + d4));
+            ml[k] = __ldcg(reinterpret_cast<const float2 *>(p + NT * D) + cl);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (c + k >= parts) ma[k].x = mb[k].x = -INFINITY;  // (no part: no weight)
-          fold_parts(oa, Ma, La, va, ma);
-          fold_parts(ob, Mb, Lb, vb, mb);
+            if (c + k >= parts) ml[k].x = -INFINITY;  // (no part: no weight)
+          fold_parts(y, My, Ly, v, ml);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int cc = k ? cl + kStep : cl;
-          if (cc >= s.nrows) continue;
-          const float4 v = k ? ob : oa;
-          const float g = a.v_mul / (k ? Lb : La);
-          const int64_t at = ms->hr[cc];
-          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at * D + d4) =
-              make_uint2(pack_bf16x2(v.x * g, v.y * g), pack_bf16x2(v.z * g, v.w * g));
-          if (d4 == 0 && a.lse_out)
-            a.lse_out[at] = ((k ? Mb : Ma) + __log2f(k ? Lb : La)) * 0.6931471805599453f;
-        }
+        const float g = a.v_mul / Ly;
+        const int64_t at = ms->hr[cl];
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at * D + d4) =
+            make_uint2(pack_bf16x2(y.x * g, y.y * g), pack_bf16x2(y.z * g, y.w * g));
+        if (d4 == 0 && a.lse_out) a.lse_out[at] = (My + __log2f(Ly)) * 0.6931471805599453f;
       }
     }
   }
