@@ -20,26 +20,37 @@
 // Types. Stored values are exact in fp16, so cached tiles multiply in fp16: Q is
 // scaled per row by a power of two so that its largest element is in [2^14, 2^15)
 // (8 significant bits stay exact down to 2^-28 of it), P is rounded to fp16 (2^-11).
-// Window tiles keep bf16 K, V and Q and round P to bf16. Sums, maxima and both
-// accumulators are float.
+// Window tiles keep bf16 K, V and Q and round P to bf16 (2^-8), as the bf16 cache's
+// kernel does. Sums, references and both accumulators are float.
 //
-// Work. Row tile m of (sequence, KV head) holds up to NT = 64 or 128 of its
-// group * n query rows (row r = query r / group, head r % group); its key tiles (128
-// cached tokens each, then 128 window rows each) are units of work. All units of the
-// launch are one line, cut into equal shares, one CTA a share: every SM gets the
-// same number of tiles whatever the batch looks like. A row tile whose units lie in
-// several shares is put together by the CTA that arrives last at its counter, from
-// float partials in the workspace, in unit order (the result does not depend on who
-// is last). No CTA waits on another.
+// Work. A row tile holds up to NT = 64 of the group * n query rows of a (sequence, KV
+// head): row r = query r / group, head r % group. Its key tiles (128 cached tokens each,
+// then 128 window rows each) are units of work; what a row tile costs beside them counts
+// as kSegmentTiles units more. All units of the launch are one line, cut into equal
+// shares, one CTA a share: every SM gets the same work whatever the batch looks like. A row tile whose units lie in several shares is put together by the CTA that
+// arrives last at its counter, from float partials in the workspace, in the order of the
+// line (the result does not depend on who is last). No CTA waits on another.
 //
 // Roles of a CTA's warps:
 //   0        producer: page ids -> one bulk copy per page (K and V of a head are one
-//            contiguous piece) into a ring of stages
-//   1, 2     MMA issuers of S^T and of O^T (one lane each)
-//   dequant  K warpgroup and V warpgroup (one warpgroup for both with NT = 128)
-//   softmax  a warpgroup per 32 columns, thread = key lane: online softmax whose
-//            per-column reference moves only when a score exceeds it by 2^8, so the
-//            columns' maxima are not reduced over the lanes tile by tile
+//            contiguous piece) into a ring of five tiles
+//   1, 2     MMA issuers of S^T and of O^T (one elected lane each); 3 is spare
+//   4 - 11   a warpgroup dequantises K (thread = key), one V^T (thread = dim)
+//   12 - 27  four softmax warpgroups of 16 columns each, thread = key. A column's
+//            reference is 0, or moves when its scores lie outside [2^-2, 2^15] of it: a
+//            tile takes no maximum over the lanes, only a vote on whether some column
+//            has to move. With 16 columns a thread needs 88 registers, which lets 16
+//            warps run side by side (32 columns a thread: 8 warps, and spills).
+//
+// Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 49,152 to
+// 65,536 cached tokens and 64 window rows 291 us, 2.1 TB/s of 4-bit cache, against 329 us
+// of the bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes. Time
+// is 28 us + 1.2 us (about 2300 cycles) per key tile of a CTA. The bound is the chain of
+// a tile through the softmax warps (S^T ready, tensor memory -> registers, vote, 2^x,
+// P stored and handed on: 2000 to 2400 cycles against 512 of MMA), with the issue slots
+// at 68 % and the ALU pipe, which converts the codes, at 52 %; DRAM is at a third of its
+// rate, and neither a deeper ring, V^T on two warpgroups, fewer barriers nor polls that
+// sleep change the time by more than 2 %.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -226,14 +237,6 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld4f(uint32_t taddr, float (&r)[4]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -288,23 +291,22 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[16], int lane
   return SUM ? w[0] + got : fmaxf(w[0], got);
 }
 
-// Wait for a phase of an mbarrier. Every 64 polls it looks whether another thread of
-// the CTA gave up, and gives up itself after `budget` SM cycles.
+// Wait for a phase of an mbarrier. Every 64 polls (wait_polls) it looks whether another
+// thread of the CTA gave up, and gives up itself after `wait_cycles`; the kernel's end
+// reports that. (Fifteen copies of this are inlined: a report in each, or a second loop of
+// polls before the clock is read, costs the instruction cache 3 to 5 % of the time.)
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                           int32_t *err, long long budget) {
+                                           const AttnArgs &a) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  while (true) {
+  do {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < a.wait_polls; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > budget) {
-      *abort_flag = 1;
-      set_err(err, D2F_ERR_TIMEOUT);
-      return false;
-    }
-  }
+  } while (clock64() - t0 <= a.wait_cycles);
+  *abort_flag = 1;
+  return false;
 }
 // Arrive on an mbarrier from the warp's first lane (the warp's earlier accesses ordered
 // before it), without a branch.
@@ -527,10 +529,9 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       // the others wait in the named barrier, which takes no issue slots.
       if (quad == 0) {
         if (!win)
-          ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a.err, a.wait_cycles);
+          ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a);
         if (reuse)
-          ok = wait_phase(smem_u32(do_k ? &ms->s_full[kb] : &ms->pv_done[kb]), free_ph, abort_flag,
-                          a.err, a.wait_cycles) && ok;
+          ok = wait_phase(smem_u32(do_k ? &ms->s_full[kb] : &ms->pv_done[kb]), free_ph, abort_flag, a) && ok;
       }
       ok = named_sync_and(do_k ? C::kBarK : C::kBarK + 1, 128, ok);
       if (rare(!ok)) break;
@@ -769,111 +770,109 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
   if (warp < 4) {
     set_regs_dec<C::kRegCtl>();
     if (warp == 0) {
-    // ============================ producer =======================================
-    constexpr int ppt = kKeys / B;
-    int cu = 0;  // cached tiles so far: stage cu % kStages
-    bool ok = true;
-#pragma unroll 1
-    for (long long w = ms->wb; w < ms->we && ok;) {
-      const Seg s = segment(a, pre, ms->k0, w, ms->we);
-      w += s.units;
-      const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
-      const int t1 = min(s.t0 + s.len, s.Tc);
-      auto fetch = [&](int t) -> int {  // page id of this lane's slot of tile t
-        return t < t1 && lane < ppt && (int64_t)t * kKeys + lane * B < s.C
-                   ? __ldg(pt + (int64_t)t * ppt + lane) : -1;
-      };
-      int id = fetch(s.t0);
-#pragma unroll 1
-      for (int t = s.t0; t < t1; ++t, ++cu) {
-        const int next = fetch(t + 1);
-        const int st = cu % C::kStages;
-        if (cu >= C::kStages) {
-          ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a.err, a.wait_cycles);
-          ok = __all_sync(0xffffffffu, ok);
-          if (rare(!ok)) break;
-        }
-        const int first = t * kKeys + lane * B;  // first token of the slot
-        int valid = lane < ppt ? min(max(s.C - first, 0), B) : 0;
-        if (valid > 0 && (id < 0 || id >= a.num_pages)) {
-          set_err(a.err, D2F_ERR_BAD_INDEX);
-          valid = 0;
-        }
-        if (lane < 16) ms->pvalid[st][lane] = (uint8_t)valid;
-        const unsigned have = __ballot_sync(0xffffffffu, valid > 0);
-        const bool whole = __all_sync(0xffffffffu, lane >= ppt || valid == B);
-        if (lane == 0) ms->ragged[st] = !whole;
-        const uint32_t full = smem_u32(&ms->full[st]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * (uint32_t)page_bytes);
-        __syncwarp();
-        if (valid > 0)
-          bulk_load(sb + C::kRing + st * C::kStage + lane * page_bytes,
-                    a.kv4_pool + ((int64_t)id * a.num_heads_kv + s.g) * page_bytes, page_bytes, full);
-        id = next;
-      }
-    }
-    if (lane == 0) {  // every copy issued must have landed before the CTA ends
-#pragma unroll 1
-      for (int i = max(0, cu - C::kStages); i < cu; ++i) {
-        volatile int no_abort = 0;
-        wait_phase(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err,
-                  kDrainCycles);
-      }
-    }
-  } else if (warp == 1 || warp == 2) {
-    // ============================ MMA issuers ======================================
-    if (elect_one()) {
+      // ============================ producer =======================================
+      constexpr int ppt = kKeys / B;
+      int cu = 0;  // cached tiles so far: stage cu % kStages
       bool ok = true;
-      int u = 0, sg = 0;
-      const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
-      const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
 #pragma unroll 1
       for (long long w = ms->wb; w < ms->we && ok;) {
         const Seg s = segment(a, pre, ms->k0, w, ms->we);
         w += s.units;
-        if (s.len == 0) continue;
-        const int ncols = (s.nrows + 15) & ~15;
-        if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a.err, a.wait_cycles);
-        ++sg;
+        const int32_t *pt = a.page_table + (int64_t)s.b * a.max_pages_per_seq;
+        const int t1 = min(s.t0 + s.len, s.Tc);
+        auto fetch = [&](int t) -> int {  // page id of this lane's slot of tile t
+          return t < t1 && lane < ppt && (int64_t)t * kKeys + lane * B < s.C
+                     ? __ldg(pt + (int64_t)t * ppt + lane) : -1;
+        };
+        int id = fetch(s.t0);
 #pragma unroll 1
-        for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
-          const int bf = t >= s.Tc;  // window tiles are bf16
-          const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
-          if (warp == 1) {
-            ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a.err, a.wait_cycles) &&
-                 (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag,
-                                     a.err, a.wait_cycles));
+        for (int t = s.t0; t < t1; ++t, ++cu) {
+          const int next = fetch(t + 1);
+          const int st = cu % C::kStages;
+          if (cu >= C::kStages) {
+            ok = wait_phase(smem_u32(&ms->empty[st]), (cu / C::kStages - 1) & 1, abort_flag, a);
+            ok = __all_sync(0xffffffffu, ok);
             if (rare(!ok)) break;
-            tc_fence_after();
-            const uint32_t id = idesc(bf, ncols, 0);
-            const uint64_t qd = smem_desc_advance(q_desc, bf ? C::kQbf - C::kQ16 : 0);
-            const uint32_t sd = tmem + C::kTmS + (u & 1) * NT, ka = tmem + C::kTmK + kb * (D / 2);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              umma_bf16_tmem_a(sd, ka + k * 8,
-                               smem_desc_advance(qd, (k >> 2) * (NT * 128) + (k & 3) * 32), id, k > 0);
-            umma_commit(smem_u32(&ms->s_full[u & 1]));
-          } else {
-            ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a.err, a.wait_cycles) &&
-                 wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a.err, a.wait_cycles);
-            if (rare(!ok)) break;
-            tc_fence_after();
-            const uint32_t id = idesc(bf, ncols, 1);
-            const uint64_t pd = smem_desc_advance(p_desc, (u & 1) * C::kPBytes);
-            const uint32_t va = tmem + C::kTmV + kb * (kKeys / 2);
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
-                               id, t > s.t0 || k > 0);
-            umma_commit(smem_u32(&ms->pv_done[u & 1]));
           }
+          const int first = t * kKeys + lane * B;  // first token of the slot
+          int valid = lane < ppt ? min(max(s.C - first, 0), B) : 0;
+          if (valid > 0 && (id < 0 || id >= a.num_pages)) {
+            set_err(a.err, D2F_ERR_BAD_INDEX);
+            valid = 0;
+          }
+          if (lane < 16) ms->pvalid[st][lane] = (uint8_t)valid;
+          const unsigned have = __ballot_sync(0xffffffffu, valid > 0);
+          const bool whole = __all_sync(0xffffffffu, lane >= ppt || valid == B);
+          if (lane == 0) ms->ragged[st] = !whole;
+          const uint32_t full = smem_u32(&ms->full[st]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * (uint32_t)page_bytes);
+          __syncwarp();
+          if (valid > 0)
+            bulk_load(sb + C::kRing + st * C::kStage + lane * page_bytes,
+                      a.kv4_pool + ((int64_t)id * a.num_heads_kv + s.g) * page_bytes, page_bytes, full);
+          id = next;
         }
       }
-      umma_commit(smem_u32(&ms->drain));
-      volatile int no_abort = 0;
-      wait_phase(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
-    }
+      if (lane == 0) {  // every copy issued must have landed before the CTA ends
+#pragma unroll 1
+        for (int i = max(0, cu - C::kStages); i < cu; ++i) {
+          volatile int no_abort = 0;
+          mbar_wait(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err, kDrainCycles);
+        }
+      }
+    } else if (warp == 1 || warp == 2) {
+      // ============================ MMA issuers ======================================
+      if (elect_one()) {
+        bool ok = true;
+        int u = 0, sg = 0;
+        const uint64_t q_desc = smem_desc_sw128(sb + C::kQ16, 16, 1024);
+        const uint64_t p_desc = smem_desc_sw128(sb + C::kP, 1024, C::kPSbo);
+#pragma unroll 1
+        for (long long w = ms->wb; w < ms->we && ok;) {
+          const Seg s = segment(a, pre, ms->k0, w, ms->we);
+          w += s.units;
+          if (s.len == 0) continue;
+          const int ncols = (s.nrows + 15) & ~15;
+          if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a);
+          ++sg;
+#pragma unroll 1
+          for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
+            const int bf = t >= s.Tc;  // window tiles are bf16
+            const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
+            if (warp == 1) {
+              ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a) &&
+                   (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag, a));
+              if (rare(!ok)) break;
+              tc_fence_after();
+              const uint32_t id = idesc(bf, ncols, 0);
+              const uint64_t qd = smem_desc_advance(q_desc, bf ? C::kQbf - C::kQ16 : 0);
+              const uint32_t sd = tmem + C::kTmS + (u & 1) * NT, ka = tmem + C::kTmK + kb * (D / 2);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                umma_bf16_tmem_a(sd, ka + k * 8,
+                                 smem_desc_advance(qd, (k >> 2) * (NT * 128) + (k & 3) * 32), id, k > 0);
+              umma_commit(smem_u32(&ms->s_full[u & 1]));
+            } else {
+              ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a) &&
+                   wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a);
+              if (rare(!ok)) break;
+              tc_fence_after();
+              const uint32_t id = idesc(bf, ncols, 1);
+              const uint64_t pd = smem_desc_advance(p_desc, (u & 1) * C::kPBytes);
+              const uint32_t va = tmem + C::kTmV + kb * (kKeys / 2);
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
+                                 id, t > s.t0 || k > 0);
+              umma_commit(smem_u32(&ms->pv_done[u & 1]));
+            }
+          }
+        }
+        umma_commit(smem_u32(&ms->drain));
+        volatile int no_abort = 0;
+        mbar_wait(smem_u32(&ms->drain), 0, &no_abort, a.err, kDrainCycles);
+      }
     }
   } else if (warp < 4 + 4 * C::kDq) {
     set_regs_dec<C::kRegDq>();
@@ -981,9 +980,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         // One warp of the warpgroup polls; the others wait in the named barrier, which
         // takes no issue slots.
         if (quad == 0) {
-          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a.err, a.wait_cycles);
+          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
           if (u >= 2)  // P of tile u - 2 has been read
-            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a.err, a.wait_cycles) && ok;
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a) && ok;
         }
         ok = named_sync_and(bar, 128, ok);
         if (rare(!ok)) break;
@@ -1037,8 +1036,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           // ---- move references: the columns' maxima over the tile ------------------
           // every P.V product so far must have landed in O before O is rescaled
           if (t > t_first)
-            ok = wait_phase(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a.err,
-                           a.wait_cycles) && ok;
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a) && ok;
           __syncwarp();
           tc_fence_after();
           ms->red[wg][quad][col] = transpose_reduce<false>(x, lane);
@@ -1097,7 +1095,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
       // ---- epilogue of the segment (a warpgroup that gave up joins the vote) ----------
       const int last = u - 1;
-      ok = ok && wait_phase(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a.err, a.wait_cycles);
+      ok = ok && wait_phase(smem_u32(&ms->pv_done[last & 1]), (last >> 1) & 1, abort_flag, a);
       __syncwarp();
       ms->red[wg][quad][col] = transpose_reduce<true>(l, lane);
       ok = named_sync_and(bar_all, 128 * C::kSw, ok);
@@ -1196,6 +1194,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
   __syncwarp();
   __syncthreads();  // every role is done, every copy and MMA complete
   tc_fence_after();
+  if (tid == 0 && ms->abort_flag) set_err(a.err, D2F_ERR_TIMEOUT);
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 

@@ -112,6 +112,16 @@ int force_deep() {
   return e[0] == '1' ? 1 : 0;
 }
 
+// Budget of a tensor-core kernel's waits on another role's work. D2F_WAIT_CYCLES shortens it
+// (a test switch for the give-up path; copies and MMAs are still drained in full).
+long long wait_budget() {
+  if (const char *e = getenv("D2F_WAIT_CYCLES")) {
+    const long long v = atoll(e);
+    if (v > 0 && v < kWaitCycles) return v;
+  }
+  return kWaitCycles;
+}
+
 int plan_attn(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, int D, int B,
               int dtype, int num_splits, AttnPlan *p, bool allow_tc = true) {
   if (batch < 0 || total_q < 0 || max_q < 0 || max_ctx < 0)
@@ -452,13 +462,7 @@ int attn_entry(const void *q, const void *k_win, const void *v_win, const void *
   a.tc_stages = p.stages;
   a.tc_mt = p.mt > 0 ? p.mt : 1;
   a.longest_first = p.longest_first ? 1 : 0;
-  // D2F_WAIT_CYCLES shortens the budget of the waits on another role's work (a
-  // test switch for the give-up path; copies and MMAs are still drained in full)
-  a.wait_cycles = kWaitCycles;
-  if (const char *e = getenv("D2F_WAIT_CYCLES")) {
-    const long long v = atoll(e);
-    if (v > 0 && v < kWaitCycles) a.wait_cycles = v;
-  }
+  a.wait_cycles = wait_budget();
   a.cache_ready = (flags & D2F_ATTN_CACHE_READY) ? 1 : 0;
   // the stream-K form computes the whole attention only: no fused append, no part
   a.sk = (p.sk > 0 && part == D2F_ATTN_ALL && n_append == 0 && !prev_out) ? p.sk : 0;
@@ -830,6 +834,8 @@ int kv4_plan(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, in
                           max(1, cdiv(max_ctx, 128) + cdiv(max_q, 128));
   const int sms = max(1, num_sms_current_device());
   p->splits = (int)min((long long)sms, max(1LL, units));
+  if ((long long)batch * Hkv * p->m_tiles > 0x7fffffffLL)
+    return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_kv * %d row tiles is too large", p->m_tiles);
   p->n_counters = max(batch, 1) * Hkv * p->m_tiles;
   p->off_ml = 0;
   p->off_o = align_up((size_t)p->n_counters * sizeof(int32_t));
@@ -983,7 +989,8 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
   a.num_splits = p.splits;
   a.tiles_per_split = p.tiles_per_split;
   a.m_tiles = p.m_tiles;
-  a.wait_cycles = kWaitCycles;
+  a.wait_cycles = wait_budget();
+  a.wait_polls = (int)min(64LL, a.wait_cycles);
   a.counters = reinterpret_cast<int32_t *>(workspace);
   a.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.off_ml);
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);

@@ -95,10 +95,12 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     if (bad) bad_s = 1;
     longlong2 total;
     longlong2 at = block_scan(sum, warp_sum, total);
-    if (bad_s || total.x > a.capacity) {  // an inconsistent state: nothing is written
+    if (bad_s || total.x > a.capacity) {
+      // an inconsistent state: nothing is written, but for a list length that stops the
+      // fill, and an append that reads it
       if (tid == 0) {
         set_err(a.err, D2F_ERR_INVALID_ARG);
-        if (PHASE == kPlan) *a.n_append = -1;
+        *a.n_append = -1;
       }
       return;
     }

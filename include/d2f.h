@@ -54,7 +54,12 @@
  * - window step: one CTA holds the whole window state in shared memory
  *   (block_size <= 128; about 5 bytes per window row of capacity plus per-
  *   sequence state against 227 KB: some 45,000 rows for a small batch);
- * - the no-allocation commit: the scratch bound stated at d2f_commit_noalloc.
+ * - the no-allocation commit: the scratch bound stated at d2f_commit_noalloc;
+ * - the 4-bit cache: head_dim 64 or 128, block_size 8, 16 or 32; its bf16 attention:
+ *   batch <= 1024 and, per sequence, num_heads_kv * row tiles * (key tiles + 16) below
+ *   2^31 (row tiles of up to 64 of the group * max_q_per_seq query rows, key tiles of
+ *   128 of the max_pages_per_seq * block_size cached tokens and of the window);
+ * - page map: batch <= 16384; log probabilities: n <= 65535, vocab <= 2^30, top_k <= 32.
  * The workloads this library is measured on (up to 512 window rows, batch 16,
  * 32 KV heads, 32,768 cached tokens) are far inside all of them.
  */
@@ -641,11 +646,12 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
  *   app_rows            device int32 [max_append]: first packed row, page and rows
  *                       of each new block (d2f_kv4_append's list); -1, -1, 0 past
  *                       the list
- *   n_append            device int32 [1]: entries of the list
+ *   n_append            device int32 [1]: entries of the list; -1 when nothing was
+ *                       laid out (d2f_kv4_append then does nothing)
  *   capacity            rows of slot_map; the packed rows must not exceed it
  *
  * Errors in err_word: D2F_ERR_NO_PAGE when a request was refused (the others are
- * laid out); D2F_ERR_INVALID_ARG when nothing was written: a negative num_new,
+ * laid out); D2F_ERR_INVALID_ARG when nothing but n_append was written: a negative num_new,
  * ctx_len or *free_count, a ctx_len that is no multiple of block_size, more packed
  * rows than capacity. Page ids of the free list are taken as they are.
  * D2F_ERR_UNSUPPORTED for batch > 16384.

@@ -80,6 +80,14 @@ def test_attention_refuses_other_dtypes(lib):
     assert attention(lib, dt=2) == 1
 
 
+@pytest.mark.parametrize("kw", [
+    dict(batch=1025, total=1025 * 16),                        # sequences on tensor cores
+    dict(total=2 ** 24, max_q=2 ** 24, h=256, hq=256),        # rows of one sequence x its keys
+    dict(maxp=2 ** 26, total=2 ** 16, max_q=2 ** 16, h=4, hq=4)])
+def test_attention_size_limits_of_the_tensor_core_path(lib, kw):
+    assert attention(lib, dt=0, **kw) == 2 and msg(lib)
+
+
 def page_map(lib, batch=2, b=16, maxp=4, cap=32, app=2, null=()):
     ptr = [None if i in null else P for i in range(14)]
     return lib.d2f_page_map(batch, b, maxp, cap, app, *ptr, None, None)
