@@ -35,8 +35,8 @@
 //   0        producer: page ids -> one bulk copy per page (K and V of a head are one
 //            contiguous piece) into a ring of five tiles
 //   1, 2     MMA issuers of S^T and of O^T (one elected lane each); 3 is spare
-//   4 - 11   a warpgroup dequantises K (thread = key), one V^T (thread = dim)
-//   12 - 27  four softmax warpgroups of 16 columns each, thread = key. A column's
+//   4 - 15   a warpgroup dequantises K (thread = key), two V^T (thread = dim, 64 keys each)
+//   16 - 31  four softmax warpgroups of 16 columns each, thread = key. A column's
 //            reference is 0, or moves when its scores lie outside [2^-2, 2^15] of it: a
 //            tile takes no maximum over the lanes, only a vote on whether some column
 //            has to move. With 16 columns a thread needs 88 registers, which lets 16
@@ -75,13 +75,13 @@ constexpr int NT = 64;                     // rows (columns of S^T and O^T) per 
 
 template <int D>
 struct Cfg {
-  static constexpr int kDq = 2;                       // dequantising warpgroups: K, V^T
+  static constexpr int kDq = 3;                       // dequantising warpgroups: K, two of V^T
   static constexpr int kSw = NT / 16;                 // softmax warpgroups, 16 columns each
   static constexpr int kThreads = 128 * (1 + kDq + kSw);
   // named barriers: 1 .. kSw a softmax warpgroup each, then all of them, then K, V^T
   static constexpr int kBarSoft = 1, kBarAll = kBarSoft + kSw, kBarK = kBarAll + 1;
-  static constexpr int kRegLaunch = 72;               // registers per thread at launch
-  static constexpr int kRegCtl = 40, kRegDq = 56, kRegSoft = 88;
+  static constexpr int kRegLaunch = 64;               // registers per thread at launch
+  static constexpr int kRegCtl = 40, kRegDq = 56, kRegSoft = 72;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");
   static constexpr int kBuf = 2;                      // K and V^T operand buffers in TMEM
@@ -139,8 +139,8 @@ struct Misc {
   // Per dim: first window block whose V is not finite, the value, and the first block at
   // which the sum of such values is NaN. By segment mod 4: V^T tiles run up to two
   // segments ahead of the epilogue that reads them.
-  int nf_blk[4][128], nf_nan[4][128];
-  float nf_val[4][128];
+  int nf_blk[2][4][128], nf_nan[2][4][128];
+  float nf_val[2][4][128];
   // per sequence, [batch] (each array runs on behind the struct): units before it, then
   // its first window row, window rows and cached tokens
   alignas(16) long long pre[2];
@@ -497,6 +497,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
   const int row = quad * 32 + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
   const bool do_k = warp < 8;
+  const int vhalf = (warp >> 2) - 2;  // V^T warpgroup: its 64 keys of a tile
   int u = 0, cu = 0, sg = 0;
   bool ok = true;
 #pragma unroll 1
@@ -533,7 +534,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
         if (reuse)
           ok = wait_phase(smem_u32(do_k ? &ms->s_full[kb] : &ms->pv_done[kb]), free_ph, abort_flag, a) && ok;
       }
-      ok = named_sync_and(do_k ? C::kBarK : C::kBarK + 1, 128, ok);
+      ok = named_sync_and(C::kBarK + (warp >> 2) - 1, 128, ok);
       if (rare(!ok)) break;
       tc_fence_after();
       const bool ragged = !win && ms->ragged[st];
@@ -582,9 +583,9 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       if (!do_k) {
         if (D == 128 || row < 64) {  // (lanes past the head dim: their output is never read)
           const uint32_t va = lane_base + C::kTmV + kb * (kKeys / 2);
-          if (!win) {
+          if (!rare(win)) {
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 2 * vhalf; h < 2 * vhalf + 2; ++h) {
               uint32_t x[16];
               dq_v<D, B>(stage, ms->pvalid[st], ragged, row, h, x);
               __syncwarp();
@@ -593,7 +594,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
           } else {
             const int64_t step = (int64_t)a.num_heads_kv * D;
 #pragma unroll 1
-            for (int w0 = 0; w0 < kKeys; w0 += 16) {  // 16 keys at a time
+            for (int w0 = 64 * vhalf; w0 < 64 * vhalf + 64; w0 += 16) {  // 16 keys at a time
               const int k0 = (t - Tc) * kKeys + w0;
               const int left = s.n - k0;  // window rows from here on
               const uint16_t *src = static_cast<const uint16_t *>(a.v_win) +
@@ -637,9 +638,9 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
           tmem_wait_st();
         }
         if (t == t_end - 1) {  // read by the epilogue, which follows this tile's product
-          ms->nf_blk[sg & 3][row] = nf_blk;
-          ms->nf_nan[sg & 3][row] = nf_nan;
-          ms->nf_val[sg & 3][row] = nf_val;
+          ms->nf_blk[vhalf][sg & 3][row] = nf_blk;
+          ms->nf_nan[vhalf][sg & 3][row] = nf_nan;
+          ms->nf_val[vhalf][sg & 3][row] = nf_val;
         }
         tc_fence_before();
         warp_arrive(smem_u32(&ms->v_full[kb]), lane);
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->k_full[i]), 4);
-      mbar_init(smem_u32(&ms->v_full[i]), 4);
+      mbar_init(smem_u32(&ms->v_full[i]), 8);
       mbar_init(smem_u32(&ms->s_full[i]), 1);
       mbar_init(smem_u32(&ms->s_free[i]), 4 * C::kSw);
       mbar_init(smem_u32(&ms->p_full[i]), 4 * C::kSw);
@@ -1109,7 +1110,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       const Seg s = ms->seg;
       const int live = min(16, s.nrows - col0);  // columns with a row (none or fewer: idle)
       const bool dim_on = D == 128 || row < D, whole = s.len == s.T;
-      const bool odd = s.t0 + s.len > s.Tc && ms->nf_blk[sg & 3][row] != 0x7fffffff;
+      const bool odd = s.t0 + s.len > s.Tc && min(ms->nf_blk[0][sg & 3][row], ms->nf_blk[1][sg & 3][row]) != 0x7fffffff;
       uint16_t *outp = static_cast<uint16_t *>(a.out) + row;
       constexpr int kSlotFloats = NT * D + 2 * NT;
       float *slot = a.ws_o + ((int64_t)2 * blockIdx.x + ms->slot) * kSlotFloats;
@@ -1117,12 +1118,15 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       tmem_ld16f(o_addr, o);
       tc_fence_before();
       if (rare(odd)) {  // infinite or NaN window values of this dim, for the rows that see them
-        const int nb = ms->nf_blk[sg & 3][row], nn = ms->nf_nan[sg & 3][row];
-        const float nv = ms->nf_val[sg & 3][row];
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int nb = ms->nf_blk[h][sg & 3][row], nn = ms->nf_nan[h][sg & 3][row];
+          const float nv = ms->nf_val[h][sg & 3][row];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int bj = ms->blk[col0 + j];
-          if (bj >= nb) o[j] += bj >= nn ? NAN : nv;
+          for (int j = 0; j < 16; ++j) {
+            const int bj = ms->blk[col0 + j];
+            if (nb != 0x7fffffff && bj >= nb) o[j] += bj >= nn ? NAN : nv;
+          }
         }
       }
       if (whole) {
