@@ -34,7 +34,7 @@
 // Roles of a CTA's warps:
 //   0        producer: page ids -> one bulk copy per page (K and V of a head are one
 //            contiguous piece) into a ring of five tiles
-//   1, 2     MMA issuers of S^T and of O^T (one elected lane each); 3 is spare
+//   1        MMA issuer (one elected lane); 2 and 3 are spare
 //   4 - 15   a warpgroup dequantises K (thread = key), two V^T (thread = dim, 64 keys each)
 //   16 - 31  four softmax warpgroups of 16 columns each, thread = key. A column's
 //            reference is 0, or moves when its scores lie outside [2^-2, 2^15] of it: a
@@ -117,9 +117,9 @@ struct Misc {
   using C = Cfg<D>;
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t k_full[2], v_full[2];
-  // (s_full: S^T is there, and its K operand buffer free; pv_done: O^T is up to date, P
-  // and the V^T operand buffer free)
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
+  // (s_full: S^T is there, its K operand buffer free, and P of two tiles before; p_full:
+  // P is there, and S^T read; pv_done: O^T is up to date, the V^T operand buffer free)
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_base;
   int abort_flag;
   int last, slot, c0, c1, second; // composition: the last to arrive; the row tile's shares
@@ -677,12 +677,11 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       mbar_init(smem_u32(&ms->k_full[i]), 4);
       mbar_init(smem_u32(&ms->v_full[i]), 8);
       mbar_init(smem_u32(&ms->s_full[i]), 1);
-      mbar_init(smem_u32(&ms->s_free[i]), 4 * C::kSw);
       mbar_init(smem_u32(&ms->p_full[i]), 4 * C::kSw);
       mbar_init(smem_u32(&ms->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&ms->q_full), 4 * C::kSw);
-    mbar_init(smem_u32(&ms->drain), 2);
+    mbar_init(smem_u32(&ms->drain), 1);
     ms->abort_flag = 0;
     mbar_fence_init();
   }
@@ -822,8 +821,12 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           mbar_wait(smem_u32(&ms->full[i % C::kStages]), (i / C::kStages) & 1, &no_abort, a.err, kDrainCycles);
         }
       }
-    } else if (warp == 1 || warp == 2) {
-      // ============================ MMA issuers ======================================
+    } else if (warp == 1) {
+      // ============================ MMA issuer =======================================
+      // S^T of tile u, then O^T += of tile u - 1. One thread issues both, so S^T of tile u
+      // follows the O^T product of tile u - 2: it may overwrite that tile's S^T (whose
+      // readers have handed over P), and its commit tells the softmax warps that the
+      // P buffer is free too.
       if (elect_one()) {
         bool ok = true;
         int u = 0, sg = 0;
@@ -834,39 +837,42 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           const Seg s = segment(a, pre, ms->k0, w, ms->we);
           w += s.units;
           if (s.len == 0) continue;
-          const int ncols = (s.nrows + 15) & ~15;
-          if (warp == 1) ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a);
+          const int ncols = (s.nrows + 15) & ~15, t_end = s.t0 + s.len;
+          ok = wait_phase(smem_u32(&ms->q_full), sg & 1, abort_flag, a);
           ++sg;
 #pragma unroll 1
-          for (int t = s.t0; t < s.t0 + s.len && ok; ++t, ++u) {
-            const int bf = t >= s.Tc;  // window tiles are bf16
-            const int kb = u % C::kBuf, kph = (u / C::kBuf) & 1;
-            if (warp == 1) {
-              ok = wait_phase(smem_u32(&ms->k_full[kb]), kph, abort_flag, a) &&
-                   (u < 2 || wait_phase(smem_u32(&ms->s_free[u & 1]), ((u >> 1) - 1) & 1, abort_flag, a));
+          for (int t = s.t0; ok; ++t) {
+            if (t < t_end) {
+              const int bf = t >= s.Tc;  // window tiles are bf16
+              ok = wait_phase(smem_u32(&ms->k_full[u & 1]), (u >> 1) & 1, abort_flag, a);
               if (rare(!ok)) break;
               tc_fence_after();
               const uint32_t id = idesc(bf, ncols, 0);
               const uint64_t qd = smem_desc_advance(q_desc, bf ? C::kQbf - C::kQ16 : 0);
-              const uint32_t sd = tmem + C::kTmS + (u & 1) * NT, ka = tmem + C::kTmK + kb * (D / 2);
+              const uint32_t sd = tmem + C::kTmS + (u & 1) * NT;
+              const uint32_t ka = tmem + C::kTmK + (u & 1) * (D / 2);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
                 umma_bf16_tmem_a(sd, ka + k * 8,
                                  smem_desc_advance(qd, (k >> 2) * (NT * 128) + (k & 3) * 32), id, k > 0);
               umma_commit(smem_u32(&ms->s_full[u & 1]));
-            } else {
-              ok = wait_phase(smem_u32(&ms->v_full[kb]), kph, abort_flag, a) &&
-                   wait_phase(smem_u32(&ms->p_full[u & 1]), (u >> 1) & 1, abort_flag, a);
+              ++u;
+            }
+            if (t > s.t0) {
+              const int v = t < t_end ? u - 2 : u - 1;  // the tile before
+              ok = wait_phase(smem_u32(&ms->v_full[v & 1]), (v >> 1) & 1, abort_flag, a) &&
+                   wait_phase(smem_u32(&ms->p_full[v & 1]), (v >> 1) & 1, abort_flag, a);
               if (rare(!ok)) break;
               tc_fence_after();
-              const uint32_t id = idesc(bf, ncols, 1);
-              const uint64_t pd = smem_desc_advance(p_desc, (u & 1) * C::kPBytes);
-              const uint32_t va = tmem + C::kTmV + kb * (kKeys / 2);
+              const uint32_t id = idesc(t > s.Tc, ncols, 1);
+              const uint64_t pd = smem_desc_advance(p_desc, (v & 1) * C::kPBytes);
+              const uint32_t va = tmem + C::kTmV + (v & 1) * (kKeys / 2);
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
                 umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
-                                 id, t > s.t0 || k > 0);
-              umma_commit(smem_u32(&ms->pv_done[u & 1]));
+                                 id, t > s.t0 + 1 || k > 0);
+              umma_commit(smem_u32(&ms->pv_done[v & 1]));
+              if (t == t_end) break;
             }
           }
         }
@@ -980,17 +986,11 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const int sbuf = u & 1;
         // One warp of the warpgroup polls; the others wait in the named barrier, which
         // takes no issue slots.
-        if (quad == 0) {
-          ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
-          if (u >= 2)  // P of tile u - 2 has been read
-            ok = wait_phase(smem_u32(&ms->pv_done[sbuf]), ((u >> 1) - 1) & 1, abort_flag, a) && ok;
-        }
+        if (quad == 0) ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
         ok = named_sync_and(bar, 128, ok);
         if (rare(!ok)) break;
         tc_fence_after();
         if (idle) {
-          tc_fence_before();
-          warp_arrive(smem_u32(&ms->s_free[sbuf]), lane);
           warp_arrive(smem_u32(&ms->p_full[sbuf]), lane);
           continue;
         }
@@ -1071,8 +1071,6 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
           }
           named_sync(bar, 128);  // nm is written, and red may be written again
         }
-        tc_fence_before();
-        warp_arrive(smem_u32(&ms->s_free[sbuf]), lane);
         // ---- P = 2^x; the row sums take the unrounded values ------------------------
         const uint32_t pb = sb + C::kP + sbuf * C::kPBytes + row * 128;
         float p[16];
@@ -1091,6 +1089,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         sts128(pb + (((2 * wg) ^ (row & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
         sts128(pb + (((2 * wg + 1) ^ (row & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
         fence_proxy_async_smem();
+        tc_fence_before();
         warp_arrive(smem_u32(&ms->p_full[sbuf]), lane);
       }
 
