@@ -17,30 +17,34 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kOneCtaRows = 16384;  // slots + 4 per list entry
 
-// Exclusive running sum over the CTA's threads of (x, y), and the totals.
-__device__ longlong2 block_scan(longlong2 v, longlong2 *warp_sum, longlong2 &total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  longlong2 inc = v;
+__device__ __forceinline__ longlong2 warp_scan(longlong2 v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc.x, o);
-    const long long y = __shfl_up_sync(0xffffffffu, inc.y, o);
+    const long long x = __shfl_up_sync(0xffffffffu, v.x, o);
+    const long long y = __shfl_up_sync(0xffffffffu, v.y, o);
     if (lane >= o) {
-      inc.x += x;
-      inc.y += y;
+      v.x += x;
+      v.y += y;
     }
   }
+  return v;
+}
+
+// Exclusive running sum over the CTA's threads of (x, y), and the totals.
+__device__ longlong2 block_scan(longlong2 v, longlong2 *warp_sum, longlong2 &total) {
+  static_assert(kWarps == 32, "one lane per warp");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const longlong2 inc = warp_scan(v, lane);
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  longlong2 base = make_longlong2(0, 0);
-  total = base;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) base = total;
-    total.x += warp_sum[w].x;
-    total.y += warp_sum[w].y;
-  }
+  const longlong2 all = warp_scan(warp_sum[lane], lane);
+  const int before = warp > 0 ? warp - 1 : 0;
+  const long long bx = __shfl_sync(0xffffffffu, all.x, before);
+  const long long by = __shfl_sync(0xffffffffu, all.y, before);
+  total.x = __shfl_sync(0xffffffffu, all.x, 31);
+  total.y = __shfl_sync(0xffffffffu, all.y, 31);
   __syncthreads();
-  return make_longlong2(base.x + inc.x - v.x, base.y + inc.y - v.y);
+  return make_longlong2((warp > 0 ? bx : 0) + inc.x - v.x, (warp > 0 ? by : 0) + inc.y - v.y);
 }
 
 // Largest i of [0, n) with start[i] <= x (start ascending, start[0] <= x).
@@ -178,25 +182,30 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     const int r0 = (int)(4 * q), r1 = min(r0 + 4, a.capacity);
     int64_t slot[4];
     int b = r0 < n_rows ? find(row0, batch, r0) : 0;
-    int next = 0, have = -1;
-    int64_t base = 0;  // page * B of page number `have`
-    if (r0 < n_rows) next = b + 1 < batch ? row0[b + 1] : n_rows;
+    int next = 0, o = 0;      // end of the request's rows; offset in the page
+    const int *page = nullptr;  // the request's page of this row on the list
+    int64_t base = -1;        // page * B, -1: a refused request
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = r0 + j;
       slot[j] = -1;
       if (r >= n_rows) continue;
-      while (r >= next) {
-        ++b;
-        next = b + 1 < batch ? row0[b + 1] : n_rows;
+      const bool turn = r >= next;  // another request (the first row's is known)
+      if (turn) {
+        if (j == 0) next = b + 1 < batch ? row0[b + 1] : n_rows;
+        while (r >= next) {
+          ++b;
+          next = b + 1 < batch ? row0[b + 1] : n_rows;
+        }
+        const int t = r - row0[b];
+        page = a.free_pages + (free0 - 1 - page0[b] - t / B);
+        o = t % B;
+      } else if (++o == B) {
+        o = 0;
+        --page;
       }
-      if (ctxp[b] < 0) continue;
-      const int t = r - row0[b], p = page0[b] + t / B;
-      if (p != have) {
-        base = (int64_t)a.free_pages[free0 - 1 - p] * B;
-        have = p;
-      }
-      slot[j] = base + t % B;
+      if (turn || o == 0) base = ctxp[b] < 0 ? -1 : (int64_t)*page * B;
+      if (base >= 0) slot[j] = base + o;
     }
     if (r1 - r0 == 4 && (reinterpret_cast<uintptr_t>(a.slot) & 15) == 0) {
       reinterpret_cast<longlong2 *>(a.slot + r0)[0] = make_longlong2(slot[0], slot[1]);
