@@ -39,18 +39,23 @@
 //   16 - 31  four softmax warpgroups of 16 columns each, thread = key. A column's
 //            reference is 0, or moves when its scores lie outside [2^-2, 2^15] of it: a
 //            tile takes no maximum over the lanes, only a vote on whether some column
-//            has to move. With 16 columns a thread needs 88 registers, which lets 16
-//            warps run side by side (32 columns a thread: 8 warps, and spills).
+//            has to move. With 16 columns a thread stays within 72 registers, which lets
+//            16 warps run side by side (32 columns a thread: 8 warps, and spills).
 //
-// Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 49,152 to
-// 65,536 cached tokens and 64 window rows 291 us, 2.1 TB/s of 4-bit cache, against 329 us
-// of the bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes. Time
-// is 28 us + 1.2 us (about 2300 cycles) per key tile of a CTA. The bound is the chain of
-// a tile through the softmax warps (S^T ready, tensor memory -> registers, vote, 2^x,
-// P stored and handed on: 2000 to 2400 cycles against 512 of MMA), with the issue slots
-// at 68 % and the ALU pipe, which converts the codes, at 52 %; DRAM is at a third of its
-// rate, and neither a deeper ring, V^T on two warpgroups, fewer barriers nor polls that
-// sleep change the time by more than 2 %.
+// Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 32,768
+// cached tokens and 64 window rows 259 us, 2.4 TB/s of 4-bit cache, against 329 us of the
+// bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes; 16 sequences
+// of 251 to 4096 tokens 111 us; one of 1024 tokens 19 us. Time is 28 us + 1.05 us (about
+// 2000 cycles) per key tile of a CTA. The 28 us are code that runs once a segment, fetched
+// from L2 or DRAM. A tile is bound by the hand-overs between its roles, each of which
+// takes 300 to 1000 cycles: with all conversions and exponentials taken out it still needs
+// 225 us on the first shape (without K's conversion 244, V's 248, the exponentials 253).
+// The tensor pipe is active 23 % of the cycles, the ALU, which converts the codes, 49 %,
+// the issue slots 67 %, DRAM 30 %. What shortened the chain: one issuer whose order
+// stands for two waits (272 -> 259), V^T on two warpgroups (285 -> 272), small code (the
+// hot loops of all roles share the instruction cache: V^T's loop unrolled by two costs
+// 10 %). What did not: a deeper ring, a third K buffer, a K chunk in a V^T warpgroup, polls
+// that sleep, polls by every warp.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -68,7 +73,7 @@ constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K ex
 constexpr float kHigh = 15.0f, kLow = -2.0f;
 constexpr int kMaxBatch = kKv4MaxBatch;
 // What a row tile costs beside its key tiles (its queries, the pipeline's start, its
-// output: about 7 us, against 1.2 us a key tile), in key tiles.
+// output: about 7 us, against 1.05 us a key tile), in key tiles.
 constexpr int kSegmentTiles = 6;
 
 constexpr int NT = 64;                     // rows (columns of S^T and O^T) per row tile
@@ -81,6 +86,7 @@ struct Cfg {
   // named barriers: 1 .. kSw a softmax warpgroup each, then all of them, then K, V^T
   static constexpr int kBarSoft = 1, kBarAll = kBarSoft + kSw, kBarK = kBarAll + 1;
   static constexpr int kRegLaunch = 64;               // registers per thread at launch
+  // (80 for the softmax warps and 48 for the others: no spills here, but 2 to 8 % slower)
   static constexpr int kRegCtl = 40, kRegDq = 56, kRegSoft = 72;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");
