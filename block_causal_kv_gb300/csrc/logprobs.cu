@@ -4,8 +4,11 @@
 // Source: "확산 언어 모델(Diffusion LLM)이란 무엇인가", §토큰 순서의 이론 (largest
 // probabilities and entropy of a position's prediction).
 //
-// With m = max l, S = sum exp(l - m), E = sum exp(l - m)(l - m):
-//   log p_t = l_t - m - ln S,  H = ln S - E / S.
+// With m = max l, s = sum exp(l - m) over all logits but one that is m, and
+// E = sum exp(l - m)(l - m):
+//   log p_t = l_t - m - ln(1 + s),  H = ln(1 + s) - E / (1 + s).
+// The 1 stays out of the sum: where one token has nearly all the probability, its log
+// probability is -s, which 1 + s would keep only to 2^-24 of 1.
 // Grid (slices, rows) as in the commit kernel: CTA (s, r) reduces vocabulary slice s
 // of row r; the CTA that arrives last at a row's counter composes the slices.
 // Measured: 384 rows of 152,064 bf16 logits, half of them with a token, 20 alternatives:
@@ -77,19 +80,19 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane
 
 // ---- softmax terms -----------------------------------------------------------
 struct Terms {
-  float m, s, e;  // maximum, sum of exp(l - m), sum of exp(l - m)(l - m)
+  // maximum; sum of exp(l - m) but for one that is m (none yet: m = -inf); sum of
+  // exp(l - m)(l - m)
+  float m, s, e;
 };
 
-__device__ __forceinline__ Terms combine(const Terms &a, const Terms &b) {
+__device__ __forceinline__ Terms combine(const Terms &x, const Terms &y) {
+  const bool first = x.m >= y.m;
+  const Terms a = first ? x : y, b = first ? y : x;  // b's maximum becomes a logit like others
+  const float bs = b.s + (b.m > -INFINITY ? 1.f : 0.f);
+  const float d = b.m == a.m ? 0.f : fmaxf(b.m - a.m, -1e30f);
+  const float w = fast_exp2(d * kLog2e);
   // a part without any finite term has s = 0 and e = 0; NaN sums stay NaN
-  Terms r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = a.m == r.m ? 0.f : fmaxf(a.m - r.m, -1e30f);
-  const float db = b.m == r.m ? 0.f : fmaxf(b.m - r.m, -1e30f);
-  const float wa = fast_exp2(da * kLog2e), wb = fast_exp2(db * kLog2e);
-  r.s = a.s * wa + b.s * wb;
-  r.e = wa * fmaf(da, a.s, a.e) + wb * fmaf(db, b.s, b.e);
-  return r;
+  return Terms{a.m, fmaf(bs, w, a.s), fmaf(w, fmaf(d, bs, b.e), a.e)};
 }
 
 __device__ __forceinline__ Terms warp_combine(Terms v) {
@@ -196,29 +199,42 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
     float vm = x[0];
 #pragma unroll
     for (int j = 1; j < VEC; ++j) vm = fmaxf(vm, x[j]);
+    float y[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) y[j] = x[j];
     if (vm > m) {
+      // the old maximum joins the sums, the new one stays out of them
       const float d = fmaxf(m - vm, -1e30f);
       const float w = fast_exp2(d * kLog2e);
-      float s = 0.f;
+      float s = m > -INFINITY ? 1.f : 0.f;
+      const float old = s * w;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += acc[j];
       e = w * fmaf(d, s, e);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[j] *= w;
+      acc[0] += old;
       m = vm;
-      if (TOP) {
-        int first = 0;
+      bool out = vm == INFINITY;  // (infinity - infinity has to stay: the row is NaN)
 #pragma unroll
-        for (int j = VEC - 1; j > 0; --j)
-          if (x[j] == vm) first = j;
-        idx = v + (x[0] == vm ? 0 : first);
+      for (int j = 0; j < VEC; ++j) {
+        if (!out && x[j] == vm) {
+          y[j] = -INFINITY;
+          out = true;
+          if (TOP) idx = v + j;
+        }
+      }
+      if (TOP && vm == INFINITY) {
+#pragma unroll
+        for (int j = VEC - 1; j >= 0; --j)
+          if (x[j] == vm) idx = v + j;
       }
     }
     // a logit of -inf adds nothing (also while no finite one has come: m = -inf)
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float raw = x[j] - ref;
+      const float raw = y[j] - ref;
       const float d = raw < -1e30f ? -1e30f : raw;  // keeps NaN
       const float t = fast_exp2(d * kLog2e);
       acc[j] += t;
@@ -284,9 +300,21 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
     return key;
   };
   if constexpr (TOP) {
-    // a thread whose logits are all -inf offers the first of them
-    const bool any = v0 + tid * VEC < v0 + n_full || tail_on;
-    if (m == -INFINITY) idx = v0 + tid * VEC < v0 + n_full ? v0 + tid * VEC : v_tail;
+    // A thread without a logit above -inf offers the first of its -inf ones; one whose
+    // logits are all NaN has nothing to offer (its key would count as one of the k).
+    bool any = m > -INFINITY;
+    if (!any) {
+      for (int v = v0 + tid * VEC; v < v0 + n_full && !any; v += STEP)
+        for (int j = 0; j < VEC && !any; ++j) {
+          const float x = load_scalar<DT>(row, v + j);
+          any = x == x;
+          idx = v + j;
+        }
+      if (!any && tail_on) {
+        any = x_tail == x_tail;
+        idx = v_tail;
+      }
+    }
     const uint64_t mine = any ? make_key(m, idx) : 0;
     uint64_t key = cta_merge(bitonic_sort(mine, lane));
     if (tid == a.top_k - 1) bound_s = key;  // (top_k <= 32: a lane of warp 0)
@@ -368,10 +396,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
     }
   }
   if (warp == 0) {
-    const float ln_s = logf(t.s);
-    if (lane == 0) {
+    const float ln_s = log1pf(t.s);
+    if (lane == 0) {  // (a row without a logit above -inf: -inf + inf)
       a.logprob[r] = load_scalar<DT>(row, tok) - t.m - ln_s;
-      if (a.entropy) a.entropy[r] = ln_s - t.e / t.s;
+      if (a.entropy) a.entropy[r] = t.m == -INFINITY ? NAN : ln_s - t.e / (1.f + t.s);
     }
     if (TOP && lane < a.top_k) {
       const bool have = top.key != 0;

@@ -84,6 +84,34 @@ def test_ties_and_order(V, dtype):
     check(x, tok.tolist(), 32, r)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [9, 1000, 126464])
+def test_nearly_certain_tokens_keep_their_precision(V, dtype):
+    """A token with nearly all the probability: log p = -ln(1 + s) and the entropy are tiny sums
+    of positive terms. Each term is off by 2^-22 of the exponential and by its argument's
+    rounding (|d| <= 60: 60 * 1.45 * 2^-24), the sums by at most V / 256 + 80 steps of 2^-24, the
+    logarithm and quotient by a few: relative to the value, not to 1."""
+    dev = device()
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn((12, V), generator=g)
+    tok = torch.randint(0, V, (12,), generator=g)
+    x[torch.arange(12), tok] = torch.tensor([8.0, 12, 14, 16, 18, 20, 22, 24, 26, 28, 30, 40])
+    x = x.to(dtype)
+    r = d2f.token_logprobs(x.to(dev), tok.to(torch.int32).to(dev), top_k=2)
+    z = x.double() - x.double().max(-1, keepdim=True).values
+    p = z.exp()
+    p[torch.arange(12), tok] = 0
+    s = p.sum(-1)                                   # (without the token's own 1)
+    lp = -torch.log1p(s)
+    ent = torch.log1p(s) - (p * z).sum(-1) / (1 + s)
+    rel = 2.0 ** -18 + (V / 256 + 90) * 2.0 ** -24
+    assert (x.float().argmax(-1) == tok).all()
+    assert ((r["logprob"].cpu().double() - lp).abs() <= rel * lp.abs()).all()
+    assert ((r["entropy"].cpu().double() - ent).abs() <= 2 * rel * ent).all()
+    assert (r["top_id"][:, 0].cpu() == tok).all()
+    assert torch.equal(r["top_logprob"][:, 0], r["logprob"])
+
+
 @pytest.mark.parametrize("V", [50, 30000])
 def test_masked_and_broken_logits(V):
     """-inf almost everywhere; all -inf; NaN; +inf: the row's sums are NaN, the list is not."""
@@ -109,6 +137,33 @@ def test_masked_and_broken_logits(V):
     # a token of probability zero
     r = d2f.token_logprobs(x.to(dev)[:1], torch.tensor([0], dtype=torch.int32, device=dev))
     assert torch.isneginf(r["logprob"]).all()
+
+
+@pytest.mark.parametrize("dtype,V,pad", [(torch.bfloat16, 9000, 0), (torch.bfloat16, 9001, 4),
+                                         (torch.float32, 9003, 0), (torch.float32, 40, 0)])
+def test_alternatives_beside_nan_are_the_lowest_indices(dtype, V, pad):
+    """Rows of NaN and -inf: the -inf logits are alternatives in order of index, whatever
+    shares the vocabulary pass gives a thread; fewer of them than k leave -1."""
+    dev = device()
+    g = torch.Generator().manual_seed(3)
+    x = torch.full((6, V + pad), float("-inf"))
+    x[0, :V][torch.arange(V) % 2048 < 96] = float("nan")  # whole threads without a number
+    x[1, :V - 3] = float("nan")
+    x[2, :V] = torch.where(torch.rand(V, generator=g) < 0.9, float("nan"), float("-inf"))
+    x[3, :V] = float("nan")
+    x[4, 7:V] = float("nan")
+    x[4, 20] = 1.5
+    x[5, :V] = torch.where(torch.rand(V, generator=g) < 0.5, float("nan"), float("-inf"))
+    x[5, V - 1] = -2.0
+    x = x.to(dtype)
+    k = 10
+    r = d2f.token_logprobs(x.to(dev)[:, :V], torch.arange(6, dtype=torch.int32, device=dev), top_k=k)
+    for row in range(6):
+        v = x[row, :V].float().numpy()
+        real = np.nonzero(~np.isnan(v))[0]
+        want = real[np.argsort(-v[real], kind="stable")][:k].tolist()
+        assert r["top_id"][row].tolist() == want + [-1] * (k - len(want))
+    assert torch.isnan(r["logprob"]).all() and torch.isnan(r["entropy"]).all()
 
 
 def test_rows_without_a_token_and_bad_indices():
