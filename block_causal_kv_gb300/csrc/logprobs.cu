@@ -12,9 +12,11 @@
 // Grid (slices, rows) as in the commit kernel: CTA (s, r) reduces vocabulary slice s
 // of row r; the CTA that arrives last at a row's counter composes the slices.
 // Measured: 384 rows of 152,064 bf16 logits, half of them with a token, 20 alternatives:
-// 34 us, 1.8 TB/s (without alternatives 25 us, 2.4 TB/s); 48 rows of 126,464 and 5
-// alternatives 16 us. The bytes alone would take 9 and 2 us; the rest is the chain of a
-// CTA (stream, reduce, second look, compose), at 58 % of the issue slots on the former.
+// 36 us, 1.7 TB/s (22 us without alternatives); 48 rows of 126,464 and 5 alternatives 17 us. The bytes alone would take
+// 9 and 2 us; the rest is the chain of a CTA (stream, reduce, second look, compose), at
+// about 60 % of the issue slots on the former. Keeping the maximum's 1 out of the sum is 3
+// and 1 us of it; four vectors at a time (one by one: 41 and 18 us; with a reference of
+// the whole warp, which moves less often: 35 and 18 us).
 //
 // The k largest logits of a slice come from a second look at few of its elements. In the
 // pass every thread keeps the largest of its own logits and where it was. The k-th
@@ -195,67 +197,65 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
   int idx = 0;  // (TOP) where m is
   TopList top;
 
-  auto fold = [&](const float (&x)[VEC], int v) {
-    float vm = x[0];
+  // NV vectors at once, from v on every STEP: in a warp one of 32 maxima moves for most
+  // vectors of a row, and so moves once for all of them.
+  constexpr int STEP = kThreads * VEC;  // logits of one vector per thread
+  auto fold = [&](auto &x, int v) {
+    constexpr int NV = sizeof(x) / sizeof(x[0]);
+    float vm = x[0][0];
 #pragma unroll
-    for (int j = 1; j < VEC; ++j) vm = fmaxf(vm, x[j]);
-    float y[VEC];
+    for (int u = 0; u < NV; ++u)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) y[j] = x[j];
+      for (int j = 0; j < VEC; ++j) vm = fmaxf(vm, x[u][j]);
     if (vm > m) {
       // the old maximum joins the sums, the new one stays out of them
-      const float d = fmaxf(m - vm, -1e30f);
-      const float w = fast_exp2(d * kLog2e);
+      const float w = fast_exp2(fmaxf(m - vm, -1e30f) * kLog2e);
       float s = m > -INFINITY ? 1.f : 0.f;
       const float old = s * w;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += acc[j];
-      e = w * fmaf(d, s, e);
+      e = w * fmaf(fmaxf(m - vm, -1e30f), s, e);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[j] *= w;
-      acc[0] += old;
+      acc[0] += vm == INFINITY ? NAN : old;  // (infinity: the row's sums are NaN)
       m = vm;
-      bool out = vm == INFINITY;  // (infinity - infinity has to stay: the row is NaN)
+      bool out = false;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (!out && x[j] == vm) {
-          y[j] = -INFINITY;
-          out = true;
-          if (TOP) idx = v + j;
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const bool here = !out && x[u][j] == vm;
+          out = out || here;
+          if (here) x[u][j] = -INFINITY;
+          if (TOP && here) idx = v + u * STEP + j;
         }
-      }
-      if (TOP && vm == INFINITY) {
-#pragma unroll
-        for (int j = VEC - 1; j >= 0; --j)
-          if (x[j] == vm) idx = v + j;
-      }
     }
     // a logit of -inf adds nothing (also while no finite one has come: m = -inf)
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float raw = y[j] - ref;
-      const float d = raw < -1e30f ? -1e30f : raw;  // keeps NaN
-      const float t = fast_exp2(d * kLog2e);
-      acc[j] += t;
-      e = fmaf(t, d, e);
-    }
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float raw = x[u][j] - ref;
+        const float d = raw < -1e30f ? -1e30f : raw;  // keeps NaN
+        const float t = fast_exp2(d * kLog2e);
+        acc[j] += t;
+        e = fmaf(t, d, e);
+      }
   };
 
   // ---- stream the slice --------------------------------------------------------
-  constexpr int STEP = kThreads * VEC;       // logits of one vector per thread
   const int n_full = (v1 - v0) / VEC * VEC;  // whole vectors
   for (int base = v0; base < v0 + n_full; base += STEP * kUnroll) {  // CTA-uniform
     float x[kUnroll][VEC];
-    bool on[kUnroll];
     if constexpr (PATH == 1) {
+      constexpr uint32_t kNone = DT == D2F_BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
       uint4 raw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int v = base + u * STEP + tid * VEC;
-        on[u] = v < v0 + n_full;
         const uint4 *p = reinterpret_cast<const uint4 *>(row + (int64_t)v * elt);
-        raw[u] = on[u] ? (TOP ? __ldg(p) : __ldcs(p)) : make_uint4(0, 0, 0, 0);
+        raw[u] = v < v0 + n_full ? (TOP ? __ldg(p) : __ldcs(p)) : make_uint4(kNone, kNone, kNone, kNone);
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) unpack<DT>(raw[u], x[u]);
@@ -263,13 +263,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int v = base + u * STEP + tid;
-        on[u] = v < v0 + n_full;
-        x[u][0] = on[u] ? load_scalar<DT>(row, v) : 0.f;
+        x[u][0] = v < v0 + n_full ? load_scalar<DT>(row, v) : -INFINITY;
       }
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (on[u]) fold(x[u], base + u * STEP + tid * VEC);
+    fold(x, base + tid * VEC);
   }
   // the slice's last elements, fewer than one vector
   const int v_tail = v0 + n_full + tid;
@@ -277,10 +274,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
   float x_tail = 0.f;
   if (tail_on) {
     x_tail = load_scalar<DT>(row, v_tail);
-    float one[VEC];
-    one[0] = x_tail;
+    float one[1][VEC];
+    one[0][0] = x_tail;
 #pragma unroll
-    for (int j = 1; j < VEC; ++j) one[j] = -INFINITY;
+    for (int j = 1; j < VEC; ++j) one[0][j] = -INFINITY;
     fold(one, v_tail);
   }
 
