@@ -954,6 +954,8 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
     return fail(D2F_ERR_INVALID_ARG, "max_ctx %d exceeds max_pages_per_seq * block_size", max_ctx);
   if (max_pages_per_seq > 0 && (!kv_pool || !page_table))
     return fail(D2F_ERR_INVALID_ARG, "a cached context needs kv_pool and page_table");
+  if ((long long)max_pages_per_seq * block_size > 0x7fffff00LL)  // (token numbers are 32-bit)
+    return fail(D2F_ERR_UNSUPPORTED, "max_pages_per_seq * block_size is too large");
   if (!(softmax_scale > 0.f && softmax_scale < 3e38f))
     return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0 and finite");
   const void *ptrs[] = {q, k_win, v_win, kv_pool, out};

@@ -58,7 +58,8 @@
  * - the 4-bit cache: head_dim 64 or 128, block_size 8, 16 or 32; its bf16 attention:
  *   batch <= 1024 and, per sequence, num_heads_kv * row tiles * (key tiles + 16) below
  *   2^31 (row tiles of up to 64 of the group * max_q_per_seq query rows, key tiles of
- *   128 of the max_pages_per_seq * block_size cached tokens and of the window);
+ *   128 of the max_pages_per_seq * block_size cached tokens, which stay below 2^31, and
+ *   of the window);
  * - page map: batch <= 16384; log probabilities: n <= 65535, vocab <= 2^30, top_k <= 32.
  * The workloads this library is measured on (up to 512 window rows, batch 16,
  * 32 KV heads, 32,768 cached tokens) are far inside all of them.

@@ -80,6 +80,11 @@ def test_attention_refuses_other_dtypes(lib):
     assert attention(lib, dt=2) == 1
 
 
+@pytest.mark.parametrize("dt", [0, 1])
+def test_attention_refuses_page_tables_past_32_bits(lib, dt):
+    assert attention(lib, dt=dt, maxp=2 ** 27) == 2 and "max_pages_per_seq" in msg(lib)
+
+
 @pytest.mark.parametrize("kw", [
     dict(batch=1025, total=1025 * 16),                        # sequences on tensor cores
     dict(total=2 ** 24, max_q=2 ** 24, h=256, hq=256),        # rows of one sequence x its keys
