@@ -534,7 +534,7 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       const uint32_t stage = sb + C::kRing + st * C::kStage;
       // One warp of the warpgroup polls, for the tile's bytes and for the operand buffer;
       // the others wait in the named barrier, which takes no issue slots.
-      if (quad == 0) {
+      if (quad == (do_k ? 2 : vhalf ? 3 : 2)) {
         if (!win)
           ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a);
         if (reuse)
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         const int sbuf = u & 1;
         // One warp of the warpgroup polls; the others wait in the named barrier, which
         // takes no issue slots.
-        if (quad == 0) ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
+        if (quad == (wg & 3)) ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
         ok = named_sync_and(bar, 128, ok);
         if (rare(!ok)) break;
         tc_fence_after();
