@@ -173,43 +173,38 @@ def _dev(t, name, dtype=None):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
-class _On:
-    """Checks that the given tensors are contiguous CUDA tensors of one device and makes
-    it the current one: the stream (that device's current one unless given) and the
-    launch belong to it. Entries are (name, tensor or None, dtype or None)."""
-
-    __slots__ = ("_guard", "_given", "_index")
-
-    def __init__(self, stream, *tensors):
-        dev = None
-        for name, t, dtype in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-                _dev(t, name, dtype)
-            if dev is None:
-                dev = t.get_device()
-            elif t.get_device() != dev:
-                raise ValueError("%s is on cuda:%d, the others on cuda:%d" %
-                                 (name, t.get_device(), dev))
-        self._index = dev
-        self._guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-        self._given = stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        if self._given is None:
-            return torch._C._cuda_getCurrentRawStream(self._index)
-        return self._given.cuda_stream
-
-    def __exit__(self, *exc):
-        return None if self._guard is None else self._guard.__exit__(*exc)
-
-
-def _shape(t, name, shape):
-    if t is not None and t.shape != shape:
+def _refuse(name, t, dtype, shape, dev):
+    """Raise for the tensor that `_device` found wrong, with the reason."""
+    _dev(t, name, dtype)
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s is on cuda:%d, the others on cuda:%d" % (name, t.get_device(), dev))
+
+
+def _device(*tensors):
+    """The device of the given tensors, which must be contiguous CUDA tensors of that device.
+    Entries are (name, tensor or None, dtype, shape or None). (One loop with the cheapest checks: it
+    is a third of what a small call costs.)"""
+    dev = tensors[0][1].get_device()
+    for name, t, dtype, shape in tensors:
+        if t is not None and (t.dtype is not dtype or (shape is not None and t.shape != shape) or
+                              t.get_device() != dev or not t.is_contiguous()):
+            _refuse(name, t, dtype, shape, dev)
+    if dev < 0:
+        _dev(tensors[0][1], tensors[0][0])
+    return dev
+
+
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream) with `dev` current; its current stream unless one is given."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != 0:
+        _check(status)
 
 
 def status_string(status):
@@ -497,7 +492,7 @@ def kv4_pool(device, *, num_pages, num_heads_kv, head_dim, block_size):
 def _kv4_pool_shape(pool, num_heads_kv, head_dim, block_size):
     if pool.dim() != 3:
         raise ValueError("the 4-bit pool is [num_pages, num_heads_kv, page bytes]")
-    _shape(pool, "pool", (pool.shape[0], num_heads_kv, kv4_page_bytes(head_dim, block_size)))
+    return (pool.shape[0], num_heads_kv, kv4_page_bytes(head_dim, block_size))
 
 
 def kv4_append(k_win, v_win, src_row, dst_page, pool, *, block_size, n_rows=None, k_exp=0,
@@ -505,23 +500,19 @@ def kv4_append(k_win, v_win, src_row, dst_page, pool, *, block_size, n_rows=None
     """Quantise blocks (rows src_row[a] .. + n_rows[a] of K/V [rows, Hkv, D]; n_rows None:
     block_size each) into pages dst_page[a] of a 4-bit pool. With n_append_dev (int32 [1]
     on the device) the list's length is read there, at most len(src_row)."""
-    lib = load()
-    total_q, hkv, d = k_win.shape
-    _shape(v_win, "v_win", k_win.shape)
-    _kv4_pool_shape(pool, hkv, d, block_size)
+    shape = k_win.shape
+    total_q, hkv, d = shape
     n = src_row.shape[0]
-    _shape(src_row, "src_row", (n,))
-    _shape(dst_page, "dst_page", (n,))
-    _shape(n_rows, "n_rows", (n,))
-    _shape(n_append_dev, "n_append_dev", (1,))
-    with _On(stream, ("k_win", k_win, k_win.dtype), ("v_win", v_win, k_win.dtype),
-             ("src_row", src_row, torch.int32), ("dst_page", dst_page, torch.int32),
-             ("pool", pool, torch.uint8), ("n_rows", n_rows, torch.int32),
-             ("n_append_dev", n_append_dev, torch.int32), ("err", err, torch.int32)) as s:
-        _check(lib.d2f_kv4_append(
-            _ptr(k_win), _ptr(v_win), _ptr(src_row), _ptr(dst_page), _ptr(n_rows),
-            _ptr(n_append_dev), n, total_q, _ptr(pool), hkv, d, block_size, pool.shape[0],
-            int(k_exp), int(v_exp), _dtype_code(k_win), _ptr(err), s))
+    i32 = torch.int32
+    dev = _device(("k_win", k_win, k_win.dtype, shape), ("v_win", v_win, k_win.dtype, shape),
+                  ("src_row", src_row, i32, (n,)), ("dst_page", dst_page, i32, (n,)),
+                  ("pool", pool, torch.uint8, _kv4_pool_shape(pool, hkv, d, block_size)),
+                  ("n_rows", n_rows, i32, (n,)), ("n_append_dev", n_append_dev, i32, (1,)),
+                  ("err", err, i32, None))
+    _launch(load().d2f_kv4_append, dev, stream, k_win.data_ptr(), v_win.data_ptr(),
+            src_row.data_ptr(), dst_page.data_ptr(), _ptr(n_rows), _ptr(n_append_dev), n, total_q,
+            pool.data_ptr(), hkv, d, block_size, pool.shape[0], int(k_exp), int(v_exp),
+            _dtype_code(k_win), _ptr(err))
 
 
 def kv4_read(pool, slot, *, head_dim, block_size, dtype=torch.bfloat16, k_exp=0, v_exp=0,
@@ -529,23 +520,20 @@ def kv4_read(pool, slot, *, head_dim, block_size, dtype=torch.bfloat16, k_exp=0,
     """Tokens at int64 slots (page * block_size + offset; -1 gives zeros) of a 4-bit pool.
 
     Returns (k, v) [len(slot), Hkv, D] of `dtype`, exact."""
-    lib = load()
-    hkv = pool.shape[1]
-    _kv4_pool_shape(pool, hkv, head_dim, block_size)
+    pool_shape = _kv4_pool_shape(pool, pool.shape[1], head_dim, block_size)
+    hkv = pool_shape[1]
     n = slot.shape[0]
-    _shape(slot, "slot", (n,))
     shape = (n, hkv, head_dim)
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=pool.device)
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=pool.device)
-    _shape(k, "k", shape)
-    _shape(v, "v", shape)
-    with _On(stream, ("pool", pool, torch.uint8), ("slot", slot, torch.int64), ("k", k, dtype),
-             ("v", v, dtype), ("err", err, torch.int32)) as s:
-        _check(lib.d2f_kv4_read(_ptr(pool), _ptr(slot), n, _ptr(k), _ptr(v), hkv, head_dim,
-                                block_size, pool.shape[0], int(k_exp), int(v_exp), _dtype_code(k),
-                                _ptr(err), s))
+    dev = _device(("pool", pool, torch.uint8, pool_shape), ("slot", slot, torch.int64, (n,)),
+                  ("k", k, dtype, shape), ("v", v, dtype, shape),
+                  ("err", err, torch.int32, None))
+    _launch(load().d2f_kv4_read, dev, stream, pool.data_ptr(), slot.data_ptr(), n, k.data_ptr(),
+            v.data_ptr(), hkv, head_dim, block_size, pool_shape[0], int(k_exp), int(v_exp),
+            _dtype_code(k), _ptr(err))
     return k, v
 
 
@@ -572,41 +560,37 @@ def block_attn_kv4(q, k_win, v_win, pool, page_table, ctx_len, q_start, *, block
     block_attn with one 4-bit pool in place of k_pool and v_pool.
 
     Returns (out [total_q, Hq, D] like q, lse [total_q, Hq] float32 or None)."""
-    lib = load()
     total_q, hq, d = q.shape
     hkv = k_win.shape[1]
     batch = ctx_len.shape[0]
-    _shape(k_win, "k_win", (total_q, hkv, d))
-    _shape(v_win, "v_win", (total_q, hkv, d))
-    _kv4_pool_shape(pool, hkv, d, block_size)
-    _shape(ctx_len, "ctx_len", (batch,))
-    _shape(q_start, "q_start", (batch + 1,))
-    _shape(page_table, "page_table", (batch, page_table.shape[-1]))
+    max_pages = page_table.shape[-1]
     dt = _dtype_code(q)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
-    _shape(out, "out", q.shape)
     if lse is None and want_lse:
         lse = torch.empty((total_q, hq), dtype=torch.float32, device=q.device)
-    _shape(lse, "lse", (total_q, hq))
     if workspace is None:
         workspace = attn_kv4_workspace(q.device, batch=batch, total_q=total_q,
                                        max_q_per_seq=max_q_per_seq, max_ctx=max_ctx,
                                        num_heads_q=hq, num_heads_kv=hkv, head_dim=d,
                                        block_size=block_size, dtype=dt)
-    with _On(stream, ("q", q, q.dtype), ("k_win", k_win, q.dtype), ("v_win", v_win, q.dtype),
-             ("pool", pool, torch.uint8), ("page_table", page_table, torch.int32),
-             ("ctx_len", ctx_len, torch.int32), ("q_start", q_start, torch.int32),
-             ("out", out, q.dtype), ("lse", lse, torch.float32), ("workspace", workspace, None),
-             ("err", err, torch.int32)) as s:
-        _check(lib.d2f_block_attn_kv4(
-            _ptr(q), _ptr(k_win), _ptr(v_win), _ptr(pool), _ptr(page_table), page_table.shape[1],
-            _ptr(ctx_len), _ptr(q_start), _ptr(out), _ptr(lse), batch, total_q, max_q_per_seq,
-            max_ctx, hq, hkv, d, block_size, pool.shape[0], int(k_exp), int(v_exp), dt,
-            float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _ptr(err), s))
+    qd, i32 = q.dtype, torch.int32
+    win = (total_q, hkv, d)
+    dev = _device(("q", q, qd, q.shape), ("k_win", k_win, qd, win), ("v_win", v_win, qd, win),
+                  ("pool", pool, torch.uint8, _kv4_pool_shape(pool, hkv, d, block_size)),
+                  ("page_table", page_table, i32, (batch, max_pages)),
+                  ("ctx_len", ctx_len, i32, (batch,)), ("q_start", q_start, i32, (batch + 1,)),
+                  ("out", out, qd, q.shape), ("lse", lse, torch.float32, (total_q, hq)),
+                  ("workspace", workspace, workspace.dtype, None),
+                  ("err", err, i32, None))
+    _launch(load().d2f_block_attn_kv4, dev, stream, q.data_ptr(), k_win.data_ptr(),
+            v_win.data_ptr(), pool.data_ptr(), page_table.data_ptr(), max_pages,
+            ctx_len.data_ptr(), q_start.data_ptr(), out.data_ptr(), _ptr(lse), batch, total_q,
+            max_q_per_seq, max_ctx, hq, hkv, d, block_size, pool.shape[0], int(k_exp), int(v_exp),
+            dt, float(softmax_scale), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(err))
     return out, lse
 
 
@@ -623,38 +607,33 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
     Returns a dict: page_table, ctx_len, row_start [batch + 1], admitted uint8 [batch], slot
     int64 [capacity], app_src / app_dst / app_rows [max_append] and n_append [1] (the list
     kv4_append takes), free_count [1]."""
-    lib = load()
     batch = num_new.shape[0]
-    dev = num_new.device
-    _shape(num_new, "num_new", (batch,))
-    _shape(ctx_len, "ctx_len", (batch,))
-    _shape(page_table, "page_table", (batch, page_table.shape[-1]))
-    _shape(free_count, "free_count", (1,))
+    device = num_new.device
+    max_pages = page_table.shape[-1]
     if capacity < 0 or max_append < 0:
         raise ValueError("capacity and max_append must not be negative")
+    i32 = torch.int32
     # the int32 results, one allocation (no gradients here, so the split without view
     # tracking does: 8 us for the seven against 13 with it and 10 for seven allocations)
     ctx_new, free_new, row_start, n_append, src, dst, rows = torch.empty(
-        2 * batch + 3 + 3 * max_append, dtype=torch.int32,
-        device=dev).unsafe_split_with_sizes(
+        2 * batch + 3 + 3 * max_append, dtype=i32, device=device).unsafe_split_with_sizes(
             [batch, 1, batch + 1, 1, max_append, max_append, max_append])
     if ctx_len_out is None:
         ctx_len_out = ctx_new
     if free_count_out is None:
         free_count_out = free_new
-    _shape(ctx_len_out, "ctx_len_out", (batch,))
-    _shape(free_count_out, "free_count_out", (1,))
-    admitted = torch.empty(batch, dtype=torch.uint8, device=dev)
-    slot = torch.empty(capacity, dtype=torch.int64, device=dev)
-    with _On(stream, ("num_new", num_new, torch.int32), ("ctx_len", ctx_len, torch.int32),
-             ("page_table", page_table, torch.int32), ("free_pages", free_pages, torch.int32),
-             ("free_count", free_count, torch.int32), ("ctx_len_out", ctx_len_out, torch.int32),
-             ("free_count_out", free_count_out, torch.int32), ("err", err, torch.int32)) as s:
-        _check(lib.d2f_page_map(
-            batch, block_size, page_table.shape[1], capacity, max_append, _ptr(num_new),
-            _ptr(ctx_len), _ptr(free_pages), _ptr(free_count), _ptr(page_table),
-            _ptr(ctx_len_out), _ptr(free_count_out), _ptr(row_start), _ptr(admitted), _ptr(slot),
-            _ptr(src), _ptr(dst), _ptr(rows), _ptr(n_append), _ptr(err), s))
+    admitted = torch.empty(batch, dtype=torch.uint8, device=device)
+    slot = torch.empty(capacity, dtype=torch.int64, device=device)
+    dev = _device(("num_new", num_new, i32, (batch,)), ("ctx_len", ctx_len, i32, (batch,)),
+                  ("page_table", page_table, i32, (batch, max_pages)),
+                  ("free_pages", free_pages, i32, None),
+                  ("free_count", free_count, i32, (1,)), ("ctx_len_out", ctx_len_out, i32, (batch,)),
+                  ("free_count_out", free_count_out, i32, (1,)), ("err", err, i32, None))
+    _launch(load().d2f_page_map, dev, stream, batch, block_size, max_pages, capacity, max_append,
+            num_new.data_ptr(), ctx_len.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+            page_table.data_ptr(), ctx_len_out.data_ptr(), free_count_out.data_ptr(),
+            row_start.data_ptr(), admitted.data_ptr(), slot.data_ptr(), src.data_ptr(),
+            dst.data_ptr(), rows.data_ptr(), n_append.data_ptr(), _ptr(err))
     return {"page_table": page_table, "ctx_len": ctx_len_out, "row_start": row_start,
             "admitted": admitted, "slot": slot, "app_src": src, "app_dst": dst,
             "app_rows": rows, "n_append": n_append, "free_count": free_count_out}
@@ -684,40 +663,34 @@ def token_logprobs(logits, tokens, *, logit_row=None, top_k=0, want_entropy=True
 
     logits may be a row-strided view ([rows, vocab] with stride(1) == 1). Returns
     dict(logprob [n], entropy [n] or None, top_id [n, top_k], top_logprob [n, top_k])."""
-    lib = load()
     if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA tensor with unit stride along the vocabulary")
     n = tokens.shape[0]
     rows, vocab = logits.shape
     if logit_row is None and rows < n:
         raise ValueError("%d tokens for %d logit rows" % (n, rows))
-    _shape(tokens, "tokens", (n,))
-    _shape(logit_row, "logit_row", (n,))
     dt = _dtype_code(logits)
-    dev = logits.device
-    if tokens.device != dev:
-        raise ValueError("tokens is on %s, logits on %s" % (tokens.device, dev))
+    device, f32, i32 = logits.device, torch.float32, torch.int32
+    if tokens.device != device:
+        raise ValueError("tokens is on %s, logits on %s" % (tokens.device, device))
     if logprob is None:
-        logprob = torch.empty(n, dtype=torch.float32, device=dev)
+        logprob = torch.empty(n, dtype=f32, device=device)
     if entropy is None and want_entropy:
-        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        entropy = torch.empty(n, dtype=f32, device=device)
     if top_id is None:
-        top_id = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        top_id = torch.empty((n, top_k), dtype=i32, device=device)
     if top_logprob is None:
-        top_logprob = torch.empty((n, top_k), dtype=torch.float32, device=dev)
-    _shape(logprob, "logprob", (n,))
-    _shape(entropy, "entropy", (n,))
-    _shape(top_id, "top_id", (n, top_k))
-    _shape(top_logprob, "top_logprob", (n, top_k))
+        top_logprob = torch.empty((n, top_k), dtype=f32, device=device)
     if workspace is None:
-        workspace = logprobs_workspace(dev, n=n, vocab=vocab, top_k=top_k, dtype=dt)
+        workspace = logprobs_workspace(device, n=n, vocab=vocab, top_k=top_k, dtype=dt)
     stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
-    with _On(stream, ("tokens", tokens, torch.int32), ("logit_row", logit_row, torch.int32),
-             ("logprob", logprob, torch.float32), ("entropy", entropy, torch.float32),
-             ("top_id", top_id, torch.int32), ("top_logprob", top_logprob, torch.float32),
-             ("workspace", workspace, None), ("err", err, torch.int32)) as s:
-        _check(lib.d2f_token_logprobs(
-            _ptr(logits), stride, dt, vocab, rows, _ptr(logit_row), _ptr(tokens), n, top_k,
-            _ptr(logprob), _ptr(entropy), _ptr(top_id), _ptr(top_logprob), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(err), s))
+    dev = _device(("tokens", tokens, i32, (n,)), ("logit_row", logit_row, i32, (n,)),
+                  ("logprob", logprob, f32, (n,)), ("entropy", entropy, f32, (n,)),
+                  ("top_id", top_id, i32, (n, top_k)), ("top_logprob", top_logprob, f32, (n, top_k)),
+                  ("workspace", workspace, workspace.dtype, None),
+                  ("err", err, i32, None))
+    _launch(load().d2f_token_logprobs, dev, stream, logits.data_ptr(), stride, dt, vocab, rows,
+            _ptr(logit_row), tokens.data_ptr(), n, top_k, logprob.data_ptr(), _ptr(entropy),
+            top_id.data_ptr(), top_logprob.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(err))
     return {"logprob": logprob, "entropy": entropy, "top_id": top_id, "top_logprob": top_logprob}
