@@ -43,19 +43,20 @@
 //            16 warps run side by side (32 columns a thread: 8 warps, and spills).
 //
 // Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 32,768
-// cached tokens and 64 window rows 259 us, 2.4 TB/s of 4-bit cache, against 329 us of the
+// cached tokens and 64 window rows 249 us, 2.5 TB/s of 4-bit cache, against 329 us of the
 // bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes; 16 sequences
-// of 251 to 4096 tokens 111 us; one of 1024 tokens 19 us. Time is 28 us + 1.05 us (about
-// 2000 cycles) per key tile of a CTA. The 28 us are code that runs once a segment, fetched
+// of 251 to 4096 tokens 111 us; one of 1024 tokens 19 us. Time is 28 us + 1.0 us (about
+// 1900 cycles) per key tile of a CTA. The 28 us are code that runs once a segment, fetched
 // from L2 or DRAM. A tile is bound by the hand-overs between its roles, each of which
-// takes 300 to 1000 cycles: with all conversions and exponentials taken out it still needs
-// 225 us on the first shape (without K's conversion 244, V's 248, the exponentials 253).
-// The tensor pipe is active 23 % of the cycles, the ALU, which converts the codes, 49 %,
-// the issue slots 67 %, DRAM 30 %. What shortened the chain: one issuer whose order
-// stands for two waits (272 -> 259), V^T on two warpgroups (285 -> 272), small code (the
-// hot loops of all roles share the instruction cache: V^T's loop unrolled by two costs
-// 10 %). What did not: a deeper ring, a third K buffer, a K chunk in a V^T warpgroup, polls
-// that sleep, polls by every warp.
+// takes 300 to 1000 cycles: when it took 259 us on the first shape, it still needed 225
+// with all conversions and exponentials taken out (without K's conversion 244, V's 248,
+// the exponentials 253). The tensor pipe is active 23 % of the cycles, the ALU, which
+// converts the codes, 54 %, the issue slots 71 %, DRAM 31 %. What shortened the chain: one
+// issuer whose order stands for two waits (272 -> 259), V^T on two warpgroups (285 ->
+// 272), polling warps on different schedulers (259 -> 249), small code (the hot loops of
+// all roles share the instruction cache: V^T's loop unrolled by two costs 10 %). What did
+// not: a deeper ring, a third K buffer, a K chunk in a V^T warpgroup, polls that sleep,
+// polls by every warp.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -73,7 +74,7 @@ constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K ex
 constexpr float kHigh = 15.0f, kLow = -2.0f;
 constexpr int kMaxBatch = kKv4MaxBatch;
 // What a row tile costs beside its key tiles (its queries, the pipeline's start, its
-// output: about 7 us, against 1.05 us a key tile), in key tiles.
+// output: about 7 us, against 1.0 us a key tile), in key tiles.
 constexpr int kSegmentTiles = 6;
 
 constexpr int NT = 64;                     // rows (columns of S^T and O^T) per row tile
@@ -502,8 +503,9 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
   const int row = quad * 32 + lane;
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  const bool do_k = warp < 8;
-  const int vhalf = (warp >> 2) - 2;  // V^T warpgroup: its 64 keys of a tile
+  const int dq = (warp >> 2) - 1;  // the warpgroup
+  const bool do_k = dq == 0;
+  const int vhalf = dq - 1;        // V^T warpgroup: its 64 keys of a tile
   int u = 0, cu = 0, sg = 0;
   bool ok = true;
 #pragma unroll 1
@@ -532,15 +534,16 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       const bool win = t >= Tc;
       const int st = cu % C::kStages;
       const uint32_t stage = sb + C::kRing + st * C::kStage;
-      // One warp of the warpgroup polls, for the tile's bytes and for the operand buffer;
-      // the others wait in the named barrier, which takes no issue slots.
-      if (quad == (do_k ? 2 : vhalf ? 3 : 2)) {
+      // One warp of the warpgroup polls, for the tile's bytes and for the operand buffer
+      // (not beside the producer or the issuer, warps 0 and 1); the others wait in the
+      // named barrier, which takes no issue slots.
+      if (quad == 2 + (dq == 2)) {
         if (!win)
           ok = wait_phase(smem_u32(&ms->full[st]), (cu / C::kStages) & 1, abort_flag, a);
         if (reuse)
           ok = wait_phase(smem_u32(do_k ? &ms->s_full[kb] : &ms->pv_done[kb]), free_ph, abort_flag, a) && ok;
       }
-      ok = named_sync_and(C::kBarK + (warp >> 2) - 1, 128, ok);
+      ok = named_sync_and(C::kBarK + dq, 128, ok);
       if (rare(!ok)) break;
       tc_fence_after();
       const bool ragged = !win && ms->ragged[st];
@@ -990,8 +993,8 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 #pragma unroll 1
       for (; t < t_end; ++t, ++u) {
         const int sbuf = u & 1;
-        // One warp of the warpgroup polls; the others wait in the named barrier, which
-        // takes no issue slots.
+        // One warp of the warpgroup polls, another scheduler's for every warpgroup (all on
+        // one: 4 % slower); the others wait in the named barrier, which takes no issue slots.
         if (quad == (wg & 3)) ok = wait_phase(smem_u32(&ms->s_full[sbuf]), (u >> 1) & 1, abort_flag, a);
         ok = named_sync_and(bar, 128, ok);
         if (rare(!ok)) break;
