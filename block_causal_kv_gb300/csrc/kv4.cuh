@@ -85,6 +85,25 @@ __device__ __forceinline__ uint32_t e2m1x2_bits(float lo, float hi) {
   return r;
 }
 
+// The same of eight halves (four pairs), as one word.
+__device__ __forceinline__ uint32_t half8_to_codes(const uint32_t (&h)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n\tcvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
+  return r;
+}
+// (x, y) *= f
+__device__ __forceinline__ void mul2(float &x, float &y, float f) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(f));
+}
+
 __device__ __forceinline__ float e2m1_value(uint32_t nibble) {
   return half_lo(e2m1x2_to_half2(nibble & 0xfu));
 }

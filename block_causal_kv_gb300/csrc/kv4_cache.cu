@@ -17,72 +17,99 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sixteen consecutive elements as floats.
+// Sixteen consecutive elements.
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]);
+struct Group;
 template <>
-__device__ __forceinline__ void load16<uint16_t>(const uint16_t *p, float (&x)[16]) {
+struct Group<uint16_t> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const uint16_t *p) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + h);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * h + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * h + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + h);
+      w[4 * h] = v.x;
+      w[4 * h + 1] = v.y;
+      w[4 * h + 2] = v.z;
+      w[4 * h + 3] = v.w;
     }
   }
-}
-template <>
-__device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + h);
-    x[4 * h] = v.x;
-    x[4 * h + 1] = v.y;
-    x[4 * h + 2] = v.z;
-    x[4 * h + 3] = v.w;
+    for (int j = 0; j < 8; ++j) w[j] = 0;
   }
-}
+};
+template <>
+struct Group<float> {
+  float x[16];
+  __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + h);
+      x[4 * h] = v.x;
+      x[4 * h + 1] = v.y;
+      x[4 * h + 2] = v.z;
+      x[4 * h + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = 0.f;
+  }
+};
 
 // Scale bits and the sixteen codes (two words, element 0 in the lowest nibble) of one group.
 //
-// The definition's quotient is the float y / s. With bf16 elements the code can be had
-// from y * (1 / s) instead: y has 8 significant bits and a midpoint between two codes
-// times s has at most 7, so a quotient that is not a midpoint is at least 2^-8 (relative)
-// away from it; rounded to fp16 (error 2^-11, the product's own error 2^-23 beside it)
-// it stays on its side, and an exact midpoint comes out as itself. Sixteen divisions a
-// group would make the kernel compute-bound (35,000 tokens x 32 heads: 440 us with them).
-template <typename T>
-__device__ __forceinline__ uint32_t encode16(const float (&x)[16], float mul, uint32_t (&code)[2]) {
+// The definition's quotient is the float y / s with y = x * mul. With bf16 elements the
+// code can be had from x * (mul / s) instead (mul is a power of two): y has 8 significant
+// bits and a midpoint between two codes times s has at most 7, so a quotient that is not
+// a midpoint is at least 2^-8 (relative) away from it; rounded to fp16 (error 2^-11, the
+// product's own error 2^-23 beside it) it stays on its side, and an exact midpoint comes
+// out as itself. Sixteen divisions a group would make the kernel compute-bound (35,000
+// tokens x 32 heads: 440 us with them). The largest magnitude is that of the bits, two
+// halves at a time (a NaN's are above infinity's).
+__device__ __forceinline__ uint32_t encode16(const Group<uint16_t> &g, float mul,
+                                             uint32_t (&code)[2]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = __vmaxu2(top, g.w[j] & 0x7fff7fffu);
+  const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u)) * mul;
+  const uint32_t sb = e4m3_bits(__fdiv_rn(amax, 6.0f));
+  const float s = e4m3_value(sb);
+  const float f = s == 0.f ? 0.f : mul * __fdiv_rn(1.0f, s);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = g.w[4 * w + j];
+      float a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xffff0000u);
+      mul2(a, b, f);
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(b), "f"(a));
+    }
+    const uint32_t c = half8_to_codes(h);
+    code[w] = s == 0.f ? 0u : c;  // (no negative zeros in a group without a scale)
+  }
+  return sb;
+}
+__device__ __forceinline__ uint32_t encode16(const Group<float> &g, float mul,
+                                             uint32_t (&code)[2]) {
   float y[16], amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    y[j] = x[j] * mul;
+    y[j] = g.x[j] * mul;
     amax = fmax_nan(amax, fabsf(y[j]));
   }
   const uint32_t sb = e4m3_bits(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(sb);
-  const float inv = s == 0.f ? 0.f : __fdiv_rn(1.0f, s);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     uint32_t c = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float a = y[8 * w + 2 * j], b = y[8 * w + 2 * j + 1];
-      float qa, qb;
-      if constexpr (sizeof(T) == 2) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b * inv), "f"(a * inv));
-        qa = half_lo(h);
-        qb = half_hi(h);
-      } else {
-        qa = s == 0.f ? 0.f : __fdiv_rn(a, s);
-        qb = s == 0.f ? 0.f : __fdiv_rn(b, s);
-      }
-      c |= e2m1x2_bits(qa, qb) << (8 * j);
+      c |= e2m1x2_bits(s == 0.f ? 0.f : __fdiv_rn(a, s), s == 0.f ? 0.f : __fdiv_rn(b, s)) << (8 * j);
     }
-    code[w] = s == 0.f ? 0u : c;  // (no negative zeros in a group without a scale)
+    code[w] = s == 0.f ? 0u : c;
   }
   return sb;
 }
@@ -114,16 +141,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a)
 #pragma unroll
   for (int i = threadIdx.x; i < 2 * per; i += kThreads) {
     const int which = i / per, t = (i % per) / NG, grp = i % NG;
-    float x[16];
-    if (t < rows) {
-      load16<T>(reinterpret_cast<const T *>(which ? a.v_win : a.k_win) +
-                    ((int64_t)(src + t) * a.num_heads_kv + g) * D + grp * 16, x);
-    } else {  // slots past the block's rows hold zeros
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = 0.f;
-    }
+    Group<T> x;
+    if (t < rows)
+      x.load(reinterpret_cast<const T *>(which ? a.v_win : a.k_win) +
+             ((int64_t)(src + t) * a.num_heads_kv + g) * D + grp * 16);
+    else
+      x.zero();  // slots past the block's rows hold zeros
     uint32_t code[2];
-    const uint32_t sb = encode16<T>(x, which ? a.v_mul : a.k_mul, code);
+    const uint32_t sb = encode16(x, which ? a.v_mul : a.k_mul, code);
     if (which == 0) {
       *reinterpret_cast<uint2 *>(page + ((grp >> 1) * B + t) * 16 + (grp & 1) * 8) =
           make_uint2(code[0], code[1]);
@@ -236,8 +261,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
         const uint32_t h = e2m1x2_to_half2(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 0xffu);
-        k[j] = half_lo(h) * s;
-        k[j + 1] = half_hi(h) * s;
+        k[j] = half_lo(h);
+        k[j + 1] = half_hi(h);
+        mul2(k[j], k[j + 1], s);
       }
     }
     store16<T>(k_out + ((i0 + t) * a.num_heads_kv + g) * D + grp * 16, k);
@@ -273,7 +299,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
       const uint32_t c = ((w0[o / 8] >> (4 * (o % 8))) & 15u) | (((w1[o / 8] >> (4 * (o % 8))) & 15u) << 4);
       const uint32_t h = e2m1x2_to_half2(c);
       const float s = e4m3_value(sc[o / 4] >> (8 * (o % 4))) * a.v_mul;
-      const float x = half_lo(h) * s, y = half_hi(h) * s;
+      float x = half_lo(h), y = half_hi(h);
+      mul2(x, y, s);
       if constexpr (sizeof(T) == 2)
         *reinterpret_cast<uint32_t *>(out + o * step) = pack_bf16x2(x, y);
       else
