@@ -114,17 +114,39 @@ __device__ __forceinline__ uint32_t encode16(const Group<float> &g, float mul,
   return sb;
 }
 
+// 8 x 8 nibbles: o[d] gets nibble d of r[0] .. r[7], in that order.
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&r)[8]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {  // halves of words, four apart
+    const uint32_t a = r[t], b = r[t + 4];
+    r[t] = __byte_perm(a, b, 0x5410);
+    r[t + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int t = 0; t < 8; t += t & 1 ? 3 : 1) {  // bytes, two apart: t = 0, 1, 4, 5
+    const uint32_t a = r[t], b = r[t + 2];
+    r[t] = __byte_perm(a, b, 0x6240);
+    r[t + 2] = __byte_perm(a, b, 0x7351);
+  }
+#pragma unroll
+  for (int t = 0; t < 8; t += 2) {  // nibbles
+    const uint32_t a = r[t], b = r[t + 1];
+    r[t] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+    r[t + 1] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+  }
+}
+
 // One CTA per (append entry, KV head). A thread owns one group of 16 elements of one
-// token; K codes go straight to the page. The V codes of a page are transposed through
-// shared memory: there a thread owns a dim and collects its nibble of every token (one
-// 16-byte read brings two tokens' codes of its group, shared by the group's dims), so
-// the page is written in words and not in bytes.
+// token; the page is put together in shared memory and written in 16-byte pieces. V's
+// codes are transposed there by one thread per eight dims, 8 tokens x 8 dims at a time
+// in registers (a thread per dim that collects its nibbles: 130 against 1XX us).
 template <typename T, int D, int B>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a) {
   constexpr int NG = D / 16;
   constexpr Kv4Layout L{D, B};
-  __shared__ uint2 v_s[NG][B];                // codes of a (group, token)
-  __shared__ __align__(16) uint8_t sc_s[2 * B * NG];  // K scales, V scales, in page order
+  // V codes of a (group, token); a row more than the tokens, against bank conflicts
+  __shared__ uint2 v_s[NG][B + 1];
+  __shared__ uint4 page_s[B * D * 9 / 128];
   grid_dependency_wait();
   const int ap = blockIdx.x / a.num_heads_kv;
   const int g = blockIdx.x % a.num_heads_kv;
@@ -136,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a)
     if (threadIdx.x == 0 && g == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
     return;
   }
-  uint8_t *page = a.pool + ((int64_t)dst * a.num_heads_kv + g) * L.page_bytes();
+  uint8_t *image = reinterpret_cast<uint8_t *>(page_s);
   constexpr int per = B * NG;  // groups of one tensor
 #pragma unroll
   for (int i = threadIdx.x; i < 2 * per; i += kThreads) {
@@ -150,37 +172,36 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a)
     uint32_t code[2];
     const uint32_t sb = encode16(x, which ? a.v_mul : a.k_mul, code);
     if (which == 0) {
-      *reinterpret_cast<uint2 *>(page + ((grp >> 1) * B + t) * 16 + (grp & 1) * 8) =
+      *reinterpret_cast<uint2 *>(image + ((grp >> 1) * B + t) * 16 + (grp & 1) * 8) =
           make_uint2(code[0], code[1]);
-      sc_s[t * NG + grp] = (uint8_t)sb;
+      image[L.k_scales() + t * NG + grp] = (uint8_t)sb;
     } else {
       v_s[grp][t] = make_uint2(code[0], code[1]);
-      sc_s[per + grp * B + t] = (uint8_t)sb;
+      image[L.v_scales() + grp * B + t] = (uint8_t)sb;
     }
   }
   __syncthreads();
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x, grp = d >> 4, sh = 4 * (d & 7);
-    uint32_t out[B / 8];
+  if (threadIdx.x < D / 8) {
+    const int d8 = threadIdx.x;  // dims 8 d8 .. 8 d8 + 7
+    uint32_t out[B];             // word w of dim i: out[i * (B / 8) + w]
 #pragma unroll
     for (int w = 0; w < B / 8; ++w) {
-      uint32_t c = 0;
+      uint32_t r[8];
 #pragma unroll
-      for (int t = 0; t < 8; t += 2) {
-        const uint4 two = *reinterpret_cast<const uint4 *>(&v_s[grp][8 * w + t]);
-        const uint32_t w0 = d & 8 ? two.y : two.x, w1 = d & 8 ? two.w : two.z;
-        c |= (((w0 >> sh) & 15u) | (((w1 >> sh) & 15u) << 4)) << (4 * t);
-      }
-      out[w] = c;
+      for (int t = 0; t < 8; ++t)
+        r[t] = reinterpret_cast<const uint32_t *>(&v_s[d8 >> 1][8 * w + t])[d8 & 1];
+      transpose_nibbles(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i * (B / 8) + w] = r[i];
     }
-    uint8_t *p = page + L.v_codes() + d * (B / 2);
-    if constexpr (B == 8) *reinterpret_cast<uint32_t *>(p) = out[0];
-    if constexpr (B == 16) *reinterpret_cast<uint2 *>(p) = make_uint2(out[0], out[1]);
-    if constexpr (B == 32) *reinterpret_cast<uint4 *>(p) = make_uint4(out[0], out[1], out[2], out[3]);
-  } else {
-    for (int i = threadIdx.x - D; i < 2 * per / 16; i += kThreads - D)
-      reinterpret_cast<uint4 *>(page + L.k_scales())[i] = reinterpret_cast<const uint4 *>(sc_s)[i];
+    uint4 *p = reinterpret_cast<uint4 *>(image + L.v_codes() + d8 * 4 * B);
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i)
+      p[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
   }
+  __syncthreads();
+  uint4 *page = reinterpret_cast<uint4 *>(a.pool + ((int64_t)dst * a.num_heads_kv + g) * L.page_bytes());
+  for (int i = threadIdx.x; i < L.page_bytes() / 16; i += kThreads) page[i] = page_s[i];
 }
 
 template <typename T>
