@@ -64,18 +64,27 @@ struct Group<float> {
 // bits and a midpoint between two codes times s has at most 7, so a quotient that is not
 // a midpoint is at least 2^-8 (relative) away from it; rounded to fp16 (error 2^-11, the
 // product's own error 2^-23 beside it) it stays on its side, and an exact midpoint comes
-// out as itself. Sixteen divisions a group would make the kernel compute-bound (35,000
-// tokens x 32 heads: 440 us with them). The largest magnitude is that of the bits, two
-// halves at a time (a NaN's are above infinity's).
+// out as itself, also with a reciprocal that is a step off. The scale's quotient by 6 goes
+// the same way (a midpoint between two e4m3 values has at most 5 bits, times 6 at most 7;
+// what fp16 cannot hold is above 448 or rounds to 0). Eighteen divisions a group would make
+// the kernel compute-bound (35,000 tokens x 32 heads: 440 us with them). The largest
+// magnitude is that of the bits, two halves at a time (a NaN's are above infinity's).
 __device__ __forceinline__ uint32_t encode16(const Group<uint16_t> &g, float mul,
                                              uint32_t (&code)[2]) {
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = __vmaxu2(top, g.w[j] & 0x7fff7fffu);
   const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u)) * mul;
-  const uint32_t sb = e4m3_bits(__fdiv_rn(amax, 6.0f));
+  uint32_t sb;
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 t;\n\tcvt.rn.f16x2.f32 h, %1, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 t, h;\n\tcvt.u32.u16 %0, t;\n\t}"
+      : "=r"(sb)
+      : "f"(amax * (1.0f / 6.0f)));
+  sb &= 0xffu;
   const float s = e4m3_value(sb);
-  const float f = s == 0.f ? 0.f : mul * __fdiv_rn(1.0f, s);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float f = s == 0.f ? 0.f : mul * inv;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     uint32_t h[4];
@@ -314,18 +323,29 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
     }
     T *out = v_out + ((i0 + t0 - o0) * a.num_heads_kv + g) * D + d;  // of token 0 of the page
     const int64_t step = (int64_t)a.num_heads_kv * D;
+    const int n_run = t1 - t0;
 #pragma unroll
-    for (int o = 0; o < B; ++o) {
-      if (o < o0 || o >= o0 + (t1 - t0)) continue;
-      const uint32_t c = ((w0[o / 8] >> (4 * (o % 8))) & 15u) | (((w1[o / 8] >> (4 * (o % 8))) & 15u) << 4);
-      const uint32_t h = e2m1x2_to_half2(c);
-      const float s = e4m3_value(sc[o / 4] >> (8 * (o % 4))) * a.v_mul;
-      float x = half_lo(h), y = half_hi(h);
-      mul2(x, y, s);
-      if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint32_t *>(out + o * step) = pack_bf16x2(x, y);
-      else
-        *reinterpret_cast<float2 *>(out + o * step) = make_float2(x, y);
+    for (int q = 0; q < B / 8; ++q) {
+      // both dims' codes of a token in one byte: tokens 0, 2, 4, 6 and 1, 3, 5, 7
+      const uint32_t even = (w0[q] & 0x0f0f0f0fu) | ((w1[q] << 4) & 0xf0f0f0f0u);
+      const uint32_t odd = ((w0[q] >> 4) & 0x0f0f0f0fu) | (w1[q] & 0xf0f0f0f0u);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t s2 = e4m3x2_to_half2(sc[2 * q + p / 2] >> (16 * (p & 1)));  // two tokens'
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int o = 8 * q + 2 * p + k;
+          if ((unsigned)(o - o0) >= (unsigned)n_run) continue;
+          const uint32_t h = e2m1x2_to_half2((k ? odd : even) >> (8 * p));
+          const float s = (k ? half_hi(s2) : half_lo(s2)) * a.v_mul;
+          float x = half_lo(h), y = half_hi(h);
+          mul2(x, y, s);
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint32_t *>(out + o * step) = pack_bf16x2(x, y);
+          else
+            *reinterpret_cast<float2 *>(out + o * step) = make_float2(x, y);
+        }
+      }
     }
   }
 }
