@@ -7,9 +7,10 @@
 //
 // Both move bytes once: an append reads 2 D elements a token and head and writes 9/16 of
 // that many bytes, a read the reverse. Measured (16 prompts of 251 to 4096 tokens, 30,000
-// tokens, 32 heads, D = 128, B = 16, bf16): append 159 us and read 134 us, 4.0 and 4.7 TB/s.
-// Neither is at the memory's rate: the conversions keep the issue slots 75 % and 64 % busy
-// (ALU 52 % and 57 %). A step's 8 blocks of 4 heads take 6 us for both, which is launches.
+// tokens, 32 heads, D = 128, B = 16, bf16): append 121 us and read 107 us, 5.2 and 5.9 TB/s.
+// Neither is quite at the memory's rate: the conversions keep the issue slots 70 % and 73 %
+// busy (ALU 63 % and 60 %), and every warp waits for its loads once. A step's 8 blocks of 4
+// heads take 6 us for both, which is launches.
 #include "kv4.cuh"
 
 namespace d2f {
@@ -148,7 +149,7 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&r)[8]) {
 // One CTA per (append entry, KV head). A thread owns one group of 16 elements of one
 // token; the page is put together in shared memory and written in 16-byte pieces. V's
 // codes are transposed there by one thread per eight dims, 8 tokens x 8 dims at a time
-// in registers (a thread per dim that collects its nibbles: 130 against 1XX us).
+// in registers (a thread per dim that collects its nibbles: 130 us against 125).
 template <typename T, int D, int B>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendArgs a) {
   constexpr int NG = D / 16;
@@ -238,7 +239,9 @@ __device__ __forceinline__ void store16<float>(float *p, const float (&x)[16]) {
 // time. (Gathering V element by element took twice as long: eight cache lines a load.)
 constexpr int kReadRows = 64;
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
+// CTAs an SM: eight where 32 registers do without spills (B = 16: 228 us for the append and
+// read of 30,000 tokens, 237 without a bound), five else.
+__global__ void __launch_bounds__(kThreads, (B <= 16 ? 8 : 5)) read_kernel(const Kv4ReadArgs a) {
   constexpr int NG = D / 16;
   constexpr Kv4Layout L{D, B};
   __shared__ int64_t slot_s[kReadRows];  // -1: none
@@ -277,26 +280,38 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadArgs a) {
   }
   __syncthreads();
   T *k_out = reinterpret_cast<T *>(a.k_out), *v_out = reinterpret_cast<T *>(a.v_out);
-  for (int i = tid; i < n * NG; i += kThreads) {
-    const int t = i / NG, grp = i % NG;
-    const int64_t slot = slot_s[t];
-    float k[16];
+  constexpr int kK = 2;  // groups of a thread at once: every load before any use
+  for (int i0k = tid; i0k < n * NG; i0k += kK * kThreads) {
+    uint2 w[kK];
+    uint32_t sc[kK];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) k[j] = 0.f;
-    if (slot >= 0) {
-      const int o = (int)(slot % B);
-      const uint8_t *page = a.pool + (slot / B * a.num_heads_kv + g) * L.page_bytes();
-      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(page + ((grp >> 1) * B + o) * 16 + (grp & 1) * 8));
-      const float s = e4m3_value(__ldg(page + L.k_scales() + o * NG + grp)) * a.k_mul;
+    for (int q = 0; q < kK; ++q) {
+      const int i = i0k + q * kThreads, t = i / NG, grp = i % NG;
+      const int64_t slot = i < n * NG ? slot_s[t] : -1;
+      w[q] = make_uint2(0, 0);
+      sc[q] = 0;
+      if (slot >= 0) {
+        const int o = (int)(slot % B);
+        const uint8_t *page = a.pool + (slot / B * a.num_heads_kv + g) * L.page_bytes();
+        w[q] = __ldg(reinterpret_cast<const uint2 *>(page + ((grp >> 1) * B + o) * 16 + (grp & 1) * 8));
+        sc[q] = __ldg(page + L.k_scales() + o * NG + grp);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kK; ++q) {
+      const int i = i0k + q * kThreads, t = i / NG, grp = i % NG;
+      if (i >= n * NG) break;
+      const float s = e4m3_value(sc[q]) * a.k_mul;
+      float k[16];
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
-        const uint32_t h = e2m1x2_to_half2(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 0xffu);
+        const uint32_t h = e2m1x2_to_half2(((j < 8 ? w[q].x : w[q].y) >> (4 * (j & 7))) & 0xffu);
         k[j] = half_lo(h);
         k[j + 1] = half_hi(h);
         mul2(k[j], k[j + 1], s);
       }
+      store16<T>(k_out + ((i0 + t) * a.num_heads_kv + g) * D + grp * 16, k);
     }
-    store16<T>(k_out + ((i0 + t) * a.num_heads_kv + g) * D + grp * 16, k);
   }
   constexpr int kHalves = D / 64;  // warps a run
   const int d = 64 * (warp % kHalves) + 2 * lane;
