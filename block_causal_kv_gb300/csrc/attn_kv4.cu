@@ -107,6 +107,7 @@ struct Cfg {
 
 struct SeqMeta {
   int q0, n, C, items;  // items: row tiles of the sequences before it
+  int tiles, rows;      // row tiles of a KV head (of `rows` rows)
 };
 struct Seg {      // the part of one row tile that lies in a CTA's share
   int q0, n, C;   // sequence: first window row, window rows, cached tokens
@@ -339,12 +340,9 @@ struct RowTiles {
   int tiles, rows;
 };
 __device__ __forceinline__ RowTiles row_tiles(int total) {
-  RowTiles r;
-  r.tiles = (total + NT - 1) / NT;
-  if (r.tiles == 0) return {0, 16};
-  r.rows = ((total + r.tiles - 1) / r.tiles + 15) & ~15;
-  r.tiles = (total + r.rows - 1) / r.rows;
-  return r;
+  if (total <= NT) return {total > 0, (total + 15) & ~15};
+  const unsigned t = (unsigned)(total + NT - 1) / NT, rows = (((unsigned)total + t - 1) / t + 15) & ~15;
+  return {(int)(((unsigned)total + rows - 1) / rows), (int)rows};
 }
 
 // The segment that starts at unit w of the line (w < w1: end of the share). A row tile
@@ -362,7 +360,7 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   s.q0 = meta[lo].q0;
   s.n = meta[lo].n;
   s.C = meta[lo].C;
-  const RowTiles rt = row_tiles(a.group * s.n);
+  const unsigned tiles = meta[lo].tiles;
   s.Tc = (s.C + kKeys - 1) / kKeys;
   s.T = s.Tc + (s.n + kKeys - 1) / kKeys;
   const int units = s.T + k0;
@@ -372,10 +370,10 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   s.units = (int)min((long long)(units - off), w1 - w);
   s.t0 = max(0, off - k0);
   s.len = max(0, off + s.units - k0) - s.t0;
-  s.g = it / rt.tiles;
-  const int m = it - s.g * rt.tiles;
-  s.r0 = m * rt.rows;
-  s.nrows = min(rt.rows, a.group * s.n - s.r0);
+  s.g = (unsigned)it / tiles;
+  const int m = it - s.g * tiles;
+  s.r0 = m * meta[lo].rows;
+  s.nrows = min(meta[lo].rows, a.group * s.n - s.r0);
   s.item = (s.b * a.num_heads_kv + s.g) * a.m_tiles + m;
   return s;
 }
@@ -716,10 +714,11 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         int q0, n, ctx;
         if (load_seq_meta(a, b, q0, n, ctx)) {
           const int T = (int)((ctx + kKeys - 1LL) / kKeys) + (n + kKeys - 1) / kKeys;
-          it = a.num_heads_kv * row_tiles(a.group * n).tiles;
+          const RowTiles rt = row_tiles(a.group * n);
+          it = a.num_heads_kv * rt.tiles;
           u = (long long)T * it;
           if (it > 0) longest = max(longest, T);
-          meta[b] = SeqMeta{q0, n, ctx, 0};
+          meta[b] = SeqMeta{q0, n, ctx, 0, rt.tiles, rt.rows};
         } else if (blockIdx.x == 0) {
           set_err(a.err, D2F_ERR_INVALID_ARG);
         }
@@ -752,7 +751,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
     int k0 = kSegmentTiles;
     if (items > 0 && items <= n && (long long)longest * items == tiles) {
       const int k = (int)n / items;
-      if ((longest + k - 1) / k <= tiles / n + kSegmentTiles) {
+      if ((longest + k - 1) / k <= share(tiles, n) + kSegmentTiles) {
         n = (long long)items * k;
         k0 = 0;
       }
@@ -1157,10 +1156,10 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         __stcg(reinterpret_cast<float2 *>(slot + NT * D) + col0 + lane, make_float2(M, L));
       named_sync(bar_all, 128 * C::kSw);
       if (stid == 0) {
-        __threadfence();  // (the barrier ordered the others' stores before this)
+        // (release and acquire at once: the barrier ordered the others' stores before it,
+        // and the next one orders their loads behind it)
         const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == ms->c1 - ms->c0;
         if (is_last) a.counters[s.item] = 0;
-        __threadfence();
         ms->last = is_last;
       }
       named_sync(bar_all, 128 * C::kSw);
@@ -1212,7 +1211,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
 
 template <int D>
 constexpr int smem_bytes(int batch) {
-  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * (batch + 2) + 16 * batch;
+  return Cfg<D>::kMisc + (int)sizeof(Misc<D>) + 8 * (batch + 2) + (int)sizeof(SeqMeta) * batch;
 }
 
 template <int D, int B>
