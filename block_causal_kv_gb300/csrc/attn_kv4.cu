@@ -45,9 +45,11 @@
 // Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 32,768
 // cached tokens and 64 window rows 249 us, 2.5 TB/s of 4-bit cache, against 329 us of the
 // bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes; 16 sequences
-// of 251 to 4096 tokens 111 us; one of 1024 tokens 19 us. Time is 28 us + 1.0 us (about
-// 1900 cycles) per key tile of a CTA. The 28 us are code that runs once a segment, fetched
-// from L2 or DRAM. A tile is bound by the hand-overs between its roles, each of which
+// of 251 to 4096 tokens 105 us; one of 1024 tokens 17 us. Time is some 25 us + 1.0 us (about
+// 1900 cycles) per key tile of a CTA. Of the 25 us, 4 are the start (sequence metadata, work
+// line, first page ids), 1 the queries, 2 the first tile, 2 the window tile, 2 the part and
+// its arrival, 3 the composition: straight code that runs once, much of it instruction
+// fetches. A tile is bound by the hand-overs between its roles, each of which
 // takes 300 to 1000 cycles: when it took 259 us on the first shape, it still needed 225
 // with all conversions and exponentials taken out (without K's conversion 244, V's 248,
 // the exponentials 253). The tensor pipe is active 23 % of the cycles, the ALU, which
@@ -520,6 +522,20 @@ __device__ __forceinline__ void dequant_role(const AttnArgs &a, Misc<D> *ms, uin
       Seg &keep = ms->dseg[warp - 4];
       if (lane == 0) keep = s;
       __syncwarp();
+      // The first window tile's rows to L1: the tile loads them in four steps, each of which
+      // waits for its loads (one short context 19 -> 17 us, the ragged batch 109 -> 105).
+      if (s.t0 + s.len > s.Tc) {
+        constexpr int kLines = D / 64;  // 128-byte lines of a row
+        const int first = max(s.t0 - s.Tc, 0) * kKeys;
+        const char *base = static_cast<const char *>(do_k ? a.k_win : a.v_win);
+#pragma unroll
+        for (int c = 0; c < (do_k ? kLines : 1); ++c) {
+          const int key = do_k ? row : 64 * vhalf + row / kLines, line = do_k ? c : row % kLines;
+          if (first + key < s.n && (do_k || row < 64 * kLines))
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                base + ((int64_t)(s.q0 + first + key) * a.num_heads_kv + s.g) * (2 * D) + 128 * line));
+        }
+      }
     }
     const Seg &s = ms->dseg[warp - 4];
     int nf_blk = 0x7fffffff, nf_nan = 0x7fffffff;  // see Misc
