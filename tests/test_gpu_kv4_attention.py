@@ -79,6 +79,18 @@ def test_ragged_batch(hq, hkv, D, B, dtype):
     check(p, out, lse)
 
 
+@pytest.mark.parametrize("hq,hkv,D,B", SHAPES[::3])
+def test_bf16_on_the_cuda_core_path(hq, hkv, D, B, monkeypatch):
+    """The switch that forces the CUDA-core kernel (its weights are not rounded: inside the
+    tensor-core path's bounds)."""
+    dev = device()
+    monkeypatch.setenv("D2F_ATTN_PATH", "simt")
+    p = problem([0, 1, B, 129, 300], [1, 2, 3, 1, 3], hq=hq, hkv=hkv, D=D, B=B,
+                dtype=torch.bfloat16, seed=hq + D + B)
+    out, lse = run(p, dev)
+    check(p, out, lse)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("ctx,blocks,B", [
     ([2500], [1], 16), ([1024], [3], 16), ([4001, 17], [2, 4], 32), ([1999, 0, 640], [4, 1, 2], 8)])
