@@ -29,7 +29,9 @@
 // as kSegmentTiles units more. All units of the launch are one line, cut into equal
 // shares, one CTA a share: every SM gets the same work whatever the batch looks like. A row tile whose units lie in several shares is put together by the CTA that
 // arrives last at its counter, from float partials in the workspace, in the order of the
-// line (the result does not depend on who is last). No CTA waits on another.
+// line (the result does not depend on who is last). No CTA waits on another. The counter is
+// that of the share which holds the row tile's first key tile: a share has one end, so it
+// cuts off one row tile at most, and the counters are as many as CTAs whatever the batch is.
 //
 // Roles of a CTA's warps:
 //   0        producer: page ids -> one bulk copy per page (K and V of a head are one
@@ -119,7 +121,6 @@ struct Seg {      // the part of one row tile that lies in a CTA's share
   int T, Tc;
   int units;      // units of the line that the segment covers
   long long w0;   // first unit of the row tile on the line
-  int item;       // its counter
 };
 
 template <int D>
@@ -376,7 +377,6 @@ __device__ __forceinline__ Seg segment(const AttnArgs &a, const long long *pre, 
   const int m = it - s.g * tiles;
   s.r0 = m * meta[lo].rows;
   s.nrows = min(meta[lo].rows, a.group * s.n - s.r0);
-  s.item = (s.b * a.num_heads_kv + s.g) * a.m_tiles + m;
   return s;
 }
 
@@ -1174,8 +1174,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       if (stid == 0) {
         // (release and acquire at once: the barrier ordered the others' stores before it,
         // and the next one orders their loads behind it)
-        const bool is_last = atomic_add_acq_rel(a.counters + s.item, 1) == ms->c1 - ms->c0;
-        if (is_last) a.counters[s.item] = 0;
+        int32_t *counter = a.counters + ms->c0;
+        const bool is_last = atomic_add_acq_rel(counter, 1) == ms->c1 - ms->c0;
+        if (is_last) *counter = 0;
         ms->last = is_last;
       }
       named_sync(bar_all, 128 * C::kSw);

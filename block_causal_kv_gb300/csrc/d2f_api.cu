@@ -53,6 +53,14 @@ int cuda_fail(cudaError_t e, const char *what) {
   return fail(D2F_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Bytes of the arrival counters at a workspace's start. They are zero at rest, everything
+// behind them is written before it is read. A workspace serves calls of different sizes one
+// after another, so the region is the same for all of them: four counters an SM, as many as
+// any automatic plan counts (n more only where a caller's num_splits asks for them).
+size_t counter_bytes(long long n) {
+  return align_up((size_t)max(n, 4LL * max(1, num_sms_current_device())) * sizeof(int32_t));
+}
+
 // ---------------------------------------------------------------------------
 // Attention plan
 // ---------------------------------------------------------------------------
@@ -247,8 +255,8 @@ int plan_attn(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, i
     p->tiles_per_split = cdiv(t_max, p->splits);
     p->n_counters = 0;
     p->off_ml = p->off_o = p->off_sk = p->bytes = 0;
-    if (p->sk) {  // pair counters, then 2 slots per CTA
-      p->off_sk = align_up((size_t)max(batch, 1) * Hkv * sizeof(int32_t));
+    if (p->sk) {  // pair counters (the planner's form: fewer than SMs), then 2 slots per CTA
+      p->off_sk = counter_bytes((long long)max(batch, 1) * Hkv);
       p->bytes = p->off_sk + (size_t)2 * p->sk * kSkSlotBytes;
     }
     return D2F_OK;
@@ -264,7 +272,8 @@ int plan_attn(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, i
   p->splits = splits;
   p->n_counters = max(batch, 1) * Hkv * max(1, cdiv((long long)G * max_q, kSimtRows));
   const size_t n_hr = (size_t)total_q * Hq;
-  p->off_ml = align_up((size_t)p->n_counters * sizeof(int32_t));
+  // (splits that the planner chose mean at most two row tiles an SM; one split counts nothing)
+  p->off_ml = counter_bytes(splits > 1 ? p->n_counters : 0);
   if (splits > 1) {
     p->off_o = p->off_ml + align_up((size_t)splits * n_hr * sizeof(float2));
     p->bytes = p->off_o + align_up((size_t)splits * n_hr * D * sizeof(float));
@@ -836,9 +845,9 @@ int kv4_plan(int batch, int total_q, int max_q, int max_ctx, int Hq, int Hkv, in
   p->splits = (int)min((long long)sms, max(1LL, units));
   if ((long long)batch * Hkv * p->m_tiles > 0x7fffffffLL)
     return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_kv * %d row tiles is too large", p->m_tiles);
-  p->n_counters = max(batch, 1) * Hkv * p->m_tiles;
+  p->n_counters = p->splits;  // one a CTA: the row tile that its share cuts off at the end
   p->off_ml = 0;
-  p->off_o = align_up((size_t)p->n_counters * sizeof(int32_t));
+  p->off_o = counter_bytes(p->n_counters);
   const size_t slot = ((size_t)p->rows * D + 2 * p->rows) * sizeof(float);
   p->bytes = p->off_o + 2 * slot * p->splits;  // two partial row tiles a CTA
   return D2F_OK;

@@ -73,7 +73,8 @@ struct AttnArgs {
   uint8_t *sk_slots;     // stream-K: [2 * grid] partial slots of kSkSlotBytes
   const uint8_t *kv4_pool;  // non-null: the cache is the 4-bit pool (kv4.cuh), k_pool / v_pool unused
   float k_mul, v_mul;       // ... and 2^k_exp, 2^v_exp
-  int32_t *counters;     // [batch * Hkv * m_tiles] merge arrival counters (zero at rest)
+  int32_t *counters;     // merge arrival counters (zero at rest): [batch * Hkv * m_tiles], 4-bit
+                         // cache: [grid]
   float2 *ws_ml;         // [num_splits][total_q * Hq] (max in log2 units, sum)
   float *ws_o;           // [num_splits][total_q * Hq][head_dim] unnormalised partial output
   int32_t *err;

@@ -43,7 +43,11 @@
  * - Workspace: caller-provided device memory of at least the size the matching
  *   *_workspace_size query returns. It must be zero-filled before its first use
  *   (e.g. cudaMemsetAsync); every call leaves it ready for the next call on the
- *   same stream. Calls that share one workspace must not overlap in time.
+ *   same stream. Calls that share one workspace must not overlap in time (captured
+ *   graphs that may run at the same time need one each). The attention entry points
+ *   with num_splits 0 leave it ready for a call of other sizes too, so one workspace
+ *   of the largest size serves all of them in turn; the commit's is for one total_q
+ *   and block_size, and zeroed again before a call with others.
  *
  * Size limits (a call beyond one returns D2F_ERR_UNSUPPORTED before anything is
  * enqueued):
@@ -602,7 +606,7 @@ int d2f_block_attn_kv4_workspace_size(int batch, int total_q, int max_q_per_seq,
  * that a row does not see never reaches it, not even with infinite or NaN K or V;
  * slots of a page past ctx_len may hold anything. ctx_len need not be a multiple of
  * block_size. The workspace is the caller's, zeroed once (and again after a device
- * error); captured graphs that may run at the same time need one each.
+ * error); calls of any sizes and both dtypes may use it in turn.
  */
 int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, const void *kv_pool,
                        const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,
