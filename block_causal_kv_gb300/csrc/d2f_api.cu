@@ -1099,8 +1099,8 @@ int plan_logprobs(int n, int vocab, int top_k, int dtype, LogprobsPlan *p) {
   splits = cdiv(vocab, chunk);
   p->splits = splits;
   p->chunk = chunk;
-  // the counters come first: their place does not depend on the split count
-  p->off_partial = align_up((size_t)n * sizeof(int32_t));
+  // (several slices a row mean at most four rows an SM)
+  p->off_partial = counter_bytes(splits > 1 ? n : 0);
   p->off_top = p->off_partial + align_up((size_t)n * splits * sizeof(float4));
   p->bytes = splits > 1 ? p->off_top + align_up((size_t)n * splits * top_k * sizeof(uint64_t)) : 0;
   return D2F_OK;

@@ -45,9 +45,10 @@
  *   (e.g. cudaMemsetAsync); every call leaves it ready for the next call on the
  *   same stream. Calls that share one workspace must not overlap in time (captured
  *   graphs that may run at the same time need one each). The attention entry points
- *   with num_splits 0 leave it ready for a call of other sizes too, so one workspace
- *   of the largest size serves all of them in turn; the commit's is for one total_q
- *   and block_size, and zeroed again before a call with others.
+ *   with num_splits 0 and the log probabilities leave it ready for calls of other
+ *   sizes and for one another too, so one workspace of the largest size serves all
+ *   of them in turn; the commit's is for one total_q and block_size, and zeroed
+ *   again before a call with others.
  *
  * Size limits (a call beyond one returns D2F_ERR_UNSUPPORTED before anything is
  * enqueued):
