@@ -53,6 +53,17 @@ int cuda_fail(cudaError_t e, const char *what) {
   return fail(D2F_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// The caller's workspace against the bytes that a plan needs (the kernels read and write it in
+// pieces of up to 16 bytes).
+int check_workspace(const void *workspace, size_t got, size_t need) {
+  if (need > 0 && (!workspace || got < need))
+    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                workspace ? got : (size_t)0);
+  if (need > 0 && !aligned16(workspace))
+    return fail(D2F_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+  return D2F_OK;
+}
+
 // Bytes of the arrival counters at a workspace's start. They are zero at rest, everything
 // behind them is written before it is read. A workspace serves calls of different sizes one
 // after another, so the region is the same for all of them: four counters an SM, as many as
@@ -436,9 +447,8 @@ int attn_entry(const void *q, const void *k_win, const void *v_win, const void *
   const void *ptrs[] = {q, k_win, v_win, k_pool, v_pool, out};
   for (const void *x : ptrs)
     if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
-    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
-                workspace ? workspace_bytes : (size_t)0);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
 
   AttnArgs a{};
   a.q = q;
@@ -628,9 +638,8 @@ int d2f_commit_metric(const void *logits, int64_t row_stride, int dtype, int voc
     return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
   if (row_stride < vocab) return fail(D2F_ERR_INVALID_ARG, "row_stride < vocab");
   if (num_logit_rows <= 0) return fail(D2F_ERR_INVALID_ARG, "num_logit_rows must be > 0");
-  if (!workspace || workspace_bytes < p.bytes)
-    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
-                workspace ? workspace_bytes : (size_t)0);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
   const int elt = dtype == D2F_BF16 ? 2 : 4;
   const bool vec_ok = aligned16(logits) && ((row_stride * elt) % 16 == 0);
   const int path = vec_ok ? 1 : 0;
@@ -970,9 +979,8 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
   const void *ptrs[] = {q, k_win, v_win, kv_pool, out};
   for (const void *x : ptrs)
     if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
-    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
-                workspace ? workspace_bytes : (size_t)0);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
   AttnArgs a{};
   a.q = q;
   a.k_win = k_win;
@@ -1122,16 +1130,15 @@ int d2f_token_logprobs(const void *logits, int64_t row_stride, int dtype, int vo
                        float *top_logprob, void *workspace, size_t workspace_bytes,
                        int32_t *err_word, void *stream) {
   LogprobsPlan p{};
-  const int st = plan_logprobs(n, vocab, top_k, dtype, &p);
+  int st = plan_logprobs(n, vocab, top_k, dtype, &p);
   if (st != D2F_OK) return st;
   if (n == 0) return D2F_OK;
   if (!logits || !tokens || !logprob || (top_k > 0 && (!top_id || !top_logprob)))
     return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
   if (row_stride < vocab) return fail(D2F_ERR_INVALID_ARG, "row_stride < vocab");
   if (num_logit_rows <= 0) return fail(D2F_ERR_INVALID_ARG, "num_logit_rows must be > 0");
-  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
-    return fail(D2F_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.bytes,
-                workspace ? workspace_bytes : (size_t)0);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
   const int elt = dtype == D2F_BF16 ? 2 : 4;
   const int path = aligned16(logits) && (row_stride * elt) % 16 == 0 ? 1 : 0;
   LogprobsArgs a{};

@@ -41,9 +41,9 @@
  *   of sequence b lives in page page_table[b*max_pages_per_seq + t/B], slot t%B.
  * - GQA: query head h reads KV head h / (num_heads_q / num_heads_kv).
  * - Workspace: caller-provided device memory of at least the size the matching
- *   *_workspace_size query returns. It must be zero-filled before its first use
- *   (e.g. cudaMemsetAsync); every call leaves it ready for the next call on the
- *   same stream. Calls that share one workspace must not overlap in time (captured
+ *   *_workspace_size query returns, 16-byte aligned (else D2F_ERR_INVALID_ARG). It
+ *   must be zero-filled before its first use (e.g. cudaMemsetAsync); every call
+ *   leaves it ready for the next call on the same stream. Calls that share one workspace must not overlap in time (captured
  *   graphs that may run at the same time need one each). The attention entry points
  *   with num_splits 0 and the log probabilities leave it ready for calls of other
  *   sizes and for one another too, so one workspace of the largest size serves all
