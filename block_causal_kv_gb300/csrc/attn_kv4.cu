@@ -39,8 +39,8 @@
 //   1        MMA issuer (one elected lane); 2 and 3 are spare
 //   4 - 15   a warpgroup dequantises K (thread = key), two V^T (thread = dim, 64 keys each)
 //   16 - 31  four softmax warpgroups of 16 columns each, thread = key. A column's
-//            reference is 0, or moves when its scores lie outside [2^-2, 2^15] of it: a
-//            tile takes no maximum over the lanes, only a vote on whether some column
+//            reference moves only when its scores leave a wide range round it: a tile
+//            takes no maximum over the lanes, only a vote on whether some column
 //            has to move. With 16 columns a thread stays within 72 registers, which lets
 //            16 warps run side by side (32 columns a thread: 8 warps, and spills).
 //
@@ -69,13 +69,16 @@ namespace d2f {
 namespace {
 
 constexpr int kKeys = 128;                 // keys per tile (UMMA M of S^T, K extent of O^T)
-// References. P is fp16, so a column's scores should lie around its reference: at most
-// 2^15 above it (then the reference moves), and the largest at least 2^-2 of it, so that
-// what falls into fp16's subnormals (below 2^-14, steps of 2^-24) is nothing beside the
-// column's sum. A column starts with the reference 0 (scores as they are) and keeps it
-// if its first tile has a score in that range, which saves most row tiles the search
-// for a maximum over the lanes.
-constexpr float kHigh = 15.0f, kLow = -2.0f;
+// References. P is fp16, whose numbers end at 2^16 and whose steps are 2^-24 below 2^-14,
+// so a column's largest weight should lie near the top of that range: a weight errs by
+// 2^-11 of itself and by 2^-25 at most (one below that is lost to the output, while the
+// float sum holds it). The largest weight is at least 2^kLow = 2^6, so the second part is
+// 2^-31 of it: N cached tokens lose N 2^-31 of the sum at most, 2^-11 at a million. A
+// reference moves when a score rises 2^15 above it, and then to 2^kLift = 2^10 below that
+// score. A column starts with the reference 2^-kStart (scores in log2 units, plus 7) and
+// keeps it if its first tile has a score in [2^-1, 2^8], which saves most row tiles the
+// search for a maximum over the lanes (columns without a query have scores of 1).
+constexpr float kHigh = 15.0f, kLow = 6.0f, kLift = 10.0f, kStart = 7.0f;
 constexpr int kMaxBatch = kKv4MaxBatch;
 // What a row tile costs beside its key tiles (its queries, the pipeline's start, its
 // output: about 7 us, against 1.0 us a key tile), in key tiles.
@@ -137,7 +140,7 @@ struct Misc {
   long long W, wb, we;            // units of the line, and this CTA's share of them
   int n_cta, k0;                  // CTAs with a share; units of a row tile before its tiles
   alignas(16) float c[NT];        // cached tiles: factor of a score, log2 units
-  alignas(16) float nm[NT];       // minus the column's reference (0: none yet)
+  alignas(16) float nm[NT];       // minus the column's reference
   alignas(16) int blk[NT];        // window block of the column's query (no row: sees all)
   alignas(16) long long hr[NT];   // output row (window row * heads + head) of the column
   Seg seg;                        // the softmax warps' current segment
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         if (part == 0) {
           const float up = __int_as_float((127 + e) << 23);
           ms->c[qr] = a.scale_log2 * a.k_mul * up;
-          ms->nm[qr] = 0.f;
+          ms->nm[qr] = kStart;
           ms->hr[qr] = hr;
           ms->blk[qr] = qr < s.nrows ? (r / G) / B : 0x7fffffff;
         }
@@ -1001,7 +1004,7 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
       float l[16];  // this key lane's share of the columns' sums
 #pragma unroll
       for (int j = 0; j < 16; ++j) l[j] = 0.f;
-      float m_col = 0.f;  // reference of column `col`
+      float m_col = -kStart;  // reference of column `col`
       bool settled = false;  // every column has had a score near its reference
       unsigned seen_mask = 0;  // columns that have seen a key (kept while not settled)
       const int t_first = t;
@@ -1073,9 +1076,9 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
                                    fmaxf(ms->red[wg][2][col], ms->red[wg][3][col]));
           const bool seen = rise > -INFINITY;
           const bool move = seen && (rise > kHigh || (!settled && rise < kLow && !(seen_mask >> col & 1)));
-          const float d_col = move ? rise : 0.f;
+          const float d_col = move ? rise - kLift : 0.f;
           // (a column that has seen no key yet has nothing to rescale)
-          const float a_col = !move ? 1.f : !(seen_mask >> col & 1) ? 0.f : fast_exp2(-rise);
+          const float a_col = !move ? 1.f : !(seen_mask >> col & 1) ? 0.f : fast_exp2(-d_col);
           m_col += d_col;
           seen_mask |= __ballot_sync(0xffffffffu, seen) & 0xffffu;
           settled = seen_mask == 0xffffu;
