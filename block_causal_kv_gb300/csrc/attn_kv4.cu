@@ -20,8 +20,10 @@
 // Types. Stored values are exact in fp16, so cached tiles multiply in fp16: Q is
 // scaled per row by a power of two so that its largest element is in [2^14, 2^15)
 // (8 significant bits stay exact down to 2^-28 of it), P is rounded to fp16 (2^-11).
-// Window tiles keep bf16 K, V and Q and round P to bf16 (2^-8), as the bf16 cache's
-// kernel does. Sums, references and both accumulators are float.
+// Window tiles keep bf16 K, V and Q; fp16 could not hold every V. P is then a pair of
+// bf16, its value rounded and what that left (2^-16 together), each multiplied with V^T:
+// one bf16 (2^-8) would be the largest error of a short context's output beside the
+// output's own rounding. Sums, references and both accumulators are float.
 //
 // Work. A row tile holds up to NT = 64 of the group * n query rows of a (sequence, KV
 // head): row r = query r / group, head r % group. Its key tiles (128 cached tokens each,
@@ -103,11 +105,13 @@ struct Cfg {
   // TMEM columns: two S buffers, O, then the K and V^T operands (two halves a column)
   static constexpr uint32_t kTmS = 0, kTmO = 2 * NT, kTmK = 3 * NT, kTmV = kTmK + kBuf * (D / 2);
   static_assert(kTmV + kBuf * (kKeys / 2) <= 512, "TMEM columns");
-  // shared memory: Q in fp16 and in bf16, two P buffers, the ring, the small arrays
+  // shared memory: Q in fp16 and in bf16, two P buffers, one for the second half of a window
+  // tile's P, the ring, the small arrays
   static constexpr int kQBytes = NT * D * 2;
   static constexpr int kPBytes = kKeys * NT * 2;
   static constexpr int kStage = kKeys * D * 9 / 8;
-  static constexpr int kQ16 = 0, kQbf = kQBytes, kP = 2 * kQBytes, kRing = kP + 2 * kPBytes;
+  static constexpr int kQ16 = 0, kQbf = kQBytes, kP = 2 * kQBytes, kPlo = kP + 2 * kPBytes,
+                       kRing = kPlo + kPBytes;
   static constexpr int kMisc = kRing + kStages * kStage;
   static constexpr int kPSbo = 1024;                  // bytes between 8-key groups of P
 };
@@ -891,13 +895,21 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
                    wait_phase(smem_u32(&ms->p_full[v & 1]), (v >> 1) & 1, abort_flag, a);
               if (rare(!ok)) break;
               tc_fence_after();
-              const uint32_t id = idesc(t > s.Tc, ncols, 1);
-              const uint64_t pd = smem_desc_advance(p_desc, (v & 1) * C::kPBytes);
+              const bool win = t > s.Tc;
+              const uint32_t id = idesc(win, ncols, 1);
+              uint64_t pd = smem_desc_advance(p_desc, (v & 1) * C::kPBytes);
               const uint32_t va = tmem + C::kTmV + (v & 1) * (kKeys / 2);
+              // (a window tile's P is a pair: the same products again for its second halves)
+#pragma unroll 1
+              for (bool again = false;; again = true) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8, smem_desc_advance(pd, k * 2 * C::kPSbo),
-                                 id, t > s.t0 + 1 || k > 0);
+                for (int k = 0; k < kKeys / 16; ++k)
+                  umma_bf16_tmem_a(tmem + C::kTmO, va + k * 8,
+                                   smem_desc_advance(pd, k * 2 * C::kPSbo), id,
+                                   again || t > s.t0 + 1 || k > 0);
+                if (!win || again) break;
+                pd = smem_desc_advance(p_desc, C::kPlo - C::kP);
+              }
               umma_commit(smem_u32(&ms->pv_done[v & 1]));
               if (t == t_end) break;
             }
@@ -1107,8 +1119,25 @@ __global__ void __launch_bounds__((Cfg<D>::kThreads), 1) attn_kv4_kernel(const A
         for (int j = 0; j < 16; j += 2) add2(l[j], l[j + 1], l[j], l[j + 1], p[j], p[j + 1]);
         uint32_t h[8];
         if (win) {
+          const uint32_t lo = sb + C::kPlo + row * 128;
+          // (the one buffer of second halves: the window tile before must be done with it)
+          if (rare(t > max(t_first, Tc))) {
+            ok = wait_phase(smem_u32(&ms->pv_done[sbuf ^ 1]), ((u - 1) >> 1) & 1, abort_flag, a);
+            ok = named_sync_and(bar, 128, ok);
+            if (rare(!ok)) break;
+          }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = pack_bf16x2(p[2 * j] * win_unit, p[2 * j + 1] * win_unit);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t r[4];
+#pragma unroll
+            for (int j = 4 * i; j < 4 * i + 4; ++j) {
+              const float x0 = p[2 * j] * win_unit, x1 = p[2 * j + 1] * win_unit;
+              h[j] = pack_bf16x2(x0, x1);
+              r[j - 4 * i] = pack_bf16x2(x0 - __uint_as_float(h[j] << 16),
+                                         x1 - __uint_as_float(h[j] & 0xffff0000u));
+            }
+            sts128(lo + (((2 * wg + i) ^ (row & 7)) << 4), make_uint4(r[0], r[1], r[2], r[3]));
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[j] = pack_half2(p[2 * j], p[2 * j + 1]);

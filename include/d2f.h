@@ -602,12 +602,16 @@ int d2f_block_attn_kv4_workspace_size(int batch, int total_q, int max_q_per_seq,
  *
  * Arguments as d2f_block_attn, with kv_pool, k_exp and v_exp in place of k_pool and
  * v_pool. The result is the attention over the stored values (code * scale * 2^e).
- * D2F_BF16 runs on tensor cores, D2F_F32 on CUDA cores. A cached page whose id is
- * out of range is left out of the softmax (err_word = D2F_ERR_BAD_INDEX). A key
- * that a row does not see never reaches it, not even with infinite or NaN K or V;
- * slots of a page past ctx_len may hold anything. ctx_len need not be a multiple of
- * block_size. The workspace is the caller's, zeroed once (and again after a device
- * error); calls of any sizes and both dtypes may use it in turn.
+ * D2F_BF16 runs on tensor cores, D2F_F32 on CUDA cores. Scores, sums and products are
+ * float. On tensor cores the weights of the product with V are rounded: a cached key's
+ * to fp16 (2^-11 of itself; one below 2^-31 of its row's largest may be lost, so N
+ * cached tokens lose N 2^-31 of the sum at most), a window key's to a pair of bf16
+ * (2^-16); window values of 2^(100 + v_exp) or more may overflow that product.
+ * A cached page whose id is out of range is left out of the softmax (err_word =
+ * D2F_ERR_BAD_INDEX). A key that a row does not see never reaches it, not even with
+ * infinite or NaN K or V; slots of a page past ctx_len may hold anything. ctx_len need
+ * not be a multiple of block_size. The workspace is the caller's, zeroed once (and again
+ * after a device error); calls of any sizes and both dtypes may use it in turn.
  */
 int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, const void *kv_pool,
                        const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,

@@ -21,7 +21,8 @@ def check(p, out, lse):
     Score: a float32 sum of D exact products in any order, each addition may truncate (2^-23),
     scaled once. A weight errs by twice that (numerator and normaliser), by 2^-20 of the
     exponential, and by the sums over the keys: 16 keys a step of the matrix product (truncating),
-    128 a step of the normaliser. Cached weights round to fp16, window weights to bf16. A cached weight that fp16 cannot hold errs by half its smallest number, 2^-25, where
+    128 a step of the normaliser. Cached weights round to fp16, window weights to a pair of bf16
+    (2^-16). A cached weight that fp16 cannot hold errs by half its smallest number, 2^-25, where
     the largest weight is at least 2^6. The output rounds once."""
     o, l, ac, aw, sabs = ref.attention(p["q"], p["k_win"], p["v_win"], p["kv"], p["vv"],
                                        p["table"], p["ctx"], p["q_start"], p["B"], p["scale"])
@@ -29,7 +30,7 @@ def check(p, out, lse):
     keys = max(p["ctx"]) + int(np.diff(p["q_start"]).max())
     ds = (p["D"] + 4) * 2.0 ** -23 * sabs
     w = 2 * ds + 2.0 ** -20 + (keys / 16 + 64) * 2.0 ** -23
-    err = w[..., None] * (ac + aw) + 2.0 ** -11 * ac + 2.0 ** -8 * aw
+    err = w[..., None] * (ac + aw) + 2.0 ** -11 * ac + 2.0 ** -16 * aw
     hkv = p["k_win"].shape[1]
     G = p["q"].shape[1] // hkv
     for b, c in enumerate(p["ctx"]):
@@ -70,6 +71,31 @@ def test_many_small_weights_beside_a_large_one(top, ctx):
     p["k_win"].zero_()
     p["k_win"][..., 0] = top - 100
     p["v_win"].zero_()
+    check(p, *run(p, dev))
+
+
+@pytest.mark.parametrize("blocks,hq,hkv,D,B", [([1], 4, 4, 128, 16), ([3, 1, 2], 4, 2, 64, 16),
+                                               ([40], 1, 1, 128, 8), ([9, 17], 2, 1, 64, 32),
+                                               ([12], 7, 1, 128, 32)])
+@pytest.mark.parametrize("v_exp", [0, -3, 2])
+def test_window_weights(blocks, hq, hkv, D, B, v_exp):
+    """No cached tokens: windows of one and of several key tiles."""
+    dev = device()
+    p = problem([0] * len(blocks), blocks, hq=hq, hkv=hkv, D=D, B=B, dtype=torch.bfloat16,
+                seed=sum(blocks), v_exp=v_exp, v_scale=2.0 ** v_exp)
+    check(p, *run(p, dev))
+
+
+@pytest.mark.parametrize("ctx,blocks,hq,hkv,D,B", [
+    ([0, 1, 15, 16, 127, 128, 129, 300], [1, 2, 3, 1, 4, 2, 1, 3], 4, 4, 128, 16),
+    ([2500], [1], 2, 2, 128, 16), ([4001, 17], [2, 4], 5, 1, 64, 32),
+    ([200, 640], [40, 18], 1, 1, 128, 8), ([900], [9], 7, 1, 64, 16)])
+@pytest.mark.parametrize("k_scale", [1.0, 6.0])
+def test_cached_and_window_weights(ctx, blocks, hq, hkv, D, B, k_scale):
+    """Flat scores, and scores so far apart that the references move."""
+    dev = device()
+    p = problem(ctx, blocks, hq=hq, hkv=hkv, D=D, B=B, dtype=torch.bfloat16, seed=len(ctx) + D,
+                k_scale=k_scale, k_exp=1, v_exp=-2, v_scale=0.25)
     check(p, *run(p, dev))
 
 
