@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const int nn = a.num_new[b], c = a.ctx_len[b];
-      if (nn < 0 || c < 0 || c % B != 0) {
+      if (nn < 0 || c < 0 || (nn > 0 && c % B != 0)) {
         bad = true;
         continue;
       }

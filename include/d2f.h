@@ -631,8 +631,9 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
  * uses. It lays a batch's prompts out before their K/V exist, so a request enters
  * the cache without a host readback.
  *
- * Request b brings num_new[b] >= 0 tokens behind its ctx_len[b] cached ones (a
- * multiple of block_size: pages hold whole blocks). The tokens of all requests are
+ * Request b brings num_new[b] >= 0 tokens behind its ctx_len[b] cached ones. With
+ * new tokens that is a multiple of block_size (pages are written whole); a request
+ * without any keeps its context, of any length, and needs no page. The tokens of all requests are
  * packed rows: those of request b are row_start[b] .. row_start[b+1] - 1. Request b
  * needs ceil(num_new[b] / block_size) pages. Requests are admitted in order while
  * the pages of all so far fit both *free_count and max_append (those behind the
@@ -662,8 +663,8 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
  *
  * Errors in err_word: D2F_ERR_NO_PAGE when a request was refused (the others are
  * laid out); D2F_ERR_INVALID_ARG when nothing but n_append was written: a negative num_new,
- * ctx_len or *free_count, a ctx_len that is no multiple of block_size, more packed
- * rows than capacity. Page ids of the free list are taken as they are.
+ * ctx_len or *free_count, new tokens behind a ctx_len that is no multiple of
+ * block_size, more packed rows than capacity. Page ids of the free list are taken as they are.
  * D2F_ERR_UNSUPPORTED for batch > 16384.
  */
 int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
