@@ -1032,12 +1032,14 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
 // ---------------------------------------------------------------------------
 // Page map
 // ---------------------------------------------------------------------------
-int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
-                 const int32_t *num_new, const int32_t *ctx_len, const int32_t *free_pages,
-                 const int32_t *free_count, int32_t *page_table, int32_t *ctx_len_out,
-                 int32_t *free_count_out, int32_t *row_start, uint8_t *admitted,
-                 int64_t *slot_map, int32_t *app_src, int32_t *app_dst, int32_t *app_rows,
-                 int32_t *n_append, int32_t *err_word, void *stream) {
+int d2f_page_map_flags(int batch, int block_size, int max_pages_per_seq, int capacity,
+                       int max_append, const int32_t *num_new, const int32_t *ctx_len,
+                       const int32_t *free_pages, const int32_t *free_count, int32_t *page_table,
+                       int32_t *ctx_len_out, int32_t *free_count_out, int32_t *row_start,
+                       uint8_t *admitted, int64_t *slot_map, int32_t *app_src, int32_t *app_dst,
+                       int32_t *app_rows, int32_t *n_append, unsigned flags, int32_t *err_word,
+                       void *stream) {
+  if (flags & ~D2F_PAGE_MAP_FRESH) return fail(D2F_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
   if (batch < 0 || block_size < 1 || max_pages_per_seq < 0 || capacity < 0 || max_append < 0)
     return fail(D2F_ERR_INVALID_ARG, "size out of range");
   if (batch > kPageMapMaxBatch)
@@ -1068,9 +1070,22 @@ int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity,
   a.app_rows = app_rows;
   a.n_append = n_append;
   a.err = err_word;
+  a.fresh = (flags & D2F_PAGE_MAP_FRESH) ? 1 : 0;
   const cudaError_t e = launch_page_map(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "page map launch");
   return D2F_OK;
+}
+
+int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
+                 const int32_t *num_new, const int32_t *ctx_len, const int32_t *free_pages,
+                 const int32_t *free_count, int32_t *page_table, int32_t *ctx_len_out,
+                 int32_t *free_count_out, int32_t *row_start, uint8_t *admitted,
+                 int64_t *slot_map, int32_t *app_src, int32_t *app_dst, int32_t *app_rows,
+                 int32_t *n_append, int32_t *err_word, void *stream) {
+  return d2f_page_map_flags(batch, block_size, max_pages_per_seq, capacity, max_append, num_new,
+                            ctx_len, free_pages, free_count, page_table, ctx_len_out,
+                            free_count_out, row_start, admitted, slot_map, app_src, app_dst,
+                            app_rows, n_append, 0, err_word, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -146,6 +146,7 @@ struct PageMapArgs {
   int64_t *slot;
   int32_t *app_src, *app_dst, *app_rows, *n_append;
   int32_t *err;
+  int fresh;  // D2F_PAGE_MAP_FRESH
 };
 
 struct Kv4AppendArgs {

@@ -79,11 +79,9 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
   const int tid = threadIdx.x, B = a.block_size, batch = a.batch;
   if (PHASE == kPlan) grid_launch_dependents();  // (the fill waits for this grid's end)
   grid_dependency_wait();
-  // a fill behind a plan that refused its inputs does nothing
-  if (PHASE == kFill && *a.n_append < 0) return;
   const int per = (batch + kThreads - 1) / kThreads;  // consecutive requests of a thread
   const int b0 = min(tid * per, batch), b1 = min(b0 + per, batch);
-  int n_pages, n_rows, free0;
+  int n_pages = 0, n_rows = 0, free0 = 0;  // (0: an inconsistent state, empty maps)
 
   if (PHASE & kPlan) {
     free0 = *a.free_count;
@@ -105,20 +103,26 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     if (bad) bad_s = 1;
     longlong2 total;
     longlong2 at = block_scan(sum, warp_sum, total);
-    if (bad_s || total.x > a.capacity) {
-      // an inconsistent state: nothing is written, but for a list length that stops the
-      // fill, and an append that reads it
+    const bool refused = bad_s || total.x > a.capacity;  // an inconsistent state
+    if (refused) {
+      for (int b = b0; b < b1; ++b) {
+        a.row_start[b] = 0;
+        a.admitted[b] = 0;
+        if (a.fresh) a.ctx_out[b] = a.ctx_len[b];
+      }
       if (tid == 0) {
         set_err(a.err, D2F_ERR_INVALID_ARG);
+        a.row_start[batch] = 0;
         *a.n_append = -1;
+        if (a.fresh) *a.free_out = free0;
       }
-      return;
+    } else {
+      n_rows = (int)total.x;
     }
-    n_rows = (int)total.x;
     const long long most = min(free0, a.max_append);
     // requests are admitted while the running sum of pages fits
     long long mine = 0, given = 0;
-    for (int b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1 && !refused; ++b) {
       const int nn = a.num_new[b], c = a.ctx_len[b];
       const long long need = ((long long)nn + B - 1) / B;
       const bool fits = c / B + need <= a.max_pages_per_seq && (long long)c + nn <= 0x7fffffffLL;
@@ -138,12 +142,12 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
     }
     block_scan(make_longlong2(given, 0), warp_sum, total);
     n_pages = (int)total.x;
-    if (tid == 0) {
+    if (tid == 0 && !refused) {
       a.row_start[batch] = n_rows;
       *a.n_append = n_pages;
       *a.free_out = free0 - n_pages;
     }
-  } else {
+  } else if (*a.n_append >= 0) {
     // the plan's results: admission, starts and the context after it
     longlong2 sum = make_longlong2(0, 0);
     for (int b = b0; b < b1; ++b)

@@ -45,12 +45,15 @@ EXPORTS = ("d2f_version", "d2f_status_string", "d2f_last_error_string",
            "d2f_kv_append_dev", "d2f_block_attn_append_dev", "d2f_window_step",
            "d2f_kv4_page_bytes", "d2f_kv4_append", "d2f_kv4_read",
            "d2f_block_attn_kv4_workspace_size", "d2f_block_attn_kv4", "d2f_page_map",
+           "d2f_page_map_flags",
            "d2f_token_logprobs_workspace_size", "d2f_token_logprobs")
 
 # attention parts of block_attn(part=...) (include/d2f.h D2F_ATTN_*)
 ATTN_ALL, ATTN_CACHED, ATTN_WINDOW = 0, 1, 2
 # d2f_block_attn_flags: the cache and window layout are final before the preceding kernel
 CACHE_READY = 1
+# d2f_page_map_flags: ctx_len_out / free_count_out hold nothing yet
+PAGE_MAP_FRESH = 1
 # confidence metrics of commit(metric=...) (include/d2f.h D2F_CONF_*)
 CONF_PMAX, CONF_NEG_ENTROPY, CONF_MARGIN, CONF_LOGIT_GAP = 0, 1, 2, 3
 
@@ -130,6 +133,8 @@ def load(path=LIB_PATH):
                                        [ctypes.c_float, _P, _SZ, _P, _P])
     lib.d2f_page_map.restype = _I
     lib.d2f_page_map.argtypes = [_I] * 5 + [_P] * 16
+    lib.d2f_page_map_flags.restype = _I
+    lib.d2f_page_map_flags.argtypes = [_I] * 5 + [_P] * 14 + [ctypes.c_uint, _P, _P]
     lib.d2f_token_logprobs_workspace_size.restype = _I
     lib.d2f_token_logprobs_workspace_size.argtypes = [_I] * 4 + [ctypes.POINTER(_SZ)]
     lib.d2f_token_logprobs.restype = _I
@@ -614,7 +619,8 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
     """Lay out num_new[b] new tokens of each request behind its ctx_len[b] cached ones, with
     pages off the free list (d2f_page_map). page_table is written in place; ctx_len_out and
     free_count_out are new tensors unless given (ctx_len and free_count themselves update
-    in place).
+    in place). An inconsistent state lays out nothing (n_append -1, admitted 0, slot -1, an
+    empty list) and leaves the contexts and the free count as they were.
 
     Returns a dict: page_table, ctx_len, row_start [batch + 1], admitted uint8 [batch], slot
     int64 [capacity], app_src / app_dst / app_rows [max_append] and n_append [1] (the list
@@ -631,6 +637,9 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
         stream, torch.empty, 2 * batch + 3 + 3 * max_append, dtype=i32,
         device=device).unsafe_split_with_sizes(
             [batch, 1, batch + 1, 1, max_append, max_append, max_append])
+    # a refused state leaves tensors that were given as they are, and the inputs in new ones
+    # (PAGE_MAP_FRESH writes both: one that was given beside a new one takes its input too)
+    flags = 0 if ctx_len_out is not None and free_count_out is not None else PAGE_MAP_FRESH
     if ctx_len_out is None:
         ctx_len_out = ctx_new
     if free_count_out is None:
@@ -642,11 +651,11 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
                   ("free_pages", free_pages, i32, None),
                   ("free_count", free_count, i32, (1,)), ("ctx_len_out", ctx_len_out, i32, (batch,)),
                   ("free_count_out", free_count_out, i32, (1,)), ("err", err, i32, None))
-    _launch(load().d2f_page_map, dev, stream, batch, block_size, max_pages, capacity, max_append,
+    _launch(load().d2f_page_map_flags, dev, stream, batch, block_size, max_pages, capacity, max_append,
             num_new.data_ptr(), ctx_len.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
             page_table.data_ptr(), ctx_len_out.data_ptr(), free_count_out.data_ptr(),
             row_start.data_ptr(), admitted.data_ptr(), slot.data_ptr(), src.data_ptr(),
-            dst.data_ptr(), rows.data_ptr(), n_append.data_ptr(), _ptr(err))
+            dst.data_ptr(), rows.data_ptr(), n_append.data_ptr(), flags, _ptr(err))
     return {"page_table": page_table, "ctx_len": ctx_len_out, "row_start": row_start,
             "admitted": admitted, "slot": slot, "app_src": src, "app_dst": dst,
             "app_rows": rows, "n_append": n_append, "free_count": free_count_out}

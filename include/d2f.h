@@ -662,9 +662,11 @@ int d2f_block_attn_kv4(const void *q, const void *k_win, const void *v_win, cons
  *   capacity            rows of slot_map; the packed rows must not exceed it
  *
  * Errors in err_word: D2F_ERR_NO_PAGE when a request was refused (the others are
- * laid out); D2F_ERR_INVALID_ARG when nothing but n_append was written: a negative num_new,
- * ctx_len or *free_count, new tokens behind a ctx_len that is no multiple of
- * block_size, more packed rows than capacity. Page ids of the free list are taken as they are.
+ * laid out); D2F_ERR_INVALID_ARG for an inconsistent state: a negative num_new, ctx_len
+ * or *free_count, new tokens behind a ctx_len that is no multiple of block_size, more
+ * packed rows than capacity. Then nothing is laid out: page_table, ctx_len_out and
+ * free_count_out are left as they were, row_start and admitted are 0, slot_map is -1, the
+ * list is empty and n_append -1. Page ids of the free list are taken as they are.
  * D2F_ERR_UNSUPPORTED for batch > 16384.
  */
 int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity, int max_append,
@@ -673,6 +675,22 @@ int d2f_page_map(int batch, int block_size, int max_pages_per_seq, int capacity,
                  int32_t *free_count_out, int32_t *row_start, uint8_t *admitted,
                  int64_t *slot_map, int32_t *app_src, int32_t *app_dst, int32_t *app_rows,
                  int32_t *n_append, int32_t *err_word, void *stream);
+
+/*
+ * d2f_page_map_flags -- d2f_page_map with launch flags.
+ *
+ *   flags  0 or D2F_PAGE_MAP_FRESH: ctx_len_out and free_count_out hold nothing yet; an
+ *          inconsistent state writes ctx_len and *free_count to them instead of leaving
+ *          them as they were. Unknown bits give D2F_ERR_INVALID_ARG.
+ */
+#define D2F_PAGE_MAP_FRESH 1u
+int d2f_page_map_flags(int batch, int block_size, int max_pages_per_seq, int capacity,
+                       int max_append, const int32_t *num_new, const int32_t *ctx_len,
+                       const int32_t *free_pages, const int32_t *free_count, int32_t *page_table,
+                       int32_t *ctx_len_out, int32_t *free_count_out, int32_t *row_start,
+                       uint8_t *admitted, int64_t *slot_map, int32_t *app_src, int32_t *app_dst,
+                       int32_t *app_rows, int32_t *n_append, unsigned flags, int32_t *err_word,
+                       void *stream);
 
 /* ------------------------------------------------------------------------- */
 /* Log probabilities of given tokens                                         */
