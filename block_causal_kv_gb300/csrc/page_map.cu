@@ -228,11 +228,16 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapArgs a)
   }
 }
 
+constexpr size_t smem_bytes(int batch) { return (size_t)batch * 3 * sizeof(int); }
+
 template <int PHASE>
 cudaError_t launch_phase(const PageMapArgs &a, unsigned grid, size_t smem, cudaStream_t s) {
   if (smem > 48 * 1024) {
+    // the largest batch's bytes, not this one's: another thread may be about to launch with
+    // more than this call needs
     const cudaError_t e = cudaFuncSetAttribute(
-        page_map_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        page_map_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)smem_bytes(kPageMapMaxBatch));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -251,7 +256,7 @@ cudaError_t launch_phase(const PageMapArgs &a, unsigned grid, size_t smem, cudaS
 }  // namespace
 
 cudaError_t launch_page_map(const PageMapArgs &a, cudaStream_t s) {
-  const size_t smem = (size_t)a.batch * 3 * sizeof(int);
+  const size_t smem = smem_bytes(a.batch);
   // One CTA does it all up to some ten thousand rows; beyond, a second launch fills the
   // maps on every SM.
   if ((long long)a.capacity + 4LL * a.max_append <= kOneCtaRows)
