@@ -36,6 +36,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+// Logits further below the maximum than this count as this far (their weight is 0 in any case):
+// times 2^30 of them it still is a finite float, so that the weight makes the product 0.
+constexpr float kFar = -1e28f;
 
 // ---- ordered keys ------------------------------------------------------------
 // Larger key = larger logit, or the same logit at a lower index. 0 is below every key.
@@ -91,7 +94,7 @@ __device__ __forceinline__ Terms combine(const Terms &x, const Terms &y) {
   const bool first = x.m >= y.m;
   const Terms a = first ? x : y, b = first ? y : x;  // b's maximum becomes a logit like others
   const float bs = b.s + (b.m > -INFINITY ? 1.f : 0.f);
-  const float d = b.m == a.m ? 0.f : fmaxf(b.m - a.m, -1e30f);
+  const float d = b.m == a.m ? 0.f : fmaxf(b.m - a.m, kFar);
   const float w = fast_exp2(d * kLog2e);
   // a part without any finite term has s = 0 and e = 0; NaN sums stay NaN
   return Terms{a.m, fmaf(bs, w, a.s), fmaf(w, fmaf(d, bs, b.e), a.e)};
@@ -209,12 +212,12 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
       for (int j = 0; j < VEC; ++j) vm = fmaxf(vm, x[u][j]);
     if (vm > m) {
       // the old maximum joins the sums, the new one stays out of them
-      const float w = fast_exp2(fmaxf(m - vm, -1e30f) * kLog2e);
+      const float w = fast_exp2(fmaxf(m - vm, kFar) * kLog2e);
       float s = m > -INFINITY ? 1.f : 0.f;
       const float old = s * w;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += acc[j];
-      e = w * fmaf(fmaxf(m - vm, -1e30f), s, e);
+      e = w * fmaf(fmaxf(m - vm, kFar), s, e);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[j] *= w;
       acc[0] += vm == INFINITY ? NAN : old;  // (infinity: the row's sums are NaN)
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float raw = x[u][j] - ref;
-        const float d = raw < -1e30f ? -1e30f : raw;  // keeps NaN
+        const float d = raw < kFar ? kFar : raw;  // keeps NaN
         const float t = fast_exp2(d * kLog2e);
         acc[j] += t;
         e = fmaf(t, d, e);
