@@ -149,3 +149,24 @@ def test_results_stay_the_callers_until_it_is_done(name):
         other = [torch.full(s, 3, dtype=t, device=dev) for s, t in shapes]
     torch.cuda.synchronize()
     assert same(kept, want) and len(other) == len(kept)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_on_a_forked_stream(name):
+    """A captured call on a stream that was forked off the capturing one."""
+    dev = device()
+    call, _ = make(name, dev)
+    want = expected(call)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(1 if name == "commit" else 3):  # (a commit changes its state)
+        for x in got:
+            x.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(got, want)

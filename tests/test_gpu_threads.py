@@ -48,3 +48,29 @@ def test_page_maps_of_large_batches():
                 assert r["slot"].tolist() == [48, 49, 50] + [-1] * 5 and int(r["n_append"]) == 1
         return run
     together([job(b) for b in (16384, 5000, 9000, 12000)])
+
+
+def test_attention_and_log_probabilities():
+    """Short and long, small and large calls of the two operators with a workspace, one each."""
+    from test_gpu_workspaces import attention_call, logprobs_call, workspace
+    from test_gpu_kv4_attention import problem
+    dev = device()
+    bf, f32 = torch.bfloat16, torch.float32
+    calls = [attention_call(problem(ctx, blocks, hq=h, hkv=h, D=D, B=B, dtype=dt, seed=h), dev)
+             for ctx, blocks, h, D, B, dt in (
+                 ([1900], [1], 4, 128, 16, bf), ([40] * 300, [1] * 300, 1, 128, 16, bf),
+                 ([300, 700], [2, 1], 6, 64, 8, bf), ([500], [1], 4, 128, 16, f32))]
+    calls += [logprobs_call(n, 60000, dt, 5, dev) for n, dt in ((3, bf), (300, f32))]
+    torch.cuda.synchronize()
+
+    def job(call, size):
+        def body():
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ws = workspace(size, dev)
+                first = [x.clone() for x in call(ws)]
+                for _ in range(300):
+                    got = call(ws)
+                torch.cuda.current_stream().synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(first, got))
+        return body
+    together([job(*c) for c in calls])
