@@ -6,6 +6,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "d2f_internal.cuh"
 
 namespace d2f {
@@ -28,9 +30,12 @@ bool pdl_enabled() {
 }
 
 int num_sms_current_device() {
+  static std::atomic<int> known[64];  // (plans ask several times a call)
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -5,6 +5,9 @@ and the current CUDA stream to the C entry point of the same name, and raises
 D2FError on a non-OK status. No computation happens here; there is no CPU
 fallback: if libd2f.so is missing the import fails.
 
+With `stream` a call runs there instead. What it makes itself (results, a workspace) belongs to
+that stream; the caller orders its inputs before the call and its use of the results after it.
+
     from block_causal_kv_gb300 import d2f
     out, lse = d2f.block_attn(q, k_win, v_win, k_pool, v_pool, page_table, ctx_len,
                               q_start, block_size=16, max_q_per_seq=48, max_ctx=1024)
@@ -167,12 +170,14 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _new(stream, make, *args, **kw):
-    """make(*args, **kw): a tensor that a call on `stream` writes. It is made on that stream (its
-    fill, or what used its memory before, is ordered with the call there), and its memory is kept
-    for what the caller's current stream does with it."""
-    if stream is None:
-        return make(*args, **kw)
+def _on(stream, make):
+    """make, for a tensor that a call on `stream` writes (None: the current one). It is made on that
+    stream (its fill, or what used its memory before, is ordered with the call there), and its
+    memory is kept for what the caller's current stream does with it."""
+    return make if stream is None else functools.partial(_make_on, stream, make)
+
+
+def _make_on(stream, make, *args, **kw):
     current = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         t = make(*args, **kw)
@@ -281,16 +286,17 @@ def block_attn(q, k_win, v_win, k_pool, v_pool, page_table, ctx_len, q_start, *,
     dt = _dtype_code(q)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
+    empty = _on(stream, torch.empty)
     if out is None:
-        out = _new(stream, torch.empty_like, q)
+        out = _on(stream, torch.empty_like)(q)
     _dev(out, "out", q.dtype)
     if lse is None and want_lse:
-        lse = _new(stream, torch.empty, (total_q, hq), dtype=torch.float32, device=q.device)
+        lse = empty((total_q, hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _new(stream, attn_workspace, q.device, batch=batch, total_q=total_q,
-                         max_q_per_seq=max_q_per_seq, max_ctx=max_ctx, num_heads_q=hq,
-                         num_heads_kv=hkv, head_dim=d, block_size=block_size, dtype=dt,
-                         num_splits=num_splits)
+        workspace = _on(stream, attn_workspace)(
+            q.device, batch=batch, total_q=total_q, max_q_per_seq=max_q_per_seq, max_ctx=max_ctx,
+            num_heads_q=hq, num_heads_kv=hkv, head_dim=d, block_size=block_size, dtype=dt,
+            num_splits=num_splits)
     args = (_ptr(q), _ptr(k_win), _ptr(v_win), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
             page_table.shape[1] if page_table is not None else 0, _ptr(ctx_len), _ptr(q_start),
             _ptr(out), _ptr(lse), batch, total_q, max_q_per_seq, max_ctx, hq, hkv, d, block_size,
@@ -363,17 +369,18 @@ def commit(logits, tokens, masked, q_start, block_phase, tau, *, block_size, mas
     rows, vocab = logits.shape
     dt = _dtype_code(logits)
     dev = tokens.device
+    empty = _on(stream, torch.empty)
     if want_outputs:
         if conf is None:
-            conf = _new(stream, torch.empty, total_q, dtype=torch.float32, device=dev)
+            conf = empty(total_q, dtype=torch.float32, device=dev)
         if argmax is None:
-            argmax = _new(stream, torch.empty, total_q, dtype=torch.int32, device=dev)
+            argmax = empty(total_q, dtype=torch.int32, device=dev)
         if block_remaining is None:
-            block_remaining = _new(stream, torch.empty, max(total_q // block_size, 1),
-                                   dtype=torch.int32, device=dev)
+            block_remaining = empty(max(total_q // block_size, 1), dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = _new(stream, commit_workspace, dev, total_q=total_q, vocab=vocab,
-                         block_size=block_size, dtype=dt, num_splits=num_splits)
+        workspace = _on(stream, commit_workspace)(dev, total_q=total_q, vocab=vocab,
+                                                  block_size=block_size, dtype=dt,
+                                                  num_splits=num_splits)
     _dev(early_gap, "early_gap", torch.float32)
     _dev(stopped, "stopped", torch.uint8)
     if metric == CONF_PMAX and early_gap is None:
@@ -542,10 +549,11 @@ def kv4_read(pool, slot, *, head_dim, block_size, dtype=torch.bfloat16, k_exp=0,
     hkv = pool_shape[1]
     n = slot.shape[0]
     shape = (n, hkv, head_dim)
+    empty = _on(stream, torch.empty)
     if k is None:
-        k = _new(stream, torch.empty, shape, dtype=dtype, device=pool.device)
+        k = empty(shape, dtype=dtype, device=pool.device)
     if v is None:
-        v = _new(stream, torch.empty, shape, dtype=dtype, device=pool.device)
+        v = empty(shape, dtype=dtype, device=pool.device)
     dev = _device(("pool", pool, torch.uint8, pool_shape), ("slot", slot, torch.int64, (n,)),
                   ("k", k, dtype, shape), ("v", v, dtype, shape),
                   ("err", err, torch.int32, None))
@@ -585,14 +593,15 @@ def block_attn_kv4(q, k_win, v_win, pool, page_table, ctx_len, q_start, *, block
     dt = _dtype_code(q)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
+    empty = _on(stream, torch.empty)
     if out is None:
-        out = _new(stream, torch.empty_like, q)
+        out = _on(stream, torch.empty_like)(q)
     if lse is None and want_lse:
-        lse = _new(stream, torch.empty, (total_q, hq), dtype=torch.float32, device=q.device)
+        lse = empty((total_q, hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _new(stream, attn_kv4_workspace, q.device, batch=batch, total_q=total_q,
-                         max_q_per_seq=max_q_per_seq, max_ctx=max_ctx, num_heads_q=hq,
-                         num_heads_kv=hkv, head_dim=d, block_size=block_size, dtype=dt)
+        workspace = _on(stream, attn_kv4_workspace)(
+            q.device, batch=batch, total_q=total_q, max_q_per_seq=max_q_per_seq, max_ctx=max_ctx,
+            num_heads_q=hq, num_heads_kv=hkv, head_dim=d, block_size=block_size, dtype=dt)
     qd, i32 = q.dtype, torch.int32
     win = (total_q, hkv, d)
     dev = _device(("q", q, qd, q.shape), ("k_win", k_win, qd, win), ("v_win", v_win, qd, win),
@@ -631,11 +640,11 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
     if capacity < 0 or max_append < 0:
         raise ValueError("capacity and max_append must not be negative")
     i32 = torch.int32
+    empty = _on(stream, torch.empty)
     # the int32 results, one allocation (no gradients here, so the split without view
     # tracking does: 8 us for the seven against 13 with it and 10 for seven allocations)
-    ctx_new, free_new, row_start, n_append, src, dst, rows = _new(
-        stream, torch.empty, 2 * batch + 3 + 3 * max_append, dtype=i32,
-        device=device).unsafe_split_with_sizes(
+    ctx_new, free_new, row_start, n_append, src, dst, rows = empty(
+        2 * batch + 3 + 3 * max_append, dtype=i32, device=device).unsafe_split_with_sizes(
             [batch, 1, batch + 1, 1, max_append, max_append, max_append])
     # a refused state leaves tensors that were given as they are, and the inputs in new ones
     # (PAGE_MAP_FRESH writes both: one that was given beside a new one takes its input too)
@@ -644,8 +653,8 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
         ctx_len_out = ctx_new
     if free_count_out is None:
         free_count_out = free_new
-    admitted = _new(stream, torch.empty, batch, dtype=torch.uint8, device=device)
-    slot = _new(stream, torch.empty, capacity, dtype=torch.int64, device=device)
+    admitted = empty(batch, dtype=torch.uint8, device=device)
+    slot = empty(capacity, dtype=torch.int64, device=device)
     dev = _device(("num_new", num_new, i32, (batch,)), ("ctx_len", ctx_len, i32, (batch,)),
                   ("page_table", page_table, i32, (batch, max_pages)),
                   ("free_pages", free_pages, i32, None),
@@ -695,17 +704,18 @@ def token_logprobs(logits, tokens, *, logit_row=None, top_k=0, want_entropy=True
     device, f32, i32 = logits.device, torch.float32, torch.int32
     if tokens.device != device:
         raise ValueError("tokens is on %s, logits on %s" % (tokens.device, device))
+    empty = _on(stream, torch.empty)
     if logprob is None:
-        logprob = _new(stream, torch.empty, n, dtype=f32, device=device)
+        logprob = empty(n, dtype=f32, device=device)
     if entropy is None and want_entropy:
-        entropy = _new(stream, torch.empty, n, dtype=f32, device=device)
+        entropy = empty(n, dtype=f32, device=device)
     if top_id is None:
-        top_id = _new(stream, torch.empty, (n, top_k), dtype=i32, device=device)
+        top_id = empty((n, top_k), dtype=i32, device=device)
     if top_logprob is None:
-        top_logprob = _new(stream, torch.empty, (n, top_k), dtype=f32, device=device)
+        top_logprob = empty((n, top_k), dtype=f32, device=device)
     if workspace is None:
-        workspace = _new(stream, logprobs_workspace, device, n=n, vocab=vocab, top_k=top_k,
-                         dtype=dt)
+        workspace = _on(stream, logprobs_workspace)(device, n=n, vocab=vocab, top_k=top_k,
+                                                    dtype=dt)
     stride = logits.stride(0) if rows > 1 else max(logits.stride(0), vocab)
     dev = _device(("tokens", tokens, i32, (n,)), ("logit_row", logit_row, i32, (n,)),
                   ("logprob", logprob, f32, (n,)), ("entropy", entropy, f32, (n,)),
