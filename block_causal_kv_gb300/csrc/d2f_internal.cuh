@@ -64,8 +64,8 @@ struct AttnArgs {
   const void *prev_out;    // part 2: a kept cached part to compose with ([total_q][Hq][D], as out)
   const float *prev_lse;   // ... its natural-log normaliser [total_q][Hq]; NULL: no composition
   long long wait_cycles; // tensor-core path: budget of each wait on another role's work
-  int wait_polls;        // 4-bit cache: polls of such a wait before it looks at the clock
                          // (kWaitCycles; less only to test the give-up path)
+  int wait_polls;        // 4-bit cache: polls of such a wait before it looks at the clock
   int cache_ready;        // D2F_ATTN_CACHE_READY: producers may load cached tiles before
                          // the dependency wait
   int sk;                // tensor-core path: stream-K form (see attn_tc.cu), else 0
