@@ -46,23 +46,27 @@
 //            has to move. With 16 columns a thread stays within 72 registers, which lets
 //            16 warps run side by side (32 columns a thread: 8 warps, and spills).
 //
-// Measured (B = 16, D = 128, 32 heads, CUDA graph, L2 flushed): 4 sequences of 32,768
-// cached tokens and 64 window rows 249 us, 2.5 TB/s of 4-bit cache, against 329 us of the
-// bf16 cache's kernel on the same lengths, which reads 3.6 times the bytes; 16 sequences
-// of 251 to 4096 tokens 105 us; one of 1024 tokens 17 us. Time is some 25 us + 1.0 us (about
-// 1900 cycles) per key tile of a CTA. Of the 25 us, 4 are the start (sequence metadata, work
-// line, first page ids), 1 the queries, 2 the first tile, 2 the window tile, 2 the part and
-// its arrival, 3 the composition: straight code that runs once, much of it instruction
-// fetches. A tile is bound by the hand-overs between its roles, each of which
-// takes 300 to 1000 cycles: when it took 259 us on the first shape, it still needed 225
-// with all conversions and exponentials taken out (without K's conversion 244, V's 248,
-// the exponentials 253). The tensor pipe is active 23 % of the cycles, the ALU, which
-// converts the codes, 54 %, the issue slots 71 %, DRAM 31 %. What shortened the chain: one
-// issuer whose order stands for two waits (272 -> 259), V^T on two warpgroups (285 ->
-// 272), polling warps on different schedulers (259 -> 249), small code (the hot loops of
-// all roles share the instruction cache: V^T's loop unrolled by two costs 10 %). What did
-// not: a deeper ring, a third K buffer, a K chunk in a V^T warpgroup, polls that sleep,
-// polls by every warp.
+// Measured (B = 16, D = 128, in a CUDA graph, L2 flushed; in brackets the bf16 cache's
+// kernel on the same lengths, which reads 3.6 times the bytes). 32 heads: 4 sequences of
+// 32,768 cached tokens and 64 window rows 243 us (336), 2.5 TB/s of 4-bit cache; 16
+// sequences of 251 to 4096 tokens 101 us (126); one sequence of 1024, 4096 and 8192
+// tokens and 48 rows 17.6, 23 and 30 us (12, 19 and 31). 28 query heads on 4 KV heads, 8
+// sequences of 8192 tokens and 48 rows 105 us (65): each of its six row tiles
+// dequantises the cache again. A CTA takes some 14 us once, 1.0 us (about 1900 cycles) a
+// key tile, and 7 us for each row tile that it begins beside the first. Of the 14 us, 4
+// are the start (sequence metadata, work line, first page ids), 1 the queries, 2 the first
+// tile, 2 the window tile, 2 the part and its arrival, 3 the composition: straight code
+// that runs once, much of it instruction fetches. A tile is bound by the hand-overs between
+// its roles, each of which takes 300 to 1000 cycles: when the longest contexts took 259 us,
+// they still needed 225 with all conversions and exponentials taken out (without K's
+// conversion 244, V's 248, the exponentials 253). The tensor pipe is active 24 % of the
+// cycles, the ALU, which converts the codes, 54 %, the issue slots 71 %, DRAM 32 %. What
+// shortened the chain: one issuer whose order stands for two waits (272 -> 259), V^T on
+// two warpgroups (285 -> 272), polling warps on different schedulers (259 -> 249), small
+// code (the hot loops of all roles share the instruction cache: V^T's loop unrolled by two
+// costs 10 %, the window's second products in a loop of their own 2 %). What did not: a
+// deeper ring, a third K buffer, a K chunk in a V^T warpgroup, polls that sleep, polls by
+// every warp.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -96,7 +100,8 @@ struct Cfg {
   // named barriers: 1 .. kSw a softmax warpgroup each, then all of them, then K, V^T
   static constexpr int kBarSoft = 1, kBarAll = kBarSoft + kSw, kBarK = kBarAll + 1;
   static constexpr int kRegLaunch = 64;               // registers per thread at launch
-  // (80 for the softmax warps and 48 for the others: no spills here, but 2 to 8 % slower)
+  // (68 bytes of spill stores and 92 of loads; 80 for the softmax warps and 48 for the
+  // others: no spills, but 2 to 8 % slower)
   static constexpr int kRegCtl = 40, kRegDq = 56, kRegSoft = 72;
   static_assert(kRegCtl + kDq * kRegDq + kSw * kRegSoft <= (1 + kDq + kSw) * kRegLaunch,
                 "register split within the launch's allocation");

@@ -64,7 +64,10 @@ __device__ __forceinline__ void ld4_kv4(const AttnArgs &a, const uint8_t *tile, 
   }
 }
 
-// KV4: the cached tokens come from a 4-bit pool.
+// KV4: the cached tokens come from a 4-bit pool. Measured (float32, D = 128, 48 window rows, 32
+// heads): one sequence of 1024 and 2048 cached tokens 90 and 158 us, eight of 2048 1.3 ms, 10
+// TFLOP/s. Bound by the CUDA cores' products, the shared-memory loads that feed them and the
+// decoding, which every 16 query rows repeat (V's codes a byte an element).
 template <typename T, int D, bool KV4>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnArgs a) {
   constexpr int DPL = D / 32;

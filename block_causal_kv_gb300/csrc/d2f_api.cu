@@ -1120,7 +1120,8 @@ int plan_logprobs(int n, int vocab, int top_k, int dtype, LogprobsPlan *p) {
   // second look and its list. Measured on GB300 (us, bf16): 48 rows of 126,464, 5
   // alternatives: 6 slices 14.8 (8: 16.1, 12: 16.2, 4: 16.2); 384 rows of 152,064, half
   // of them with a token, 20 alternatives: 3 slices 32.8 (4: 39.6, 2: 41.1); all with a
-  // token: 1 slice 56.8 (3: 57.4, 2: 65.2).
+  // token: 1 slice 56.8 (3: 57.4, 2: 65.2). 1 to 16 rows, 7 or 9 slices each: 11 to 14
+  // whatever their number, the chain of one CTA.
   int splits = (int)min(8LL * sms / max(n, 1), (long long)(vocab / 16384));
   splits = max(1, min(splits, 64));
   const int chunk = cdiv(cdiv(vocab, splits), vec) * vec;

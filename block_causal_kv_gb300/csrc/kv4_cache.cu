@@ -7,7 +7,9 @@
 //
 // Both move bytes once: an append reads 2 D elements a token and head and writes 9/16 of
 // that many bytes, a read the reverse. Measured (16 prompts of 251 to 4096 tokens, 30,000
-// tokens, 32 heads, D = 128, B = 16, bf16): append 121 us and read 107 us, 5.2 and 5.9 TB/s.
+// tokens, 32 heads, D = 128, B = 16, bf16): append 121 us and read 105 us, 5.2 and 6.0 TB/s;
+// float32, twice the elements' bytes: 215 and 187 us, 5.2 and 6.0 TB/s (its append makes the
+// definition's divisions, 17 a group, beside twice the loads).
 // Neither is quite at the memory's rate: the conversions keep the issue slots 70 % and 73 %
 // busy (ALU 63 % and 60 %), and every warp waits for its loads once. A step's 8 blocks of 4
 // heads take 6 us for both, which is launches.

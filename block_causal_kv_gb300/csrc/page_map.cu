@@ -9,8 +9,8 @@
 // Every CTA that fills the maps forms the sums itself (a few thousand additions)
 // and then finds a row's or a page's request by bisection in shared memory.
 //
-// Measured: 16 requests (512 rows at most) 6.6 us, 1024 requests with 2 million rows
-// 18.8 us, of which the 17 MB of the slot map would take 3: two launches, each a chain of
+// Measured: 16 requests (512 rows at most) 7.0 us, 1024 requests with 2 million rows
+// 18.4 us, of which the 17 MB of the slot map would take 3: two launches, each a chain of
 // dependent loads and barriers (7 us for the plan), and some 300 instructions per four
 // rows (bisection, one division a request). Every CTA planning for itself, in one launch,
 // took as long.

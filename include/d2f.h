@@ -602,6 +602,9 @@ int d2f_block_attn_kv4_workspace_size(int batch, int total_q, int max_q_per_seq,
  *
  * Arguments as d2f_block_attn, with kv_pool, k_exp and v_exp in place of k_pool and
  * v_pool. The result is the attention over the stored values (code * scale * 2^e).
+ * The cache takes 0.28 of a bf16 one's memory. The call is the faster one for long
+ * contexts (on GB300, with a KV head per query head, from some 8,000 cached tokens of a
+ * batch on) and the slower one for short contexts and for many query heads a KV head.
  * D2F_BF16 runs on tensor cores, D2F_F32 on CUDA cores. Scores, sums and products are
  * float. On tensor cores the weights of the product with V are rounded: a cached key's
  * to fp16 (2^-11 of itself; one below 2^-31 of its row's largest may be lost, so N
