@@ -660,9 +660,9 @@ def page_map(num_new, ctx_len, page_table, free_pages, free_count, *, block_size
                   ("free_pages", free_pages, i32, None),
                   ("free_count", free_count, i32, (1,)), ("ctx_len_out", ctx_len_out, i32, (batch,)),
                   ("free_count_out", free_count_out, i32, (1,)), ("err", err, i32, None))
-    _launch(load().d2f_page_map_flags, dev, stream, batch, block_size, max_pages, capacity, max_append,
-            num_new.data_ptr(), ctx_len.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-            page_table.data_ptr(), ctx_len_out.data_ptr(), free_count_out.data_ptr(),
+    _launch(load().d2f_page_map_flags, dev, stream, batch, block_size, max_pages, capacity,
+            max_append, num_new.data_ptr(), ctx_len.data_ptr(), free_pages.data_ptr(),
+            free_count.data_ptr(), page_table.data_ptr(), ctx_len_out.data_ptr(), free_count_out.data_ptr(),
             row_start.data_ptr(), admitted.data_ptr(), slot.data_ptr(), src.data_ptr(),
             dst.data_ptr(), rows.data_ptr(), n_append.data_ptr(), flags, _ptr(err))
     return {"page_table": page_table, "ctx_len": ctx_len_out, "row_start": row_start,

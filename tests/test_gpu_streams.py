@@ -170,3 +170,24 @@ def test_captured_on_a_forked_stream(name):
         g.replay()
         torch.cuda.synchronize()
         assert same(got, want)
+
+
+def test_results_without_elements():
+    """No alternatives, no rows, no list: tensors without memory, made on another stream."""
+    dev = device()
+    side = torch.cuda.Stream()
+    x = torch.randn((2, 50), device=dev)
+    tok = torch.tensor([3, 4], dtype=torch.int32, device=dev)
+    zero, none = tok[:0], torch.zeros((0, 3), dtype=torch.int32, device=dev)
+    count = torch.tensor([1], dtype=torch.int32, device=dev)
+    pool = d2f.kv4_pool(dev, num_pages=1, num_heads_kv=1, head_dim=64, block_size=8)
+    torch.cuda.synchronize()
+    r = d2f.token_logprobs(x, tok, top_k=0, stream=side)
+    m = d2f.page_map(zero, zero, none, tok, count, block_size=8, capacity=0, max_append=0, stream=side)
+    k, v = d2f.kv4_read(pool, torch.zeros(0, dtype=torch.int64, device=dev), head_dim=64,
+                        block_size=8, stream=side)
+    torch.cuda.synchronize()
+    want = torch.log_softmax(x.double(), -1)[[0, 1], tok.long()]
+    assert torch.allclose(r["logprob"].double(), want, atol=1e-5) and r["top_id"].shape == (2, 0)
+    assert m["slot"].numel() == 0 and m["row_start"].tolist() == [0] and int(m["free_count"]) == 1
+    assert k.shape == v.shape == (0, 1, 64)
