@@ -770,7 +770,7 @@ int d2f_window_step(int batch, int block_size, int max_blocks, int capacity,
     return fail(D2F_ERR_INVALID_ARG, "tau_add / tau_act must not be NaN");
   if (block_size > 128) return fail(D2F_ERR_UNSUPPORTED, "block_size > 128");
   const size_t smem = d2f::window_smem_bytes(batch, capacity, block_size);
-  if (smem > 227 * 1024)
+  if (smem > (size_t)kWindowMaxSmem)
     return fail(D2F_ERR_UNSUPPORTED, "window state of %zu bytes exceeds one CTA's shared memory",
                 smem);
   if (!q_start || !tokens || !masked || !block_phase || !row_pos || !ctx_len || !next_block ||

@@ -200,6 +200,7 @@ cudaError_t launch_kv4_read(const Kv4ReadArgs &a, int dtype, int D, cudaStream_t
 // path: 0 scalar loads, 1 128-bit loads
 cudaError_t launch_logprobs(const LogprobsArgs &a, int dtype, int path, cudaStream_t s);
 size_t window_smem_bytes(int batch, int capacity, int block_size);
+constexpr int kWindowMaxSmem = 227 * 1024 - 16;  // (16: the kernel's static shared memory)
 cudaError_t launch_attn_simt(const AttnArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s, char *why, size_t why_len);
 int attn_tc_deep_slots(int cs);  // resident CTAs of the 6-stage head_dim-128 variant

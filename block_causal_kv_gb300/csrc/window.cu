@@ -21,6 +21,8 @@
 //      the free list in (sequence, block) order whatever the thread count;
 //   5. write the per-sequence state, the append list and the phases;
 //   6. write the repacked rows from shared memory.
+#include <atomic>
+
 #include "d2f_internal.cuh"
 
 namespace d2f {
@@ -250,16 +252,18 @@ size_t window_smem_bytes(int batch, int capacity, int block_size) {
 
 cudaError_t launch_window(const WindowArgs &a, cudaStream_t stream) {
   const size_t smem = window_smem_bytes(a.batch, a.capacity, a.block_size);
-  // The opt-in above 48 KB is a per-device function attribute: set it when a larger
-  // size is first needed, not on every launch.
-  static int opted[64] = {0};
+  // The opt-in above 48 KB is a per-device function attribute, set when it is first needed:
+  // to the largest state's bytes, not this one's, so that no thread lowers it between
+  // another's setting and its launch.
+  static std::atomic<bool> opted[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (smem > 48 * 1024 && (dev >= 64 || (int)smem > opted[dev])) {
-    e = cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024 && (dev >= 64 || !opted[dev])) {
+    e = cudaFuncSetAttribute(window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kWindowMaxSmem);
     if (e != cudaSuccess) return e;
-    if (dev < 64) opted[dev] = (int)smem;
+    if (dev < 64) opted[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);

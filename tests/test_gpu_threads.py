@@ -1,4 +1,7 @@
 """Calls of different sizes from several threads at once, each on a stream of its own."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -74,3 +77,40 @@ def test_attention_and_log_probabilities():
                 assert all(torch.equal(a, b) for a, b in zip(first, got))
         return body
     together([job(*c) for c in calls])
+
+
+WINDOW_STEPS = """
+import sys, threading, torch
+sys.path.insert(0, %r)
+from block_causal_kv_gb300 import d2f
+d2f.load()
+dev = torch.device("cuda:0")
+caps = [38000, 12000, 20000, 30000, 36000, 15000, 25000, 11000]
+start, failed = threading.Barrier(len(caps)), []
+def job(cap):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            st = d2f.WindowState(dev, batch=1, block_size=1, max_blocks=4, max_pages_per_seq=4,
+                                 num_free=4, mask_id=9, capacity=cap)
+            torch.cuda.current_stream().synchronize()
+            start.wait()
+            for _ in range(20):
+                d2f.window_step(st, tau_add=0.5, tau_act=1.0, use_stopped=False)
+            torch.cuda.current_stream().synchronize()
+    except Exception as e:
+        failed.append(repr(e))
+threads = [threading.Thread(target=job, args=(c,)) for c in caps]
+[t.start() for t in threads]
+[t.join() for t in threads]
+sys.exit("; ".join(failed) if failed else 0)
+"""
+
+
+def test_first_window_steps_of_a_process():
+    """States of 65 to 226 KB, whose first calls of a process meet (in three processes)."""
+    device()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", WINDOW_STEPS % root], capture_output=True,
+                           text=True, timeout=120)
+        assert r.returncode == 0, r.stderr[-500:]
