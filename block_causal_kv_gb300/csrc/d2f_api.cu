@@ -1187,4 +1187,277 @@ int d2f_token_logprobs(const void *logits, int64_t row_stride, int dtype, int vo
   return D2F_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Token rows into the paged cache
+// ---------------------------------------------------------------------------
+int d2f_kv_store(const void *k, const void *v, const int64_t *slot, int n, void *k_pool,
+                 void *v_pool, int num_heads_kv, int head_dim, int block_size, int num_pages,
+                 int dtype, int32_t *err_word, void *stream) {
+  if (dtype != D2F_BF16 && dtype != D2F_F32)
+    return fail(D2F_ERR_INVALID_ARG, "dtype must be D2F_BF16 or D2F_F32");
+  if (n < 0 || num_heads_kv <= 0 || head_dim <= 0 || block_size < 1 || num_pages < 0)
+    return fail(D2F_ERR_INVALID_ARG, "size out of range");
+  const int elt = dtype == D2F_BF16 ? 2 : 4;
+  const long long row = (long long)num_heads_kv * head_dim;
+  if (head_dim > (1 << 20) || row > (1 << 28) || row * n / 512 > 0x7fffffffLL)
+    return fail(D2F_ERR_UNSUPPORTED, "n * num_heads_kv * head_dim is too large");
+  if (n == 0) return D2F_OK;
+  if (!k || !v || !slot || (num_pages > 0 && (!k_pool || !v_pool)))
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+    return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  StoreArgs a{};
+  a.k = k;
+  a.v = v;
+  a.slot = slot;
+  a.n = n;
+  a.num_heads_kv = num_heads_kv;
+  a.block_size = block_size;
+  a.num_pages = num_pages;
+  a.row_bytes = head_dim * elt;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.err = err_word;
+  const cudaError_t e = launch_store(a, a.row_bytes % 16 == 0 ? 16 : elt,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_store launch");
+  return D2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention of prompts
+// ---------------------------------------------------------------------------
+namespace {
+struct PromptPlan {
+  int tile_q, head_chunk, chunks, tiles, splits;
+  size_t off_ml, off_o, bytes;
+};
+
+// Sizes that the attention of prompts and of single tokens share.
+int seq_sizes(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype) {
+  if (batch < 0 || max_ctx < 0)
+    return fail(D2F_ERR_INVALID_ARG, "negative size (batch %d, max_ctx %d)", batch, max_ctx);
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+    return fail(D2F_ERR_INVALID_ARG, "num_heads_q (%d) must be a positive multiple of num_heads_kv (%d)",
+                Hq, Hkv);
+  if (dtype != D2F_BF16 && dtype != D2F_F32)
+    return fail(D2F_ERR_INVALID_ARG, "dtype must be D2F_BF16 or D2F_F32");
+  if (B < 1) return fail(D2F_ERR_INVALID_ARG, "block_size %d out of range", B);
+  if (D != 32 && D != 64 && D != 128)
+    return fail(D2F_ERR_UNSUPPORTED, "head_dim %d: supported are 32, 64 and 128", D);
+  if (B > 256) return fail(D2F_ERR_UNSUPPORTED, "block_size %d > 256", B);
+  if (Hq > 65535 || batch > 65535)
+    return fail(D2F_ERR_UNSUPPORTED, "batch %d and num_heads_q %d must be <= 65535", batch, Hq);
+  return D2F_OK;
+}
+
+int plan_prompt(int batch, int rows, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
+                PromptPlan *p) {
+  const int st = seq_sizes(batch, max_ctx, Hq, Hkv, D, B, dtype);
+  if (st != D2F_OK) return st;
+  if (rows < 0) return fail(D2F_ERR_INVALID_ARG, "rows %d < 0", rows);
+  if (rows > (1 << 30)) return fail(D2F_ERR_UNSUPPORTED, "rows must be <= 2^30");
+  const int G = Hq / Hkv;
+  p->head_chunk = min(G, kPromptSimtRows);
+  p->chunks = cdiv(G, p->head_chunk);
+  p->tile_q = kPromptSimtRows / p->head_chunk;
+  p->tiles = rows / p->tile_q + batch;
+  const long long items = (long long)p->tiles * Hkv * p->chunks;
+  // Few row tiles and many keys: the keys are split, up to one CTA an SM and at least four key
+  // tiles each.
+  const int sms = max(1, num_sms_current_device());
+  const long long t_max = cdiv(max_ctx, 64) + (long long)cdiv(rows, 64);
+  const long long most = items > 0 ? sms / items : 1;
+  p->splits = (int)max(1LL, min(min(most, t_max / 4), (long long)kPromptMaxSplits));
+  if (items * p->splits > 0x7fffffffLL || (long long)rows * Hq / 8 > 0x7ffffff0LL)
+    return fail(D2F_ERR_UNSUPPORTED, "%d rows of %d heads are too many", rows, Hq);
+  const size_t n_hr = (size_t)rows * Hq;
+  p->off_ml = counter_bytes(0);  // (the other entry points' counters stay zero)
+  p->off_o = p->off_ml + align_up(p->splits * n_hr * sizeof(float2));
+  p->bytes = p->splits > 1 ? p->off_o + p->splits * n_hr * D * sizeof(float) : 0;
+  return D2F_OK;
+}
+}  // namespace
+
+int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_heads_q,
+                                   int num_heads_kv, int head_dim, int block_size, int dtype,
+                                   size_t *bytes) {
+  if (!bytes) return fail(D2F_ERR_INVALID_ARG, "bytes is NULL");
+  PromptPlan p{};
+  const int st = plan_prompt(batch, rows, max_ctx, num_heads_q, num_heads_kv, head_dim, block_size,
+                             dtype, &p);
+  if (st != D2F_OK) return st;
+  *bytes = p.bytes;
+  return D2F_OK;
+}
+
+int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *row_start,
+                    const void *k_pool, const void *v_pool, const int32_t *page_table,
+                    int max_pages_per_seq, const int32_t *ctx_len, void *out, float *lse_out,
+                    int batch, int rows, int max_ctx, int num_heads_q, int num_heads_kv,
+                    int head_dim, int block_size, int num_pages, int dtype, int mask_block,
+                    float softmax_scale, void *workspace, size_t workspace_bytes,
+                    int32_t *err_word, void *stream) {
+  PromptPlan p{};
+  int st = plan_prompt(batch, rows, max_ctx, num_heads_q, num_heads_kv, head_dim, block_size, dtype,
+                       &p);
+  if (st != D2F_OK) return st;
+  if (mask_block < 0) return fail(D2F_ERR_INVALID_ARG, "mask_block %d < 0", mask_block);
+  if (!(softmax_scale > 0.f && softmax_scale < 3e38f))
+    return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0 and finite");
+  if (max_pages_per_seq < 0 || num_pages < 0)
+    return fail(D2F_ERR_INVALID_ARG, "max_pages_per_seq / num_pages negative");
+  if ((long long)max_pages_per_seq * block_size > 0x7fffff00LL)  // (token numbers are 32-bit)
+    return fail(D2F_ERR_UNSUPPORTED, "max_pages_per_seq * block_size is too large");
+  if (ctx_len && (long long)max_pages_per_seq * block_size < max_ctx)
+    return fail(D2F_ERR_INVALID_ARG, "max_ctx %d exceeds max_pages_per_seq * block_size", max_ctx);
+  if (!ctx_len && max_ctx > 0)
+    return fail(D2F_ERR_INVALID_ARG, "max_ctx %d without ctx_len", max_ctx);
+  if (batch == 0 || rows == 0) return D2F_OK;
+  if (!q || !k || !v || !row_start || !out)
+    return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (ctx_len && max_pages_per_seq > 0 && (!k_pool || !v_pool || !page_table || num_pages <= 0))
+    return fail(D2F_ERR_INVALID_ARG, "a cached prefix needs k_pool, v_pool, page_table and pages");
+  const void *ptrs[] = {q, k, v, k_pool, v_pool, out};
+  for (const void *x : ptrs)
+    if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
+  PromptArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.row_start = row_start;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.page_table = page_table;
+  a.ctx_len = ctx_len;
+  a.max_pages_per_seq = max_pages_per_seq;
+  a.out = out;
+  a.lse_out = lse_out;
+  a.batch = batch;
+  a.rows = rows;
+  a.num_heads_q = num_heads_q;
+  a.num_heads_kv = num_heads_kv;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_pages = num_pages;
+  a.group = num_heads_q / num_heads_kv;
+  a.mask_block = mask_block == 0 || mask_block > rows ? rows : mask_block;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.tile_q = p.tile_q;
+  a.head_chunk = p.head_chunk;
+  a.chunks = p.chunks;
+  a.num_splits = p.splits;
+  a.tiles = p.tiles;
+  a.wait_cycles = wait_budget();
+  a.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.off_ml);
+  a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
+  a.err = err_word;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_prompt_simt(a, dtype, s);
+  if (e != cudaSuccess) return cuda_fail(e, "CUDA-core prompt attention launch");
+  if (p.splits > 1) {
+    e = launch_prompt_merge(a, dtype, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention composition launch");
+  }
+  return D2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention of one new token a sequence
+// ---------------------------------------------------------------------------
+namespace {
+struct TokenPlan {
+  int head_chunk, chunks, splits;
+  size_t off_partial, bytes;
+};
+
+int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype, TokenPlan *p) {
+  const int st = seq_sizes(batch, max_ctx, Hq, Hkv, D, B, dtype);
+  if (st != D2F_OK) return st;
+  const int sms = max(1, num_sms_current_device());
+  const int G = Hq / Hkv;
+  p->head_chunk = kTokenSimtHeads;
+  p->chunks = cdiv(G, p->head_chunk);
+  const long long pairs = (long long)max(batch, 1) * Hkv * p->chunks;
+  if (pairs > 0x7fffffffLL / 64)
+    return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_q is too large");
+  // Four CTAs an SM, at least 64 keys each; at most 64 parts to compose.
+  p->splits = (int)max(1LL, min(min(4LL * sms / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
+  p->off_partial = counter_bytes(p->splits > 1 ? pairs : 0);
+  const size_t part = (size_t)p->head_chunk * (D * sizeof(float) + sizeof(float2));
+  p->bytes = p->splits > 1 ? p->off_partial + pairs * p->splits * part : 0;
+  return D2F_OK;
+}
+}  // namespace
+
+int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int num_heads_kv,
+                                  int head_dim, int block_size, int dtype, size_t *bytes) {
+  if (!bytes) return fail(D2F_ERR_INVALID_ARG, "bytes is NULL");
+  TokenPlan p{};
+  const int st = plan_token(batch, max_ctx, num_heads_q, num_heads_kv, head_dim, block_size, dtype, &p);
+  if (st != D2F_OK) return st;
+  *bytes = p.bytes;
+  return D2F_OK;
+}
+
+int d2f_token_attn(const void *q, const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                   const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,
+                   void *out, float *lse_out, int batch, int max_ctx, int num_heads_q,
+                   int num_heads_kv, int head_dim, int block_size, int num_pages, int dtype,
+                   float softmax_scale, void *workspace, size_t workspace_bytes,
+                   int32_t *err_word, void *stream) {
+  TokenPlan p{};
+  int st = plan_token(batch, max_ctx, num_heads_q, num_heads_kv, head_dim, block_size, dtype, &p);
+  if (st != D2F_OK) return st;
+  if (!(softmax_scale > 0.f && softmax_scale < 3e38f))
+    return fail(D2F_ERR_INVALID_ARG, "softmax_scale must be > 0 and finite");
+  if (max_pages_per_seq < 0 || num_pages < 0)
+    return fail(D2F_ERR_INVALID_ARG, "max_pages_per_seq / num_pages negative");
+  if ((long long)max_pages_per_seq * block_size > 0x7fffff00LL)  // (token numbers are 32-bit)
+    return fail(D2F_ERR_UNSUPPORTED, "max_pages_per_seq * block_size is too large");
+  if ((long long)max_pages_per_seq * block_size < max_ctx)
+    return fail(D2F_ERR_INVALID_ARG, "max_ctx %d exceeds max_pages_per_seq * block_size", max_ctx);
+  if ((k_new == nullptr) != (v_new == nullptr))
+    return fail(D2F_ERR_INVALID_ARG, "k_new and v_new go together");
+  if (batch == 0) return D2F_OK;
+  if (!q || !ctx_len || !out) return fail(D2F_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (max_pages_per_seq > 0 && (!k_pool || !v_pool || !page_table || num_pages <= 0))
+    return fail(D2F_ERR_INVALID_ARG, "the cache needs k_pool, v_pool, page_table and pages");
+  const void *ptrs[] = {q, k_new, v_new, k_pool, v_pool, out};
+  for (const void *x : ptrs)
+    if (x && !aligned16(x)) return fail(D2F_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != D2F_OK) return st;
+  TokenArgs a{};
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.page_table = page_table;
+  a.ctx_len = ctx_len;
+  a.max_pages_per_seq = max_pages_per_seq;
+  a.out = out;
+  a.lse_out = lse_out;
+  a.batch = batch;
+  a.num_heads_q = num_heads_q;
+  a.num_heads_kv = num_heads_kv;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_pages = num_pages;
+  a.group = num_heads_q / num_heads_kv;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.head_chunk = p.head_chunk;
+  a.chunks = p.chunks;
+  a.num_splits = p.splits;
+  a.counters = static_cast<int32_t *>(workspace);
+  a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_partial);
+  a.err = err_word;
+  const cudaError_t e = launch_token_simt(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "CUDA-core token attention launch");
+  return D2F_OK;
+}
+
 }  // extern "C"

@@ -187,7 +187,68 @@ struct LogprobsArgs {
   int32_t *err;
 };
 
+// Attention of packed prompt rows (prompt_tc.cu, prompt_simt.cu). An item is a row tile (up to
+// tile_q queries of one request) of one KV head, times a chunk of its query heads, times a split
+// of its keys.
+struct PromptArgs {
+  const void *q, *k, *v;       // [rows][heads][head_dim], packed rows
+  const int32_t *row_start;    // [batch + 1]
+  const void *k_pool, *v_pool; // cached prefix; unused without ctx_len
+  const int32_t *page_table, *ctx_len;
+  int max_pages_per_seq;
+  void *out;
+  float *lse_out;
+  int batch, rows, num_heads_q, num_heads_kv, head_dim, block_size, num_pages;
+  int group;                   // num_heads_q / num_heads_kv
+  int mask_block;              // rows i, j of a request: j is seen iff j / mask_block <= i / mask_block
+  float scale_log2;            // softmax_scale * log2(e)
+  int tile_q;                  // queries of a row tile
+  int head_chunk, chunks;      // query heads of an item, chunks of a group
+  int num_splits;              // key splits; more than 1: partials and a second launch
+  int tiles;                   // row tiles: rows / tile_q + batch, some of them empty
+  long long wait_cycles;       // budget of each wait on another role's work
+  float2 *ws_ml;               // [num_splits][rows * Hq] (max in log2 units, sum)
+  float *ws_o;                 // [num_splits][rows * Hq][head_dim] unnormalised
+  int32_t *err;
+};
+constexpr int kPromptSimtRows = 64;  // packed rows (query, head) of a CUDA-core tile
+constexpr int kPromptMaxSplits = 16;
+
+constexpr int kTokenSimtHeads = 4;  // query heads of a CTA, CUDA-core path of the token attention
+// One new token a sequence over the paged cache (token_simt.cu).
+struct TokenArgs {
+  const void *q;               // [batch][Hq][head_dim]
+  const void *k_new, *v_new;   // [batch][Hkv][head_dim], or NULL: no new key
+  void *k_pool, *v_pool;
+  const int32_t *page_table, *ctx_len;
+  int max_pages_per_seq;
+  void *out;
+  float *lse_out;
+  int batch, num_heads_q, num_heads_kv, head_dim, block_size, num_pages;
+  int group;
+  float scale_log2;
+  int head_chunk, chunks;      // query heads of a CTA, chunks of a group
+  int num_splits;              // CTAs sharing the keys of a (sequence, KV head, chunk)
+  int32_t *counters;           // arrivals (zero at rest)
+  float *partial;
+  int32_t *err;
+};
+
+struct StoreArgs {
+  const void *k, *v;           // [n][Hkv][head_dim]
+  const int64_t *slot;         // [n]
+  int n, num_heads_kv, block_size, num_pages;
+  int row_bytes;               // head_dim * element size
+  void *k_pool, *v_pool;
+  int32_t *err;
+};
+
 // Launchers (one per translation unit). Return cudaSuccess or the launch error.
+cudaError_t launch_prompt_simt(const PromptArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_prompt_merge(const PromptArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_token_simt(const TokenArgs &a, int dtype, cudaStream_t s);
+// unit: bytes a thread moves at a time (16, or the element size)
+cudaError_t launch_store(const StoreArgs &a, int unit, cudaStream_t s);
 // path: 0 scalar loads, 1 128-bit loads (see commit.cu)
 cudaError_t launch_commit(const CommitArgs &a, int dtype, int path, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs &a, bool vec_ok, cudaStream_t s);

@@ -1,0 +1,66 @@
+// d2f_kv_store kernel: token rows of K and V to their slots of the paged cache.
+//
+// Source: "D2F: 확산 언어 모델이 KV 캐시를 얻고 자기회귀 모델보다 2.5배 빨라지는
+// 방법", §운영 관점 (the paged cache; a page holds one block).
+//
+// A copy: row r of the source is Hkv pieces of head_dim elements, one after another; each
+// piece goes to its own place, k_pool[page][g][offset]. A thread moves kBatch units of
+// 16 bytes (whole elements where head_dim does not allow that), all loads before the stores.
+#include "d2f_internal.cuh"
+
+namespace d2f {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;
+
+template <typename U>
+__global__ void __launch_bounds__(kThreads) store_kernel(const StoreArgs a) {
+  const uint32_t per_head = a.row_bytes / sizeof(U);
+  const uint32_t per_row = per_head * a.num_heads_kv;
+  const int64_t total = (int64_t)a.n * per_row;
+  const int64_t slots = (int64_t)a.num_pages * a.block_size;
+  const U *src = static_cast<const U *>(blockIdx.y ? a.v : a.k);
+  U *dst = static_cast<U *>(blockIdx.y ? a.v_pool : a.k_pool);
+  const int64_t e0 = (int64_t)blockIdx.x * (kThreads * kBatch) + threadIdx.x;
+  U x[kBatch];
+  int64_t to[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int64_t e = e0 + i * kThreads;
+    to[i] = -1;
+    if (e < total) {
+      x[i] = __ldcs(src + e);
+      const int64_t r = e / per_row;
+      const uint32_t c = (uint32_t)(e - r * per_row), g = c / per_head;
+      const int64_t slot = __ldg(a.slot + r);
+      if (slot >= 0 && slot < slots) {
+        const int64_t page = slot / a.block_size, off = slot - page * a.block_size;
+        to[i] = ((page * a.num_heads_kv + g) * a.block_size + off) * per_head + (c - g * per_head);
+      } else if (slot != -1 && c == 0) {
+        set_err(a.err, D2F_ERR_BAD_INDEX);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (to[i] >= 0) dst[to[i]] = x[i];
+}
+
+template <typename U>
+cudaError_t launch_t(const StoreArgs &a, cudaStream_t s) {
+  const int64_t total = (int64_t)a.n * a.num_heads_kv * (a.row_bytes / (int)sizeof(U));
+  const int64_t per = kThreads * kBatch;
+  store_kernel<U><<<dim3((unsigned)((total + per - 1) / per), 2), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_store(const StoreArgs &a, int unit, cudaStream_t s) {
+  if (unit == 16) return launch_t<uint4>(a, s);
+  if (unit == 4) return launch_t<uint32_t>(a, s);
+  return launch_t<uint16_t>(a, s);
+}
+
+}  // namespace d2f

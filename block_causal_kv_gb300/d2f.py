@@ -19,6 +19,10 @@ that stream; the caller orders its inputs before the call and its use of the res
     out, lse = d2f.block_attn_kv4(q, k_win, v_win, pool, page_table, ctx_len, q_start,
                                   block_size=16, max_q_per_seq=48, max_ctx=1024)
     lp = d2f.token_logprobs(logits, res["argmax"], top_k=5)
+    out, lse = d2f.prompt_attn(q, k, v, row_start, mask_block=1)
+    d2f.kv_store(k, v, slot, k_pool, v_pool, block_size=16)
+    out, lse = d2f.token_attn(q, k_pool, v_pool, page_table, ctx_len, k_new=k, v_new=v,
+                              block_size=16, max_ctx=1024)
 """
 import ctypes
 import functools
@@ -49,7 +53,9 @@ EXPORTS = ("d2f_version", "d2f_status_string", "d2f_last_error_string",
            "d2f_kv4_page_bytes", "d2f_kv4_append", "d2f_kv4_read",
            "d2f_block_attn_kv4_workspace_size", "d2f_block_attn_kv4", "d2f_page_map",
            "d2f_page_map_flags",
-           "d2f_token_logprobs_workspace_size", "d2f_token_logprobs")
+           "d2f_token_logprobs_workspace_size", "d2f_token_logprobs", "d2f_kv_store",
+           "d2f_prompt_attn_workspace_size", "d2f_prompt_attn",
+           "d2f_token_attn_workspace_size", "d2f_token_attn")
 
 # attention parts of block_attn(part=...) (include/d2f.h D2F_ATTN_*)
 ATTN_ALL, ATTN_CACHED, ATTN_WINDOW = 0, 1, 2
@@ -143,6 +149,18 @@ def load(path=LIB_PATH):
     lib.d2f_token_logprobs.restype = _I
     lib.d2f_token_logprobs.argtypes = ([_P, ctypes.c_int64, _I, _I, _I, _P, _P, _I, _I] +
                                        [_P] * 4 + [_P, _SZ, _P, _P])
+    lib.d2f_kv_store.restype = _I
+    lib.d2f_kv_store.argtypes = [_P, _P, _P, _I, _P, _P] + [_I] * 5 + [_P, _P]
+    lib.d2f_prompt_attn_workspace_size.restype = _I
+    lib.d2f_prompt_attn_workspace_size.argtypes = [_I] * 8 + [ctypes.POINTER(_SZ)]
+    lib.d2f_prompt_attn.restype = _I
+    lib.d2f_prompt_attn.argtypes = ([_P] * 7 + [_I] + [_P] * 3 + [_I] * 10 +
+                                    [ctypes.c_float, _P, _SZ, _P, _P])
+    lib.d2f_token_attn_workspace_size.restype = _I
+    lib.d2f_token_attn_workspace_size.argtypes = [_I] * 7 + [ctypes.POINTER(_SZ)]
+    lib.d2f_token_attn.restype = _I
+    lib.d2f_token_attn.argtypes = ([_P] * 6 + [_I] + [_P] * 3 + [_I] * 8 +
+                                   [ctypes.c_float, _P, _SZ, _P, _P])
     _lib = lib
     return lib
 
@@ -727,3 +745,147 @@ def token_logprobs(logits, tokens, *, logit_row=None, top_k=0, want_entropy=True
             top_id.data_ptr(), top_logprob.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _ptr(err))
     return {"logprob": logprob, "entropy": entropy, "top_id": top_id, "top_logprob": top_logprob}
+
+
+# ---------------------------------------------------------------------------
+# prompts and single tokens over the bf16 / float cache
+# ---------------------------------------------------------------------------
+def _pools(k_pool, v_pool, dtype, hkv, block_size, d):
+    """The checks of a cache's two pools and its number of pages."""
+    shape = (k_pool.shape[0], hkv, block_size, d)
+    return (("k_pool", k_pool, dtype, shape), ("v_pool", v_pool, dtype, shape)), shape[0]
+
+
+def kv_store(k, v, slot, k_pool, v_pool, *, block_size, err=None, stream=None):
+    """Token rows k, v [n, Hkv, D] into int64 slots (page * block_size + offset; -1: the row is
+    skipped) of the paged cache [pages, Hkv, block_size, D] (d2f_kv_store)."""
+    shape, dt = k.shape, k.dtype
+    n, hkv, d = shape
+    pools, pages = _pools(k_pool, v_pool, dt, hkv, block_size, d)
+    dev = _device(("k", k, dt, shape), ("v", v, dt, shape), ("slot", slot, torch.int64, (n,)),
+                  *pools, ("err", err, torch.int32, None))
+    _launch(load().d2f_kv_store, dev, stream, k.data_ptr(), v.data_ptr(), slot.data_ptr(), n,
+            k_pool.data_ptr(), v_pool.data_ptr(), hkv, d, block_size, pages, _dtype_code(k),
+            _ptr(err))
+
+
+def prompt_attn_workspace_size(batch, rows, max_ctx, num_heads_q, num_heads_kv, head_dim,
+                               block_size, dtype=BF16):
+    lib = load()
+    n = _SZ(0)
+    _check(lib.d2f_prompt_attn_workspace_size(batch, rows, max_ctx, num_heads_q, num_heads_kv,
+                                              head_dim, block_size, dtype, ctypes.byref(n)))
+    return n.value
+
+
+def prompt_attn_workspace(device, **kw):
+    """A zero-filled workspace of the size prompt_attn_workspace_size(**kw) returns."""
+    with torch.cuda.device(device):
+        return torch.zeros(max(prompt_attn_workspace_size(**kw), 1), dtype=torch.uint8,
+                           device=device)
+
+
+def prompt_attn(q, k, v, row_start, *, mask_block=1, k_pool=None, v_pool=None, page_table=None,
+                ctx_len=None, block_size=16, max_ctx=0, softmax_scale=None, out=None, lse=None,
+                want_lse=True, workspace=None, err=None, stream=None):
+    """Attention of packed prompts (one layer): rows row_start[b] .. row_start[b + 1] of q
+    [rows, Hq, D] and k, v [rows, Hkv, D] are request b's; row i sees row j of its request where
+    j // mask_block <= i // mask_block (1: causal, 0: all rows). With ctx_len (and k_pool, v_pool,
+    page_table, block_size, max_ctx) every row also sees its request's ctx_len[b] cached tokens.
+
+    Returns (out [rows, Hq, D] like q, lse [rows, Hq] float32 or None); rows behind the last
+    request are left as they are (unwritten memory where the call makes out and lse)."""
+    rows, hq, d = q.shape
+    hkv = k.shape[1]
+    batch = row_start.shape[0] - 1
+    dt = _dtype_code(q)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    empty = _on(stream, torch.empty)
+    if out is None:
+        out = _on(stream, torch.empty_like)(q)
+    if lse is None and want_lse:
+        lse = empty((rows, hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _on(stream, prompt_attn_workspace)(
+            q.device, batch=batch, rows=rows, max_ctx=max_ctx, num_heads_q=hq, num_heads_kv=hkv,
+            head_dim=d, block_size=block_size, dtype=dt)
+    qd, i32 = q.dtype, torch.int32
+    pages = max_pages = 0
+    checks = ()
+    if ctx_len is not None:
+        if k_pool is None or v_pool is None or page_table is None:
+            raise ValueError("a cached prefix goes with k_pool, v_pool and page_table")
+        max_pages = page_table.shape[-1]
+        checks, pages = _pools(k_pool, v_pool, qd, hkv, block_size, d)
+        checks += (("page_table", page_table, i32, (batch, max_pages)),
+                   ("ctx_len", ctx_len, i32, (batch,)))
+    else:
+        k_pool = v_pool = page_table = None
+    dev = _device(("q", q, qd, q.shape), ("k", k, qd, (rows, hkv, d)), ("v", v, qd, (rows, hkv, d)),
+                  ("row_start", row_start, i32, (batch + 1,)), *checks,
+                  ("out", out, qd, q.shape), ("lse", lse, torch.float32, (rows, hq)),
+                  ("workspace", workspace, workspace.dtype, None), ("err", err, i32, None))
+    _launch(load().d2f_prompt_attn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            row_start.data_ptr(), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), max_pages,
+            _ptr(ctx_len), out.data_ptr(), _ptr(lse), batch, rows, max_ctx, hq, hkv, d, block_size,
+            pages, dt, int(mask_block), float(softmax_scale), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(err))
+    return out, lse
+
+
+def token_attn_workspace_size(batch, max_ctx, num_heads_q, num_heads_kv, head_dim, block_size,
+                              dtype=BF16):
+    lib = load()
+    n = _SZ(0)
+    _check(lib.d2f_token_attn_workspace_size(batch, max_ctx, num_heads_q, num_heads_kv, head_dim,
+                                             block_size, dtype, ctypes.byref(n)))
+    return n.value
+
+
+def token_attn_workspace(device, **kw):
+    """A zero-filled workspace of the size token_attn_workspace_size(**kw) returns."""
+    with torch.cuda.device(device):
+        return torch.zeros(max(token_attn_workspace_size(**kw), 1), dtype=torch.uint8,
+                           device=device)
+
+
+def token_attn(q, k_pool, v_pool, page_table, ctx_len, *, block_size, max_ctx, k_new=None,
+               v_new=None, softmax_scale=None, out=None, lse=None, want_lse=True, workspace=None,
+               err=None, stream=None):
+    """Attention of one new token a sequence, q [batch, Hq, D], over its ctx_len[b] tokens in the
+    paged cache and, with k_new / v_new [batch, Hkv, D], over itself; its K and V are then
+    written to slot ctx_len[b] of its pages (one layer; ctx_len is not changed). A negative
+    ctx_len[b] leaves the sequence out.
+
+    Returns (out [batch, Hq, D] like q, lse [batch, Hq] float32 or None)."""
+    batch, hq, d = q.shape
+    hkv = k_pool.shape[1]
+    max_pages = page_table.shape[-1]
+    dt = _dtype_code(q)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _on(stream, torch.empty_like)(q)
+    if lse is None and want_lse:
+        lse = _on(stream, torch.empty)((batch, hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _on(stream, token_attn_workspace)(
+            q.device, batch=batch, max_ctx=max_ctx, num_heads_q=hq, num_heads_kv=hkv, head_dim=d,
+            block_size=block_size, dtype=dt)
+    qd, i32 = q.dtype, torch.int32
+    pools, pages = _pools(k_pool, v_pool, qd, hkv, block_size, d)
+    new = (batch, hkv, d)
+    dev = _device(("q", q, qd, q.shape), ("k_new", k_new, qd, new), ("v_new", v_new, qd, new),
+                  *pools, ("page_table", page_table, i32, (batch, max_pages)),
+                  ("ctx_len", ctx_len, i32, (batch,)), ("out", out, qd, q.shape),
+                  ("lse", lse, torch.float32, (batch, hq)),
+                  ("workspace", workspace, workspace.dtype, None), ("err", err, i32, None))
+    _launch(load().d2f_token_attn, dev, stream, q.data_ptr(), _ptr(k_new), _ptr(v_new),
+            k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), max_pages,
+            ctx_len.data_ptr(), out.data_ptr(), _ptr(lse), batch, max_ctx, hq, hkv, d, block_size,
+            pages, dt, float(softmax_scale), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _ptr(err))
+    return out, lse

@@ -65,7 +65,9 @@
  *   2^31 (row tiles of up to 64 of the group * max_q_per_seq query rows, key tiles of
  *   128 of the max_pages_per_seq * block_size cached tokens, which stay below 2^31, and
  *   of the window);
- * - page map: batch <= 16384; log probabilities: n <= 65535, vocab <= 2^30, top_k <= 32.
+ * - page map: batch <= 16384; log probabilities: n <= 65535, vocab <= 2^30, top_k <= 32;
+ * - prompt and token attention: batch and num_heads_q <= 65535, head_dim 32, 64 or 128,
+ *   block_size <= 256, rows <= 2^30.
  * The workloads this library is measured on (up to 512 window rows, batch 16,
  * 32 KV heads, 32,768 cached tokens) are far inside all of them.
  */
@@ -734,6 +736,129 @@ int d2f_token_logprobs(const void *logits, int64_t row_stride, int dtype, int vo
                        int top_k, float *logprob, float *entropy, int32_t *top_id,
                        float *top_logprob, void *workspace, size_t workspace_bytes,
                        int32_t *err_word, void *stream);
+
+/* ------------------------------------------------------------------------- */
+/* Prompts and single tokens over the bf16 / float cache                     */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * d2f_kv_store -- token rows into their slots of the paged cache: the prompts that
+ * d2f_page_map laid out, or any other rows ([P1] §운영 관점: the paged cache). The
+ * counterpart of d2f_kv4_append and d2f_kv4_read for a pool of dtype values.
+ *
+ *   k_pool[slot[r] / B][g][slot[r] % B][:] = k[r][g][:], the same for V: a bitwise copy.
+ *
+ *   k, v    device [n][num_heads_kv][head_dim], dtype
+ *   slot    device int64 [n]: page * block_size + offset, or -1: the row is skipped
+ *           (d2f_page_map's slot map). Another slot outside the pool is skipped too, with
+ *           err_word = D2F_ERR_BAD_INDEX. Slots must be distinct.
+ *   k_pool, v_pool  device [num_pages][num_heads_kv][block_size][head_dim], dtype
+ * Any head_dim and block_size. Device buffers are 16-byte aligned.
+ */
+int d2f_kv_store(const void *k, const void *v, const int64_t *slot, int n, void *k_pool,
+                 void *v_pool, int num_heads_kv, int head_dim, int block_size, int num_pages,
+                 int dtype, int32_t *err_word, void *stream);
+
+/* Workspace bytes for d2f_prompt_attn with the same sizes, on the current device. */
+int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_heads_q,
+                                   int num_heads_kv, int head_dim, int block_size, int dtype,
+                                   size_t *bytes);
+
+/*
+ * d2f_prompt_attn -- one layer's attention of a batch's prompts, packed row behind row,
+ * optionally behind cached tokens (a prefix that is in the cache already, an earlier
+ * turn). It computes what the windows of d2f_block_attn later read from the cache.
+ *
+ * Request b brings the rows row_start[b] .. row_start[b+1] - 1 (any number, as d2f_page_map
+ * lays them out) behind its ctx_len[b] cached tokens. Query head h of row i (counted from the
+ * request's first row) attends to
+ *   (a) every cached token t < ctx_len[b], read through the page table, and
+ *   (b) every row j of the same request with j / mask_block <= i / mask_block
+ * ([P1] §블록 단위 인과 어텐션: bidirectional inside a block, causal between blocks). mask_block
+ * 1 is the causal mask of an autoregressive model, 0 lets every row see all rows of its request
+ * (the bidirectional prompt of a masked diffusion model).
+ *   scores = softmax_scale * <q, k>, out = softmax(scores) . v.
+ *
+ *   q           device [rows][num_heads_q][head_dim], dtype
+ *   k, v        device [rows][num_heads_kv][head_dim], dtype
+ *   row_start   device int32 [batch+1], row_start[0] = 0, row_start[batch] <= rows. Rows from
+ *               row_start[batch] on belong to no request: their out and lse are left as they are.
+ *   ctx_len     device int32 [batch], 0 <= ctx_len[b] <= max_pages_per_seq * block_size, the cached
+ *               tokens BEFORE these rows (not d2f_page_map's ctx_len_out), or NULL: none
+ *               (then k_pool, v_pool and page_table are ignored and max_ctx is 0)
+ *   k_pool,
+ *   v_pool      device [num_pages][num_heads_kv][block_size][head_dim], dtype; not written.
+ *               Slots of a page past ctx_len[b] may hold anything.
+ *   page_table  device int32 [batch][max_pages_per_seq]
+ *   out         device [rows][num_heads_q][head_dim], dtype
+ *   lse_out     device float [rows][num_heads_q] natural-log normaliser, or NULL
+ *   max_ctx     host hint used only to split the keys of few rows among CTAs
+ *   block_size  1..256 (the page; ctx_len need not be a multiple of it)
+ *   head_dim    32, 64 or 128
+ * A key that a row does not see never reaches it, not even with infinite or NaN K or V.
+ * Results do not depend on the order in which CTAs run. Device buffers are 16-byte aligned.
+ *
+ * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
+ * are left out of the softmax); D2F_ERR_INVALID_ARG for a row_start that is negative, decreases
+ * or passes rows, or a ctx_len out of range: requests with such lengths are skipped, and
+ * with an inconsistent row_start others may be too. Nothing outside the buffers is touched.
+ * Limits: batch and num_heads_q <= 65535, rows <= 2^30. The workspace needs no zeroing, and may
+ * be any entry point's.
+ */
+int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *row_start,
+                    const void *k_pool, const void *v_pool, const int32_t *page_table,
+                    int max_pages_per_seq, const int32_t *ctx_len, void *out, float *lse_out,
+                    int batch, int rows, int max_ctx, int num_heads_q, int num_heads_kv,
+                    int head_dim, int block_size, int num_pages, int dtype, int mask_block,
+                    float softmax_scale, void *workspace, size_t workspace_bytes,
+                    int32_t *err_word, void *stream);
+
+/* Workspace bytes for d2f_token_attn with the same sizes, on the current device. */
+int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int num_heads_kv,
+                                  int head_dim, int block_size, int dtype, size_t *bytes);
+
+/*
+ * d2f_token_attn -- one layer's attention of one new token a sequence over the paged cache,
+ * and the append of its K and V, in one launch: a step of autoregressive decoding (a window of
+ * one block of one row) over the pages that D2F's windows use.
+ *
+ * Query head h of sequence b attends to its ctx_len[b] cached tokens and, with k_new / v_new, to
+ * the new token itself, whose K and V are written to slot ctx_len[b] of the sequence:
+ * page_table[b][ctx_len[b] / B], offset ctx_len[b] % B. ctx_len is not changed (the caller adds 1
+ * for the next step).
+ *
+ *   q            device [batch][num_heads_q][head_dim], dtype
+ *   k_new,v_new  device [batch][num_heads_kv][head_dim], dtype, or both NULL: the cached tokens
+ *                only, nothing is written
+ *   k_pool,
+ *   v_pool       device [num_pages][num_heads_kv][block_size][head_dim], dtype. Sequences may
+ *                share pages that they only read; the slots written must be distinct, and no
+ *                sequence may read one.
+ *   page_table   device int32 [batch][max_pages_per_seq]
+ *   ctx_len      device int32 [batch], at most max_pages_per_seq * block_size; negative: the
+ *                sequence has no token in this call (a finished one in a padded batch), nothing of
+ *                it is read or written
+ *   out          device [batch][num_heads_q][head_dim], dtype; a sequence without any key gets 0
+ *   lse_out      device float [batch][num_heads_q] natural-log normaliser (-inf without any
+ *                key), or NULL
+ *   max_ctx      host hint used only to split the cache's length among CTAs
+ *   block_size   1..256; head_dim 32, 64 or 128
+ * Slots at or past ctx_len may hold anything.
+ *
+ * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
+ * are left out of the softmax) and for a new token without a page (its page-table row is full or
+ * the id out of range: it takes part in the attention and is not stored); D2F_ERR_INVALID_ARG
+ * for a ctx_len past the page table (the sequence is skipped).
+ * Limits: batch and num_heads_q <= 65535. The workspace is the caller's, zeroed once (and again
+ * after a device error); calls of any sizes may use it in turn, with those of the attention
+ * entry points and the log probabilities.
+ */
+int d2f_token_attn(const void *q, const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                   const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,
+                   void *out, float *lse_out, int batch, int max_ctx, int num_heads_q,
+                   int num_heads_kv, int head_dim, int block_size, int num_pages, int dtype,
+                   float softmax_scale, void *workspace, size_t workspace_bytes,
+                   int32_t *err_word, void *stream);
 
 #ifdef __cplusplus
 }
