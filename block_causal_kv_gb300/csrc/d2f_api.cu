@@ -1229,6 +1229,7 @@ int d2f_kv_store(const void *k, const void *v, const int64_t *slot, int n, void 
 // ---------------------------------------------------------------------------
 namespace {
 struct PromptPlan {
+  bool tc;
   int tile_q, head_chunk, chunks, tiles, splits;
   size_t off_ml, off_o, bytes;
 };
@@ -1258,15 +1259,19 @@ int plan_prompt(int batch, int rows, int max_ctx, int Hq, int Hkv, int D, int B,
   if (rows < 0) return fail(D2F_ERR_INVALID_ARG, "rows %d < 0", rows);
   if (rows > (1 << 30)) return fail(D2F_ERR_UNSUPPORTED, "rows must be <= 2^30");
   const int G = Hq / Hkv;
-  p->head_chunk = min(G, kPromptSimtRows);
+  // tensor cores: pairs of 128-row tiles, all heads of a group in a tile, pages that fill a tile
+  p->tc = dtype == D2F_BF16 && (D == 64 || D == 128) && G <= 128 && B % 8 == 0 && 128 % B == 0 &&
+          !force_simt();
+  const int keys = p->tc ? 128 : 64;
+  p->head_chunk = p->tc ? G : min(G, kPromptSimtRows);
   p->chunks = cdiv(G, p->head_chunk);
-  p->tile_q = kPromptSimtRows / p->head_chunk;
+  p->tile_q = p->tc ? 2 * (128 / G) : kPromptSimtRows / p->head_chunk;
   p->tiles = rows / p->tile_q + batch;
   const long long items = (long long)p->tiles * Hkv * p->chunks;
   // Few row tiles and many keys: the keys are split, up to one CTA an SM and at least four key
   // tiles each.
   const int sms = max(1, num_sms_current_device());
-  const long long t_max = cdiv(max_ctx, 64) + (long long)cdiv(rows, 64);
+  const long long t_max = cdiv(max_ctx, keys) + (long long)cdiv(rows, keys);
   const long long most = items > 0 ? sms / items : 1;
   p->splits = (int)max(1LL, min(min(most, t_max / 4), (long long)kPromptMaxSplits));
   if (items * p->splits > 0x7fffffffLL || (long long)rows * Hq / 8 > 0x7ffffff0LL)
@@ -1355,8 +1360,17 @@ int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
   a.err = err_word;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_prompt_simt(a, dtype, s);
-  if (e != cudaSuccess) return cuda_fail(e, "CUDA-core prompt attention launch");
+  cudaError_t e;
+  if (p.tc) {
+    char why[256] = "";
+    e = launch_prompt_tc(a, s, why, sizeof why);
+    if (e != cudaSuccess && why[0])
+      return fail(D2F_ERR_CUDA, "tensor-core prompt attention: %s (%s)", why, cudaGetErrorString(e));
+    if (e != cudaSuccess) return cuda_fail(e, "tensor-core prompt attention launch");
+  } else {
+    e = launch_prompt_simt(a, dtype, s);
+    if (e != cudaSuccess) return cuda_fail(e, "CUDA-core prompt attention launch");
+  }
   if (p.splits > 1) {
     e = launch_prompt_merge(a, dtype, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention composition launch");

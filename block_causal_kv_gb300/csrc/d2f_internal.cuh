@@ -245,6 +245,7 @@ struct StoreArgs {
 
 // Launchers (one per translation unit). Return cudaSuccess or the launch error.
 cudaError_t launch_prompt_simt(const PromptArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t s, char *why, size_t why_len);
 cudaError_t launch_prompt_merge(const PromptArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_token_simt(const TokenArgs &a, int dtype, cudaStream_t s);
 // unit: bytes a thread moves at a time (16, or the element size)

@@ -1,0 +1,793 @@
+// Tensor-core path of d2f_prompt_attn (bf16, head_dim 64 or 128, up to 128 query heads a KV
+// head, pages of 8 to 128 tokens).
+//
+// Source of the mask: "D2F: 확산 언어 모델이 KV 캐시를 얻고 자기회귀 모델보다 2.5배 빨라지는
+// 방법", §블록 단위 인과 어텐션 (bidirectional inside a block, causal between blocks).
+//
+// Per row: x = scale <q, k>, out = sum 2^(x' - m) v / sum 2^(x' - m) with x' = x log2 e, one pass
+// over the keys. m is a reference that follows the row's maximum: it moves only when a tile's
+// maximum lies more than 2^8 above it, so the accumulator is rarely rescaled. Scores, weights,
+// sums and both accumulators are float. The weights enter the product with V as bf16 (2^-8 of
+// each, the type of the MMA's operands; the sum keeps the unrounded ones).
+//
+// Work. An item is a pair of row tiles of 128 rows of one (request, KV head), times a split of
+// its keys. The G = Hq / Hkv query heads of the KV head are packed into the rows (row r = query
+// r / G, head r % G, 128 / G queries a tile), so a K/V tile that is read once serves all of them.
+// A CTA keeps an SM (its two row tiles, a ring of K and V tiles of 128 keys) and takes
+// further items from the launch's own grid (cluster launch control: a CTA that has loaded its
+// item's last tile cancels one that has not started and does its work), so that the next
+// item's queries and keys load while the last one computes, and unequal items even out. Items
+// of a request's last rows, which see the most keys, come first.
+//
+// Roles of a CTA's warps:
+//   0        producer: which request an item belongs to, tensor copies of the queries and of the
+//            K and V tiles (of the pages for cached keys, one box a page and 64 columns)
+//   1, 2     MMA issuer of row tile 0 and 1 (one lane): S = Q K^T, then O += P V with P in TMEM
+//            over S. The tiles' chains S -> softmax -> P V are apart, so one tile's products
+//            run while the other's weights are computed.
+//   4 - 11   softmax: a warpgroup a row tile, a thread a row
+// TMEM columns: S / P of tile 0 and 1 (128 each), O of tile 0 and 1 (D each).
+//
+// What a row does not see. Scores of keys past a row's limit are replaced by -inf, whatever they
+// were. V of keys that no row sees (rows of another request, slots past the context) is zeroed in
+// shared memory before the product. V of keys that only some rows of the tile see has to be
+// finite for the product (0 * infinity is not 0): where the mask cuts through a tile the
+// softmax threads look, and a tile with an infinity or NaN is multiplied by the threads, each
+// with the keys that its row sees.
+//
+// Every wait is bounded; a CTA whose wait ran out records D2F_ERR_TIMEOUT, drains its copies and
+// MMAs, frees TMEM and returns.
+#include <stdio.h>
+
+#include <mutex>
+
+#include "attn_common.cuh"
+#include "seq_attn.cuh"
+#include "tensor_map.cuh"
+
+namespace d2f {
+namespace {
+
+constexpr int kKeys = 128;  // keys of a tile
+constexpr int kThreads = 384;
+// Registers: 168 a thread at launch (3 * 128 threads); the producer's and issuers' warpgroup
+// gives up what the softmax warpgroups take (a row's 128 scores).
+constexpr int kRegLaunch = 168, kRegCtl = 72, kRegSoft = 216;
+static_assert(kRegCtl + 2 * kRegSoft <= 3 * kRegLaunch, "register split within the launch's allocation");
+constexpr float kMove = 8.f;         // the reference moves when a score is 2^kMove above it
+constexpr float kNothing = -1e30f;   // reference of a row that has seen no key
+
+struct Item {
+  int b, q0, n, C;      // request, its first row, rows, cached tokens (b < 0: no more items)
+  int i0, g, split;     // first query of the pair, KV head, split
+  int t0, t1, Tc;       // key tiles of this item, tiles of the cached keys
+  int tw[2];            // end of each row tile's key tiles
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * 128 * 128;  // bytes of 128 rows: 64-column halves, 128-byte rows
+  static constexpr int kEntries = D == 128 ? 5 : 8;  // ring entries, K and V tiles in turn
+  static constexpr int kRing = 2 * kTile;            // (the two Q tiles come first)
+  static constexpr int kBars = kRing + kEntries * kTile;
+  static constexpr uint32_t kTmO = 256;              // TMEM column of O
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];           // ring
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], scan[2], drain[2];
+  uint64_t slot_full[2], slot_empty[2], clc;
+  __align__(16) uint32_t clc_answer[4];
+  Item slot[2];
+  int bad[8];                           // ring entry: pages of the tile are missing
+  int odd[2][2];                        // number (+ 1) of a tile with infinite or NaN V, two looks in turn
+  int skip[2];                          // the threads have done this tile's product with V
+  int abort;
+  uint32_t tmem;
+};
+template <int D>
+constexpr int smem_bytes() {
+  return Cfg<D>::kBars + (int)sizeof(Bars) + 1024;  // (1024: the base is aligned by hand)
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// Ask for a CTA of this grid that has not started; the answer lands at `answer`.
+__device__ __forceinline__ void clc_ask(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          answer),
+      "r"(bar)
+      : "memory");
+}
+// The index of the CTA whose work came with the answer, or -1.
+__device__ __forceinline__ int clc_read(uint32_t answer) {
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return ok ? (int)x : -1;
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
+  return r;
+}
+// 128 consecutive 32-bit TMEM columns of this thread's lane, two loads and one wait.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, "
+      "%40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, "
+      "%56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%64, %65, %66, %67, %68, %69, %70, %71, "
+      "%72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, "
+      "%88, %89, %90, %91, %92, %93, %94, %95, "
+      "%96, %97, %98, %99, %100, %101, %102, %103, "
+      "%104, %105, %106, %107, %108, %109, %110, %111, "
+      "%112, %113, %114, %115, %116, %117, %118, %119, "
+      "%120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]),
+        "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]),
+        "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]),
+        "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]),
+        "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]),
+        "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]),
+        "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]),
+        "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
+        "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr), "r"(taddr + 64)
+      : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
+// The product with V of one tile by the threads: each row adds the keys below its limit.
+// `p`: TMEM columns of the row's weights, `o` of its output (taken as 0 when `first`).
+template <int D>
+__device__ __noinline__ void slow_pv(uint32_t p, uint32_t o, uint32_t v, uint4 sees, bool first) {
+  for (int dc = 0; dc < D / 32; ++dc) {
+    uint32_t acc[32];
+    if (first) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[j] = 0;
+    } else {
+      tmem_ld32(o + dc * 32, acc);
+    }
+    for (int c = 0; c < kKeys / 2; ++c) {
+      const uint32_t w = tmem_ld1(p + c);
+      const uint32_t word = c < 16 ? sees.x : c < 32 ? sees.y : c < 48 ? sees.z : sees.w;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = 2 * c + e;
+        if (!(word >> (key & 31) & 1u)) continue;
+        const float x = e ? __uint_as_float(w & 0xffff0000u) : __uint_as_float(w << 16);
+        const uint32_t row = v + (dc >> 1) * (128 * 128) + key * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 y = ld_shared_v4(row + ((((dc & 1) * 4 + q) ^ (key & 7)) << 4));
+          const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float &a0 = reinterpret_cast<float &>(acc[q * 8 + 2 * j]);
+            float &a1 = reinterpret_cast<float &>(acc[q * 8 + 2 * j + 1]);
+            a0 = fmaf(x, __uint_as_float(z[j] << 16), a0);
+            a1 = fmaf(x, __uint_as_float(z[j] & 0xffff0000u), a1);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    tmem_st32(o + dc * 32, acc);
+  }
+  tmem_wait_st();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_kp,
+                     const __grid_constant__ CUtensorMap tm_vp) {
+  using L = Cfg<D>;
+  constexpr int NE = L::kEntries;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  Bars *bars = reinterpret_cast<Bars *>(smem_raw + (sb - smem_u32(smem_raw)) + L::kBars);
+  volatile int *abort_flag = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, QI = a.tile_q / 2;  // queries of a row tile
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < NE; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->empty[i]), 2);  // the two issuers
+    }
+    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 2);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&bars->s_full[w]), 1);
+      mbar_init(smem_u32(&bars->p_full[w]), 4);  // the warps of a softmax warpgroup
+      mbar_init(smem_u32(&bars->o_full[w]), 1);
+      mbar_init(smem_u32(&bars->o_empty[w]), 4);
+      mbar_init(smem_u32(&bars->scan[w]), 4);
+      mbar_init(smem_u32(&bars->drain[w]), 1);
+      mbar_init(smem_u32(&bars->slot_full[w]), 1);
+      mbar_init(smem_u32(&bars->slot_empty[w]), 10);  // issuers and softmax warps
+      bars->odd[w][0] = bars->odd[w][1] = bars->skip[w] = 0;
+    }
+    mbar_init(smem_u32(&bars->clc), 1);
+    bars->abort = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem), 512);
+    tmem_relinquish();
+  }
+  if (warp == 3 && blockIdx.x == 0) seq_report(a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp < 4) {
+    reg_dec<kRegCtl>();
+    if (warp == 0) {
+      // ============ producer ====================================================
+      uint32_t e = 0, items = 0, asked = 0;
+      bool ok = true;
+      int it = blockIdx.x;
+      const int pages = kKeys / a.block_size;  // pages of a tile (cached keys)
+      while (true) {
+        Item w;
+        w.split = it % a.num_splits;
+        const int rest = it / a.num_splits;
+        w.g = rest % a.num_heads_kv;
+        const SeqTile s = seq_tile(a, a.tiles - 1 - rest / a.num_heads_kv);
+        w.t0 = w.t1 = 0;
+        bool asking = false;
+        auto ask = [&] {  // (at most one question at a time, none after a "no")
+          asking = true;
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the last answer has been read
+            mbar_arrive_expect_tx(smem_u32(&bars->clc), 16);
+            clc_ask(smem_u32(bars->clc_answer), smem_u32(&bars->clc));
+          }
+        };
+        if (s.live) {
+          w.b = s.b;
+          w.q0 = s.q0;
+          w.n = s.n;
+          w.C = s.C;
+          w.i0 = s.tile * a.tile_q;
+          w.Tc = (s.C + kKeys - 1) / kKeys;
+          int T = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int first = w.i0 + i * QI, end = min(first + QI, s.n);
+            w.tw[i] = first >= s.n ? 0 : w.Tc + (seq_limit(end - 1, s.n, a.mask_block) + kKeys - 1) / kKeys;
+            T = max(T, w.tw[i]);
+          }
+          int s_eff;
+          if (!split_range(T, a.num_splits, w.split, w.t0, w.t1, s_eff)) w.t0 = w.t1 = 0;
+          const int sl = items & 1;
+          ok = mbar_wait(smem_u32(&bars->slot_empty[sl]), ((items >> 1) & 1) ^ 1, abort_flag, a.err,
+                         a.wait_cycles);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            bars->slot[sl] = w;
+            mbar_arrive(smem_u32(&bars->slot_full[sl]));
+          }
+          ok = mbar_wait(smem_u32(&bars->q_empty), (items & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++items;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&bars->q_full);
+            mbar_arrive_expect_tx(bar, 2 * L::kHalves * QI * G * 128);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int h = 0; h < L::kHalves; ++h)
+                tma_load_3d(sb + i * L::kTile + h * 16384, &tm_q, bar, h * 64, w.g * G,
+                            w.q0 + w.i0 + i * QI);
+          }
+          // page ids of the next cached tile, one a lane
+          const int32_t *table = a.page_table + (int64_t)w.b * a.max_pages_per_seq;
+          auto page_of = [&](int t) {
+            const int at = t * pages + lane;
+            return lane < pages && t < w.Tc && at * a.block_size < w.C ? __ldg(table + at) : 0;
+          };
+          int page = w.t0 < w.Tc ? page_of(w.t0) : 0;
+          for (int t = w.t0; t < w.t1 && ok; ++t) {
+            if (t == w.t1 - 1) ask();
+            const bool cached = t < w.Tc;
+            const bool need = cached && lane < pages && (t * pages + lane) * a.block_size < w.C;
+            const bool good = need && page >= 0 && page < a.num_pages;
+            const int next = t + 1 < w.Tc ? page_of(t + 1) : 0;
+            const uint32_t n_good = __popc(__ballot_sync(0xffffffffu, good));
+            const bool bad = __any_sync(0xffffffffu, need && !good);
+            if (bad && lane == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const int ent = e % NE;
+              ok = mbar_wait(smem_u32(&bars->empty[ent]), ((e / NE) & 1) ^ 1, abort_flag, a.err,
+                             a.wait_cycles);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const uint32_t bar = smem_u32(&bars->full[ent]), dst = sb + L::kRing + ent * L::kTile;
+              if (cached) {
+                if (lane == 0) {
+                  bars->bad[ent] = bad;
+                  mbar_arrive_expect_tx(bar, n_good * a.block_size * 128 * L::kHalves);
+                }
+                __syncwarp();
+                if (good) {
+#pragma unroll
+                  for (int h = 0; h < L::kHalves; ++h)
+                    tma_load_3d(dst + h * 16384 + lane * a.block_size * 128, kv ? &tm_vp : &tm_kp, bar,
+                                h * 64, 0, page * a.num_heads_kv + w.g);
+                }
+              } else if (lane == 0) {
+                mbar_arrive_expect_tx(bar, L::kTile);
+#pragma unroll
+                for (int h = 0; h < L::kHalves; ++h)
+                  tma_load_3d(dst + h * 16384, kv ? &tm_v : &tm_k, bar, h * 64, w.g,
+                              w.q0 + (t - w.Tc) * kKeys);
+              }
+              ++e;
+            }
+            page = next;
+          }
+          if (!ok) {
+            asked += asking;
+            break;
+          }
+        }
+        if (!asking) ask();
+        ok = mbar_wait(smem_u32(&bars->clc), asked & 1, abort_flag, a.err, a.wait_cycles);
+        ok = __all_sync(0xffffffffu, ok);
+        ++asked;
+        if (!ok) break;
+        it = clc_read(smem_u32(bars->clc_answer));
+        __syncwarp();
+        if (it < 0) break;
+      }
+      if (ok) {  // no more items
+        const int sl = items & 1;
+        ok = mbar_wait(smem_u32(&bars->slot_empty[sl]), ((items >> 1) & 1) ^ 1, abort_flag, a.err,
+                       a.wait_cycles);
+        if (ok && lane == 0) {
+          bars->slot[sl].b = -1;
+          mbar_arrive(smem_u32(&bars->slot_full[sl]));
+        }
+      }
+      // Drain: what was asked for has landed before the CTA ends.
+      if (lane == 0) {
+        volatile int no_abort = 0;
+        if (items) mbar_wait(smem_u32(&bars->q_full), (items - 1) & 1, &no_abort, a.err, kDrainCycles);
+        for (uint32_t u = e > (uint32_t)NE ? e - NE : 0; u < e; ++u)
+          mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
+        if (asked) mbar_wait(smem_u32(&bars->clc), (asked - 1) & 1, &no_abort, a.err, kDrainCycles);
+      }
+    } else if (warp <= 2 && lane == 0) {
+      // ============ MMA issuer of row tile w ====================================
+      const int w = warp - 1;
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kKeys, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+      const uint64_t q_desc = smem_desc_sw128(sb + w * L::kTile, 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(sb + L::kRing, 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(sb + L::kRing, 16384, 1024);
+      const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
+      uint32_t e = 0, tiles = 0, outs = 0;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait(smem_u32(bar), parity, abort_flag, a.err, a.wait_cycles);
+      };
+      for (uint32_t item = 0;; ++item) {
+        const int sl = item & 1;
+        if (!wait(&bars->slot_full[sl], (item >> 1) & 1)) break;
+        const int b = bars->slot[sl].b, t0 = bars->slot[sl].t0, t1 = bars->slot[sl].t1;
+        const int tw = min(t1, bars->slot[sl].tw[w]);
+        mbar_arrive(smem_u32(&bars->slot_empty[sl]));
+        if (b < 0) break;
+        if (!wait(&bars->q_full, item & 1)) break;
+        bool ok = true;
+        for (int t = t0; t < t1; ++t, e += 2) {
+          const int ek = e % NE, ev = (e + 1) % NE;
+          ok = wait(&bars->full[ek], (e / NE) & 1);
+          if (!ok) break;
+          if (t >= tw) {  // this row tile sees none of these keys
+            mbar_arrive(smem_u32(&bars->empty[ek]));
+          } else {
+            tc_fence_after();
+            const uint64_t kd = smem_desc_advance(k_desc, ek * L::kTile);
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(ts, smem_desc_advance(q_desc, h * 16384 + kk * 32),
+                          smem_desc_advance(kd, h * 16384 + kk * 32), idesc_qk, (h | kk) ? 1u : 0u);
+            umma_commit(smem_u32(&bars->s_full[w]));
+            umma_commit(smem_u32(&bars->empty[ek]));
+            if (t == tw - 1) umma_commit(smem_u32(&bars->q_empty));
+          }
+          ok = wait(&bars->full[ev], ((e + 1) / NE) & 1);
+          if (!ok) break;
+          if (t >= tw) {
+            mbar_arrive(smem_u32(&bars->empty[ev]));
+          } else {
+            if (t == t0) ok = wait(&bars->o_empty[w], (outs & 1) ^ 1);
+            ok = ok && wait(&bars->p_full[w], tiles & 1);
+            if (!ok) break;
+            ++tiles;
+            tc_fence_after();
+            if (*(volatile int *)&bars->skip[w]) {
+              mbar_arrive(smem_u32(&bars->empty[ev]));
+            } else {
+              const uint64_t vd = smem_desc_advance(v_desc, ev * L::kTile);
+#pragma unroll
+              for (int ks = 0; ks < kKeys / 16; ++ks)
+                umma_bf16_tmem_a(to, ts + ks * 8, smem_desc_advance(vd, ks * 2048), idesc_pv,
+                                 (t > t0 || ks > 0) ? 1u : 0u);
+              umma_commit(smem_u32(&bars->empty[ev]));
+            }
+          }
+        }
+        if (!ok) break;
+        if (tw > t0) {
+          umma_commit(smem_u32(&bars->o_full[w]));
+          ++outs;
+        } else {
+          mbar_arrive(smem_u32(&bars->q_empty));
+        }
+      }
+      umma_commit(smem_u32(&bars->drain[w]));
+      volatile int no_abort = 0;
+      mbar_wait(smem_u32(&bars->drain[w]), 0, &no_abort, a.err, kDrainCycles);
+    }
+  } else {
+    // ============ softmax: warpgroup w, a thread a row ==========================
+    reg_inc<kRegSoft>();
+    const int w = (warp >> 2) - 1;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tmem + lane_base + w * 128, to = tmem + lane_base + L::kTmO + w * D;
+    const int qi = row / G, qh = row % G;
+    const int64_t n_hr = (int64_t)a.rows * a.num_heads_q;
+    const float sl2 = a.scale_log2;
+    uint32_t e = 0, tiles = 0, outs = 0, scans = 0;
+    int was_odd = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+      const bool x = mbar_wait(smem_u32(bar), parity, abort_flag, a.err, a.wait_cycles);
+      return __all_sync(0xffffffffu, x);
+    };
+    for (uint32_t item = 0;; ++item) {
+      const int sl = item & 1;
+      if (!wait(&bars->slot_full[sl], (item >> 1) & 1)) break;
+      const Item x = bars->slot[sl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->slot_empty[sl]));
+      if (x.b < 0) break;
+      const int i = x.i0 + w * QI + qi;                // query of the row
+      const bool rv = qi < QI && i < x.n;
+      const int limit = rv ? seq_limit(i, x.n, a.mask_block) : 0;  // new rows it sees
+      const int tw = min(x.t1, x.tw[w]);
+      float m_ref = kNothing, l = 0.f;
+      bool ok = true;
+      for (int t = x.t0; t < tw; ++t) {
+        const uint32_t ev = e + 2 * (t - x.t0) + 1;
+        const bool cached = t < x.Tc;
+        const int base = (cached ? t : t - x.Tc) * kKeys;
+        const int valid = min(kKeys, (cached ? x.C : x.n) - base);    // keys of this request
+        const int lim = cached ? valid : min(valid, limit - base);    // keys that the row sees
+        bool bad = false;
+        if (cached) {
+          ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
+          if (!ok) break;
+          bad = *(volatile int *)&bars->bad[ev % NE] != 0;
+        }
+        uint4 sees = make_uint4(~0u, ~0u, ~0u, ~0u);
+        bool odd = false;
+        // Where the mask cuts differs from row to row; the whole warpgroup takes part in the look at
+        // V. Some row does not see a key below `valid`: the first one does not.
+        const int first_lim = cached ? valid
+                                     : min(valid, seq_limit(min(x.i0 + w * QI, x.n - 1), x.n, a.mask_block) - base);
+        const bool look = bad || valid < kKeys || first_lim < valid;
+        if (look) {
+          uint32_t word[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int y = lim - 32 * k;
+            word[k] = y >= 32 ? ~0u : y <= 0 ? 0u : (1u << y) - 1u;
+          }
+          bool key_ok = row < valid;
+          if (bad) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int key = base + 32 * k + lane;
+              int page = -1;
+              if (key < x.C)
+                page = __ldg(a.page_table + (int64_t)x.b * a.max_pages_per_seq + key / a.block_size);
+              const bool good = page >= 0 && page < a.num_pages;
+              word[k] &= __ballot_sync(0xffffffffu, good);
+              if (k == (warp & 3)) key_ok = key_ok && good;
+            }
+          }
+          sees = make_uint4(word[0], word[1], word[2], word[3]);
+          ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
+          if (!ok) break;
+          const uint32_t v_row = sb + L::kRing + (ev % NE) * L::kTile + row * 128;
+          if (!key_ok) {
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) st_shared_zero(v_row + h * 16384 + c * 16);
+          } else if (first_lim < valid) {
+            uint32_t hit = 0;  // exponents of all ones carry into the sign's place
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint4 y = ld_shared_v4(v_row + h * 16384 + (((c + row) & 7) << 4));
+                hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                       ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+              }
+            odd = (hit & 0x80008000u) != 0;
+          }
+          fence_proxy_async_smem();  // the zeros, before the MMA reads V
+          odd = __any_sync(0xffffffffu, odd);
+          if (lane == 0) {
+            if (odd) *(volatile int *)&bars->odd[w][scans & 1] = (int)tiles + 1;
+            mbar_arrive(smem_u32(&bars->scan[w]));
+          }
+          ok = wait(&bars->scan[w], scans & 1);
+          if (!ok) break;
+          odd = *(volatile int *)&bars->odd[w][scans & 1] == (int)tiles + 1;
+          ++scans;
+        }
+        ok = wait(&bars->s_full[w], tiles & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[128];
+        tmem_ld128(ts, r);
+        if (look) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) {
+            const uint32_t word = j < 32 ? sees.x : j < 64 ? sees.y : j < 96 ? sees.z : sees.w;
+            if (!(word >> (j & 31) & 1u)) r[j] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 128; j += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmax3(mx[k], __uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        const bool first = t == x.t0;
+        const bool move = rv && (top > m_ref + kMove || (m_ref == kNothing && top > kNothing));
+        if (__any_sync(0xffffffffu, move)) {
+          const float m_new = move ? top : m_ref;
+          const float alpha = fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+          l *= alpha;
+          if (!first) {  // (P V of the tile before is complete: S of this one came after it)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + c * 32, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(to + c * 32, o);
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float x0, x1;
+            fma2_bc(x0, x1, __uint_as_float(r[c * 64 + 2 * j]), __uint_as_float(r[c * 64 + 2 * j + 1]), sl2,
+                    -m_ref);
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], sum[2 * (j & 1)], sum[2 * (j & 1) + 1], x0, x1);
+            p[j] = pack_bf16x2(x0, x1);
+          }
+          tmem_st32(ts + c * 32, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        if (odd || was_odd) {
+          if (odd)
+            slow_pv<D>(ts, to, sb + L::kRing + (ev % NE) * L::kTile, sees, first);
+          if (warp % 4 == 0 && lane == 0) *(volatile int *)&bars->skip[w] = odd;
+          was_odd = odd;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w]));
+        ++tiles;
+      }
+      if (!ok) break;
+      e += 2 * (x.t1 - x.t0);
+      const int64_t hr = rv ? (int64_t)(x.q0 + i) * a.num_heads_q + x.g * G + qh : 0;
+      if (a.num_splits > 1) {
+        float *dst = a.ws_o + (x.split * n_hr + hr) * D;
+        if (rv) a.ws_ml[x.split * n_hr + hr] = make_float2(m_ref == kNothing ? -INFINITY : m_ref, l);
+        if (tw > x.t0) {
+          if (!wait(&bars->o_full[w], outs & 1)) break;
+          ++outs;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            if (rv)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4 *>(dst + c * 32 + 4 * j) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty[w]));
+        }
+      } else if (tw > x.t0) {
+        if (!wait(&bars->o_full[w], outs & 1)) break;
+        ++outs;
+        tc_fence_after();
+        const float inv = 1.0f / l;
+        uint16_t *dst = static_cast<uint16_t *>(a.out) + hr * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(to + c * 32, o);
+          if (rv) {
+            uint32_t y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              y[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4 *>(dst + c * 32 + 8 * j) =
+                  make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty[w]));
+        if (rv && a.lse_out) a.lse_out[hr] = (m_ref + __log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  }
+
+  // ---- teardown ---------------------------------------------------------------
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_d(const PromptArgs &a, cudaStream_t s, char *why, size_t why_len) {
+  constexpr int bytes = smem_bytes<D>();
+  cudaFuncAttributes fa;
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncGetAttributes(&fa, prompt_tc_kernel<D>);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kRegLaunch) {  // the register split counts on it
+        snprintf(why, why_len, "%d registers a thread, the kernel expects %d", fa.numRegs, kRegLaunch);
+        return cudaErrorInvalidConfiguration;
+      }
+      e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  // Rows of 64 columns (128 bytes, swizzled), `box` of them a copy.
+  const cuuint64_t rowb = (cuuint64_t)D * 2;
+  auto map = [&](CUtensorMap *m, const void *base, cuuint64_t d1, cuuint64_t d2, cuuint64_t s1, cuuint64_t s2,
+                 cuuint32_t b1, cuuint32_t b2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, d1, d2}, strides[2] = {s1, s2};
+    const cuuint32_t box[3] = {64, b1, b2};
+    return encode_bf16_sw128(m, base, 3, dims, strides, box);
+  };
+  const int Hq = a.num_heads_q, Hk = a.num_heads_kv, B = a.block_size;
+  CUtensorMap q, k, v, kp, vp;
+  bool ok = map(&q, a.q, Hq, a.rows, rowb, Hq * rowb, a.group, a.tile_q / 2) &&
+            map(&k, a.k, Hk, a.rows, rowb, Hk * rowb, 1, kKeys) &&
+            map(&v, a.v, Hk, a.rows, rowb, Hk * rowb, 1, kKeys);
+  if (a.ctx_len && a.num_pages > 0) {
+    const cuuint64_t tiles = (cuuint64_t)a.num_pages * Hk;
+    ok = ok && map(&kp, a.k_pool, B, tiles, rowb, B * rowb, B, 1) &&
+         map(&vp, a.v_pool, B, tiles, rowb, B * rowb, B, 1);
+  } else {  // (no cached key is read)
+    kp = k;
+    vp = v;
+  }
+  if (!ok) {
+    snprintf(why, why_len, "cuTensorMapEncodeTiled is missing or rejected a tensor (alignment or size)");
+    return cudaErrorInvalidValue;
+  }
+  const int64_t items = (int64_t)a.tiles * Hk * a.num_splits;
+  prompt_tc_kernel<D><<<(unsigned)items, kThreads, bytes, s>>>(a, q, k, v, kp, vp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t s, char *why, size_t why_len) {
+  return a.head_dim == 128 ? launch_d<128>(a, s, why, why_len) : launch_d<64>(a, s, why, why_len);
+}
+
+}  // namespace d2f
