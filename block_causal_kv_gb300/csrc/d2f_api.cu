@@ -1383,7 +1383,8 @@ int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *
 // ---------------------------------------------------------------------------
 namespace {
 struct TokenPlan {
-  int head_chunk, chunks, splits;
+  bool tc;
+  int head_chunk, chunks, splits, grid;
   size_t off_partial, bytes;
 };
 
@@ -1392,11 +1393,19 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
   if (st != D2F_OK) return st;
   const int sms = max(1, num_sms_current_device());
   const int G = Hq / Hkv;
-  p->head_chunk = kTokenSimtHeads;
+  p->tc = dtype == D2F_BF16 && (D == 64 || D == 128) && !force_simt();
+  p->head_chunk = !p->tc ? kTokenSimtHeads : G <= 8 ? 8 : 16;
   p->chunks = cdiv(G, p->head_chunk);
   const long long pairs = (long long)max(batch, 1) * Hkv * p->chunks;
   if (pairs > 0x7fffffffLL / 64)
     return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_q is too large");
+  if (p->tc) {  // two partial slots a CTA, a counter a CTA
+    p->splits = 1;
+    p->grid = min(sms, kTokenMaxGrid);
+    p->off_partial = counter_bytes(p->grid);
+    p->bytes = p->off_partial + (size_t)2 * p->grid * p->head_chunk * (D + 2) * sizeof(float);
+    return D2F_OK;
+  }
   // Four CTAs an SM, at least 64 keys each; at most 64 parts to compose.
   p->splits = (int)max(1LL, min(min(4LL * sms / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
   p->off_partial = counter_bytes(p->splits > 1 ? pairs : 0);
@@ -1466,9 +1475,15 @@ int d2f_token_attn(const void *q, const void *k_new, const void *v_new, void *k_
   a.head_chunk = p.head_chunk;
   a.chunks = p.chunks;
   a.num_splits = p.splits;
+  a.grid = p.grid;
   a.counters = static_cast<int32_t *>(workspace);
   a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_partial);
   a.err = err_word;
+  if (p.tc) {
+    const cudaError_t e = launch_token_tc(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tensor-core token attention launch");
+    return D2F_OK;
+  }
   const cudaError_t e = launch_token_simt(a, dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "CUDA-core token attention launch");
   return D2F_OK;

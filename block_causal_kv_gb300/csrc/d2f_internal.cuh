@@ -215,7 +215,7 @@ constexpr int kPromptSimtRows = 64;  // packed rows (query, head) of a CUDA-core
 constexpr int kPromptMaxSplits = 16;
 
 constexpr int kTokenSimtHeads = 4;  // query heads of a CTA, CUDA-core path of the token attention
-// One new token a sequence over the paged cache (token_simt.cu).
+// One new token a sequence over the paged cache (token_attn.cu, token_simt.cu).
 struct TokenArgs {
   const void *q;               // [batch][Hq][head_dim]
   const void *k_new, *v_new;   // [batch][Hkv][head_dim], or NULL: no new key
@@ -228,11 +228,14 @@ struct TokenArgs {
   int group;
   float scale_log2;
   int head_chunk, chunks;      // query heads of a CTA, chunks of a group
-  int num_splits;              // CTAs sharing the keys of a (sequence, KV head, chunk)
+  int num_splits;              // CUDA cores: CTAs sharing the keys of a (sequence, KV head, chunk)
+  int grid;                    // tensor cores: CTAs that share all of the work
   int32_t *counters;           // arrivals (zero at rest)
   float *partial;
   int32_t *err;
 };
+constexpr int kTokenScanBatch = 1024;  // tensor cores: largest batch whose work is cut into shares
+constexpr int kTokenMaxGrid = 256;     // ... and the most shares
 
 struct StoreArgs {
   const void *k, *v;           // [n][Hkv][head_dim]
@@ -247,6 +250,7 @@ struct StoreArgs {
 cudaError_t launch_prompt_simt(const PromptArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_prompt_tc(const PromptArgs &a, cudaStream_t s, char *why, size_t why_len);
 cudaError_t launch_prompt_merge(const PromptArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_token_tc(const TokenArgs &a, cudaStream_t s);
 cudaError_t launch_token_simt(const TokenArgs &a, int dtype, cudaStream_t s);
 // unit: bytes a thread moves at a time (16, or the element size)
 cudaError_t launch_store(const StoreArgs &a, int unit, cudaStream_t s);

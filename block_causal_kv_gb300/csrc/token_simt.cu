@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
       if (d == 0) ml[at] = make_float2(top, sum);
     } else {
       const int64_t hr = (int64_t)b * a.num_heads_q + g * a.group + h0 + h;
-      const bool none = C == 0 && !a.k_new;
+      const bool none = top == -INFINITY && sum == 0.f;  // no key
       store_out<T>(static_cast<T *>(a.out) + hr * D + d, none ? 0.f : acc / sum);
       if (d == 0 && a.lse_out) a.lse_out[hr] = (top + __log2f(sum)) * 0.6931471805599453f;
     }
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
       acc = fmaf(w, __ldcg(a.partial + (at + (int64_t)i * HC) * D + d), acc);
     }
     const int64_t hr = (int64_t)b * a.num_heads_q + g * a.group + h0 + h;
-    const bool none = C == 0 && !a.k_new;
+    const bool none = top == -INFINITY && sum == 0.f;  // no key
     store_out<T>(static_cast<T *>(a.out) + hr * D + d, none ? 0.f : acc / sum);
     if (d == 0 && a.lse_out) a.lse_out[hr] = (top + __log2f(sum)) * 0.6931471805599453f;
   }
