@@ -1385,6 +1385,7 @@ namespace {
 struct TokenPlan {
   bool tc;
   int head_chunk, chunks, splits, grid;
+  bool line;
   size_t off_partial, bytes;
 };
 
@@ -1399,11 +1400,16 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
   const long long pairs = (long long)max(batch, 1) * Hkv * p->chunks;
   if (pairs > 0x7fffffffLL / 64)
     return fail(D2F_ERR_UNSUPPORTED, "batch * num_heads_q is too large");
-  if (p->tc) {  // two partial slots a CTA, a counter a CTA
+  if (p->tc) {  // two counters; two partial slots a run, three runs a warp
     p->splits = 1;
-    p->grid = min(sms, kTokenMaxGrid);
-    p->off_partial = counter_bytes(p->grid);
-    p->bytes = p->off_partial + (size_t)2 * p->grid * p->head_chunk * (D + 2) * sizeof(float);
+    p->grid = sms;
+    // With four (sequence, KV head)s a warp they balance by themselves, and the composition of
+    // cut ones (a CTA a query head, 30 us for 30,000 of them) is left out.
+    p->line = batch <= kTokenScanBatch && pairs < 4LL * p->grid * kTokenWarps;
+    p->off_partial = counter_bytes(0);
+    p->bytes = p->off_partial;
+    if (p->line) p->bytes += (size_t)6 * p->grid * kTokenWarps * min(G, p->head_chunk) * (D + 4) *
+                                    sizeof(float);
     return D2F_OK;
   }
   // Four CTAs an SM, at least 64 keys each; at most 64 parts to compose.
@@ -1476,6 +1482,7 @@ int d2f_token_attn(const void *q, const void *k_new, const void *v_new, void *k_
   a.chunks = p.chunks;
   a.num_splits = p.splits;
   a.grid = p.grid;
+  a.line = p.line;
   a.counters = static_cast<int32_t *>(workspace);
   a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_partial);
   a.err = err_word;

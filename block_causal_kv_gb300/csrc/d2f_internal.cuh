@@ -229,13 +229,14 @@ struct TokenArgs {
   float scale_log2;
   int head_chunk, chunks;      // query heads of a CTA, chunks of a group
   int num_splits;              // CUDA cores: CTAs sharing the keys of a (sequence, KV head, chunk)
-  int grid;                    // tensor cores: CTAs that share all of the work
+  int grid;                    // tensor cores: CTAs
+  bool line;                   // ... the work is one line, cut anywhere (else whole pairs are runs)
   int32_t *counters;           // arrivals (zero at rest)
   float *partial;
   int32_t *err;
 };
-constexpr int kTokenScanBatch = 1024;  // tensor cores: largest batch whose work is cut into shares
-constexpr int kTokenMaxGrid = 256;     // ... and the most shares
+constexpr int kTokenWarps = 8;         // tensor cores: warps of a CTA, a CTA an SM
+constexpr int kTokenScanBatch = 1024;  // ... the largest batch whose work may be one line
 
 struct StoreArgs {
   const void *k, *v;           // [n][Hkv][head_dim]

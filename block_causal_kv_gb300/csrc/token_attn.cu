@@ -6,23 +6,28 @@
 //
 // A read of the cache bounds it: every K and V element is used for the G query heads of its group
 // and no more. So the products take the small tensor instructions (mma.sync m16n8k16), whose
-// operands are registers, and K and V go from memory to registers and nowhere else:
+// operands are registers:
 //   S^T [16 keys x 8 heads] = K [16 keys x D] Q^T,  O^T [D x 8 heads] += V^T [D x 16 keys] P^T.
 // The sums over D and over keys may run in any order, so a thread's operand elements are chosen
 // for its loads: 16 bytes (8 dims) of K of two keys per 32 dims, and 16 bytes of V of four keys
 // per 64 dims, whose pairs of keys are put together by byte permutes. P^T's layout comes from
 // S^T's by 8 x 8 transposes in registers.
 //
-// A warp takes 16 keys at a time: V of these keys is requested before S is computed, K of the next
-// ones right after, so a warp always has 4 to 8 KB on the way. 12 warps a CTA (16 with
-// head_dim 64, 8 with more than eight heads a group), a CTA an SM.
+// A warp takes 16 keys at a time (a chunk: 8 KB with head_dim 128) through a ring of its own in
+// shared memory, filled by 16-byte asynchronous copies, so it waits for nobody but its copies.
+// The copies run ahead across everything that the warp does, 128 KB an SM are always on the
+// way. (With K and V loaded to registers, 4 to 8 KB a warp: 4 x 32,768 tokens of 32 heads 392 us.)
+// Rows lie in shared memory with their 16-byte pieces permuted (place()), so that the stores and
+// both operands' loads meet no bank twice.
 //
-// All chunks of 16 keys of the launch, (sequence, KV head, 16 heads, chunk), are one line cut into
-// equal shares, one CTA a share: every SM reads the same number of bytes whatever the lengths.
-// The warps of a CTA compose their parts of a (sequence, KV head) in shared memory; where it lies
-// in several shares, the CTA that arrives last composes the parts from the workspace, in the
-// order of the line. The arrival counter is that of the share with the first chunk: a share cuts
-// off one at its end at most. No CTA waits on another.
+// All chunks of the launch, (sequence, KV head, 8 or 16 heads, chunk), are one line, cut into runs:
+// three quarters of it one run a warp, the rest two smaller runs a warp, handed out on arrival
+// (SMs differ in bandwidth by some 15 %). Every SM reads what it can whatever the lengths
+// are, and no warp waits for another. What of a (sequence, KV head) lies within a run is written
+// out; the parts of a cut one go to the workspace, and a second launch composes them in the
+// order of the line. (With the warps of a CTA on the same chunks in turn, a barrier for each
+// (sequence, KV head) and the composition by the CTA that came last, 16 x 251 to 4096 tokens of 32
+// heads took 130 us.)
 //
 // Softmax in log2 units with a reference a head and warp, which moves only when a score is more
 // than 2^8 above it. Weights enter the product with V as bf16 (2^-8 of each; the sum keeps the
@@ -32,24 +37,33 @@
 namespace d2f {
 namespace {
 
-constexpr uint32_t kNoKey = 0xffffffffu;   // row of a key that does not exist
-constexpr uint32_t kNewKey = 0xfffffffeu;  // the new token's
 constexpr float kMove = 8.f;
 constexpr float kNothing = -1e30f;         // reference of a head that has seen no key
-constexpr int kMaxGrid = kTokenMaxGrid;
-constexpr int kMinChunks = 8;              // chunks of a share at least
 
-// Pages hold fewer than 2^32 - 2 token rows of a head (128 bytes or more each).
-__device__ __forceinline__ uint4 load_row(const void *pool, const void *fresh, uint32_t row, int row_bytes,
-                                          int at) {
-  const char *p = row == kNewKey ? static_cast<const char *>(fresh)
-                                 : static_cast<const char *>(pool) + (int64_t)row * row_bytes;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (row != kNoKey)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p + at));
+// 16 bytes to shared memory, or 16 zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
+}
+// Piece x of token t of a chunk lies at x ^ place(t). Eight lanes that load 16 bytes together hold
+// K of tokens 2 i, 2 i + 1 (four pieces of each: bit 2 of the two places differs) or V of tokens
+// e, e + 2, e + 4, e + 6 (two pieces of each: bits 1 and 2 of the four differ).
+__device__ __forceinline__ uint32_t place(uint32_t t) {
+  return ((t & 1) << 2) ^ (t & 2) ^ ((t & 4) ? 5u : 0u);
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -65,214 +79,293 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 template <int D, int NQ>
 struct Cfg {
-  static constexpr int W = NQ == 2 ? 8 : D == 64 ? 16 : 12;  // warps: what the registers allow
+  static constexpr int W = kTokenWarps;
   static constexpr int kThreads = 32 * W;
-  static constexpr int HQ = 8 * NQ;            // heads of a CTA
-  static constexpr int kPitch = D + 4;
-  // shared memory: the warps' outputs (later the weights of a composition's parts and its
-  // reduction), then their (maximum, sum), then the sequences
-  static constexpr int kO = 0;
-  static constexpr int kRed = kMaxGrid * HQ * 8;
-  static constexpr int kMl = kO + (W * HQ * kPitch * 4 > kRed + kThreads * 16 ? W * HQ * kPitch * 4
-                                                                             : kRed + kThreads * 16);
-  static constexpr int kPre = kMl + W * HQ * 8;
+  static constexpr int HQ = 8 * NQ;            // heads of a run's warp
+  static constexpr int kRow = 2 * D;           // bytes of a token's K or V
+  static constexpr int kChunk = 2 * 16 * kRow;
+  static constexpr int S = D == 64 ? 6 : 3;    // chunks of a warp's ring
+  // shared memory: the rings, the sequences' places on the line and lengths, the chunks' headers
+  static constexpr int kPre = W * S * kChunk;
   static constexpr int kCtx = kPre + (kTokenScanBatch + 1) * 8;
-  static constexpr int kBytes = kCtx + kTokenScanBatch * 4;
+  static constexpr int kMeta = (kCtx + kTokenScanBatch * 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kMeta + W * S * 32;
+  static_assert(kBytes <= 232448 - 1024, "shared memory per CTA");
 };
 
-struct Seg {       // chunks u0 .. u1 - 1 of the T of a (sequence, KV head, head chunk)
-  int b, g, hc, C, u0, u1, T;
-  int64_t first;   // place of chunk 0 on the line
-  bool ok;
+// The line of `total` chunks and its runs: n1 runs of the first `a` chunks, n2 of the rest.
+struct Runs {
+  int64_t total, a, n1, n2;
+  __device__ Runs(int64_t total, int warps) : total(total) {
+    // (shorter lines: one run a warp, of a chunk at least)
+    const bool two = total >= 16LL * warps;
+    a = two ? total - total / 4 : total;
+    n1 = min((int64_t)warps, total);
+    n2 = two ? 2 * warps : 0;
+  }
+  __device__ int64_t begin(int64_t x) const {
+    return x <= n1 ? x * a / n1 : a + (x - n1) * (total - a) / n2;
+  }
+  __device__ int64_t of(int64_t u) const {  // the run that holds chunk u
+    return u < a ? ((u + 1) * n1 - 1) / a : n1 + ((u - a + 1) * n2 - 1) / (total - a);
+  }
 };
+
+// Chunks of a sequence of C cached tokens; a negative C takes no part.
+__device__ __forceinline__ int chunks_of(int C, int fresh) {
+  return C < 0 ? 0 : max(1, (C + fresh + 15) / 16);
+}
+// The length of sequence b, negative where it takes no part.
+__device__ __forceinline__ int length_of(const TokenArgs &a, int b, bool report) {
+  const int C = __ldg(a.ctx_len + b);
+  if ((long long)C > (long long)a.max_pages_per_seq * a.block_size) {
+    if (report) set_err(a.err, D2F_ERR_INVALID_ARG);
+    return -1;
+  }
+  return C;
+}
+
+struct Seg {       // chunks u0 .. u1 - 1 of the T of a (sequence, KV head, head chunk)
+  int b, pair, C, u0, u1, T;  // pair: KV head * chunks + head chunk
+  int64_t first;   // place of chunk 0 on the line
+};
+struct Meta {      // a chunk in the ring
+  uint32_t keys;   // bits 0 .. 15: the tokens exist; flags
+  int b, pair, u, C, run;
+  int pad[2];
+};
+constexpr uint32_t kFirst = 1u << 16, kLast = 1u << 17;  // of the segment
+constexpr uint32_t kWhole = 1u << 18;  // the segment is all of the pair's chunks
+constexpr uint32_t kHead = 1u << 19;   // the segment holds the pair's first chunk
+
+// Weight of a part with maximum x and sum l among parts with the maximum top. (A part whose scores
+// are all NaN has no maximum and a NaN sum; a part without keys has the weight 0.)
+__device__ __forceinline__ float weight(float x, float l, float top) {
+  return x == kNothing && l == 0.f ? 0.f : fast_exp2(x - top);
+}
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const TokenArgs a) {
   using L = Cfg<D, NQ>;
-  constexpr int W = L::W, HQ = L::HQ, NT = L::kThreads, KB = D / 32, VB = D / 64;
-  extern __shared__ __align__(16) uint8_t sm[];
-  float *o_s = reinterpret_cast<float *>(sm + L::kO);
-  float2 *ml_s = reinterpret_cast<float2 *>(sm + L::kMl);
+  constexpr int W = L::W, HQ = L::HQ, NT = L::kThreads, KB = D / 32, VB = D / 64, S = L::S;
+  extern __shared__ __align__(128) uint8_t sm[];
   int64_t *pre_s = reinterpret_cast<int64_t *>(sm + L::kPre);
   int *ctx_s = reinterpret_cast<int *>(sm + L::kCtx);
-  __shared__ int is_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  if (tid == 0) D2F_TRACE_MARK(4, 0);
   const int Hk = a.num_heads_kv, B = a.block_size, fresh = a.k_new ? 1 : 0;
-  const int heads_b = Hk * a.chunks;  // (KV head, head chunk) pairs of a sequence
-  const bool line = a.batch <= kTokenScanBatch;
-  auto chunks_of = [&](int C) -> int { return C < 0 ? 0 : max(1, (C + fresh + 15) / 16); };
-  // the length of a sequence: negative where it takes no part
-  auto length = [&](int b, bool report) -> int {
-    const int C = __ldg(a.ctx_len + b);
-    if ((long long)C > (long long)a.max_pages_per_seq * B) {
-      if (report) set_err(a.err, D2F_ERR_INVALID_ARG);
-      return -1;
-    }
-    return C;
-  };
-
-  Seg s;
-  int64_t total = 0, grid = gridDim.x, end = 0;  // places on the line; this share ends at `end`
+  const int pairs = Hk * a.chunks;  // of a sequence
+  const bool line = a.line;
+  const int warps = gridDim.x * W, me = warp * gridDim.x + blockIdx.x;
   if (line) {
-    for (int b = tid; b < a.batch; b += NT) ctx_s[b] = length(b, blockIdx.x == 0);
+    for (int b = tid; b < a.batch; b += NT) ctx_s[b] = length_of(a, b, blockIdx.x == 0);
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0) {  // places of the sequences on the line
       int64_t carry = 0;
       for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
-        int64_t x = b < a.batch ? (int64_t)chunks_of(ctx_s[b]) * heads_b : 0, sum = x;
+        const int64_t x = b < a.batch ? (int64_t)chunks_of(ctx_s[b], fresh) * pairs : 0;
+        int64_t upto = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += y;
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
         }
-        if (b < a.batch) pre_s[b] = carry + sum - x;
-        carry += __shfl_sync(0xffffffffu, sum, 31);
+        if (b < a.batch) pre_s[b] = carry + upto - x;
+        carry += __shfl_sync(0xffffffffu, upto, 31);
       }
       if (lane == 0) pre_s[a.batch] = carry;
     }
     __syncthreads();
-    total = pre_s[a.batch];
-    grid = max((int64_t)1, min(grid, (total + kMinChunks - 1) / kMinChunks));
-    if (total == 0 || blockIdx.x >= grid) return;
-    const int64_t at = blockIdx.x * total / grid;
-    end = (blockIdx.x + 1) * total / grid;
-    int lo = 0, hi = a.batch;  // pre_s[lo] <= at < pre_s[hi], lo the last such
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre_s[mid] <= at) lo = mid;
-      else hi = mid;
-    }
-    s.b = lo;
-    s.C = ctx_s[lo];
-    s.T = chunks_of(s.C);
-    const int64_t in = at - pre_s[lo];
-    const int pair = (int)(in / s.T);
-    s.g = pair / a.chunks;
-    s.hc = pair % a.chunks;
-    s.u0 = (int)(in - (int64_t)pair * s.T);
-    s.first = at - s.u0;
-    s.u1 = (int)min((int64_t)s.T, end - s.first);
-    s.ok = true;
-  } else {  // a (sequence, KV head, head chunk) a CTA
-    s.b = blockIdx.x / heads_b;
-    const int pair = blockIdx.x % heads_b;
-    s.g = pair / a.chunks;
-    s.hc = pair % a.chunks;
-    s.C = length(s.b, tid == 0);
-    s.T = chunks_of(s.C);
-    if (s.T == 0) return;
-    s.u0 = 0;
-    s.u1 = s.T;
-    s.first = 0;
-    s.ok = true;
   }
-  auto next_seg = [&](const Seg &p) -> Seg {
-    Seg n = p;
-    n.first = p.first + p.T;
-    n.ok = line && n.first < end;
-    if (!n.ok) return n;
-    if (++n.hc == a.chunks) {
-      n.hc = 0;
-      if (++n.g == Hk) {
-        n.g = 0;
-        do ++n.b;
-        while (ctx_s[n.b] < 0);  // (a sequence with chunks follows: first < end)
-        n.C = ctx_s[n.b];
-        n.T = chunks_of(n.C);
+  grid_launch_dependents();  // (the composition waits for this grid's end)
+  const Runs runs(line ? pre_s[a.batch] : 0, warps);
+  if (tid == 0) D2F_TRACE_MARK(4, 1);
+
+  // ---- the ring: the place of the copies, chunk fu of segment f of run x, which ends at `end` ----
+  const uint32_t ring = smem_u32(sm) + warp * (S * L::kChunk);
+  volatile Meta *meta = reinterpret_cast<volatile Meta *>(sm + L::kMeta) + warp * S;
+  Seg f{};
+  int fu = 0, p0 = 0, ids0 = 0, ids1 = 0;  // ids0, ids1: page-table entries p0 + lane and p0 + 32 + lane
+  int64_t x = me, x_next = 0, end = 0;
+  bool more = true;  // f is a segment
+  auto ids_at = [&](int p) -> int {
+    return p < (f.C + B - 1) / B ? __ldg(a.page_table + (int64_t)f.b * a.max_pages_per_seq + p) : 0;
+  };
+  auto enter_seg = [&] {
+    f.u1 = (int)min((int64_t)f.T, end - f.first);
+    fu = f.u0;
+    p0 = 16 * fu / B;
+    ids0 = ids_at(p0 + lane);
+    ids1 = ids_at(p0 + 32 + lane);
+  };
+  auto ask = [&] {  // (the answer is used when this run ends)
+    if (lane == 0) x_next = (line ? runs.n1 : warps) + atomicAdd(a.counters, 1);
+  };
+  auto enter_run = [&] {
+    if (line) {
+      more = x < runs.n1 + runs.n2;
+      if (!more) return;
+      if (runs.n2) ask();
+      const int64_t at = runs.begin(x);
+      end = runs.begin(x + 1);
+      int lo = 0, hi = a.batch;  // pre_s[lo] <= at < pre_s[hi], lo the last such
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre_s[mid] <= at) lo = mid;
+        else hi = mid;
+      }
+      f.b = lo;
+      f.C = ctx_s[lo];
+      f.T = chunks_of(f.C, fresh);
+      const int64_t in = at - pre_s[lo];
+      f.pair = (int)(in / f.T);
+      f.u0 = (int)(in - (int64_t)f.pair * f.T);
+      f.first = at - f.u0;
+    } else {  // a run a (sequence, KV head, head chunk)
+      while (true) {
+        more = x < (int64_t)a.batch * pairs;
+        if (!more) return;
+        ask();
+        f.b = (int)(x / pairs);
+        f.pair = (int)(x % pairs);
+        f.C = length_of(a, f.b, lane == 0);
+        f.T = chunks_of(f.C, fresh);
+        if (f.T > 0) break;
+        x = __shfl_sync(0xffffffffu, x_next, 0);
+      }
+      f.u0 = 0;
+      f.first = 0;
+      end = f.T;
+    }
+    enter_seg();
+  };
+  enter_run();
+  uint32_t filled = 0;
+  auto fill = [&](int stage) {
+    if (more) {
+      if (16 * fu / B >= p0 + 32) {
+        p0 += 32;
+        ids0 = ids1;
+        ids1 = ids_at(p0 + 32 + lane);
+      }
+      const int key = 16 * fu + (lane & 15), entry = key / B, g = f.pair / a.chunks;
+      const int lo = __shfl_sync(0xffffffffu, ids0, entry - p0), hi = __shfl_sync(0xffffffffu, ids1, entry - p0);
+      const int page = entry - p0 < 32 ? lo : hi;
+      int64_t row = -1;  // of the pool's rows, -1: no key, -2: the new token's
+      if (key < f.C) {
+        if (page >= 0 && page < a.num_pages) row = ((int64_t)page * Hk + g) * B + (key - entry * B);
+        else set_err(a.err, D2F_ERR_BAD_INDEX);
+      } else if (key == f.C && fresh) {
+        row = -2;
+      }
+      const uint32_t keys = __ballot_sync(0xffffffffu, row != -1) & 0xffffu;
+      if (lane == 0) {
+        meta[stage].keys = keys | (fu == f.u0 ? kFirst : 0) | (fu + 1 == f.u1 ? kLast : 0) |
+                           (f.u0 == 0 ? kHead : 0) | (f.u0 == 0 && f.u1 == f.T ? kWhole : 0);
+        meta[stage].b = f.b;
+        meta[stage].pair = f.pair;
+        meta[stage].u = fu;
+        meta[stage].C = f.C;
+        meta[stage].run = (int)x;
+      }
+      const uint32_t dst = ring + stage * L::kChunk;
+      const int64_t new_at = ((int64_t)f.b * Hk + g) * L::kRow;
+      constexpr int P = D / 8, per = 32 / P;  // pieces of a row, tokens a step
+      const int piece = lane % P, sub = lane / P;
+#pragma unroll
+      for (int i = 0; i < 16 / per; ++i) {
+        const int t = i * per + sub;
+        const int64_t y = __shfl_sync(0xffffffffu, row, t);
+        const uint32_t to = dst + t * L::kRow + ((piece ^ place(t & 7)) << 4);
+        const int64_t from = (y == -2 ? new_at : y < 0 ? 0 : y * L::kRow) + piece * 16;
+        copy16(to, static_cast<const char *>(y == -2 ? a.k_new : a.k_pool) + from, y != -1);
+        copy16(to + 16 * L::kRow, static_cast<const char *>(y == -2 ? a.v_new : a.v_pool) + from, y != -1);
+      }
+      ++filled;
+      if (++fu == f.u1) {
+        const int64_t next = f.first + f.T;
+        if (line && next < end) {  // the run goes on
+          f.first = next;
+          f.u0 = 0;
+          if (++f.pair == pairs) {
+            f.pair = 0;
+            do ++f.b;
+            while (ctx_s[f.b] < 0);  // (a sequence with chunks follows: next < end)
+            f.C = ctx_s[f.b];
+            f.T = chunks_of(f.C, fresh);
+          }
+          enter_seg();
+        } else {
+          x = line && !runs.n2 ? runs.n1 : __shfl_sync(0xffffffffu, x_next, 0);
+          enter_run();
+        }
       }
     }
-    n.u0 = 0;
-    n.u1 = (int)min((int64_t)n.T, end - n.first);
-    return n;
+    copy_commit();
   };
-  // page id of this lane's key of chunk u (lanes 16 .. 31: as lanes 0 .. 15), then its token row
-  auto page_of = [&](const Seg &p, int u) -> int {
-    const int key = 16 * u + (lane & 15);
-    return u < p.u1 && key < p.C ? __ldg(a.page_table + (int64_t)p.b * a.max_pages_per_seq + key / B) : 0;
-  };
-  auto row_of = [&](const Seg &p, int u, int page) -> uint32_t {
-    const int key = 16 * u + (lane & 15);
-    if (key >= p.C) return key == p.C && fresh ? kNewKey : kNoKey;
-    if (page < 0 || page >= a.num_pages) {
-      set_err(a.err, D2F_ERR_BAD_INDEX);
-      return kNoKey;
-    }
-    return (uint32_t)(((int64_t)page * Hk + p.g) * B + key % B);
-  };
-
-  uint4 q[NQ][KB], kx[2][KB], vx[4][VB];
-  uint32_t k_ok = 0;  // bits 0, 1: keys r and r + 8 of the loaded K exist
-  auto load_q = [&](const Seg &p) {
+  uint4 q[NQ][KB], qn[NQ][KB];
+  auto load_q = [&](int b, int pair) {
+    const int g = pair / a.chunks, hc = pair % a.chunks;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int h = p.hc * HQ + n * 8 + r;  // head of the group
+      const int h = hc * HQ + n * 8 + r;  // head of the group
       const char *src = static_cast<const char *>(a.q) +
-                        ((int64_t)p.b * a.num_heads_q + p.g * a.group + h) * (D * 2) + c * 16;
+                        ((int64_t)b * a.num_heads_q + g * a.group + h) * L::kRow + c * 16;
 #pragma unroll
       for (int k = 0; k < KB; ++k)
-        q[n][k] = h < a.group ? __ldg(reinterpret_cast<const uint4 *>(src + k * 64)) : make_uint4(0, 0, 0, 0);
+        qn[n][k] = h < a.group ? __ldg(reinterpret_cast<const uint4 *>(src + k * 64)) : make_uint4(0, 0, 0, 0);
     }
   };
-  auto load_k = [&](const Seg &p, uint32_t row) {
-    const void *fr = static_cast<const char *>(a.k_new) + ((int64_t)p.b * Hk + p.g) * (D * 2);
-    k_ok = 0;
+  if (more) load_q(f.b, f.pair);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t x = __shfl_sync(0xffffffffu, row, r + 8 * i);
-      if (x != kNoKey) k_ok |= 1u << i;
-#pragma unroll
-      for (int k = 0; k < KB; ++k) kx[i][k] = load_row(a.k_pool, fr, x, D * 2, k * 64 + c * 16);
-    }
-  };
+  for (int i = 0; i < S - 1; ++i) fill(i);
+  if (tid == 0) D2F_TRACE_MARK(4, 2);
 
-  uint32_t row = kNoKey;
-  int page = page_of(s, s.u0 + warp), page_next = 0;
-  load_q(s);
-  if (s.u0 + warp < s.u1) {
-    row = row_of(s, s.u0 + warp, page);
-    load_k(s, row);
-    page_next = page_of(s, s.u0 + warp + W);
-  }
-  while (true) {
-    const Seg n = next_seg(s);
-    const bool n_mine = n.ok && n.u0 + warp < n.u1;
-    page = n_mine ? page_of(n, n.u0 + warp) : 0;
-    auto enter_next = [&] {  // the next segment's first loads
-      load_q(n);
-      row = row_of(n, n.u0 + warp, page);
-      load_k(n, row);
-      page_next = page_of(n, n.u0 + warp + W);
-    };
-    float m[NQ][2], l[NQ][2], o[NQ][VB][4][4];
+  int stage = 0;
+  const uint32_t k_at = r * L::kRow + ((c ^ place(r)) << 4);                         // ^ kb << 6
+  const uint32_t v_at = 16 * L::kRow + 2 * c * L::kRow + ((r ^ place(2 * c)) << 4);  // token 2 c, ^ j << 7
+  float m[NQ][2], l[NQ][2], o[NQ][VB][4][4];
+  for (uint32_t done = 0; done < filled; ++done) {
+    copy_wait<S - 2>();
+    __syncwarp();  // this chunk has landed, and every lane is done with the one before
+    fill(stage == 0 ? S - 1 : stage - 1);
+    __syncwarp();
+    const uint32_t at = ring + stage * L::kChunk;
+    Meta mt;
+    mt.keys = meta[stage].keys;
+    mt.b = meta[stage].b;
+    mt.pair = meta[stage].pair;
+    mt.u = meta[stage].u;
+    mt.C = meta[stage].C;
+    mt.run = meta[stage].run;
+    stage = stage + 1 == S ? 0 : stage + 1;
+    const int g = mt.pair / a.chunks, hc = mt.pair % a.chunks;
+    if (mt.keys & kFirst) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      m[i][0] = m[i][1] = kNothing;
-      l[i][0] = l[i][1] = 0.f;
+      for (int i = 0; i < NQ; ++i) {
 #pragma unroll
-      for (int j = 0; j < VB; ++j)
+        for (int k = 0; k < KB; ++k) q[i][k] = qn[i][k];
+        m[i][0] = m[i][1] = kNothing;
+        l[i][0] = l[i][1] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int j = 0; j < VB; ++j)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) o[i][j][w][x] = 0.f;
-    }
-    for (int u = s.u0 + warp; u < s.u1; u += W) {
-      const void *fv = static_cast<const char *>(a.v_new) + ((int64_t)s.b * Hk + s.g) * (D * 2);
+          for (int w = 0; w < 4; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t x = __shfl_sync(0xffffffffu, row, 2 * c + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-        for (int j = 0; j < VB; ++j) vx[i][j] = load_row(a.v_pool, fv, x, D * 2, j * 128 + r * 16);
+            for (int e = 0; e < 4; ++e) o[i][j][w][e] = 0.f;
       }
-      if (fresh && s.hc == 0 && s.C >= 16 * u && s.C < 16 * u + 16) {
+    }
+    if (done + 1 < filled && (meta[stage].keys & kFirst)) load_q(meta[stage].b, meta[stage].pair);
+      if (fresh && hc == 0 && mt.C >= 16 * mt.u && mt.C < 16 * mt.u + 16) {
         // the new token to its slot, which no CTA reads in this call
-        const int pg = s.C / B < a.max_pages_per_seq
-                           ? __ldg(a.page_table + (int64_t)s.b * a.max_pages_per_seq + s.C / B) : -1;
+        const int pg = mt.C / B < a.max_pages_per_seq
+                           ? __ldg(a.page_table + (int64_t)mt.b * a.max_pages_per_seq + mt.C / B) : -1;
         if (pg < 0 || pg >= a.num_pages) {
           if (lane == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
         } else if ((lane & 15) < D / 8) {
-          const int64_t from = ((int64_t)s.b * Hk + s.g) * (D / 8) + (lane & 15);
-          const int64_t to = (((int64_t)pg * Hk + s.g) * B + s.C % B) * (D / 8) + (lane & 15);
+          const int64_t from = ((int64_t)mt.b * Hk + g) * (D / 8) + (lane & 15);
+          const int64_t to = (((int64_t)pg * Hk + g) * B + mt.C % B) * (D / 8) + (lane & 15);
           if (lane < 16)
             static_cast<uint4 *>(a.k_pool)[to] = static_cast<const uint4 *>(a.k_new)[from];
           else
@@ -281,21 +374,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
       }
       float x[NQ][4];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+      for (int i = 0; i < NQ; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          mma_bf16(x[i], kx[0][k].x, kx[1][k].x, kx[0][k].y, kx[1][k].y, q[i][k].x, q[i][k].y);
-          mma_bf16(x[i], kx[0][k].z, kx[1][k].z, kx[0][k].w, kx[1][k].w, q[i][k].z, q[i][k].w);
+      for (int k = 0; k < KB; ++k) {
+        const uint4 k0 = ld_shared_v4(at + (k_at ^ (k << 6))), k1 = ld_shared_v4(at + (k_at ^ (k << 6)) + 8 * L::kRow);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          mma_bf16(x[i], k0.x, k1.x, k0.y, k1.y, q[i][k].x, q[i][k].y);
+          mma_bf16(x[i], k0.z, k1.z, k0.w, k1.w, q[i][k].z, q[i][k].w);
         }
-      }
-      const uint32_t ok = k_ok;
-      if (u + W < s.u1) {
-        row = row_of(s, u + W, page_next);
-        load_k(s, row);
-        page_next = page_of(s, u + 2 * W);
-      } else if (n_mine) {
-        enter_next();
       }
       uint32_t p[NQ][2];
 #pragma unroll
@@ -303,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
         bool move = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[i][e] = (ok >> (e >> 1) & 1u) ? x[i][e] * a.scale_log2 : -INFINITY;
+          x[i][e] = (mt.keys >> (r + 8 * (e >> 1)) & 1u) ? x[i][e] * a.scale_log2 : -INFINITY;
           move |= x[i][e] > m[i][e & 1] + kMove;
         }
         if (__any_sync(0xffffffffu, move)) {
@@ -335,10 +422,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
       }
 #pragma unroll
       for (int j = 0; j < VB; ++j) {
-        const uint32_t v[4][4] = {{vx[0][j].x, vx[0][j].y, vx[0][j].z, vx[0][j].w},
-                                  {vx[1][j].x, vx[1][j].y, vx[1][j].z, vx[1][j].w},
-                                  {vx[2][j].x, vx[2][j].y, vx[2][j].z, vx[2][j].w},
-                                  {vx[3][j].x, vx[3][j].y, vx[3][j].z, vx[3][j].w}};
+        uint32_t v[4][4];  // tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 y = ld_shared_v4(at + (v_at ^ (j << 7) ^ ((e & 1) << 6)) + ((e & 1) + 8 * (e >> 1)) * L::kRow);
+          v[e][0] = y.x;
+          v[e][1] = y.y;
+          v[e][2] = y.z;
+          v[e][3] = y.w;
+        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {  // dims 64 j + 8 r + 2 w and + 1
           const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
@@ -347,166 +439,189 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
           for (int i = 0; i < NQ; ++i) mma_bf16(o[i][j][w], a0, a1, a2, a3, p[i][0], p[i][1]);
         }
       }
-    }
-    if (n_mine && s.u0 + warp >= s.u1) enter_next();
+    if (!(mt.keys & kLast)) continue;
 
-    // ---- the warps' parts of this segment ----
-    const int parts_w = min(W, s.u1 - s.u0);
-    const int heads = min(HQ, a.group - s.hc * HQ);
-    if (warp < parts_w) {
+    // ---- the segment's outputs, or its part ----
+    const int heads = min(HQ, a.group - hc * HQ);
+    const int64_t hr0 = (int64_t)mt.b * a.num_heads_q + g * a.group + hc * HQ;
+    const int slot_heads = min(HQ, a.group);
+    float *slot = a.partial + (2 * (int64_t)mt.run + (mt.keys & kHead ? 1 : 0)) * (slot_heads * (D + 4));
 #pragma unroll
-      for (int i = 0; i < NQ; ++i)
+    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float sum = l[i][e];
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[i][e];
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          const int h = 8 * i + 2 * c + e;
-          if (r == 0) ml_s[warp * HQ + h] = make_float2(m[i][e], sum);
-          if (h < heads) {
-            float *dst = o_s + (warp * HQ + h) * L::kPitch + 8 * r;
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const int h = 8 * i + 2 * c + e;
+        if (h >= heads) continue;
+        const bool none = m[i][e] == kNothing && sum == 0.f;  // no key
+        if (mt.keys & kWhole) {
+          const float inv = 1.0f / sum;
+          if (r == 0 && a.lse_out)
+            a.lse_out[hr0 + h] = none ? -INFINITY : (m[i][e] + __log2f(sum)) * 0.6931471805599453f;
 #pragma unroll
-            for (int j = 0; j < VB; ++j) {
-              *reinterpret_cast<float4 *>(dst + 64 * j) =
-                  make_float4(o[i][j][0][e], o[i][j][0][e + 2], o[i][j][1][e], o[i][j][1][e + 2]);
-              *reinterpret_cast<float4 *>(dst + 64 * j + 4) =
-                  make_float4(o[i][j][2][e], o[i][j][2][e + 2], o[i][j][3][e], o[i][j][3][e + 2]);
-            }
+          for (int j = 0; j < VB; ++j) {
+            uint32_t y[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              y[w] = none ? 0u : pack_bf16x2(o[i][j][w][e] * inv, o[i][j][w][e + 2] * inv);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (hr0 + h) * D + 64 * j + 8 * r) =
+                make_uint4(y[0], y[1], y[2], y[3]);
           }
-        }
-    }
-    __syncthreads();
-    const bool whole = s.u0 == 0 && s.u1 == s.T;
-    const int64_t hr0 = (int64_t)s.b * a.num_heads_q + s.g * a.group + s.hc * HQ;
-    auto put = [&](int h, int d, float4 v, float top, float sum) {  // four outputs and, once, the lse
-      const bool none = top == kNothing && sum == 0.f;  // no key
-      const float inv = none ? 0.f : 1.0f / sum;
-      uint2 y;
-      y.x = none ? 0u : pack_bf16x2(v.x * inv, v.y * inv);
-      y.y = none ? 0u : pack_bf16x2(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + (hr0 + h) * D + d) = y;
-      if (d == 0 && a.lse_out)
-        a.lse_out[hr0 + h] = none ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
-    };
-    // partial slots: (maximum, sum) [HQ], outputs [HQ][D]; two a CTA
-    constexpr int kSlot = HQ * (D + 2);
-    float *slots = a.partial;
-    float *slot = slots + (2 * (int64_t)blockIdx.x + (s.u0 == 0 ? 1 : 0)) * kSlot;
-    for (int e = tid; e < heads * (D / 4); e += NT) {
-      const int h = e / (D / 4), d = (e % (D / 4)) * 4;
-      float top = kNothing, sum = 0.f;
-      for (int w = 0; w < parts_w; ++w) top = fmaxf(top, ml_s[w * HQ + h].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < parts_w; ++w) {
-        const float2 x = ml_s[w * HQ + h];
-        // (a part whose scores are all NaN has a NaN sum and no maximum)
-        const float wt = x.x == kNothing && x.y == 0.f ? 0.f : fast_exp2(x.x - top);
-        const float4 y = *reinterpret_cast<float4 *>(o_s + (w * HQ + h) * L::kPitch + d);
-        sum = fmaf(wt, x.y, sum);
-        acc.x = fmaf(wt, y.x, acc.x);
-        acc.y = fmaf(wt, y.y, acc.y);
-        acc.z = fmaf(wt, y.z, acc.z);
-        acc.w = fmaf(wt, y.w, acc.w);
-      }
-      if (whole) {
-        put(h, d, acc, top, sum);
-      } else {
-        *reinterpret_cast<float4 *>(slot + 2 * HQ + h * D + d) = acc;
-        if (d == 0) reinterpret_cast<float2 *>(slot)[h] = make_float2(top, sum);
-      }
-    }
-    if (!whole) {
-      // shares that hold chunks of this pair: c0 .. c1, c0 with the first chunk
-      const int64_t c0 = ((s.first + 1) * grid - 1) / total, c1 = ((s.first + s.T) * grid - 1) / total;
-      const int parts = (int)(c1 - c0) + 1;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        is_last = atomic_add_acq_rel(a.counters + c0, 1) == parts - 1;
-        if (is_last) a.counters[c0] = 0;
-      }
-      __syncthreads();
-      if (is_last) {
-        __threadfence();
-        // weights of the parts, in shared memory over the warps' outputs
-        float2 *wt = reinterpret_cast<float2 *>(o_s);  // [parts][HQ]
-        auto slot_of = [&](int i) { return slots + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * kSlot; };
-        for (int e = tid; e < parts * heads; e += NT) {
-          const int i = e / heads, h = e - i * heads;
-          wt[i * HQ + h] = __ldcg(reinterpret_cast<const float2 *>(slot_of(i)) + h);
-        }
-        __syncthreads();
-        for (int h = warp; h < heads; h += W) {
-          float top = kNothing, sum = 0.f;
-          for (int i = lane; i < parts; i += 32) top = fmaxf(top, wt[i * HQ + h].x);
+        } else {
+          if (r == 0) *reinterpret_cast<float2 *>(slot + slot_heads * D + 2 * h) = make_float2(m[i][e], sum);
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          for (int i = lane; i < parts; i += 32) {
-            const float2 x = wt[i * HQ + h];
-            const float y = x.x == kNothing && x.y == 0.f ? 0.f : fast_exp2(x.x - top);
-            sum = fmaf(y, x.y, sum);
-            wt[i * HQ + h].x = y;
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          __syncwarp();
-          if (lane == 0) ml_s[h] = make_float2(top, sum);
-        }
-        __syncthreads();
-        // each output by `groups` threads, a share of the parts each
-        const int outs = heads * (D / 4), groups = max(1, NT / outs);
-        float4 *red = reinterpret_cast<float4 *>(sm + L::kRed);
-        for (int e0 = 0; e0 < outs; e0 += NT) {
-          const int e = e0 + (groups > 1 ? tid % outs : tid), gi = groups > 1 ? tid / outs : 0;
-          const int h = e / (D / 4), d = (e % (D / 4)) * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (e < outs && gi < groups) {
-#pragma unroll 8
-            for (int i = gi; i < parts; i += groups) {
-              const float y = wt[i * HQ + h].x;
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot_of(i) + 2 * HQ + h * D + d));
-              acc.x = fmaf(y, x.x, acc.x);
-              acc.y = fmaf(y, x.y, acc.y);
-              acc.z = fmaf(y, x.z, acc.z);
-              acc.w = fmaf(y, x.w, acc.w);
-            }
-          }
-          if (groups > 1) {
-            red[tid] = acc;
-            __syncthreads();
-            if (tid < outs) {
-              for (int k = 1; k < groups; ++k) {
-                const float4 x = red[k * outs + tid];
-                acc.x += x.x;
-                acc.y += x.y;
-                acc.z += x.z;
-                acc.w += x.w;
-              }
-              put(h, d, acc, ml_s[h].x, ml_s[h].y);
-            }
-          } else if (e < outs) {
-            put(h, d, acc, ml_s[h].x, ml_s[h].y);
+          for (int j = 0; j < VB; ++j) {
+            float4 *dst = reinterpret_cast<float4 *>(slot + h * D + 64 * j + 8 * r);
+            dst[0] = make_float4(o[i][j][0][e], o[i][j][0][e + 2], o[i][j][1][e], o[i][j][1][e + 2]);
+            dst[1] = make_float4(o[i][j][2][e], o[i][j][2][e + 2], o[i][j][3][e], o[i][j][3][e + 2]);
           }
         }
       }
-    }
-    if (!n.ok) break;
-    __syncthreads();  // the shared arrays are free for the next segment
-    s = n;
   }
+  if (tid == 0) D2F_TRACE_MARK(4, 3);
+  // the last warp of the launch leaves the counters as they were
+  if (lane == 0 && atomic_add_acq_rel(a.counters + 1, 1) == warps - 1) a.counters[0] = a.counters[1] = 0;
 }
 
+// Composition of the pairs whose chunks lie in several runs, a CTA a (sequence, KV head, query head).
+// Its warps share the parts.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) token_merge_kernel(const TokenArgs a, int warps, int hq) {
+  constexpr int MW = kMergeThreads / 32, VL = D / 32, N = 8;  // (a warp asks for N parts at a time)
+  __shared__ int64_t sum_s[MW][2];
+  __shared__ float acc_s[MW][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) D2F_TRACE_MARK(4, 8);
+  const int pairs = a.num_heads_kv * a.chunks, fresh = a.k_new ? 1 : 0;
+  const int b = blockIdx.x / a.num_heads_q, head = blockIdx.x % a.num_heads_q;
+  const int in_group = head % a.group, hc = in_group / hq, h = in_group % hq;
+  const int pair = head / a.group * a.chunks + hc;
+  const int C = length_of(a, b, false), T = chunks_of(C, fresh);
+  // the line's length, and the place of sequence b
+  int64_t all = 0, before = 0;
+  for (int i = tid; i < a.batch; i += kMergeThreads) {
+    const int64_t x = (int64_t)chunks_of(length_of(a, i, false), fresh) * pairs;
+    all += x;
+    if (i < b) before += x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    sum_s[warp][0] = all;
+    sum_s[warp][1] = before;
+  }
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int i = 0; i < MW; ++i) {
+    all += sum_s[i][0];
+    before += sum_s[i][1];
+  }
+  if (T == 0) return;
+  const Runs runs(all, warps);
+  const int64_t first = before + (int64_t)pair * T, r0 = runs.of(first), r1 = runs.of(first + T - 1);
+  if (r0 == r1) return;  // (written by its run)
+  const int parts = (int)(r1 - r0) + 1, slot_heads = min(hq, a.group);
+  // part i: run r0 + i, whose segment holds the pair's first chunk where i == 0
+  auto slot_of = [&](int i) { return a.partial + (2 * (r0 + i) + (i == 0 ? 1 : 0)) * (slot_heads * (D + 4)); };
+  auto ml_of = [&](int i) {
+    return __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + slot_heads * D + 2 * h));
+  };
+  if (tid == 0) D2F_TRACE_MARK(4, 9);
+  grid_dependency_wait();  // the parts
+  if (tid == 0) D2F_TRACE_MARK(4, 10);
+  // The outputs of this warp's first parts are asked for together with every part's (maximum, sum).
+  float2 ml[N];
+  float y[N][VL];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + k * MW;
+      ml[k] = make_float2(kNothing, 0.f);
+#pragma unroll
+      for (int j = 0; j < VL; ++j) y[k][j] = 0.f;
+      if (i < parts) {
+        ml[k] = ml_of(i);
+        const float *src = slot_of(i) + h * D + lane * VL;
+        if constexpr (VL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+          y[k][0] = v.x, y[k][1] = v.y, y[k][2] = v.z, y[k][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+          y[k][0] = v.x, y[k][1] = v.y;
+        }
+      }
+    }
+  };
+  load(warp);
+  // of the parts lane, lane + 32, ..: the running maximum and the sum beside it
+  float mine = kNothing, sum = 0.f, acc[VL] = {};
+  for (int i = lane; i < parts; i += 32) {
+    const float2 x = ml_of(i);
+    const float t = fmaxf(mine, x.x);
+    sum = weight(mine, sum, t) * sum + weight(x.x, x.y, t) * x.y;
+    mine = t;
+  }
+  float top = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  sum *= weight(mine, sum, top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int i0 = warp; i0 < parts; i0 += MW * N) {
+    if (i0 != warp) load(i0);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float w = weight(ml[k].x, ml[k].y, top);
+#pragma unroll
+      for (int j = 0; j < VL; ++j) acc[j] = fmaf(w, y[k][j], acc[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VL; ++j) acc_s[warp][lane * VL + j] = acc[j];
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int k = 1; k < MW; ++k)
+#pragma unroll
+    for (int j = 0; j < VL; ++j) acc[j] += acc_s[k][lane * VL + j];
+  const int64_t hr = (int64_t)b * a.num_heads_q + head;
+  const bool none = top == kNothing && sum == 0.f;  // no key
+  const float inv = 1.0f / sum;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + hr * D + lane * VL);
+#pragma unroll
+  for (int j = 0; j < VL / 2; ++j) dst[j] = none ? 0u : pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+  if (lane == 0 && a.lse_out) a.lse_out[hr] = none ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+  if (tid == 0) D2F_TRACE_MARK(4, 11);
+}
+
+// (a partial slot: an output of D floats a head, then (maximum, sum) a head, padded to 16 bytes)
 template <int D, int NQ>
 cudaError_t launch_t(const TokenArgs &a, cudaStream_t s) {
   using L = Cfg<D, NQ>;
   // (per device; every call sets the same value)
-  const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<D, NQ>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = (int64_t)a.batch * a.num_heads_kv * a.chunks;
-  const unsigned grid = a.batch <= kTokenScanBatch ? (unsigned)a.grid : (unsigned)pairs;
-  token_tc_kernel<D, NQ><<<grid, L::kThreads, L::kBytes, s>>>(a);
-  return cudaGetLastError();
+  token_tc_kernel<D, NQ><<<a.grid, L::kThreads, L::kBytes, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.line) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.batch * a.num_heads_q));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, token_merge_kernel<D>, a, a.grid * L::W, (int)L::HQ);
 }
 
 }  // namespace
@@ -515,5 +630,9 @@ cudaError_t launch_token_tc(const TokenArgs &a, cudaStream_t s) {
   if (a.head_dim == 128) return a.head_chunk == 8 ? launch_t<128, 1>(a, s) : launch_t<128, 2>(a, s);
   return a.head_chunk == 8 ? launch_t<64, 1>(a, s) : launch_t<64, 2>(a, s);
 }
+
+#ifdef D2F_TRACE
+D2F_TRACE_COPY_FN(d2f_trace_copy_token)
+#endif
 
 }  // namespace d2f
