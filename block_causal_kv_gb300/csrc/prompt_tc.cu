@@ -22,9 +22,8 @@
 // Roles of a CTA's warps:
 //   0        producer: which request an item belongs to, tensor copies of the queries and of the
 //            K and V tiles (of the pages for cached keys, one box a page and 64 columns)
-//   1, 2     MMA issuer of row tile 0 and 1 (one lane): S = Q K^T, then O += P V with P in TMEM
-//            over S. The tiles' chains S -> softmax -> P V are apart, so one tile's products
-//            run while the other's weights are computed.
+//   1        MMA issuer (one lane): S = Q K^T, then O += P V with P in TMEM over S, the row tiles
+//            in turn, so that one tile's products run while the other's weights are computed
 //   4 - 11   softmax: a warpgroup a row tile, a thread a row
 // TMEM columns: S / P of tile 0 and 1 (128 each), O of tile 0 and 1 (D each).
 //
@@ -52,7 +51,7 @@ constexpr int kKeys = 128;  // keys of a tile
 constexpr int kThreads = 384;
 // Registers: 168 a thread at launch (3 * 128 threads); the producer's and issuers' warpgroup
 // gives up what the softmax warpgroups take (a row's 128 scores).
-constexpr int kRegLaunch = 168, kRegCtl = 72, kRegSoft = 216;
+constexpr int kRegLaunch = 168, kRegCtl = 104, kRegSoft = 200;
 static_assert(kRegCtl + 2 * kRegSoft <= 3 * kRegLaunch, "register split within the launch's allocation");
 constexpr float kMove = 8.f;         // the reference moves when a score is 2^kMove above it
 constexpr float kNothing = -1e30f;   // reference of a row that has seen no key
@@ -77,7 +76,7 @@ struct Cfg {
 struct Bars {
   uint64_t full[8], empty[8];           // ring
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], scan[2], drain[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], scan[2], drain;
   uint64_t slot_full[2], slot_empty[2], clc;
   __align__(16) uint32_t clc_answer[4];
   Item slot[2];
@@ -124,6 +123,10 @@ __device__ __forceinline__ int clc_read(uint32_t answer) {
       : "memory");
   return ok ? (int)x : -1;
 }
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err,
+                                       long long budget) {
+  return mbar_wait(bar, parity, abort_flag, err, budget);
+}
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -131,6 +134,25 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// One lane of a converged warp. (The compiler knows that elect.sync picks a single lane, so it
+// does not wrap every tcgen05 instruction in a loop over the active lanes.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -140,51 +162,14 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
                : "memory");
   return r;
 }
-// 128 consecutive 32-bit TMEM columns of this thread's lane, two loads and one wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, "
-      "%8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, "
-      "%24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, "
-      "%40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, "
-      "%56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%64, %65, %66, %67, %68, %69, %70, %71, "
-      "%72, %73, %74, %75, %76, %77, %78, %79, "
-      "%80, %81, %82, %83, %84, %85, %86, %87, "
-      "%88, %89, %90, %91, %92, %93, %94, %95, "
-      "%96, %97, %98, %99, %100, %101, %102, %103, "
-      "%104, %105, %106, %107, %108, %109, %110, %111, "
-      "%112, %113, %114, %115, %116, %117, %118, %119, "
-      "%120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
-        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
-        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
-        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]),
-        "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]),
-        "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]),
-        "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]),
-        "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]),
-        "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]),
-        "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]),
-        "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
-        "=r"(r[126]), "=r"(r[127])
-      : "r"(taddr), "r"(taddr + 64)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, "
+      "%9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -197,6 +182,30 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 __device__ __forceinline__ void st_shared_zero(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
+// A row's output and the weights of its tile's first half times alpha.
+template <int D>
+__device__ __noinline__ void scale_o(uint32_t o, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(o + c, x);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * alpha);
+    tmem_st16(o + c, x);
+  }
+}
+__device__ __noinline__ void scale_p(uint32_t p, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(p + c, x);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      x[j] = pack_bf16x2(__uint_as_float(x[j] << 16) * alpha, __uint_as_float(x[j] & 0xffff0000u) * alpha);
+    tmem_st16(p + c, x);
+  }
 }
 
 // The product with V of one tile by the threads: each row adds the keys below its limit.
@@ -240,6 +249,68 @@ __device__ __noinline__ void slow_pv(uint32_t p, uint32_t o, uint32_t v, uint4 s
   tmem_wait_st();
 }
 
+// A tile that the mask cuts, or whose cached keys do not fill it: which of its keys the row sees
+// (`seen`), V of keys that no row sees zeroed, and whether V of the others has an infinity or NaN
+// that some row does not see. One thread a key row of V, all of a softmax warpgroup together.
+// `valid`: keys of this request; `lim`: those that the row sees; `first_lim`: that the first row sees.
+struct LookArgs {
+  uint32_t v_row, scan_bar;        // shared memory: this thread's key row of V, the warps' barrier
+  int valid, lim, first_lim, base, C, tag;
+  const int32_t *table;            // bad pages: this request's page table, else NULL
+  int block_size, num_pages;
+  uint32_t scans;
+};
+template <int D>
+__device__ __noinline__ bool look_at(const LookArgs &k, volatile int *odd_tag, volatile int *abort_flag,
+                                     int32_t *err, long long budget, uint4 &seen, bool &odd) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  uint32_t word[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int y = k.lim - 32 * i;
+    word[i] = y >= 32 ? ~0u : y <= 0 ? 0u : (1u << y) - 1u;
+  }
+  bool key_ok = warp * 32 + lane < k.valid;
+  if (k.table) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = k.base + 32 * i + lane;
+      const int page = key < k.C ? __ldg(k.table + key / k.block_size) : -1;
+      const bool good = page >= 0 && page < k.num_pages;
+      word[i] &= __ballot_sync(0xffffffffu, good);
+      if (i == warp) key_ok = key_ok && good;
+    }
+  }
+  seen = make_uint4(word[0], word[1], word[2], word[3]);
+  odd = false;
+  if (!key_ok) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) st_shared_zero(k.v_row + h * 16384 + c * 16);
+  } else if (k.first_lim < k.valid) {
+    uint32_t hit = 0;  // exponents of all ones carry into the sign's place
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 y = ld_shared_v4(k.v_row + h * 16384 + (((c + lane) & 7) << 4));
+        hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+               ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+      }
+    odd = (hit & 0x80008000u) != 0;
+  }
+  fence_proxy_async_smem();  // the zeros, before the MMA reads V
+  odd = __any_sync(0xffffffffu, odd);
+  if (lane == 0) {
+    if (odd) odd_tag[k.scans & 1] = k.tag;
+    mbar_arrive(k.scan_bar);
+  }
+  const bool ok = mbar_wait(k.scan_bar, k.scans & 1, abort_flag, err, budget);
+  odd = odd_tag[k.scans & 1] == k.tag;
+  return __all_sync(0xffffffffu, ok);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
@@ -258,19 +329,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < NE; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
-      mbar_init(smem_u32(&bars->empty[i]), 2);  // the two issuers
+      mbar_init(smem_u32(&bars->empty[i]), 1);
     }
     mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), 2);
+    mbar_init(smem_u32(&bars->q_empty), 1);
+    mbar_init(smem_u32(&bars->drain), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&bars->s_full[w]), 1);
       mbar_init(smem_u32(&bars->p_full[w]), 4);  // the warps of a softmax warpgroup
       mbar_init(smem_u32(&bars->o_full[w]), 1);
       mbar_init(smem_u32(&bars->o_empty[w]), 4);
       mbar_init(smem_u32(&bars->scan[w]), 4);
-      mbar_init(smem_u32(&bars->drain[w]), 1);
       mbar_init(smem_u32(&bars->slot_full[w]), 1);
-      mbar_init(smem_u32(&bars->slot_empty[w]), 10);  // issuers and softmax warps
+      mbar_init(smem_u32(&bars->slot_empty[w]), 9);  // issuer and softmax warps
       bars->odd[w][0] = bars->odd[w][1] = bars->skip[w] = 0;
     }
     mbar_init(smem_u32(&bars->clc), 1);
@@ -367,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t n_good = __popc(__ballot_sync(0xffffffffu, good));
             const bool bad = __any_sync(0xffffffffu, need && !good);
             if (bad && lane == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
-#pragma unroll
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
               const int ent = e % NE;
               ok = mbar_wait(smem_u32(&bars->empty[ent]), ((e / NE) & 1) ^ 1, abort_flag, a.err,
@@ -429,80 +500,94 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
         if (asked) mbar_wait(smem_u32(&bars->clc), (asked - 1) & 1, &no_abort, a.err, kDrainCycles);
       }
-    } else if (warp <= 2 && lane == 0) {
-      // ============ MMA issuer of row tile w ====================================
-      const int w = warp - 1;
+    } else if (warp == 1 && elect_one()) {
+      // ============ MMA issuer =================================================
+      // One thread for both row tiles: P V of a tile's last keys and S of its next ones, then the
+      // same of the other row tile, so that one tile's softmax has the time of the other's products.
+      // (Two issuers, a row tile each, fell into step: both tiles in the softmax at a time.)
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kKeys, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
-      const uint64_t q_desc = smem_desc_sw128(sb + w * L::kTile, 16, 1024);
+      const uint64_t q_desc = smem_desc_sw128(sb, 16, 1024);
       const uint64_t k_desc = smem_desc_sw128(sb + L::kRing, 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(sb + L::kRing, 16384, 1024);
-      const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
-      uint32_t e = 0, tiles = 0, outs = 0;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return mbar_wait(smem_u32(bar), parity, abort_flag, a.err, a.wait_cycles);
+      // (Elected, not lane 0: 16,384 causal rows of 28 on 4 heads 1777 -> 1343 us.)
+      const uint32_t full = smem_u32(bars->full), empty = smem_u32(bars->empty);
+      uint32_t sk = 0, pk = 0;      // ring entry of K of tile t, parity of its phase
+      uint32_t p_par = 0, o_par = 3;  // parities, a bit a row tile: p_full, o_empty
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, a.err, a.wait_cycles);
       };
       for (uint32_t item = 0;; ++item) {
         const int sl = item & 1;
-        if (!wait(&bars->slot_full[sl], (item >> 1) & 1)) break;
+        if (!wait(smem_u32(&bars->slot_full[sl]), (item >> 1) & 1)) break;
         const int b = bars->slot[sl].b, t0 = bars->slot[sl].t0, t1 = bars->slot[sl].t1;
-        const int tw = min(t1, bars->slot[sl].tw[w]);
+        const int tw0 = min(t1, bars->slot[sl].tw[0]), tw1 = min(t1, bars->slot[sl].tw[1]);
         mbar_arrive(smem_u32(&bars->slot_empty[sl]));
         if (b < 0) break;
-        if (!wait(&bars->q_full, item & 1)) break;
+        if (!wait(smem_u32(&bars->q_full), item & 1)) break;
         bool ok = true;
-        for (int t = t0; t < t1; ++t, e += 2) {
-          const int ek = e % NE, ev = (e + 1) % NE;
-          ok = wait(&bars->full[ek], (e / NE) & 1);
-          if (!ok) break;
-          if (t >= tw) {  // this row tile sees none of these keys
-            mbar_arrive(smem_u32(&bars->empty[ek]));
-          } else {
-            tc_fence_after();
-            const uint64_t kd = smem_desc_advance(k_desc, ek * L::kTile);
+        uint32_t sv = 0, pv = 0;  // V of tile t - 1
+#pragma unroll 1
+        for (int t = t0; t <= t1 && ok; ++t) {  // (t1: the last products with V)
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            const int tw = w ? tw1 : tw0;
+            const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
+            if (t > t0 && t - 1 < tw) {
+              ok = wait(full + 8 * sv, pv);
+              if (ok && t - 1 == t0) {
+                ok = wait(smem_u32(&bars->o_empty[w]), (o_par >> w) & 1);
+                o_par ^= 1u << w;
+              }
+              ok = ok && wait(smem_u32(&bars->p_full[w]), (p_par >> w) & 1);
+              if (!ok) break;
+              p_par ^= 1u << w;
+              tc_fence_after();
+              if (!*(volatile int *)&bars->skip[w]) {
+                const uint64_t vd = smem_desc_advance(v_desc, sv * L::kTile);
+                const uint32_t more = t - 1 > t0 ? 1u : 0u;
 #pragma unroll
-            for (int h = 0; h < L::kHalves; ++h)
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                  umma_bf16_tmem_a(to, ts + ks * 8, smem_desc_advance(vd, ks * 2048), idesc_pv,
+                                   ks > 0 ? 1u : more);
+              }
+              if (t == tw) umma_commit(smem_u32(&bars->o_full[w]));
+            }
+            if (w && t > t0) umma_commit(empty + 8 * sv);
+            if (t < tw) {
+              ok = wait(full + 8 * sk, pk);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t qd = smem_desc_advance(q_desc, w * L::kTile);
+              const uint64_t kd = smem_desc_advance(k_desc, sk * L::kTile);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(ts, smem_desc_advance(q_desc, h * 16384 + kk * 32),
-                          smem_desc_advance(kd, h * 16384 + kk * 32), idesc_qk, (h | kk) ? 1u : 0u);
-            umma_commit(smem_u32(&bars->s_full[w]));
-            umma_commit(smem_u32(&bars->empty[ek]));
-            if (t == tw - 1) umma_commit(smem_u32(&bars->q_empty));
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                umma_bf16(ts, smem_desc_advance(qd, at), smem_desc_advance(kd, at), idesc_qk, k ? 1u : 0u);
+              }
+              umma_commit(smem_u32(&bars->s_full[w]));
+            }
+            if (w && t < t1) {
+              umma_commit(empty + 8 * sk);
+              if (t + 1 == t1) umma_commit(smem_u32(&bars->q_empty));
+            }
           }
-          ok = wait(&bars->full[ev], ((e + 1) / NE) & 1);
-          if (!ok) break;
-          if (t >= tw) {
-            mbar_arrive(smem_u32(&bars->empty[ev]));
-          } else {
-            if (t == t0) ok = wait(&bars->o_empty[w], (outs & 1) ^ 1);
-            ok = ok && wait(&bars->p_full[w], tiles & 1);
-            if (!ok) break;
-            ++tiles;
-            tc_fence_after();
-            if (*(volatile int *)&bars->skip[w]) {
-              mbar_arrive(smem_u32(&bars->empty[ev]));
-            } else {
-              const uint64_t vd = smem_desc_advance(v_desc, ev * L::kTile);
-#pragma unroll
-              for (int ks = 0; ks < kKeys / 16; ++ks)
-                umma_bf16_tmem_a(to, ts + ks * 8, smem_desc_advance(vd, ks * 2048), idesc_pv,
-                                 (t > t0 || ks > 0) ? 1u : 0u);
-              umma_commit(smem_u32(&bars->empty[ev]));
+          if (t < t1) {
+            sv = sk + 1 == NE ? 0 : sk + 1;
+            pv = sk + 1 == NE ? pk ^ 1 : pk;
+            sk += 2;
+            if (sk >= NE) {
+              sk -= NE;
+              pk ^= 1;
             }
           }
         }
         if (!ok) break;
-        if (tw > t0) {
-          umma_commit(smem_u32(&bars->o_full[w]));
-          ++outs;
-        } else {
-          mbar_arrive(smem_u32(&bars->q_empty));
-        }
+        if (t0 == t1) umma_commit(smem_u32(&bars->q_empty));
       }
-      umma_commit(smem_u32(&bars->drain[w]));
+      umma_commit(smem_u32(&bars->drain));
       volatile int no_abort = 0;
-      mbar_wait(smem_u32(&bars->drain[w]), 0, &no_abort, a.err, kDrainCycles);
+      mbar_wait(smem_u32(&bars->drain), 0, &no_abort, a.err, kDrainCycles);
     }
   } else {
     // ============ softmax: warpgroup w, a thread a row ==========================
@@ -531,137 +616,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rv = qi < QI && i < x.n;
       const int limit = rv ? seq_limit(i, x.n, a.mask_block) : 0;  // new rows it sees
       const int tw = min(x.t1, x.tw[w]);
+      // new rows that every row of the tile sees: the first row's
+      const int first_limit = seq_limit(min(x.i0 + w * QI, x.n - 1), x.n, a.mask_block);
       float m_ref = kNothing, l = 0.f;
       bool ok = true;
       for (int t = x.t0; t < tw; ++t) {
         const uint32_t ev = e + 2 * (t - x.t0) + 1;
         const bool cached = t < x.Tc;
-        const int base = (cached ? t : t - x.Tc) * kKeys;
-        const int valid = min(kKeys, (cached ? x.C : x.n) - base);    // keys of this request
-        const int lim = cached ? valid : min(valid, limit - base);    // keys that the row sees
         bool bad = false;
-        if (cached) {
+        if (cached) {  // (S of the tile comes after its V has landed then)
           ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
           if (!ok) break;
           bad = *(volatile int *)&bars->bad[ev % NE] != 0;
         }
-        uint4 sees = make_uint4(~0u, ~0u, ~0u, ~0u);
+        const int base = (cached ? t : t - x.Tc) * kKeys;
+        const bool look = bad || base + kKeys > (cached ? x.C : first_limit);
+        uint4 sees;
         bool odd = false;
-        // Where the mask cuts differs from row to row; the whole warpgroup takes part in the look at
-        // V. Some row does not see a key below `valid`: the first one does not.
-        const int first_lim = cached ? valid
-                                     : min(valid, seq_limit(min(x.i0 + w * QI, x.n - 1), x.n, a.mask_block) - base);
-        const bool look = bad || valid < kKeys || first_lim < valid;
-        if (look) {
-          uint32_t word[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int y = lim - 32 * k;
-            word[k] = y >= 32 ? ~0u : y <= 0 ? 0u : (1u << y) - 1u;
-          }
-          bool key_ok = row < valid;
-          if (bad) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int key = base + 32 * k + lane;
-              int page = -1;
-              if (key < x.C)
-                page = __ldg(a.page_table + (int64_t)x.b * a.max_pages_per_seq + key / a.block_size);
-              const bool good = page >= 0 && page < a.num_pages;
-              word[k] &= __ballot_sync(0xffffffffu, good);
-              if (k == (warp & 3)) key_ok = key_ok && good;
-            }
-          }
-          sees = make_uint4(word[0], word[1], word[2], word[3]);
+        if (__builtin_expect(look, 0)) {
           ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
           if (!ok) break;
-          const uint32_t v_row = sb + L::kRing + (ev % NE) * L::kTile + row * 128;
-          if (!key_ok) {
-#pragma unroll
-            for (int h = 0; h < L::kHalves; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) st_shared_zero(v_row + h * 16384 + c * 16);
-          } else if (first_lim < valid) {
-            uint32_t hit = 0;  // exponents of all ones carry into the sign's place
-#pragma unroll
-            for (int h = 0; h < L::kHalves; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint4 y = ld_shared_v4(v_row + h * 16384 + (((c + row) & 7) << 4));
-                hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                       ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
-              }
-            odd = (hit & 0x80008000u) != 0;
-          }
-          fence_proxy_async_smem();  // the zeros, before the MMA reads V
-          odd = __any_sync(0xffffffffu, odd);
-          if (lane == 0) {
-            if (odd) *(volatile int *)&bars->odd[w][scans & 1] = (int)tiles + 1;
-            mbar_arrive(smem_u32(&bars->scan[w]));
-          }
-          ok = wait(&bars->scan[w], scans & 1);
+          LookArgs k;
+          k.v_row = sb + L::kRing + (ev % NE) * L::kTile + row * 128;
+          k.scan_bar = smem_u32(&bars->scan[w]);
+          k.valid = min(kKeys, (cached ? x.C : x.n) - base);
+          k.lim = cached ? k.valid : min(k.valid, limit - base);
+          k.first_lim = cached ? k.valid : min(k.valid, first_limit - base);
+          k.base = base;
+          k.C = x.C;
+          k.tag = (int)tiles + 1;
+          k.table = bad ? a.page_table + (int64_t)x.b * a.max_pages_per_seq : nullptr;
+          k.block_size = a.block_size;
+          k.num_pages = a.num_pages;
+          k.scans = scans++;
+          ok = look_at<D>(k, bars->odd[w], abort_flag, a.err, a.wait_cycles, sees, odd);
           if (!ok) break;
-          odd = *(volatile int *)&bars->odd[w][scans & 1] == (int)tiles + 1;
-          ++scans;
         }
         ok = wait(&bars->s_full[w], tiles & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[128];
-        tmem_ld128(ts, r);
-        if (look) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j) {
-            const uint32_t word = j < 32 ? sees.x : j < 64 ? sees.y : j < 96 ? sees.z : sees.w;
-            if (!(word >> (j & 31) & 1u)) r[j] = 0xff800000u;
-          }
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 128; j += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = fmax3(mx[k], __uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
         const bool first = t == x.t0;
-        const bool move = rv && (top > m_ref + kMove || (m_ref == kNothing && top > kNothing));
-        if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? top : m_ref;
-          const float alpha = fast_exp2(m_ref - m_new);
-          m_ref = m_new;
-          l *= alpha;
-          if (!first) {  // (P V of the tile before is complete: S of this one came after it)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + c * 32, o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(to + c * 32, o);
-            }
-          }
-        }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+        // 64 keys at a time
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
+          float sum[4], mx[4];
           uint32_t p[32];
+          // Weights with the reference as it is, the largest score beside them; where that is too far
+          // above the reference (seldom, and not a second time), the reference moves and the weights
+          // are computed again.
+          while (true) {
+            uint32_t r[64];
+            tmem_ld64(ts + c * 64, r);
+            if (__builtin_expect(look, 0)) {
+              const uint32_t w0 = c ? sees.z : sees.x, w1 = c ? sees.w : sees.y;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float x0, x1;
-            fma2_bc(x0, x1, __uint_as_float(r[c * 64 + 2 * j]), __uint_as_float(r[c * 64 + 2 * j + 1]), sl2,
-                    -m_ref);
-            x0 = fast_exp2(x0);
-            x1 = fast_exp2(x1);
-            add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], sum[2 * (j & 1)], sum[2 * (j & 1) + 1], x0, x1);
-            p[j] = pack_bf16x2(x0, x1);
+              for (int j = 0; j < 64; ++j)
+                if (!((j < 32 ? w0 : w1) >> (j & 31) & 1u)) r[j] = 0xff800000u;
+            }
+            // Pairs of keys in three steps, apart so that the exponentials, which bound this loop (four
+            // cycles each a warp), do not wait: argument; exponentials; sum and rounding.
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              sum[k] = 0.f;
+              mx[k] = -INFINITY;
+            }
+            const float neg = -m_ref;
+            constexpr int kA = 2, kB = 6;
+#pragma unroll
+            for (int j = 0; j < 32 + kA + kB; ++j) {
+              if (j < 32) {
+                const float x0 = __uint_as_float(r[2 * j]), x1 = __uint_as_float(r[2 * j + 1]);
+                float y0, y1;
+                mx[j & 3] = fmax3(mx[j & 3], x0, x1);
+                fma2_bc(y0, y1, x0, x1, sl2, neg);
+                r[2 * j] = __float_as_uint(y0);
+                r[2 * j + 1] = __float_as_uint(y1);
+              }
+              if (j >= kA && j < 32 + kA) {
+                const int k = 2 * (j - kA);
+                r[k] = __float_as_uint(fast_exp2(__uint_as_float(r[k])));
+                r[k + 1] = __float_as_uint(fast_exp2(__uint_as_float(r[k + 1])));
+              }
+              if (j >= kA + kB) {
+                const int k = j - kA - kB;
+                const float x0 = __uint_as_float(r[2 * k]), x1 = __uint_as_float(r[2 * k + 1]);
+                add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], sum[2 * (k & 1)], sum[2 * (k & 1) + 1], x0, x1);
+                p[k] = pack_bf16x2(x0, x1);
+              }
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            const bool move = rv && top > m_ref + kMove;
+            if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
+            // By a whole number of powers of two, so that weights of this tile's first half which are
+            // stored already keep their bits; the first time, and by more than 126, to the score itself.
+            float alpha = 1.f;
+            if (move) {
+              const float up = ceilf(top - m_ref);
+              const bool small = up <= 126.f;
+              alpha = small ? __uint_as_float((uint32_t)(127 - (int)up) << 23) : 0.f;
+              m_ref = small ? m_ref + up : top;
+            }
+            l *= alpha;
+            if (c == 1) scale_p(ts, alpha);
+            // (P V of the tile before is complete: S of this one came after it)
+            if (!first) scale_o<D>(to, alpha);
           }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st32(ts + c * 32, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
-        if (odd || was_odd) {
-          if (odd)
-            slow_pv<D>(ts, to, sb + L::kRing + (ev % NE) * L::kTile, sees, first);
+        if (__builtin_expect(odd || was_odd, 0)) {
+          if (odd) slow_pv<D>(ts, to, sb + L::kRing + (ev % NE) * L::kTile, sees, first);
           if (warp % 4 == 0 && lane == 0) *(volatile int *)&bars->skip[w] = odd;
           was_odd = odd;
         }
@@ -680,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(&bars->o_full[w], outs & 1)) break;
           ++outs;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(to + c * 32, o);
@@ -700,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv = 1.0f / l;
         uint16_t *dst = static_cast<uint16_t *>(a.out) + hr * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(to + c * 32, o);
