@@ -24,15 +24,16 @@
 //            K and V tiles (of the pages for cached keys, one box a page and 64 columns)
 //   1        MMA issuer (one lane): S = Q K^T, then O += P V with P in TMEM over S, the row tiles
 //            in turn, so that one tile's products run while the other's weights are computed
+//   2, 3     V tiles that the mask cuts, or that pages do not fill (below)
 //   4 - 11   softmax: a warpgroup a row tile, a thread a row
 // TMEM columns: S / P of tile 0 and 1 (128 each), O of tile 0 and 1 (D each).
 //
 // What a row does not see. Scores of keys past a row's limit are replaced by -inf, whatever they
 // were. V of keys that no row sees (rows of another request, slots past the context) is zeroed in
 // shared memory before the product. V of keys that only some rows of the tile see has to be
-// finite for the product (0 * infinity is not 0): where the mask cuts through a tile the
-// softmax threads look, and a tile with an infinity or NaN is multiplied by the threads, each
-// with the keys that its row sees.
+// finite for the product (0 * infinity is not 0): where the mask cuts through a tile two warps
+// look, and a tile with an infinity or NaN is multiplied by the softmax threads, each with the
+// keys that its row sees.
 //
 // Every wait is bounded; a CTA whose wait ran out records D2F_ERR_TIMEOUT, drains its copies and
 // MMAs, frees TMEM and returns.
@@ -67,21 +68,22 @@ template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * 128 * 128;  // bytes of 128 rows: 64-column halves, 128-byte rows
-  static constexpr int kEntries = D == 128 ? 5 : 8;  // ring entries, K and V tiles in turn
-  static constexpr int kRing = 2 * kTile;            // (the two Q tiles come first)
+  static constexpr int kEntries = D == 128 ? 3 : 8;  // ring entries, K and V tiles in turn
+  static constexpr int kRing = 4 * kTile;            // (two pairs of Q tiles come first)
   static constexpr int kBars = kRing + kEntries * kTile;
   static constexpr uint32_t kTmO = 256;              // TMEM column of O
 };
 
 struct Bars {
   uint64_t full[8], empty[8];           // ring
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], scan[2], drain;
+  uint64_t clean[8];                    // ... V looked at, and zeroed where nobody sees it
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain;
   uint64_t slot_full[2], slot_empty[2], clc;
   __align__(16) uint32_t clc_answer[4];
   Item slot[2];
   int bad[8];                           // ring entry: pages of the tile are missing
-  int odd[2][2];                        // number (+ 1) of a tile with infinite or NaN V, two looks in turn
+  int odd[8][2];                        // V has an infinity or NaN that not every row sees, by half
   int skip[2];                          // the threads have done this tile's product with V
   int abort;
   uint32_t tmem;
@@ -122,6 +124,18 @@ __device__ __forceinline__ int clc_read(uint32_t answer) {
       : "r"(answer)
       : "memory");
   return ok ? (int)x : -1;
+}
+// Whether the phase is over, at once (a try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err,
                                        long long budget) {
@@ -182,6 +196,29 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 __device__ __forceinline__ void st_shared_zero(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
+// 128 bytes of each of a warp's 32 rows to memory, by way of shared memory so that a store covers
+// whole lines (a thread that stores its own row touches a line with every 16 bytes: 32 lines an
+// instruction, one a cycle for the SM). `row`: the thread's row in the tile, `hr` its place in
+// memory (negative: none), a place every `row_bytes` bytes from `dst` on.
+__device__ __forceinline__ void stage_rows(uint32_t stage, int row, const uint32_t (&y)[32], int64_t hr, char *dst,
+                                        int row_bytes) {
+  const int lane = row & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + row * 128 + ((c ^ (row & 7)) << 4)),
+                 "r"(y[4 * c]), "r"(y[4 * c + 1]), "r"(y[4 * c + 2]), "r"(y[4 * c + 3])
+                 : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), c = lane & 7;  // four rows at a time, eight lanes a row
+    const int64_t at = __shfl_sync(0xffffffffu, hr, r);
+    const uint4 v = ld_shared_v4(stage + (row - lane + r) * 128 + ((c ^ (r & 7)) << 4));
+    if (at >= 0) *reinterpret_cast<uint4 *>(dst + at * row_bytes + c * 16) = v;
+  }
+  __syncwarp();
 }
 
 // A row's output and the weights of its tile's first half times alpha.
@@ -249,66 +286,40 @@ __device__ __noinline__ void slow_pv(uint32_t p, uint32_t o, uint32_t v, uint4 s
   tmem_wait_st();
 }
 
-// A tile that the mask cuts, or whose cached keys do not fill it: which of its keys the row sees
-// (`seen`), V of keys that no row sees zeroed, and whether V of the others has an infinity or NaN
-// that some row does not see. One thread a key row of V, all of a softmax warpgroup together.
-// `valid`: keys of this request; `lim`: those that the row sees; `first_lim`: that the first row sees.
-struct LookArgs {
-  uint32_t v_row, scan_bar;        // shared memory: this thread's key row of V, the warps' barrier
-  int valid, lim, first_lim, base, C, tag;
-  const int32_t *table;            // bad pages: this request's page table, else NULL
-  int block_size, num_pages;
-  uint32_t scans;
-};
+// Whether cached key `key` lies in a page of the pool.
+__device__ __forceinline__ bool page_good(const PromptArgs &a, const Item &x, int key) {
+  if (key >= x.C) return false;
+  const int page = __ldg(a.page_table + (int64_t)x.b * a.max_pages_per_seq + key / a.block_size);
+  return page >= 0 && page < a.num_pages;
+}
+// Half a tile of V in shared memory, two rows a lane: rows that no query sees become zeros; whether
+// the others hold an infinity or NaN, where the mask cuts through the tile (`cut`).
 template <int D>
-__device__ __noinline__ bool look_at(const LookArgs &k, volatile int *odd_tag, volatile int *abort_flag,
-                                     int32_t *err, long long budget, uint4 &seen, bool &odd) {
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  uint32_t word[4];
+__device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_t v, int half, int base,
+                                     int valid, bool cut, bool bad) {
+  const int lane = threadIdx.x & 31;
+  uint32_t hit = 0;  // exponents of all ones carry into the sign's place
+#pragma unroll 1
+  for (int row = half * 64 + lane; row < half * 64 + 64; row += 32) {
+    const uint32_t at = v + row * 128;
+    if (row >= valid || (bad && !page_good(a, x, base + row))) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int y = k.lim - 32 * i;
-    word[i] = y >= 32 ? ~0u : y <= 0 ? 0u : (1u << y) - 1u;
-  }
-  bool key_ok = warp * 32 + lane < k.valid;
-  if (k.table) {
+      for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = k.base + 32 * i + lane;
-      const int page = key < k.C ? __ldg(k.table + key / k.block_size) : -1;
-      const bool good = page >= 0 && page < k.num_pages;
-      word[i] &= __ballot_sync(0xffffffffu, good);
-      if (i == warp) key_ok = key_ok && good;
+        for (int c = 0; c < 8; ++c) st_shared_zero(at + h * 16384 + c * 16);
+    } else if (cut) {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 y = ld_shared_v4(at + h * 16384 + (((c + lane) & 7) << 4));
+          hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                 ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+        }
     }
   }
-  seen = make_uint4(word[0], word[1], word[2], word[3]);
-  odd = false;
-  if (!key_ok) {
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) st_shared_zero(k.v_row + h * 16384 + c * 16);
-  } else if (k.first_lim < k.valid) {
-    uint32_t hit = 0;  // exponents of all ones carry into the sign's place
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 y = ld_shared_v4(k.v_row + h * 16384 + (((c + lane) & 7) << 4));
-        hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-               ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
-      }
-    odd = (hit & 0x80008000u) != 0;
-  }
   fence_proxy_async_smem();  // the zeros, before the MMA reads V
-  odd = __any_sync(0xffffffffu, odd);
-  if (lane == 0) {
-    if (odd) odd_tag[k.scans & 1] = k.tag;
-    mbar_arrive(k.scan_bar);
-  }
-  const bool ok = mbar_wait(k.scan_bar, k.scans & 1, abort_flag, err, budget);
-  odd = odd_tag[k.scans & 1] == k.tag;
-  return __all_sync(0xffffffffu, ok);
+  return __any_sync(0xffffffffu, (hit & 0x80008000u) != 0);
 }
 
 template <int D>
@@ -330,19 +341,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NE; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
+      mbar_init(smem_u32(&bars->clean[i]), 2);
     }
-    mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), 8);  // the softmax warps
+    }
     mbar_init(smem_u32(&bars->drain), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&bars->s_full[w]), 1);
       mbar_init(smem_u32(&bars->p_full[w]), 4);  // the warps of a softmax warpgroup
       mbar_init(smem_u32(&bars->o_full[w]), 1);
       mbar_init(smem_u32(&bars->o_empty[w]), 4);
-      mbar_init(smem_u32(&bars->scan[w]), 4);
       mbar_init(smem_u32(&bars->slot_full[w]), 1);
-      mbar_init(smem_u32(&bars->slot_empty[w]), 9);  // issuer and softmax warps
-      bars->odd[w][0] = bars->odd[w][1] = bars->skip[w] = 0;
+      mbar_init(smem_u32(&bars->slot_empty[w]), 11);  // everybody but the producer
+      bars->skip[w] = 0;
     }
     mbar_init(smem_u32(&bars->clc), 1);
     bars->abort = 0;
@@ -408,18 +421,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             bars->slot[sl] = w;
             mbar_arrive(smem_u32(&bars->slot_full[sl]));
           }
-          ok = mbar_wait(smem_u32(&bars->q_empty), (items & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
+          ok = mbar_wait(smem_u32(&bars->q_empty[sl]), ((items >> 1) & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++items;
           if (lane == 0) {
-            const uint32_t bar = smem_u32(&bars->q_full);
+            const uint32_t bar = smem_u32(&bars->q_full[sl]);
             mbar_arrive_expect_tx(bar, 2 * L::kHalves * QI * G * 128);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int h = 0; h < L::kHalves; ++h)
-                tma_load_3d(sb + i * L::kTile + h * 16384, &tm_q, bar, h * 64, w.g * G,
+                tma_load_3d(sb + (2 * sl + i) * L::kTile + h * 16384, &tm_q, bar, h * 64, w.g * G,
                             w.q0 + w.i0 + i * QI);
           }
           // page ids of the next cached tile, one a lane
@@ -495,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Drain: what was asked for has landed before the CTA ends.
       if (lane == 0) {
         volatile int no_abort = 0;
-        if (items) mbar_wait(smem_u32(&bars->q_full), (items - 1) & 1, &no_abort, a.err, kDrainCycles);
+        for (uint32_t u = items > 2 ? items - 2 : 0; u < items; ++u)
+          mbar_wait(smem_u32(&bars->q_full[u & 1]), (u >> 1) & 1, &no_abort, a.err, kDrainCycles);
         for (uint32_t u = e > (uint32_t)NE ? e - NE : 0; u < e; ++u)
           mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
         if (asked) mbar_wait(smem_u32(&bars->clc), (asked - 1) & 1, &no_abort, a.err, kDrainCycles);
@@ -511,83 +525,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = smem_desc_sw128(sb + L::kRing, 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(sb + L::kRing, 16384, 1024);
       // (Elected, not lane 0: 16,384 causal rows of 28 on 4 heads 1777 -> 1343 us.)
-      const uint32_t full = smem_u32(bars->full), empty = smem_u32(bars->empty);
-      uint32_t sk = 0, pk = 0;      // ring entry of K of tile t, parity of its phase
+      const uint32_t full = smem_u32(bars->full), empty = smem_u32(bars->empty), clean = smem_u32(bars->clean);
+      uint32_t sk = 0, pk = 0;        // ring entry of the next K, parity of its phase
       uint32_t p_par = 0, o_par = 3;  // parities, a bit a row tile: p_full, o_empty
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, a.err, a.wait_cycles);
       };
-      for (uint32_t item = 0;; ++item) {
-        const int sl = item & 1;
-        if (!wait(smem_u32(&bars->slot_full[sl]), (item >> 1) & 1)) break;
-        const int b = bars->slot[sl].b, t0 = bars->slot[sl].t0, t1 = bars->slot[sl].t1;
-        const int tw0 = min(t1, bars->slot[sl].tw[0]), tw1 = min(t1, bars->slot[sl].tw[1]);
-        mbar_arrive(smem_u32(&bars->slot_empty[sl]));
-        if (b < 0) break;
-        if (!wait(smem_u32(&bars->q_full), item & 1)) break;
-        bool ok = true;
-        uint32_t sv = 0, pv = 0;  // V of tile t - 1
-#pragma unroll 1
-        for (int t = t0; t <= t1 && ok; ++t) {  // (t1: the last products with V)
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            const int tw = w ? tw1 : tw0;
-            const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
-            if (t > t0 && t - 1 < tw) {
-              ok = wait(full + 8 * sv, pv);
-              if (ok && t - 1 == t0) {
-                ok = wait(smem_u32(&bars->o_empty[w]), (o_par >> w) & 1);
-                o_par ^= 1u << w;
-              }
-              ok = ok && wait(smem_u32(&bars->p_full[w]), (p_par >> w) & 1);
-              if (!ok) break;
-              p_par ^= 1u << w;
-              tc_fence_after();
-              if (!*(volatile int *)&bars->skip[w]) {
-                const uint64_t vd = smem_desc_advance(v_desc, sv * L::kTile);
-                const uint32_t more = t - 1 > t0 ? 1u : 0u;
-#pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                  umma_bf16_tmem_a(to, ts + ks * 8, smem_desc_advance(vd, ks * 2048), idesc_pv,
-                                   ks > 0 ? 1u : more);
-              }
-              if (t == tw) umma_commit(smem_u32(&bars->o_full[w]));
-            }
-            if (w && t > t0) umma_commit(empty + 8 * sv);
-            if (t < tw) {
-              ok = wait(full + 8 * sk, pk);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t qd = smem_desc_advance(q_desc, w * L::kTile);
-              const uint64_t kd = smem_desc_advance(k_desc, sk * L::kTile);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                umma_bf16(ts, smem_desc_advance(qd, at), smem_desc_advance(kd, at), idesc_qk, k ? 1u : 0u);
-              }
-              umma_commit(smem_u32(&bars->s_full[w]));
-            }
-            if (w && t < t1) {
-              umma_commit(empty + 8 * sk);
-              if (t + 1 == t1) umma_commit(smem_u32(&bars->q_empty));
-            }
+      // The item in work and its next tile; the tile before it, whose products with V are still to come
+      // (they stay so over the change of items where the next one's operands have landed).
+      uint32_t item = 0;
+      int t = 0, t0 = 0, t1 = 0, tw0 = 0, tw1 = 0;
+      uint32_t sv = 0, pv = 0, todo = 0, last = 0, more = 0, qs = 0;  // todo, last: a bit a row tile
+      bool behind = false;
+      while (true) {
+        bool score = t < t1;
+        if (!score) {
+          const uint32_t sl = item & 1, par = (item >> 1) & 1;
+          bool ready = mbar_test(smem_u32(&bars->slot_full[sl]), par);
+          if (!ready && !behind) {
+            if (!wait(smem_u32(&bars->slot_full[sl]), par)) break;
+            ready = true;
           }
-          if (t < t1) {
-            sv = sk + 1 == NE ? 0 : sk + 1;
-            pv = sk + 1 == NE ? pk ^ 1 : pk;
-            sk += 2;
-            if (sk >= NE) {
-              sk -= NE;
-              pk ^= 1;
+          if (ready) {
+            const bool end = bars->slot[sl].b < 0;
+            if (end && !behind) break;
+            if (!end && (!behind || (mbar_test(smem_u32(&bars->q_full[sl]), par) && mbar_test(full + 8 * sk, pk)))) {
+              t0 = t = bars->slot[sl].t0;
+              t1 = bars->slot[sl].t1;
+              tw0 = min(t1, bars->slot[sl].tw[0]);
+              tw1 = min(t1, bars->slot[sl].tw[1]);
+              mbar_arrive(smem_u32(&bars->slot_empty[sl]));
+              ++item;
+              if (!wait(smem_u32(&bars->q_full[sl]), par)) break;
+              qs = 2 * sl;
+              score = t < t1;
+              if (!score) continue;  // (a split without keys)
             }
           }
         }
+        bool ok = true;
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
+          if (todo >> w & 1u) {
+            ok = wait(clean + 8 * sv, pv);
+            if (ok && !more) {
+              ok = wait(smem_u32(&bars->o_empty[w]), (o_par >> w) & 1);
+              o_par ^= 1u << w;
+            }
+            ok = ok && wait(smem_u32(&bars->p_full[w]), (p_par >> w) & 1);
+            if (!ok) break;
+            p_par ^= 1u << w;
+            tc_fence_after();
+            if (!*(volatile int *)&bars->skip[w]) {
+              const uint64_t vd = smem_desc_advance(v_desc, sv * L::kTile);
+#pragma unroll
+              for (int ks = 0; ks < kKeys / 16; ++ks)
+                umma_bf16_tmem_a(to, ts + ks * 8, smem_desc_advance(vd, ks * 2048), idesc_pv, ks > 0 ? 1u : more);
+            }
+            if (last >> w & 1u) umma_commit(smem_u32(&bars->o_full[w]));
+          }
+          if (w && behind) umma_commit(empty + 8 * sv);
+          if (score && t < (w ? tw1 : tw0)) {
+            ok = wait(full + 8 * sk, pk);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = smem_desc_advance(q_desc, (qs + w) * L::kTile);
+            const uint64_t kd = smem_desc_advance(k_desc, sk * L::kTile);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+              umma_bf16(ts, smem_desc_advance(qd, at), smem_desc_advance(kd, at), idesc_qk, k ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&bars->s_full[w]));
+          }
+        }
         if (!ok) break;
-        if (t0 == t1) umma_commit(smem_u32(&bars->q_empty));
+        behind = score;
+        todo = 0;
+        if (score) {
+          umma_commit(empty + 8 * sk);
+          todo = (t < tw0 ? 1u : 0u) | (t < tw1 ? 2u : 0u);
+          last = (t == tw0 - 1 ? 1u : 0u) | (t == tw1 - 1 ? 2u : 0u);
+          more = t > t0 ? 1u : 0u;
+          sv = sk + 1 == NE ? 0 : sk + 1;
+          pv = sk + 1 == NE ? pk ^ 1 : pk;
+          sk += 2;
+          if (sk >= NE) {
+            sk -= NE;
+            pk ^= 1;
+          }
+          ++t;
+        }
       }
       umma_commit(smem_u32(&bars->drain));
       volatile int no_abort = 0;
       mbar_wait(smem_u32(&bars->drain), 0, &no_abort, a.err, kDrainCycles);
+    } else if (warp >= 2) {
+      // ============ V of tiles that the mask cuts: half a tile a warp ============
+      const int half = warp - 2;
+      uint32_t e = 0;
+      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const uint32_t at = smem_u32(bar);
+        const bool x = mbar_try_wait(at, parity) || wait_long(at, parity, abort_flag, a.err, a.wait_cycles);
+        return __all_sync(0xffffffffu, x);
+      };
+      bool ok = true;
+      for (uint32_t item = 0; ok; ++item) {
+        const int sl = item & 1;
+        if (!wait(&bars->slot_full[sl], (item >> 1) & 1)) break;
+        const Item x = bars->slot[sl];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->slot_empty[sl]));
+        if (x.b < 0) break;
+        const int first_limit = seq_limit(min(x.i0, x.n - 1), x.n, a.mask_block);  // (the first row's)
+#pragma unroll 1
+        for (int u = 2 * x.t0; u < 2 * x.t1 && ok; ++u, ++e) {  // K and V tiles in turn
+          const uint32_t ent = e % NE;
+          ok = wait(&bars->full[ent], (e / NE) & 1);
+          if (!ok) break;
+          if (u & 1) {
+            const int t = u >> 1;
+            const bool cached = t < x.Tc;
+            const int base = (cached ? t : t - x.Tc) * kKeys, valid = (cached ? x.C : x.n) - base;
+            const bool cut = !cached && first_limit - base < min(kKeys, valid);
+            const bool bad = cached && *(volatile int *)&bars->bad[ent] != 0;
+            bool odd = false;
+            if (bad || cut || valid < kKeys)
+              odd = clean_v<D>(a, x, sb + L::kRing + ent * L::kTile, half, base, valid, cut, bad);
+            if (lane == 0) *(volatile int *)&bars->odd[ent][half] = odd;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->clean[ent]));
+        }
+      }
     }
   } else {
     // ============ softmax: warpgroup w, a thread a row ==========================
@@ -599,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qi = row / G, qh = row % G;
     const int64_t n_hr = (int64_t)a.rows * a.num_heads_q;
     const float sl2 = a.scale_log2;
-    uint32_t e = 0, tiles = 0, outs = 0, scans = 0;
+    uint32_t e = 0, tiles = 0, outs = 0;
     int was_odd = 0;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
       const bool x = mbar_wait(smem_u32(bar), parity, abort_flag, a.err, a.wait_cycles);
@@ -623,34 +694,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = x.t0; t < tw; ++t) {
         const uint32_t ev = e + 2 * (t - x.t0) + 1;
         const bool cached = t < x.Tc;
-        bool bad = false;
-        if (cached) {  // (S of the tile comes after its V has landed then)
-          ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
-          if (!ok) break;
-          bad = *(volatile int *)&bars->bad[ev % NE] != 0;
-        }
         const int base = (cached ? t : t - x.Tc) * kKeys;
-        const bool look = bad || base + kKeys > (cached ? x.C : first_limit);
+        bool look = base + kKeys > (cached ? x.C : first_limit);  // some row does not see some key
         uint4 sees;
         bool odd = false;
-        if (__builtin_expect(look, 0)) {
-          ok = wait(&bars->full[ev % NE], (ev / NE) & 1);
+        if (__builtin_expect(look || cached, 0)) {
+          ok = wait(&bars->clean[ev % NE], (ev / NE) & 1);
           if (!ok) break;
-          LookArgs k;
-          k.v_row = sb + L::kRing + (ev % NE) * L::kTile + row * 128;
-          k.scan_bar = smem_u32(&bars->scan[w]);
-          k.valid = min(kKeys, (cached ? x.C : x.n) - base);
-          k.lim = cached ? k.valid : min(k.valid, limit - base);
-          k.first_lim = cached ? k.valid : min(k.valid, first_limit - base);
-          k.base = base;
-          k.C = x.C;
-          k.tag = (int)tiles + 1;
-          k.table = bad ? a.page_table + (int64_t)x.b * a.max_pages_per_seq : nullptr;
-          k.block_size = a.block_size;
-          k.num_pages = a.num_pages;
-          k.scans = scans++;
-          ok = look_at<D>(k, bars->odd[w], abort_flag, a.err, a.wait_cycles, sees, odd);
-          if (!ok) break;
+          const volatile Bars *vb = bars;
+          const bool bad = cached && vb->bad[ev % NE];
+          look = look || bad;
+          if (look) {
+            odd = vb->odd[ev % NE][0] || vb->odd[ev % NE][1];
+            const int lim = cached ? x.C - base : limit - base;
+            uint32_t word[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int y = lim - 32 * k;
+              word[k] = y >= 32 ? ~0u : y <= 0 ? 0u : (1u << y) - 1u;
+            }
+            if (bad)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                word[k] &= __ballot_sync(0xffffffffu, page_good(a, x, base + 32 * k + lane));
+            sees = make_uint4(word[0], word[1], word[2], word[3]);
+          }
         }
         ok = wait(&bars->s_full[w], tiles & 1);
         if (!ok) break;
@@ -679,6 +747,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               sum[k] = 0.f;
               mx[k] = -INFINITY;
+            }
+            if (__builtin_expect(first && c == 0 && m_ref == kNothing, 0)) {  // an item's first scores
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                mx[j & 3] = fmax3(mx[j & 3], __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              m_ref = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2, kNothing);
             }
             const float neg = -m_ref;
             constexpr int kA = 2, kB = 6;
@@ -737,54 +811,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       e += 2 * (x.t1 - x.t0);
-      const int64_t hr = rv ? (int64_t)(x.q0 + i) * a.num_heads_q + x.g * G + qh : 0;
-      if (a.num_splits > 1) {
-        float *dst = a.ws_o + (x.split * n_hr + hr) * D;
-        if (rv) a.ws_ml[x.split * n_hr + hr] = make_float2(m_ref == kNothing ? -INFINITY : m_ref, l);
-        if (tw > x.t0) {
-          if (!wait(&bars->o_full[w], outs & 1)) break;
-          ++outs;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + c * 32, o);
-            if (rv)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4 *>(dst + c * 32 + 4 * j) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty[w]));
-        }
-      } else if (tw > x.t0) {
+      const int64_t hr = rv ? (int64_t)(x.q0 + i) * a.num_heads_q + x.g * G + qh : -1;
+      const uint32_t stage = sb + (2 * sl + w) * L::kTile;  // the queries' place: S is done with them
+      if (tw > x.t0) {
         if (!wait(&bars->o_full[w], outs & 1)) break;
         ++outs;
         tc_fence_after();
         const float inv = 1.0f / l;
-        uint16_t *dst = static_cast<uint16_t *>(a.out) + hr * D;
+        const bool parts = a.num_splits > 1;
+        char *dst = parts ? reinterpret_cast<char *>(a.ws_o + x.split * n_hr * D) : static_cast<char *>(a.out);
+        // 128 bytes of every row at a time: bf16 outputs of 64 columns, or float parts of 32
+        const int chunks = parts ? D / 32 : D / 64, row_bytes = chunks * 128;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(to + c * 32, o);
-          if (rv) {
-            uint32_t y[16];
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t y[32];
+          if (parts) {
+            tmem_ld32(to + c * 32, y);
+          } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              y[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[32];
+              tmem_ld32(to + c * 64 + h * 32, o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4 *>(dst + c * 32 + 8 * j) =
-                  make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+              for (int j = 0; j < 16; ++j)
+                y[h * 16 + j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            }
           }
+          stage_rows(stage, row, y, hr, dst + c * 128, row_bytes);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->o_empty[w]));
-        if (rv && a.lse_out) a.lse_out[hr] = (m_ref + __log2f(l)) * 0.6931471805599453f;
+        fence_proxy_async_smem();  // (the next queries come by a tensor copy)
+      } else if (!wait(&bars->q_full[sl], (item >> 1) & 1)) {
+        break;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[sl]));
+      if (rv && a.num_splits > 1)
+        a.ws_ml[x.split * n_hr + hr] = make_float2(m_ref == kNothing ? -INFINITY : m_ref, l);
+      else if (rv && a.lse_out)
+        a.lse_out[hr] = (m_ref + __log2f(l)) * 0.6931471805599453f;
     }
   }
 
