@@ -21,18 +21,19 @@
 //
 // Roles of a CTA's warps:
 //   0        producer: which request an item belongs to, tensor copies of the queries and of the
-//            K and V tiles (of the pages for cached keys, one box a page and 64 columns)
+//            K and V tiles (of the pages for cached keys, a copy a page and 64 columns; a warp
+//            issues one only every 100 cycles or so, so warp 3 takes half of a tile's pages)
 //   1        MMA issuer (one lane): S = Q K^T, then O += P V with P in TMEM over S, the row tiles
 //            in turn, so that one tile's products run while the other's weights are computed
-//   2, 3     V tiles that the mask cuts, or that pages do not fill (below)
+//   2        V tiles that the mask cuts, or that pages do not fill (below)
 //   4 - 11   softmax: a warpgroup a row tile, a thread a row
 // TMEM columns: S / P of tile 0 and 1 (128 each), O of tile 0 and 1 (D each).
 //
 // What a row does not see. Scores of keys past a row's limit are replaced by -inf, whatever they
 // were. V of keys that no row sees (rows of another request, slots past the context) is zeroed in
 // shared memory before the product. V of keys that only some rows of the tile see has to be
-// finite for the product (0 * infinity is not 0): where the mask cuts through a tile two warps
-// look, and a tile with an infinity or NaN is multiplied by the softmax threads, each with the
+// finite for the product (0 * infinity is not 0): where the mask cuts through a tile a warp
+// looks, and a tile with an infinity or NaN is multiplied by the softmax threads, each with the
 // keys that its row sees.
 //
 // Every wait is bounded; a CTA whose wait ran out records D2F_ERR_TIMEOUT, drains its copies and
@@ -83,7 +84,7 @@ struct Bars {
   __align__(16) uint32_t clc_answer[4];
   Item slot[2];
   int bad[8];                           // ring entry: pages of the tile are missing
-  int odd[8][2];                        // V has an infinity or NaN that not every row sees, by half
+  int odd[8];                           // ... V has an infinity or NaN that not every row sees
   int skip[2];                          // the threads have done this tile's product with V
   int abort;
   uint32_t tmem;
@@ -101,6 +102,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
+}
+// K or V of one page (the i-th of its tile) and KV head, a copy a 64 columns.
+template <int D>
+__device__ __forceinline__ void load_page(uint32_t tile, const CUtensorMap *map, uint32_t bar, int i,
+                                          const PromptArgs &a, int page, int g) {
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+    tma_load_3d(tile + h * 16384 + i * a.block_size * 128, map, bar, h * 64, 0, page * a.num_heads_kv + g);
 }
 // Ask for a CTA of this grid that has not started; the answer lands at `answer`.
 __device__ __forceinline__ void clc_ask(uint32_t answer, uint32_t bar) {
@@ -292,15 +301,15 @@ __device__ __forceinline__ bool page_good(const PromptArgs &a, const Item &x, in
   const int page = __ldg(a.page_table + (int64_t)x.b * a.max_pages_per_seq + key / a.block_size);
   return page >= 0 && page < a.num_pages;
 }
-// Half a tile of V in shared memory, two rows a lane: rows that no query sees become zeros; whether
+// A tile of V in shared memory, four rows a lane: rows that no query sees become zeros; whether
 // the others hold an infinity or NaN, where the mask cuts through the tile (`cut`).
 template <int D>
-__device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_t v, int half, int base,
-                                     int valid, bool cut, bool bad) {
+__device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_t v, int base, int valid,
+                                     bool cut, bool bad) {
   const int lane = threadIdx.x & 31;
   uint32_t hit = 0;  // exponents of all ones carry into the sign's place
 #pragma unroll 1
-  for (int row = half * 64 + lane; row < half * 64 + 64; row += 32) {
+  for (int row = lane; row < kKeys; row += 32) {
     const uint32_t at = v + row * 128;
     if (row >= valid || (bad && !page_good(a, x, base + row))) {
 #pragma unroll
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NE; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 1);
-      mbar_init(smem_u32(&bars->clean[i]), 2);
+      mbar_init(smem_u32(&bars->clean[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->o_full[w]), 1);
       mbar_init(smem_u32(&bars->o_empty[w]), 4);
       mbar_init(smem_u32(&bars->slot_full[w]), 1);
-      mbar_init(smem_u32(&bars->slot_empty[w]), 11);  // everybody but the producer
+      mbar_init(smem_u32(&bars->slot_empty[w]), 11);  // every warp but the producer
       bars->skip[w] = 0;
     }
     mbar_init(smem_u32(&bars->clc), 1);
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           int page = w.t0 < w.Tc ? page_of(w.t0) : 0;
           for (int t = w.t0; t < w.t1 && ok; ++t) {
-            if (t == w.t1 - 1) ask();
+            if (t == max(w.t0, w.t1 - 4)) ask();
             const bool cached = t < w.Tc;
             const bool need = cached && lane < pages && (t * pages + lane) * a.block_size < w.C;
             const bool good = need && page >= 0 && page < a.num_pages;
@@ -465,19 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mbar_arrive_expect_tx(bar, n_good * a.block_size * 128 * L::kHalves);
                 }
                 __syncwarp();
-                if (good) {
-#pragma unroll
-                  for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(dst + h * 16384 + lane * a.block_size * 128, kv ? &tm_vp : &tm_kp, bar,
-                                h * 64, 0, page * a.num_heads_kv + w.g);
-                }
-              } else if (lane == 0) {
+                if (good && lane < (pages + 1) / 2) load_page<D>(dst, kv ? &tm_vp : &tm_kp, bar, lane, a, page, w.g);
+              } else if (elect_one()) {
                 mbar_arrive_expect_tx(bar, L::kTile);
 #pragma unroll
                 for (int h = 0; h < L::kHalves; ++h)
                   tma_load_3d(dst + h * 16384, kv ? &tm_v : &tm_k, bar, h * 64, w.g,
                               w.q0 + (t - w.Tc) * kKeys);
               }
+              __syncwarp();
               ++e;
             }
             page = next;
@@ -621,9 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(smem_u32(&bars->drain));
       volatile int no_abort = 0;
       mbar_wait(smem_u32(&bars->drain), 0, &no_abort, a.err, kDrainCycles);
-    } else if (warp >= 2) {
-      // ============ V of tiles that the mask cuts: half a tile a warp ============
-      const int half = warp - 2;
+    } else if (warp == 2) {
+      // ============ V of tiles that the mask cuts =================================
       uint32_t e = 0;
       auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         const uint32_t at = smem_u32(bar);
@@ -652,12 +656,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool bad = cached && *(volatile int *)&bars->bad[ent] != 0;
             bool odd = false;
             if (bad || cut || valid < kKeys)
-              odd = clean_v<D>(a, x, sb + L::kRing + ent * L::kTile, half, base, valid, cut, bad);
-            if (lane == 0) *(volatile int *)&bars->odd[ent][half] = odd;
+              odd = clean_v<D>(a, x, sb + L::kRing + ent * L::kTile, base, valid, cut, bad);
+            if (lane == 0) *(volatile int *)&bars->odd[ent] = odd;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->clean[ent]));
         }
+      }
+    } else if (warp == 3) {
+      // ============ second producer of cached tiles: half of their pages =========
+      const int pages = kKeys / a.block_size, mine = (pages + 1) / 2;
+      uint32_t e = 0, issued = 0;
+      bool ok = true;
+      for (uint32_t item = 0; ok; ++item) {
+        const int sl = item & 1;
+        ok = mbar_wait(smem_u32(&bars->slot_full[sl]), (item >> 1) & 1, abort_flag, a.err, a.wait_cycles);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const Item x = bars->slot[sl];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->slot_empty[sl]));
+        if (x.b < 0) break;
+        const int32_t *table = a.page_table + (int64_t)x.b * a.max_pages_per_seq;
+        auto page_of = [&](int t) {
+          const int at = t * pages + lane;
+          return lane >= mine && lane < pages && t < x.Tc && at * a.block_size < x.C ? __ldg(table + at) : -1;
+        };
+        const int end = min(x.t1, x.Tc);
+        int page = x.t0 < end ? page_of(x.t0) : -1;
+        for (int t = x.t0; t < end && ok; ++t) {
+          const int next = t + 1 < end ? page_of(t + 1) : -1;
+          const bool good = page >= 0 && page < a.num_pages;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t u = e + 2 * (t - x.t0) + kv, ent = u % NE;
+            ok = mbar_wait(smem_u32(&bars->empty[ent]), ((u / NE) & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (good)
+              load_page<D>(sb + L::kRing + ent * L::kTile, kv ? &tm_vp : &tm_kp, smem_u32(&bars->full[ent]), lane, a,
+                           page, x.g);
+            issued = u + 1;
+          }
+          page = next;
+        }
+        e += 2 * (x.t1 - x.t0);
+      }
+      if (!ok && lane == 0) {  // what was asked for has landed before the CTA ends
+        volatile int no_abort = 0;
+        for (uint32_t u = issued > (uint32_t)NE ? issued - NE : 0; u < issued; ++u)
+          mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
       }
     }
   } else {
@@ -705,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool bad = cached && vb->bad[ev % NE];
           look = look || bad;
           if (look) {
-            odd = vb->odd[ev % NE][0] || vb->odd[ev % NE][1];
+            odd = vb->odd[ev % NE] != 0;
             const int lim = cached ? x.C - base : limit - base;
             uint32_t word[4];
 #pragma unroll
