@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "d2f.h"
 
 namespace d2f {
@@ -288,6 +290,19 @@ constexpr int kSkSlotBytes = 128 * 128 * 2 + 128 * 8;
 // Device helpers
 // ---------------------------------------------------------------------------
 #ifdef __CUDACC__
+// Let a kernel have `bytes` of dynamic shared memory, always the same: asked for once a device
+// (threads whose first calls meet ask twice).
+template <auto kKernel>
+cudaError_t allow_smem_once(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 __device__ __forceinline__ void set_err(int32_t *err, int code) {
   if (err) atomicCAS(err, 0, code);
 }

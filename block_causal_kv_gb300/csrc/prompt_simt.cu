@@ -322,9 +322,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
 template <typename T, int D>
 cudaError_t launch_d(const PromptArgs &a, cudaStream_t s) {
   constexpr size_t bytes = smem_bytes<D>();
-  // (per device; every call sets the same value)
-  cudaError_t e = cudaFuncSetAttribute(prompt_simt_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const cudaError_t e = allow_smem_once<&prompt_simt_kernel<T, D>>((int)bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.tiles * a.num_heads_kv * a.chunks * a.num_splits;
   prompt_simt_kernel<T, D><<<(unsigned)items, kThreads, bytes, s>>>(a);
@@ -334,6 +332,7 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t merge_d(const PromptArgs &a, cudaStream_t s) {
   const int64_t n_hr = (int64_t)a.rows * a.num_heads_q;
+  // (an ordinary launch: started early, its CTAs cost the few that still work more than they save)
   prompt_merge_kernel<T, D><<<(unsigned)((n_hr + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError();
 }

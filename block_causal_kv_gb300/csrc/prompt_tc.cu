@@ -375,11 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&bars->tmem), 512);
     tmem_relinquish();
   }
-  if (warp == 3 && blockIdx.x == 0) seq_report(a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  grid_dependency_wait();  // (what is above reads nothing that the kernel before may write)
+  if (warp == 3 && blockIdx.x == 0) seq_report(a);
 
   if (warp < 4) {
     reg_dec<kRegCtl>();
@@ -960,8 +961,17 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t s, char *why, size_t why_
     return cudaErrorInvalidValue;
   }
   const int64_t items = (int64_t)a.tiles * Hk * a.num_splits;
-  prompt_tc_kernel<D><<<(unsigned)items, kThreads, bytes, s>>>(a, q, k, v, kp, vp);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, prompt_tc_kernel<D>, a, q, k, v, kp, vp);
 }
 
 }  // namespace
