@@ -1395,7 +1395,7 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
   const int sms = max(1, num_sms_current_device());
   const int G = Hq / Hkv;
   p->tc = dtype == D2F_BF16 && (D == 64 || D == 128) && !force_simt();
-  p->head_chunk = !p->tc ? kTokenSimtHeads : G <= 8 ? 8 : 16;
+  p->head_chunk = p->tc ? (G <= 8 ? 8 : 16) : G == 1 ? 1 : G == 2 ? 2 : 4;
   p->chunks = cdiv(G, p->head_chunk);
   const long long pairs = (long long)max(batch, 1) * Hkv * p->chunks;
   if (pairs > 0x7fffffffLL / 64)
@@ -1412,9 +1412,13 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
                                     sizeof(float);
     return D2F_OK;
   }
-  // Four CTAs an SM, at least 64 keys each; at most 64 parts to compose.
-  p->splits = (int)max(1LL, min(min(4LL * sms / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
-  p->off_partial = counter_bytes(p->splits > 1 ? pairs : 0);
+  // At least 64 keys a part and at most 64 parts to compose. Float32, D = 128, whole calls: 2 CTAs
+  // an SM for four heads (1 x 4096 tokens 34 us, 48 with 4), 3 for two, 12 for one, whose uneven
+  // sequences then balance (16 x 200-4096 tokens 190 us; 212 with 8, 243 with 4).
+  // A counter a pair: more of them than the counters' region holds are not split.
+  const long long most = pairs > 4LL * sms ? 1 : (p->head_chunk == 4 ? 2 : p->head_chunk == 2 ? 3 : 12) * sms;
+  p->splits = (int)max(1LL, min(min(most / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
+  p->off_partial = counter_bytes(0);
   const size_t part = (size_t)p->head_chunk * (D * sizeof(float) + sizeof(float2));
   p->bytes = p->splits > 1 ? p->off_partial + pairs * p->splits * part : 0;
   return D2F_OK;

@@ -216,7 +216,6 @@ struct PromptArgs {
 constexpr int kPromptSimtRows = 64;  // packed rows (query, head) of a CUDA-core tile
 constexpr int kPromptMaxSplits = 16;
 
-constexpr int kTokenSimtHeads = 4;  // query heads of a CTA, CUDA-core path of the token attention
 // One new token a sequence over the paged cache (token_attn.cu, token_simt.cu).
 struct TokenArgs {
   const void *q;               // [batch][Hq][head_dim]

@@ -5,7 +5,7 @@
 // 빨라지는 방법", §운영 관점 (paged cache, one block a page); "확산 언어 모델(Diffusion
 // LLM)이란 무엇인가", §FlashBlock (attention parts recombined in log space).
 //
-// A CTA takes up to four query heads of a (sequence, KV head) and one split of its cached keys.
+// A CTA takes up to HC = 1, 2 or 4 query heads of a (sequence, KV head) and one split of its keys.
 // Eight lanes hold a key: each reads D / 8 of its dims in 16-byte pieces, the dot products are
 // summed over the eight, and every group of eight lanes keeps a softmax state (maximum, sum,
 // output) of its own, so that a key costs three shuffles a head and nothing else crosses lanes
@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kGroups = kThreads / 8;
-constexpr int HC = kTokenSimtHeads;
 
 // N elements (8 or 16 bytes) as floats
 template <typename T, int N>
@@ -51,7 +50,7 @@ __device__ __forceinline__ void load_n(const T *p, float (&x)[N]) {
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int HC>
 __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a) {
   constexpr int VEC = (D / 8 < 16 / (int)sizeof(T)) ? D / 8 : 16 / (int)sizeof(T);
   constexpr int NJ = D / 8 / VEC;  // pieces of a lane: dims (8 j + lane) VEC ..
@@ -104,12 +103,13 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
       for (int c = 0; c < VEC; ++c) q[h][j][c] *= a.scale_log2;
     }
   }
-  auto key = [&](const T *kp, const T *vp) {
-    float kx[NJ][VEC], vx[NJ][VEC];
+  auto load = [&](const T *kp, const T *vp, float (&kx)[NJ][VEC], float (&vx)[NJ][VEC]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) load_n<T, VEC>(kp + (8 * j + ln) * VEC, kx[j]);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) load_n<T, VEC>(vp + (8 * j + ln) * VEC, vx[j]);
+  };
+  auto key = [&](const float (&kx)[NJ][VEC], const float (&vx)[NJ][VEC]) {
     const uint32_t mine = 0xffu << (tid & 24);  // the eight lanes of this key
 #pragma unroll
     for (int h = 0; h < HC; ++h) {
@@ -133,20 +133,43 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
   };
   const int share = (C + a.num_splits - 1) / a.num_splits;
   const int begin = min(C, split * share), end = min(C, begin + share);
-  int page = begin + grp < end ? table[(begin + grp) / B] : 0;
-  for (int t = begin + grp; t < end; t += kGroups) {
-    const int next = t + kGroups < end ? table[(t + kGroups) / B] : 0;
-    if (page < 0 || page >= a.num_pages) {
-      set_err(a.err, D2F_ERR_BAD_INDEX);
-    } else {
-      const int64_t at = (((int64_t)page * Hk + g) * B + t % B) * D;
-      key(Kp + at, Vp + at);
+  // U keys at a time: their loads go out together
+  constexpr int U = HC == 4 ? 1 : 2;
+  int page[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int n = begin + grp + i * kGroups;
+    page[i] = n < end ? table[n / B] : 0;
+  }
+  for (int t = begin + grp; t < end; t += U * kGroups) {
+    int next[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int n = t + (U + i) * kGroups;
+      next[i] = n < end ? table[n / B] : 0;
     }
-    page = next;
+    float kx[U][NJ][VEC], vx[U][NJ][VEC];
+    bool ok[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int n = t + i * kGroups;
+      ok[i] = n < end && page[i] >= 0 && page[i] < a.num_pages;
+      if (n < end && !ok[i]) set_err(a.err, D2F_ERR_BAD_INDEX);
+      if (ok[i]) {
+        const int64_t at = (((int64_t)page[i] * Hk + g) * B + n % B) * D;
+        load(Kp + at, Vp + at, kx[i], vx[i]);
+      }
+      page[i] = next[i];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (ok[i]) key(kx[i], vx[i]);
   }
   if (split == 0 && grp == 0 && a.k_new) {
     const int64_t at = ((int64_t)b * Hk + g) * D;
-    key(static_cast<const T *>(a.k_new) + at, static_cast<const T *>(a.v_new) + at);
+    float kx[NJ][VEC], vx[NJ][VEC];
+    load(static_cast<const T *>(a.k_new) + at, static_cast<const T *>(a.v_new) + at, kx, vx);
+    key(kx, vx);
   }
 
   // ---- the CTA's groups, then the splits ----
@@ -184,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
       if (d == 0) ml[at] = make_float2(top, sum);
     } else {
       const int64_t hr = (int64_t)b * a.num_heads_q + g * a.group + h0 + h;
-      const bool none = top == -INFINITY && sum == 0.f;  // no key
+      const bool none = sum == 0.f;  // no key, or every score is -inf
       store_out<T>(static_cast<T *>(a.out) + hr * D + d, none ? 0.f : acc / sum);
       if (d == 0 && a.lse_out) a.lse_out[hr] = (top + __log2f(sum)) * 0.6931471805599453f;
     }
@@ -208,23 +231,29 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
       acc = fmaf(w, __ldcg(a.partial + (at + (int64_t)i * HC) * D + d), acc);
     }
     const int64_t hr = (int64_t)b * a.num_heads_q + g * a.group + h0 + h;
-    const bool none = top == -INFINITY && sum == 0.f;  // no key
+    const bool none = sum == 0.f;  // no key, or every score is -inf
     store_out<T>(static_cast<T *>(a.out) + hr * D + d, none ? 0.f : acc / sum);
     if (d == 0 && a.lse_out) a.lse_out[hr] = (top + __log2f(sum)) * 0.6931471805599453f;
   }
   if (tid == 0) a.counters[pair] = 0;
 }
 
+template <typename T, int D>
+cudaError_t launch_d(const TokenArgs &a, cudaStream_t s) {
+  const int64_t ctas = (int64_t)a.batch * a.num_heads_kv * a.chunks * a.num_splits;
+  if (a.head_chunk == 1) token_simt_kernel<T, D, 1><<<(unsigned)ctas, kThreads, 0, s>>>(a);
+  else if (a.head_chunk == 2) token_simt_kernel<T, D, 2><<<(unsigned)ctas, kThreads, 0, s>>>(a);
+  else token_simt_kernel<T, D, 4><<<(unsigned)ctas, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_t(const TokenArgs &a, cudaStream_t s) {
-  const int64_t ctas = (int64_t)a.batch * a.num_heads_kv * a.chunks * a.num_splits;
   switch (a.head_dim) {
-    case 32: token_simt_kernel<T, 32><<<(unsigned)ctas, kThreads, 0, s>>>(a); break;
-    case 64: token_simt_kernel<T, 64><<<(unsigned)ctas, kThreads, 0, s>>>(a); break;
-    case 128: token_simt_kernel<T, 128><<<(unsigned)ctas, kThreads, 0, s>>>(a); break;
+    case 32: return launch_d<T, 32>(a, s);
+    case 64: return launch_d<T, 64>(a, s);
+    case 128: return launch_d<T, 128>(a, s);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
