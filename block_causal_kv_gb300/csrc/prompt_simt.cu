@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
       continue;
     }
     if (cg == 0 && a.lse_out) a.lse_out[hr] = (m[x] + __log2f(l[x])) * 0.6931471805599453f;
-    const float inv = 1.0f / l[x];
+    const float inv = l[x] == 0.f ? 0.f : 1.0f / l[x];  // (0: every score is -inf)
     T *dst = static_cast<T *>(a.out) + hr * D;
     if (cols)
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = fmaf(ws, __ldcg(src + j), acc[j]);
   }
-  const float inv = 1.0f / L;
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
   T *dst = static_cast<T *>(a.out) + hr * D + lane * V;
 #pragma unroll
   for (int j = 0; j < V; ++j) store_out<T>(dst + j, acc[j] * inv);

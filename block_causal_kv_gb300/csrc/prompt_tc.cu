@@ -56,7 +56,7 @@ constexpr int kThreads = 384;
 constexpr int kRegLaunch = 168, kRegCtl = 104, kRegSoft = 200;
 static_assert(kRegCtl + 2 * kRegSoft <= 3 * kRegLaunch, "register split within the launch's allocation");
 constexpr float kMove = 8.f;         // the reference moves when a score is 2^kMove above it
-constexpr float kNothing = -1e30f;   // reference of a row that has seen no key
+constexpr float kNothing = -3.402823466e38f;  // reference of a row that has seen no key: the lowest float
 
 struct Item {
   int b, q0, n, C;      // request, its first row, rows, cached tokens (b < 0: no more items)
@@ -803,6 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx[j & 3] = fmax3(mx[j & 3], __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               m_ref = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2, kNothing);
             }
+            // (One fma a score: the reference's own key has the rounding error of m_ref for its exponent,
+            // up to 2^6 with scores of 2^30. Rounding the product first where that is large cost all
+            // calls 3 to 15 %, whichever way the choice was made.)
             const float neg = -m_ref;
             constexpr int kA = 2, kB = 6;
 #pragma unroll
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->o_full[w], outs & 1)) break;
         ++outs;
         tc_fence_after();
-        const float inv = 1.0f / l;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;  // (0: every score is -inf)
         const bool parts = a.num_splits > 1;
         char *dst = parts ? reinterpret_cast<char *>(a.ws_o + x.split * n_hr * D) : static_cast<char *>(a.out);
         // 128 bytes of every row at a time: bf16 outputs of 64 columns, or float parts of 32

@@ -38,7 +38,7 @@ namespace d2f {
 namespace {
 
 constexpr float kMove = 8.f;
-constexpr float kNothing = -1e30f;         // reference of a head that has seen no key
+constexpr float kNothing = -3.402823466e38f;  // reference of a head that has seen no key: the lowest float
 
 // 16 bytes to shared memory, or 16 zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = 8 * i + 2 * c + e;
         if (h >= heads) continue;
-        const bool none = m[i][e] == kNothing && sum == 0.f;  // no key
+        const bool none = sum == 0.f;  // no key, or every score is -inf
         if (mt.keys & kWhole) {
           const float inv = 1.0f / sum;
           if (r == 0 && a.lse_out)
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kMergeThreads) token_merge_kernel(const TokenA
 #pragma unroll
     for (int j = 0; j < VL; ++j) acc[j] += acc_s[k][lane * VL + j];
   const int64_t hr = (int64_t)b * a.num_heads_q + head;
-  const bool none = top == kNothing && sum == 0.f;  // no key
+  const bool none = sum == 0.f;  // no key, or every score is -inf
   const float inv = 1.0f / sum;
   uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + hr * D + lane * VL);
 #pragma unroll

@@ -795,7 +795,10 @@ int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_hea
  *   max_ctx     host hint used only to split the keys of few rows among CTAs
  *   block_size  1..256 (the page; ctx_len need not be a multiple of it)
  *   head_dim    32, 64 or 128
- * A key that a row does not see never reaches it, not even with infinite or NaN K or V.
+ * A key that a row does not see never reaches it, not even with infinite or NaN K or V. A row all
+ * of whose scores are -infinity gets 0, with -infinity in lse_out. Finite scores are below 5e8 in
+ * magnitude (float then tells no two keys apart that differ by less than 32); with larger
+ * ones bf16 results may be NaN.
  * Results do not depend on the order in which CTAs run. Device buffers are 16-byte aligned.
  *
  * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
@@ -819,7 +822,7 @@ int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int n
 
 /*
  * d2f_token_attn -- one layer's attention of one new token a sequence over the paged cache,
- * and the append of its K and V, in one launch: a step of autoregressive decoding (a window of
+ * and the append of its K and V, in one call: a step of autoregressive decoding (a window of
  * one block of one row) over the pages that D2F's windows use.
  *
  * Query head h of sequence b attends to its ctx_len[b] cached tokens and, with k_new / v_new, to
@@ -838,9 +841,10 @@ int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int n
  *   ctx_len      device int32 [batch], at most max_pages_per_seq * block_size; negative: the
  *                sequence has no token in this call (a finished one in a padded batch), nothing of
  *                it is read or written
- *   out          device [batch][num_heads_q][head_dim], dtype; a sequence without any key gets 0
- *   lse_out      device float [batch][num_heads_q] natural-log normaliser (-inf without any
- *                key), or NULL
+ *   out          device [batch][num_heads_q][head_dim], dtype; a sequence without any key gets 0,
+ *                and so does a head all of whose scores are -infinity
+ *   lse_out      device float [batch][num_heads_q] natural-log normaliser (-infinity where out is
+ *                0 for these reasons), or NULL
  *   max_ctx      host hint used only to split the cache's length among CTAs
  *   block_size   1..256; head_dim 32, 64 or 128
  * Slots at or past ctx_len may hold anything.
