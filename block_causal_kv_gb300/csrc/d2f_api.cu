@@ -1231,7 +1231,9 @@ namespace {
 struct PromptPlan {
   bool tc;
   int tile_q, head_chunk, chunks, tiles, splits;
-  size_t off_ml, off_o, bytes;
+  int grid;
+  bool even;
+  size_t off_count, off_ml, off_o, bytes;
 };
 
 // Sizes that the attention of prompts and of single tokens share.
@@ -1274,10 +1276,25 @@ int plan_prompt(int batch, int rows, int max_ctx, int Hq, int Hkv, int D, int B,
   const long long t_max = cdiv(max_ctx, keys) + (long long)cdiv(rows, keys);
   const long long most = items > 0 ? sms / items : 1;
   p->splits = (int)max(1LL, min(min(most, t_max / 4), (long long)kPromptMaxSplits));
+  // On the tensor cores the device, which knows the lengths, cuts them evenly (seq_even); p->splits
+  // is the most that a row tile gets. Behind prefixes of 64 key tiles (100 us) and more of several
+  // requests it is worth a second launch up to two items an SM: 8 requests of 40 to 77 rows,
+  // 28 heads on 4, behind 100 to 32,768 tokens 464 -> 216 us, 16 requests 504 -> 311.
+  p->grid = (int)min(items, 0x7fffffffLL);
+  p->even = p->tc && batch <= kPromptSplitBatch &&
+            (p->splits > 1 || (items <= 2LL * sms && batch > 1 && max_ctx >= 64 * keys));
+  if (p->even) {
+    p->grid = items <= sms ? sms : 3 * sms;
+    p->splits = (int)min(min(3LL * p->grid / items, t_max), (long long)kPromptMaxSplits);
+    p->splits = max(p->splits, 2);
+  } else if (p->tc) {
+    p->splits = 1;
+  }
   if (items * p->splits > 0x7fffffffLL || (long long)rows * Hq / 8 > 0x7ffffff0LL)
     return fail(D2F_ERR_UNSUPPORTED, "%d rows of %d heads are too many", rows, Hq);
   const size_t n_hr = (size_t)rows * Hq;
-  p->off_ml = counter_bytes(0);  // (the other entry points' counters stay zero)
+  p->off_count = counter_bytes(0);  // (the other entry points' counters stay zero)
+  p->off_ml = p->off_count + align_up(kPromptSplitBatch * sizeof(int32_t));
   p->off_o = p->off_ml + align_up(p->splits * n_hr * sizeof(float2));
   p->bytes = p->splits > 1 ? p->off_o + p->splits * n_hr * D * sizeof(float) : 0;
   return D2F_OK;
@@ -1355,7 +1372,11 @@ int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *
   a.chunks = p.chunks;
   a.num_splits = p.splits;
   a.tiles = p.tiles;
+  a.grid = p.grid;
+  a.sms = max(1, num_sms_current_device());
   a.wait_cycles = wait_budget();
+  a.split_count =
+      p.even ? reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + p.off_count) : nullptr;
   a.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.off_ml);
   a.ws_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_o);
   a.err = err_word;

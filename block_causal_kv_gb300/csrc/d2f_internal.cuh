@@ -206,8 +206,10 @@ struct PromptArgs {
   float scale_log2;            // softmax_scale * log2(e)
   int tile_q;                  // queries of a row tile
   int head_chunk, chunks;      // query heads of an item, chunks of a group
-  int num_splits;              // key splits; more than 1: partials and a second launch
+  int num_splits;              // key splits (at most); more than 1: partials and a second launch
+  int32_t *split_count;        // tensor cores: [batch] splits of a request's row tiles, chosen on the device
   int tiles;                   // row tiles: rows / tile_q + batch, some of them empty
+  int grid, sms;               // tensor cores: items, one a CTA; SMs
   long long wait_cycles;       // budget of each wait on another role's work
   float2 *ws_ml;               // [num_splits][rows * Hq] (max in log2 units, sum)
   float *ws_o;                 // [num_splits][rows * Hq][head_dim] unnormalised
@@ -215,6 +217,7 @@ struct PromptArgs {
 };
 constexpr int kPromptSimtRows = 64;  // packed rows (query, head) of a CUDA-core tile
 constexpr int kPromptMaxSplits = 16;
+constexpr int kPromptSplitBatch = 96;  // requests of a batch whose keys are split on the device
 
 // One new token a sequence over the paged cache (token_attn.cu, token_simt.cu).
 struct TokenArgs {

@@ -293,8 +293,10 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   if (q0 < 0 || q1 > a.rows || row < q0 || row >= q1 || C < 0 ||
       (long long)C > (long long)a.max_pages_per_seq * a.block_size)
     return;
+  const int splits = a.split_count ? __ldcg(a.split_count + lo) : a.num_splits;
+  if (splits <= 1) return;  // (written by its only item)
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (lane < a.num_splits) ml = __ldcg(&a.ws_ml[lane * n_hr + hr]);
+  if (lane < splits) ml = __ldcg(&a.ws_ml[lane * n_hr + hr]);
   float M = ml.x;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
   constexpr int V = D / 32;
   float acc[V] = {};
-  for (int sp = 0; sp < a.num_splits; ++sp) {
+  for (int sp = 0; sp < splits; ++sp) {
     const float ws = __shfl_sync(0xffffffffu, w, sp);
     if (ws == 0.f) continue;
     const float *src = a.ws_o + (sp * n_hr + hr) * D + lane * V;

@@ -60,7 +60,7 @@ constexpr float kNothing = -3.402823466e38f;  // reference of a row that has see
 
 struct Item {
   int b, q0, n, C;      // request, its first row, rows, cached tokens (b < 0: no more items)
-  int i0, g, split;     // first query of the pair, KV head, split
+  int i0, g, split, splits;  // first query of the pair, KV head, split of its keys
   int t0, t1, Tc;       // key tiles of this item, tiles of the cached keys
   int tw[2];            // end of each row tile's key tiles
 };
@@ -392,10 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pages = kKeys / a.block_size;  // pages of a tile (cached keys)
       while (true) {
         Item w;
-        w.split = it % a.num_splits;
-        const int rest = it / a.num_splits;
-        w.g = rest % a.num_heads_kv;
-        const SeqTile s = seq_tile(a, a.tiles - 1 - rest / a.num_heads_kv);
+        w.splits = 1;
+        SeqTile s;
+        if (a.split_count) {
+          s = seq_even(a, it, a.grid, kKeys, w.splits, w.split, w.g, it == 0 ? a.split_count : nullptr);
+        } else {
+          w.split = 0;
+          w.g = it % a.num_heads_kv;
+          s = seq_tile(a, a.tiles - 1 - it / a.num_heads_kv);
+        }
         w.t0 = w.t1 = 0;
         bool asking = false;
         auto ask = [&] {  // (at most one question at a time, none after a "no")
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             T = max(T, w.tw[i]);
           }
           int s_eff;
-          if (!split_range(T, a.num_splits, w.split, w.t0, w.t1, s_eff)) w.t0 = w.t1 = 0;
+          if (!split_range(T, w.splits, w.split, w.t0, w.t1, s_eff)) w.t0 = w.t1 = 0;
           const int sl = items & 1;
           ok = mbar_wait(smem_u32(&bars->slot_empty[sl]), ((items >> 1) & 1) ^ 1, abort_flag, a.err,
                          a.wait_cycles);
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++outs;
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.0f / l;  // (0: every score is -inf)
-        const bool parts = a.num_splits > 1;
+        const bool parts = x.splits > 1;
         char *dst = parts ? reinterpret_cast<char *>(a.ws_o + x.split * n_hr * D) : static_cast<char *>(a.out);
         // 128 bytes of every row at a time: bf16 outputs of 64 columns, or float parts of 32
         const int chunks = parts ? D / 32 : D / 64, row_bytes = chunks * 128;
@@ -900,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[sl]));
-      if (rv && a.num_splits > 1)
+      if (rv && x.splits > 1)
         a.ws_ml[x.split * n_hr + hr] = make_float2(m_ref == kNothing ? -INFINITY : m_ref, l);
       else if (rv && a.lse_out)
         a.lse_out[hr] = (m_ref + __log2f(l)) * 0.6931471805599453f;
@@ -963,9 +968,8 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t s, char *why, size_t why_
     snprintf(why, why_len, "cuTensorMapEncodeTiled is missing or rejected a tensor (alignment or size)");
     return cudaErrorInvalidValue;
   }
-  const int64_t items = (int64_t)a.tiles * Hk * a.num_splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)items);
+  cfg.gridDim = dim3((unsigned)a.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;

@@ -49,6 +49,99 @@ __device__ __forceinline__ SeqTile seq_tile(const PromptArgs &a, int t) {
   return s;
 }
 
+// Splits of the keys for `grid` items: S_b = ceil(T_b / L) a row tile of request b, T_b the
+// key tiles that its last rows see, with the smallest L for which the items are no more than that (and no
+// item has more than L key tiles, whatever the requests' lengths). All 32 lanes call this; a lane
+// holds the requests lane, lane + 32, .. Returns the row tile of item c and its place among the S
+// splits and the KV heads; the splits of every request are written to `counts` (NULL: not).
+constexpr int kSplitLeast = 4;  // key tiles
+__device__ __forceinline__ SeqTile seq_even(const PromptArgs &a, int c, int grid, int keys, int &S, int &split,
+                                            int &g, int32_t *counts) {
+  constexpr int K = kPromptSplitBatch / 32;
+  const int lane = threadIdx.x & 31, Hk = a.num_heads_kv;
+  int t[K], T[K];  // row tiles and key tiles of a request
+  long long work = 0;
+  int items = 0, longest = 1;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = 32 * k + lane;
+    t[k] = T[k] = 0;
+    if (b < a.batch) {
+      const int q0 = __ldg(a.row_start + b), q1 = __ldg(a.row_start + b + 1);
+      const int C = a.ctx_len ? __ldg(a.ctx_len + b) : 0;
+      if (q0 >= 0 && q1 > q0 && q1 <= a.rows && C >= 0 &&
+          (long long)C <= (long long)a.max_pages_per_seq * a.block_size) {
+        t[k] = (q1 - q0 + a.tile_q - 1) / a.tile_q;
+        T[k] = (C + keys - 1) / keys + (q1 - q0 + keys - 1) / keys;
+      }
+    }
+    work += (long long)t[k] * T[k];
+    items += t[k];
+    longest = max(longest, T[k]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  work *= Hk;
+  items = __reduce_add_sync(0xffffffffu, items) * Hk;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  auto splits_of = [&](int k, int L) { return t[k] ? (T[k] + L - 1) / L : 0; };
+  auto fits = [&](int L) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) n += t[k] * splits_of(k, L);
+    return __reduce_add_sync(0xffffffffu, n) * Hk <= grid;
+  };
+  // (sum t ceil(T / L) <= work / L + items, which bounds L from above)
+  int lo = max(kSplitLeast, (longest + a.num_splits - 1) / a.num_splits);
+  lo = max(lo, (int)((work + grid - 1) / grid));
+  int hi = items < grid ? (int)(work / (grid - items)) + 1 : longest;
+  hi = max(lo, min(hi, longest));
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  // Worth it? In key tiles: an item costs 3 beside its own (queries, partials), the second launch 6.
+  // Whole row tiles end with the longest, or in a second round; pieces end together.
+  const int sms = min(grid, a.sms), mean = (int)(work / sms);
+  const int whole = items <= sms ? longest : max(longest, mean + longest / 2);
+  const int cut = grid <= sms ? lo + 9 : mean + lo / 2 + 3 * (grid / sms) + 6;
+  if (cut >= whole) lo = longest;
+  SeqTile s{};
+  S = 1;
+  split = g = 0;
+  int base = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int mine = splits_of(k, lo);
+    if (counts && 32 * k + lane < a.batch) counts[32 * k + lane] = mine;
+    const int x = t[k] * mine * Hk;
+    int upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int at = c - (base + upto - x);  // place among the items of this lane's request
+    const uint32_t who = __ballot_sync(0xffffffffu, at >= 0 && at < x);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      const int rest = __shfl_sync(0xffffffffu, at, src);
+      S = __shfl_sync(0xffffffffu, mine, src);
+      s.b = 32 * k + src;
+      split = rest % S;
+      g = rest / S % Hk;
+      s.tile = rest / S / Hk;
+      s.q0 = __ldg(a.row_start + s.b);
+      s.n = __ldg(a.row_start + s.b + 1) - s.q0;
+      s.C = a.ctx_len ? __ldg(a.ctx_len + s.b) : 0;
+      s.live = true;
+    }
+    base += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return s;
+}
+
 // New rows that row i of a request of n rows sees: [0, seq_limit).
 __device__ __forceinline__ int seq_limit(int i, int n, int mask_block) {
   return min(n, (i / mask_block + 1) * mask_block);  // (mask_block <= rows + 1, checked on the host)

@@ -326,3 +326,22 @@ def test_prompts_of_one_row(dtype):
     p = tokens.batch([0, 1, 15, 16, 400, 2000], hq=8, hkv=2, D=128, B=16, dtype=dtype, seed=8)
     check(p, *prompts.run(dict(p, mask_block=1), dev))
     check(p, *tokens.run(p, dev))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,ctx", [
+    ([1, 30, 5, 66, 2, 0, 9], [9000, 0, 8192, 300, 127, 4000, 2500]),
+    ([2] * 9 + [40], [8200] * 10),                       # as long as one another: nothing is split
+    ([1] * 95 + [3], [0, 17] * 47 + [9000, 260]),        # the largest batch that is split
+    ([1] * 96 + [3], [0, 17] * 48 + [9000]),             # one more
+    ([1, 1], [20000, 0]),
+    ([130, 1, 70], [8300, 8300, 8400])])
+def test_keys_of_uneven_requests(new, ctx, D):
+    """Splits that the device chooses: requests with many, with one, and with none."""
+    dev = device()
+    p = problem(new, ctx, hq=4, hkv=2, D=D, B=16, dtype=BF, seed=len(new), mask_block=16)
+    rows = {int(r) for r in np.random.default_rng(1).choice(sum(new), min(sum(new), 60), False)}
+    out, lse = prompts.run(p, dev)
+    check(p, out, lse, rows)
+    again = prompts.run(p, dev, max_ctx=0)   # (the hint shapes the splits, nothing else)
+    check(p, *again, rows)
