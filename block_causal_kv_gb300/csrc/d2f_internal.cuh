@@ -205,6 +205,7 @@ struct PromptArgs {
   int mask_block;              // rows i, j of a request: j is seen iff j / mask_block <= i / mask_block
   float scale_log2;            // softmax_scale * log2(e)
   int tile_q;                  // queries of a row tile
+  int simt_rows;               // CUDA cores: packed rows (query, head) of a row tile, 64, 32 or 16
   int head_chunk, chunks;      // query heads of an item, chunks of a group
   int num_splits;              // key splits (at most); more than 1: partials and a second launch
   int32_t *split_count;        // tensor cores: [batch] splits of a request's row tiles, chosen on the device
@@ -215,7 +216,6 @@ struct PromptArgs {
   float *ws_o;                 // [num_splits][rows * Hq][head_dim] unnormalised
   int32_t *err;
 };
-constexpr int kPromptSimtRows = 64;  // packed rows (query, head) of a CUDA-core tile
 constexpr int kPromptMaxSplits = 16;
 constexpr int kPromptSplitBatch = 96;  // requests of a batch whose keys are split on the device
 

@@ -5,10 +5,10 @@
 // 방법", §블록 단위 인과 어텐션 (bidirectional inside a block, causal between blocks; a block
 // of one row is the causal mask, one block of all rows the bidirectional one).
 //
-// A CTA holds kPromptSimtRows packed rows (row r = query r / head_chunk, head r % head_chunk) of
-// one KV head and walks their key tiles of KT keys, the cached prefix first: S = Q K^T with four
+// A CTA holds R packed rows (row r = query r / head_chunk, head r % head_chunk) of
+// one KV head and walks their key tiles of KT keys, the cached prefix first: S = Q K^T with R / 16
 // rows and four keys a thread, the online softmax in log2 units over the 16 threads of a row, P
-// through shared memory (over K, which is done with), O += P V with four rows and D / 16 columns a
+// through shared memory (over K, which is done with), O += P V with R / 16 rows and D / 16 columns a
 // thread. Operands are float in shared memory; rows are padded by four floats so that 16 keys a
 // quarter apart fall on different banks.
 #include "attn_common.cuh"
@@ -18,7 +18,6 @@ namespace d2f {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int R = kPromptSimtRows;
 constexpr int KT = 64;
 
 template <typename T>
@@ -34,7 +33,7 @@ __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
                      bf16_bits_to_float(v.y & 0xffffu), bf16_bits_to_float(v.y >> 16));
 }
 
-template <int D>
+template <int D, int R>
 struct Smem {
   static constexpr int kPitch = D + 4;
   static constexpr int kPPitch = KT + 4;
@@ -44,21 +43,21 @@ struct Smem {
   int page[KT];         // page of a cached key, -1: no key
   static_assert(R * kPPitch <= KT * kPitch || D < 64, "P fits K's place");
 };
-template <int D>
+template <int D, int R>
 constexpr size_t smem_bytes() {
   // (with D = 32 P is larger than K and gets its own place behind the struct)
-  return sizeof(Smem<D>) + (D < 64 ? R * (KT + 4) * sizeof(float) : 0);
+  return sizeof(Smem<D, R>) + (D < 64 ? R * (KT + 4) * sizeof(float) : 0);
 }
 
-template <typename T, int D>
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  using S = Smem<D>;
+  using S = Smem<D, R>;
   S &sm = *reinterpret_cast<S *>(smem_raw);
   float *p_s = D < 64 ? reinterpret_cast<float *>(smem_raw + sizeof(S)) : &sm.k[0][0];
-  constexpr int PP = S::kPPitch;
+  constexpr int PP = S::kPPitch, RT = R / 16;  // rows a thread
   const int tid = threadIdx.x;
-  const int rg = tid >> 4, cg = tid & 15;  // rows 4 rg .. + 3; keys cg + 16 j; columns 4 cg + 64 j
+  const int rg = tid >> 4, cg = tid & 15;  // rows RT rg ..; keys cg + 16 j; columns 4 cg + 64 j
   if (blockIdx.x == 0 && tid < 32) seq_report(a);
 
   int64_t item = blockIdx.x;
@@ -94,13 +93,13 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
 
   constexpr int CJ = D / 64 > 0 ? D / 64 : 1;  // groups of four columns a thread
   const bool cols = D >= 64 || cg < D / 4;     // (D = 32: eight threads of a row hold columns)
-  float m[4], l[4], o[4][CJ][4];
-  int lim[4];  // new rows that the row sees
+  float m[RT], l[RT], o[RT][CJ][4];
+  int lim[RT];  // new rows that the row sees
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
+  for (int x = 0; x < RT; ++x) {
     m[x] = -INFINITY;
     l[x] = 0.f;
-    lim[x] = seq_limit(min(i0 + (4 * rg + x) / HC, s.n - 1), s.n, a.mask_block);
+    lim[x] = seq_limit(min(i0 + (RT * rg + x) / HC, s.n - 1), s.n, a.mask_block);
 #pragma unroll
     for (int j = 0; j < CJ; ++j)
 #pragma unroll
@@ -146,16 +145,16 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
     }
     odd = __syncthreads_or(odd);
 
-    float sc[4][4] = {};
+    float sc[RT][4] = {};
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      float4 qx[4], kx[4];
+      float4 qx[RT], kx[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) qx[x] = *reinterpret_cast<float4 *>(&sm.q[4 * rg + x][d]);
+      for (int x = 0; x < RT; ++x) qx[x] = *reinterpret_cast<float4 *>(&sm.q[RT * rg + x][d]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<float4 *>(&sm.k[cg + 16 * j][d]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < RT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           sc[x][j] = fmaf(qx[x].w, kx[j].w, fmaf(qx[x].z, kx[j].z,
@@ -167,12 +166,12 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
       const int c = cg + 16 * j;
       const bool key = cached ? sm.page[c] >= 0 : true;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < RT; ++x)
         if (key && (cached || k0 + c < lim[x])) seen |= 1u << (4 * x + j);
     }
     __syncthreads();  // K is done with: P takes its place
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < RT; ++x) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
       for (int j = 0; j < 4; ++j) {
         const float p = (seen >> (4 * x + j) & 1u) ? fast_exp2(sc[x][j] - base) : 0.f;
         sum += p;
-        p_s[(4 * rg + x) * PP + cg + 16 * j] = p;
+        p_s[(RT * rg + x) * PP + cg + 16 * j] = p;
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -205,17 +204,17 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
       if (!odd) {
 #pragma unroll 2
         for (int c = 0; c < KT; c += 4) {
-          float4 px[4];
+          float4 px[RT];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            px[x] = *reinterpret_cast<const float4 *>(&p_s[(4 * rg + x) * PP + c]);
+          for (int x = 0; x < RT; ++x)
+            px[x] = *reinterpret_cast<const float4 *>(&p_s[(RT * rg + x) * PP + c]);
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
 #pragma unroll
             for (int j = 0; j < CJ; ++j) {
               const float4 vx = *reinterpret_cast<const float4 *>(&sm.v[c + cc][4 * cg + 64 * j]);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
+              for (int x = 0; x < RT; ++x) {
                 const float p = cc == 0 ? px[x].x : cc == 1 ? px[x].y : cc == 2 ? px[x].z : px[x].w;
                 o[x][j][0] = fmaf(p, vx.x, o[x][j][0]);
                 o[x][j][1] = fmaf(p, vx.y, o[x][j][1]);
@@ -229,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
         for (int c = 0; c < KT; ++c) {
           const bool key = !cached || sm.page[c] >= 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < RT; ++x) {
             if (!key || (!cached && k0 + c >= lim[x])) continue;
-            const float p = p_s[(4 * rg + x) * PP + c];
+            const float p = p_s[(RT * rg + x) * PP + c];
 #pragma unroll
             for (int j = 0; j < CJ; ++j)
 #pragma unroll
@@ -245,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
 
   const int64_t n_hr = (int64_t)a.rows * H;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int r = 4 * rg + x, i = r / HC, h = r % HC;
+  for (int x = 0; x < RT; ++x) {
+    const int r = RT * rg + x, i = r / HC, h = r % HC;
     if (i >= ni || h >= heads) continue;
     const int64_t hr = (int64_t)(s.q0 + i0 + i) * H + g * a.group + h0 + h;
     if (a.num_splits > 1) {
@@ -321,14 +320,19 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   if (lane == 0 && a.lse_out) a.lse_out[hr] = (M + __log2f(L)) * 0.6931471805599453f;
 }
 
-template <typename T, int D>
-cudaError_t launch_d(const PromptArgs &a, cudaStream_t s) {
-  constexpr size_t bytes = smem_bytes<D>();
-  const cudaError_t e = allow_smem_once<&prompt_simt_kernel<T, D>>((int)bytes);
+template <typename T, int D, int R>
+cudaError_t launch_r(const PromptArgs &a, cudaStream_t s) {
+  constexpr size_t bytes = smem_bytes<D, R>();
+  const cudaError_t e = allow_smem_once<&prompt_simt_kernel<T, D, R>>((int)bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.tiles * a.num_heads_kv * a.chunks * a.num_splits;
-  prompt_simt_kernel<T, D><<<(unsigned)items, kThreads, bytes, s>>>(a);
+  prompt_simt_kernel<T, D, R><<<(unsigned)items, kThreads, bytes, s>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t launch_d(const PromptArgs &a, cudaStream_t s) {
+  return a.simt_rows == 64 ? launch_r<T, D, 64>(a, s)
+         : a.simt_rows == 32 ? launch_r<T, D, 32>(a, s) : launch_r<T, D, 16>(a, s);
 }
 
 template <typename T, int D>
