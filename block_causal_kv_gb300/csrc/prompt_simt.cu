@@ -306,12 +306,32 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
   constexpr int V = D / 32;
   float acc[V] = {};
-  for (int sp = 0; sp < splits; ++sp) {
-    const float ws = __shfl_sync(0xffffffffu, w, sp);
-    if (ws == 0.f) continue;
-    const float *src = a.ws_o + (sp * n_hr + hr) * D + lane * V;
+  // eight parts at a time, whose loads go out together
+  constexpr int N = 8;
+  for (int sp0 = 0; sp0 < splits; sp0 += N) {
+    float y[N][V], ws[N];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = fmaf(ws, __ldcg(src + j), acc[j]);
+    for (int k = 0; k < N; ++k) {
+      ws[k] = __shfl_sync(0xffffffffu, w, (sp0 + k) & 31);
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[k][j] = 0.f;
+      if (sp0 + k < splits && ws[k] != 0.f) {  // (a part without weight may not have been written)
+        const float *src = a.ws_o + ((int64_t)(sp0 + k) * n_hr + hr) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+          y[k][0] = x.x, y[k][1] = x.y, y[k][2] = x.z, y[k][3] = x.w;
+        } else if constexpr (V == 2) {
+          const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+          y[k][0] = x.x, y[k][1] = x.y;
+        } else {
+          y[k][0] = __ldcg(src);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = fmaf(ws[k], y[k][j], acc[j]);
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
   T *dst = static_cast<T *>(a.out) + hr * D + lane * V;
