@@ -17,7 +17,18 @@
 // further items from the launch's own grid (cluster launch control: a CTA that has loaded its
 // item's last tile cancels one that has not started and does its work), so that the next
 // item's queries and keys load while the last one computes, and unequal items even out. Items
-// of a request's last rows, which see the most keys, come first.
+// of a request's last rows, which see the most keys, come first. Where row tiles are few, or long
+// prefixes uneven, the keys are cut into even pieces and a second launch composes them
+// (seq_even, prompt_merge_kernel).
+//
+// What bounds it. A pair of 128 x 128 tiles is 4 * 1024 cycles of products for D = 128 and 2 * 512
+// of exponentials a softmax warpgroup. 16,384 causal rows, 28 heads on 4: 1227 us at full clocks,
+// 1570 TFLOP/s (81 % of the measured product rate; 1316 us in a row of calls, where the power cap
+// holds the clock at some 1.6 GHz). Without the weights' arithmetic the same loop takes 1141 us: S's
+// operands, both from shared memory, fill its bandwidth. 16 requests of 251 to 4096 rows, 32 heads
+// on 8: 772 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1085 us for the
+// long case, 890 TFLOP/s, bound by the exponentials and their chain, which are the same for half
+// the products.
 //
 // Roles of a CTA's warps:
 //   0        producer: which request an item belongs to, tensor copies of the queries and of the
@@ -26,6 +37,7 @@
 //   1        MMA issuer (one lane): S = Q K^T, then O += P V with P in TMEM over S, the row tiles
 //            in turn, so that one tile's products run while the other's weights are computed
 //   2        V tiles that the mask cuts, or that pages do not fill (below)
+//   3        half of a cached tile's pages, half of a new V tile's rows for warp 2
 //   4 - 11   softmax: a warpgroup a row tile, a thread a row
 // TMEM columns: S / P of tile 0 and 1 (128 each), O of tile 0 and 1 (D each).
 //
@@ -76,15 +88,19 @@ struct Cfg {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];           // ring
-  uint64_t clean[8];                    // ... V looked at, and zeroed where nobody sees it
+  // The u-th tile of the CTA (K and V in turn) lies in entry u % kEntries. Its landing has a barrier by
+  // its number, not by its entry: a warp that waits for the V tiles only must neither be two phases
+  // late nor find the phase of a K tile in its entry.
+  uint64_t full[16];                    // u % 16
+  uint64_t empty[8];                    // ring entry
+  uint64_t clean[8];                    // V tile (number % 8) looked at, and zeroed where nobody sees it
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain;
   uint64_t slot_full[2], slot_empty[2], clc;
   __align__(16) uint32_t clc_answer[4];
   Item slot[2];
   int bad[8];                           // ring entry: pages of the tile are missing
-  int odd[8];                           // ... V has an infinity or NaN that not every row sees
+  int odd[2][8];                        // V tile's halves: an infinity or NaN that not every row sees
   int skip[2];                          // the threads have done this tile's product with V
   int abort;
   uint32_t tmem;
@@ -295,21 +311,25 @@ __device__ __noinline__ void slow_pv(uint32_t p, uint32_t o, uint32_t v, uint4 s
   tmem_wait_st();
 }
 
+// acc += 0 y, two bf16.
+__device__ __forceinline__ void zero_times(uint32_t &acc, uint32_t y) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y), "r"(0));
+}
 // Whether cached key `key` lies in a page of the pool.
 __device__ __forceinline__ bool page_good(const PromptArgs &a, const Item &x, int key) {
   if (key >= x.C) return false;
   const int page = __ldg(a.page_table + (int64_t)x.b * a.max_pages_per_seq + key / a.block_size);
   return page >= 0 && page < a.num_pages;
 }
-// A tile of V in shared memory, four rows a lane: rows that no query sees become zeros; whether
-// the others hold an infinity or NaN, where the mask cuts through the tile (`cut`).
+// Rows r0 .. r1 - 1 of a tile of V in shared memory: rows that no query sees become zeros; whether the
+// others hold an infinity or NaN, where the mask cuts through the tile (`cut`).
 template <int D>
-__device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_t v, int base, int valid,
-                                     bool cut, bool bad) {
+__device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_t v, int r0, int r1, int base,
+                                     int valid, bool cut, bool bad) {
   const int lane = threadIdx.x & 31;
-  uint32_t hit = 0;  // exponents of all ones carry into the sign's place
+  uint32_t hit[4] = {};  // sums of 0 y: NaN where a y is not finite, else 0
 #pragma unroll 1
-  for (int row = lane; row < kKeys; row += 32) {
+  for (int row = r0 + lane; row < r1; row += 32) {
     const uint32_t at = v + row * 128;
     if (row >= valid || (bad && !page_good(a, x, base + row))) {
 #pragma unroll
@@ -322,13 +342,15 @@ __device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint4 y = ld_shared_v4(at + h * 16384 + (((c + lane) & 7) << 4));
-          hit |= ((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
-                 ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u);
+          zero_times(hit[0], y.x);
+          zero_times(hit[1], y.y);
+          zero_times(hit[2], y.z);
+          zero_times(hit[3], y.w);
         }
     }
   }
   fence_proxy_async_smem();  // the zeros, before the MMA reads V
-  return __any_sync(0xffffffffu, (hit & 0x80008000u) != 0);
+  return __any_sync(0xffffffffu, ((hit[0] | hit[1] | hit[2] | hit[3]) & 0x7fff7fffu) != 0);
 }
 
 template <int D>
@@ -347,11 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = a.group, QI = a.tile_q / 2;  // queries of a row tile
 
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < NE; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), 1);
-      mbar_init(smem_u32(&bars->empty[i]), 1);
-      mbar_init(smem_u32(&bars->clean[i]), 1);
-    }
+    for (int i = 0; i < NE; ++i) mbar_init(smem_u32(&bars->empty[i]), 1);
+    for (int i = 0; i < 16; ++i) mbar_init(smem_u32(&bars->full[i]), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bars->clean[i]), 2);  // warps 2 and 3
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 8);  // the softmax warps
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              a.wait_cycles);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              const uint32_t bar = smem_u32(&bars->full[ent]), dst = sb + L::kRing + ent * L::kTile;
+              const uint32_t bar = smem_u32(&bars->full[e & 15]), dst = sb + L::kRing + ent * L::kTile;
               if (cached) {
                 if (lane == 0) {
                   bars->bad[ent] = bad;
@@ -522,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t u = items > 2 ? items - 2 : 0; u < items; ++u)
           mbar_wait(smem_u32(&bars->q_full[u & 1]), (u >> 1) & 1, &no_abort, a.err, kDrainCycles);
         for (uint32_t u = e > (uint32_t)NE ? e - NE : 0; u < e; ++u)
-          mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
+          mbar_wait(smem_u32(&bars->full[u & 15]), (u >> 4) & 1, &no_abort, a.err, kDrainCycles);
         if (asked) mbar_wait(smem_u32(&bars->clc), (asked - 1) & 1, &no_abort, a.err, kDrainCycles);
       }
     } else if (warp == 1 && elect_one()) {
@@ -537,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = smem_desc_sw128(sb + L::kRing, 16384, 1024);
       // (Elected, not lane 0: 16,384 causal rows of 28 on 4 heads 1777 -> 1343 us.)
       const uint32_t full = smem_u32(bars->full), empty = smem_u32(bars->empty), clean = smem_u32(bars->clean);
-      uint32_t sk = 0, pk = 0;        // ring entry of the next K, parity of its phase
+      uint32_t sk = 0;                // ring entry of the next K
+      uint32_t vt = 0;                // tiles whose S has been issued; the one before it is vt - 1
       uint32_t p_par = 0, o_par = 3;  // parities, a bit a row tile: p_full, o_empty
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, a.err, a.wait_cycles);
@@ -546,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (they stay so over the change of items where the next one's operands have landed).
       uint32_t item = 0;
       int t = 0, t0 = 0, t1 = 0, tw0 = 0, tw1 = 0;
-      uint32_t sv = 0, pv = 0, todo = 0, last = 0, more = 0, qs = 0;  // todo, last: a bit a row tile
+      uint32_t sv = 0, todo = 0, last = 0, more = 0, qs = 0;  // todo, last: a bit a row tile
       bool behind = false;
       while (true) {
         bool score = t < t1;
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ready) {
             const bool end = bars->slot[sl].b < 0;
             if (end && !behind) break;
-            if (!end && (!behind || (mbar_test(smem_u32(&bars->q_full[sl]), par) && mbar_test(full + 8 * sk, pk)))) {
+            if (!end && (!behind || (mbar_test(smem_u32(&bars->q_full[sl]), par) && mbar_test(full + 16 * (vt & 7), (vt >> 3) & 1)))) {
               t0 = t = bars->slot[sl].t0;
               t1 = bars->slot[sl].t1;
               tw0 = min(t1, bars->slot[sl].tw[0]);
@@ -579,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < 2; ++w) {
           const uint32_t ts = tmem + w * 128, to = tmem + L::kTmO + w * D;
           if (todo >> w & 1u) {
-            ok = wait(clean + 8 * sv, pv);
+            ok = wait(clean + 8 * ((vt - 1) & 7), ((vt - 1) >> 3) & 1);
             if (ok && !more) {
               ok = wait(smem_u32(&bars->o_empty[w]), (o_par >> w) & 1);
               o_par ^= 1u << w;
@@ -598,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (w && behind) umma_commit(empty + 8 * sv);
           if (score && t < (w ? tw1 : tw0)) {
-            ok = wait(full + 8 * sk, pk);
+            ok = wait(full + 16 * (vt & 7), (vt >> 3) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t qd = smem_desc_advance(q_desc, (qs + w) * L::kTile);
@@ -620,12 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           last = (t == tw0 - 1 ? 1u : 0u) | (t == tw1 - 1 ? 2u : 0u);
           more = t > t0 ? 1u : 0u;
           sv = sk + 1 == NE ? 0 : sk + 1;
-          pv = sk + 1 == NE ? pk ^ 1 : pk;
+          ++vt;
           sk += 2;
-          if (sk >= NE) {
-            sk -= NE;
-            pk ^= 1;
-          }
+          if (sk >= NE) sk -= NE;
           ++t;
         }
       }
@@ -650,27 +668,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x.b < 0) break;
         const int first_limit = seq_limit(min(x.i0, x.n - 1), x.n, a.mask_block);  // (the first row's)
 #pragma unroll 1
-        for (int u = 2 * x.t0; u < 2 * x.t1 && ok; ++u, ++e) {  // K and V tiles in turn
-          const uint32_t ent = e % NE;
-          ok = wait(&bars->full[ent], (e / NE) & 1);
+        for (int t = x.t0; t < x.t1; ++t, e += 2) {  // K and V tiles in turn
+          const uint32_t ent = (e + 1) % NE, vt = e >> 1;
+          ok = wait(&bars->full[(e + 1) & 15], (e >> 4) & 1);
           if (!ok) break;
-          if (u & 1) {
-            const int t = u >> 1;
-            const bool cached = t < x.Tc;
-            const int base = (cached ? t : t - x.Tc) * kKeys, valid = (cached ? x.C : x.n) - base;
-            const bool cut = !cached && first_limit - base < min(kKeys, valid);
-            const bool bad = cached && *(volatile int *)&bars->bad[ent] != 0;
-            bool odd = false;
-            if (bad || cut || valid < kKeys)
-              odd = clean_v<D>(a, x, sb + L::kRing + ent * L::kTile, base, valid, cut, bad);
-            if (lane == 0) *(volatile int *)&bars->odd[ent] = odd;
-          }
+          const bool cached = t < x.Tc;
+          const int base = (cached ? t : t - x.Tc) * kKeys, valid = (cached ? x.C : x.n) - base;
+          const bool cut = !cached && first_limit - base < min(kKeys, valid);
+          const bool bad = cached && *(volatile int *)&bars->bad[ent] != 0;
+          bool odd = false;
+          if (bad || cut || valid < kKeys)  // (of a cached tile all rows: warp 3 has copies to issue)
+            odd = clean_v<D>(a, x, sb + L::kRing + ent * L::kTile, 0, cached ? kKeys : kKeys / 2, base, valid, cut, bad);
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->clean[ent]));
+          if (lane == 0) {
+            *(volatile int *)&bars->odd[0][vt & 7] = odd;
+            mbar_arrive(smem_u32(&bars->clean[vt & 7]));
+          }
         }
       }
     } else if (warp == 3) {
-      // ============ second producer of cached tiles: half of their pages =========
+      // ============ second producer of cached tiles: half of their pages; half of the new V =======
       const int pages = kKeys / a.block_size, mine = (pages + 1) / 2;
       uint32_t e = 0, issued = 0;
       bool ok = true;
@@ -690,28 +707,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const int end = min(x.t1, x.Tc);
         int page = x.t0 < end ? page_of(x.t0) : -1;
+        auto done = [&](uint32_t vt, bool odd) {
+          __syncwarp();
+          if (lane == 0) {
+            *(volatile int *)&bars->odd[1][vt & 7] = odd;
+            mbar_arrive(smem_u32(&bars->clean[vt & 7]));
+          }
+        };
+        auto landed = [&](uint32_t u) -> bool {
+          const bool y = mbar_wait(smem_u32(&bars->full[u & 15]), (u >> 4) & 1, abort_flag, a.err, a.wait_cycles);
+          return __all_sync(0xffffffffu, y);
+        };
         for (int t = x.t0; t < end && ok; ++t) {
           const int next = t + 1 < end ? page_of(t + 1) : -1;
           const bool good = page >= 0 && page < a.num_pages;
+          const uint32_t u0 = e + 2 * (t - x.t0);
+          // (A wait may be for a phase that cannot be followed by another before this warp has done its
+          // part: entries that it copies to, else the V tile, which is not used before `done`.)
+          if (__any_sync(0xffffffffu, good)) {
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t u = e + 2 * (t - x.t0) + kv, ent = u % NE;
-            ok = mbar_wait(smem_u32(&bars->empty[ent]), ((u / NE) & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (good)
-              load_page<D>(sb + L::kRing + ent * L::kTile, kv ? &tm_vp : &tm_kp, smem_u32(&bars->full[ent]), lane, a,
-                           page, x.g);
-            issued = u + 1;
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t u = u0 + kv, ent = u % NE;
+              ok = mbar_wait(smem_u32(&bars->empty[ent]), ((u / NE) & 1) ^ 1, abort_flag, a.err, a.wait_cycles);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              if (good)
+                load_page<D>(sb + L::kRing + ent * L::kTile, kv ? &tm_vp : &tm_kp, smem_u32(&bars->full[u & 15]), lane, a,
+                             page, x.g);
+              issued = u + 1;
+            }
+          } else {
+            ok = landed(u0 + 1);
           }
           page = next;
+          if (ok) done(u0 >> 1, false);
+        }
+        const int first_limit = seq_limit(min(x.i0, x.n - 1), x.n, a.mask_block);
+#pragma unroll 1
+        for (int t = max(end, x.t0); t < x.t1 && ok; ++t) {
+          const uint32_t u = e + 2 * (t - x.t0) + 1;
+          ok = landed(u);
+          if (!ok) break;
+          const int base = (t - x.Tc) * kKeys, valid = x.n - base;
+          const bool cut = first_limit - base < min(kKeys, valid);
+          bool odd = false;
+          if (cut || valid < kKeys)
+            odd = clean_v<D>(a, x, sb + L::kRing + u % NE * L::kTile, kKeys / 2, kKeys, base, valid, cut, false);
+          done(u >> 1, odd);
         }
         e += 2 * (x.t1 - x.t0);
       }
       if (!ok && lane == 0) {  // what was asked for has landed before the CTA ends
         volatile int no_abort = 0;
         for (uint32_t u = issued > (uint32_t)NE ? issued - NE : 0; u < issued; ++u)
-          mbar_wait(smem_u32(&bars->full[u % NE]), (u / NE) & 1, &no_abort, a.err, kDrainCycles);
+          mbar_wait(smem_u32(&bars->full[u & 15]), (u >> 4) & 1, &no_abort, a.err, kDrainCycles);
       }
     }
   } else {
@@ -753,13 +802,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 sees;
         bool odd = false;
         if (__builtin_expect(look || cached, 0)) {
-          ok = wait(&bars->clean[ev % NE], (ev / NE) & 1);
+          // (With S of an item's first tile there the issuer is past the V tile that had this barrier
+          // before, even where the other row tile of the item before had more tiles than this one.)
+          if (t == x.t0) ok = wait(&bars->s_full[w], tiles & 1);
+          ok = ok && wait(&bars->clean[(ev >> 1) & 7], (ev >> 4) & 1);
           if (!ok) break;
           const volatile Bars *vb = bars;
           const bool bad = cached && vb->bad[ev % NE];
           look = look || bad;
           if (look) {
-            odd = vb->odd[ev % NE] != 0;
+            odd = (vb->odd[0][(ev >> 1) & 7] | vb->odd[1][(ev >> 1) & 7]) != 0;
             const int lim = cached ? x.C - base : limit - base;
             uint32_t word[4];
 #pragma unroll

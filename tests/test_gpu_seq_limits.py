@@ -345,3 +345,30 @@ def test_keys_of_uneven_requests(new, ctx, D):
     check(p, out, lse, rows)
     again = prompts.run(p, dev, max_ctx=0)   # (the hint shapes the splits, nothing else)
     check(p, *again, rows)
+
+
+@pytest.mark.parametrize("mask_block", [1, 0, 1000])
+@pytest.mark.parametrize("D,B", [(64, 128), (128, 128), (128, 8)])
+def test_prompts_whose_tiles_end_apart(D, B, mask_block):
+    """The two row tiles of an item see numbers of keys that lie far apart, pages as long as a tile, more
+    items than CTAs, whole tiles of bad pages between good ones: the same bits every time."""
+    dev = device()
+    g = np.random.default_rng(D + B + mask_block)
+    new = [1100, 90, 1, 700, 2300, 40] * 4
+    ctx = [0, 700, 1500, 130, 5, 1030] * 4
+    p = problem(new, ctx, hq=12, hkv=6, D=D, B=B, dtype=BF, seed=3, mask_block=mask_block)
+    pages = p["k_pool"].shape[0]
+    p["table"][2, 256 // B:768 // B] = pages + 5
+    p["table"][5, :256 // B] = -4
+    rows = {int(r) for r in g.choice(sum(new), 40, False)}
+    rows |= {int(p["start"][b]) for b in (2, 5)}
+    t = prompts.to_gpu(p, dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = prompts.call(p, t, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 4   # the bad pages
+    check(p, out, lse, rows)
+    for _ in range(30):
+        err.zero_()
+        again = prompts.call(p, t, err=err)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and int(err) == 4
