@@ -12,6 +12,10 @@
 // until the end. The states of the CTA's groups are composed in log space, then those of
 // the splits by the CTA that arrives last. Split 0 takes the new token's key too and, for the
 // first chunk of heads, writes its K and V to their slot, which no CTA reads in this call.
+//
+// A CTA has as many heads as the group, up to four, so that K and V are read once for them. float32,
+// D = 128: 16 x 4096 tokens of 32 heads 331 us, 6.5 TB/s (577 with room for four heads in every CTA
+// and a key at a time); of 32 heads on 8 165 us, 3.3 TB/s, bound by the multiply-adds and shuffles.
 #include "attn_common.cuh"
 
 namespace d2f {
