@@ -1270,7 +1270,7 @@ int plan_prompt(int batch, int rows, int max_ctx, int Hq, int Hkv, int D, int B,
   const long long t_max = cdiv(max_ctx, keys) + (long long)cdiv(rows, keys);
   // CUDA cores: tiles of 64 rows read K and V the least often. Where they leave SMs empty and there
   // are too few keys to split, tiles have fewer rows: float32, 100 rows of 4 heads of 64 24 -> 17 us,
-  // 20 rows of 32 heads on 8 22 -> 15 (20 rows behind 4096 tokens: 122 us, 239 with 16 rows).
+  // 20 rows of 32 heads on 8 22 -> 15 (20 rows behind 4096 tokens: 110 us, 239 with 16 rows).
   for (p->simt_rows = 64;; p->simt_rows /= 2) {
     p->head_chunk = p->tc ? G : min(G, p->simt_rows);
     p->chunks = cdiv(G, p->head_chunk);
@@ -1280,9 +1280,11 @@ int plan_prompt(int batch, int rows, int max_ctx, int Hq, int Hkv, int D, int B,
     if (p->tc || p->simt_rows == 16 || items >= 2 * sms || t_max >= 8) break;
   }
   // Few row tiles and many keys: the keys are split, up to one CTA an SM and at least four key
-  // tiles each.
-  const long long most = items > 0 ? sms / items : 1;
-  p->splits = (int)max(1LL, min(min(most, t_max / 4), (long long)kPromptMaxSplits));
+  // tiles each; on the CUDA cores up to four CTAs an SM (two run at a time; causal rows are uneven) and at
+  // least two tiles: float32, 1000 rows of 4 heads of 64 40 us (69 with one CTA an SM and four
+  // tiles), 1024 rows of 8 heads of 128 91 (204; 104 with eight CTAs).
+  const long long most = items > 0 ? (p->tc ? 1 : 4) * sms / items : 1;
+  p->splits = (int)max(1LL, min(min(most, p->tc ? t_max / 4 : t_max / 2 - 1), (long long)kPromptMaxSplits));
   // On the tensor cores the device, which knows the lengths, cuts them evenly (seq_even); p->splits
   // is the most that a row tile gets. Behind prefixes of 64 key tiles (100 us) and more of several
   // requests it is worth a second launch up to two items an SM: 8 requests of 40 to 77 rows,
