@@ -803,8 +803,9 @@ int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_hea
  *
  * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
  * are left out of the softmax); D2F_ERR_INVALID_ARG for a row_start that is negative, decreases
- * or passes rows, or a ctx_len out of range: requests with such lengths are skipped, and
- * with an inconsistent row_start others may be too. Nothing outside the buffers is touched.
+ * or passes rows, or a ctx_len out of range: requests with such lengths are skipped, and with an
+ * inconsistent row_start the others' results are unspecified; D2F_ERR_TIMEOUT for a wait of the
+ * kernel's that ran out. Nothing outside the buffers is touched.
  * Limits: batch and num_heads_q <= 65535, rows <= 2^30. The workspace needs no zeroing, and may
  * be any entry point's.
  */
