@@ -211,6 +211,7 @@ struct PromptArgs {
   int32_t *split_count;        // tensor cores: [batch] splits of a request's row tiles, chosen on the device
   int tiles;                   // row tiles: rows / tile_q + batch, some of them empty
   int grid, sms;               // tensor cores: items, one a CTA; SMs
+  bool fold;                   // ... an item's row tiles are the i-th from either end of a request
   long long wait_cycles;       // budget of each wait on another role's work
   float2 *ws_ml;               // [num_splits][rows * Hq] (max in log2 units, sum)
   float *ws_o;                 // [num_splits][rows * Hq][head_dim] unnormalised

@@ -10,8 +10,8 @@
 // sums and both accumulators are float. The weights enter the product with V as bf16 (2^-8 of
 // each, the type of the MMA's operands; the sum keeps the unrounded ones).
 //
-// Work. An item is a pair of row tiles of 128 rows of one (request, KV head), times a split of
-// its keys. The G = Hq / Hkv query heads of the KV head are packed into the rows (row r = query
+// Work. An item is a pair of row tiles of 128 rows of one (request, KV head) (neighbours, or from both
+// ends of the request: `fold`), times a split of its keys. The G = Hq / Hkv query heads of the KV head are packed into the rows (row r = query
 // r / G, head r % G, 128 / G queries a tile), so a K/V tile that is read once serves all of them.
 // A CTA keeps an SM (its two row tiles, a ring of K and V tiles of 128 keys) and takes
 // further items from the launch's own grid (cluster launch control: a CTA that has loaded its
@@ -22,11 +22,11 @@
 // (seq_even, prompt_merge_kernel).
 //
 // What bounds it. A pair of 128 x 128 tiles is 4 * 1024 cycles of products for D = 128 and 2 * 512
-// of exponentials a softmax warpgroup. 16,384 causal rows, 28 heads on 4: 1227 us at full clocks,
-// 1570 TFLOP/s (81 % of the measured product rate; 1316 us in a row of calls, where the power cap
+// of exponentials a softmax warpgroup. 16,384 causal rows, 28 heads on 4: 1217 us at full clocks,
+// 1580 TFLOP/s (82 % of the measured product rate; 1300 us in a row of calls, where the power cap
 // holds the clock at some 1.6 GHz). Without the weights' arithmetic the same loop takes 1141 us: S's
 // operands, both from shared memory, fill its bandwidth. 16 requests of 251 to 4096 rows, 32 heads
-// on 8: 772 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1085 us for the
+// on 8: 768 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1085 us for the
 // long case, 890 TFLOP/s, bound by the exponentials and their chain, which are the same for half
 // the products.
 //
@@ -72,7 +72,8 @@ constexpr float kNothing = -3.402823466e38f;  // reference of a row that has see
 
 struct Item {
   int b, q0, n, C;      // request, its first row, rows, cached tokens (b < 0: no more items)
-  int i0, g, split, splits;  // first query of the pair, KV head, split of its keys
+  int i0[2];            // first query of each row tile
+  int g, split, splits; // KV head, split of the keys
   int t0, t1, Tc;       // key tiles of this item, tiles of the cached keys
   int tw[2];            // end of each row tile's key tiles
 };
@@ -436,12 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.q0 = s.q0;
           w.n = s.n;
           w.C = s.C;
-          w.i0 = s.tile * a.tile_q;
+          w.i0[0] = s.tile * (a.fold ? QI : a.tile_q);
+          w.i0[1] = w.i0[0] + QI;
+          if (a.fold) {
+            const int other = (s.n + QI - 1) / QI - 1 - s.tile;
+            w.i0[1] = other > s.tile ? other * QI : s.n;  // (s.n: the middle one is alone)
+          }
           w.Tc = (s.C + kKeys - 1) / kKeys;
           int T = 0;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int first = w.i0 + i * QI, end = min(first + QI, s.n);
+            const int first = w.i0[i], end = min(first + QI, s.n);
             w.tw[i] = first >= s.n ? 0 : w.Tc + (seq_limit(end - 1, s.n, a.mask_block) + kKeys - 1) / kKeys;
             T = max(T, w.tw[i]);
           }
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int h = 0; h < L::kHalves; ++h)
                 tma_load_3d(sb + (2 * sl + i) * L::kTile + h * 16384, &tm_q, bar, h * 64, w.g * G,
-                            w.q0 + w.i0 + i * QI);
+                            w.q0 + w.i0[i]);
           }
           // page ids of the next cached tile, one a lane
           const int32_t *table = a.page_table + (int64_t)w.b * a.max_pages_per_seq;
@@ -666,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->slot_empty[sl]));
         if (x.b < 0) break;
-        const int first_limit = seq_limit(min(x.i0, x.n - 1), x.n, a.mask_block);  // (the first row's)
+        const int first[2] = {seq_limit(min(x.i0[0], x.n - 1), x.n, a.mask_block),  // (the first rows')
+                              seq_limit(min(x.i0[1], x.n - 1), x.n, a.mask_block)};
 #pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, e += 2) {  // K and V tiles in turn
           const uint32_t ent = (e + 1) % NE, vt = e >> 1;
@@ -674,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const bool cached = t < x.Tc;
           const int base = (cached ? t : t - x.Tc) * kKeys, valid = (cached ? x.C : x.n) - base;
-          const bool cut = !cached && first_limit - base < min(kKeys, valid);
+          const bool cut = !cached && ((t < x.tw[0] && first[0] - base < min(kKeys, valid)) ||
+                                       (t < x.tw[1] && first[1] - base < min(kKeys, valid)));
           const bool bad = cached && *(volatile int *)&bars->bad[ent] != 0;
           bool odd = false;
           if (bad || cut || valid < kKeys)  // (of a cached tile all rows: warp 3 has copies to issue)
@@ -742,14 +750,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = next;
           if (ok) done(u0 >> 1, false);
         }
-        const int first_limit = seq_limit(min(x.i0, x.n - 1), x.n, a.mask_block);
+        const int first[2] = {seq_limit(min(x.i0[0], x.n - 1), x.n, a.mask_block),
+                              seq_limit(min(x.i0[1], x.n - 1), x.n, a.mask_block)};
 #pragma unroll 1
         for (int t = max(end, x.t0); t < x.t1 && ok; ++t) {
           const uint32_t u = e + 2 * (t - x.t0) + 1;
           ok = landed(u);
           if (!ok) break;
           const int base = (t - x.Tc) * kKeys, valid = x.n - base;
-          const bool cut = first_limit - base < min(kKeys, valid);
+          const bool cut = (t < x.tw[0] && first[0] - base < min(kKeys, valid)) ||
+                           (t < x.tw[1] && first[1] - base < min(kKeys, valid));
           bool odd = false;
           if (cut || valid < kKeys)
             odd = clean_v<D>(a, x, sb + L::kRing + u % NE * L::kTile, kKeys / 2, kKeys, base, valid, cut, false);
@@ -786,12 +796,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->slot_empty[sl]));
       if (x.b < 0) break;
-      const int i = x.i0 + w * QI + qi;                // query of the row
+      const int i = x.i0[w] + qi;                      // query of the row
       const bool rv = qi < QI && i < x.n;
       const int limit = rv ? seq_limit(i, x.n, a.mask_block) : 0;  // new rows it sees
       const int tw = min(x.t1, x.tw[w]);
       // new rows that every row of the tile sees: the first row's
-      const int first_limit = seq_limit(min(x.i0 + w * QI, x.n - 1), x.n, a.mask_block);
+      const int first_limit = seq_limit(min(x.i0[w], x.n - 1), x.n, a.mask_block);
       float m_ref = kNothing, l = 0.f;
       bool ok = true;
       for (int t = x.t0; t < tw; ++t) {
