@@ -15,7 +15,8 @@
 //
 // A CTA has as many heads as the group, up to four, so that K and V are read once for them. float32,
 // D = 128: 16 x 4096 tokens of 32 heads 331 us, 6.5 TB/s (577 with room for four heads in every CTA
-// and a key at a time); of 32 heads on 8 165 us, 3.3 TB/s, bound by the multiply-adds and shuffles.
+// and a key at a time); of 32 heads on 8 143 us, 3.7 TB/s (165 with one key
+// at a time): two CTAs an SM, whose registers four heads fill, wait for their loads.
 #include "attn_common.cuh"
 
 namespace d2f {
@@ -137,8 +138,9 @@ __global__ void __launch_bounds__(kThreads) token_simt_kernel(const TokenArgs a)
   };
   const int share = (C + a.num_splits - 1) / a.num_splits;
   const int begin = min(C, split * share), end = min(C, begin + share);
-  // U keys at a time: their loads go out together
-  constexpr int U = HC == 4 ? 1 : 2;
+  // U keys at a time: their loads go out together. (Two heads: 235 us with two keys, 204 with four, 16 x
+  // 4096 tokens of 32 heads on 16; one head 336 and 388, four heads 143 and, with three, 157.)
+  constexpr int U = HC == 2 ? 4 : 2;
   int page[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
