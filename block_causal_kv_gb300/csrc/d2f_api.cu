@@ -1450,10 +1450,12 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
     return D2F_OK;
   }
   // At least 64 keys a part and at most 64 parts to compose. Float32, D = 128, whole calls: 2 CTAs
-  // an SM for four heads (1 x 4096 tokens 34 us, 48 with 4), 3 for two, 12 for one, whose uneven
-  // sequences then balance (16 x 200-4096 tokens 190 us; 212 with 8, 243 with 4).
-  // A counter a pair: more of them than the counters' region holds are not split.
-  const long long most = pairs > 4LL * sms ? 1 : (p->head_chunk == 4 ? 2 : p->head_chunk == 2 ? 3 : 12) * sms;
+  // an SM for four heads (1 x 4096 tokens 34 us, 48 with 4); for two heads 2 (1 x 4096 tokens 34 us,
+  // 41 with 3) and, with more pairs than SMs, 6, where uneven sequences balance (16 x 200-4096 tokens
+  // 138 us, 188 with 3; 16 x 4096 218, 204); for one head 12 (16 x 200-4096 tokens 190 us, 212 with 8,
+  // 243 with 4). A counter a pair: more of them than the counters' region holds are not split.
+  const int ctas = p->head_chunk == 4 ? 2 : p->head_chunk == 2 ? (pairs <= sms ? 2 : 6) : 12;
+  const long long most = pairs > 4LL * sms ? 1 : ctas * sms;
   p->splits = (int)max(1LL, min(min(most / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
   p->off_partial = counter_bytes(0);
   const size_t part = (size_t)p->head_chunk * (D * sizeof(float) + sizeof(float2));
