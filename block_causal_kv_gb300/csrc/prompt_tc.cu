@@ -26,8 +26,8 @@
 // 1580 TFLOP/s (82 % of the measured product rate; 1300 us in a row of calls, where the power cap
 // holds the clock at some 1.6 GHz). Without the weights' arithmetic the same loop takes 1141 us: S's
 // operands, both from shared memory, fill its bandwidth. 16 requests of 251 to 4096 rows, 32 heads
-// on 8: 768 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1085 us for the
-// long case, 890 TFLOP/s, bound by the exponentials and their chain, which are the same for half
+// on 8: 768 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1105 us for the
+// long case, 870 TFLOP/s, bound by the exponentials and their chain, which are the same for half
 // the products.
 //
 // Roles of a CTA's warps:
