@@ -1449,12 +1449,14 @@ int plan_token(int batch, int max_ctx, int Hq, int Hkv, int D, int B, int dtype,
                                     sizeof(float);
     return D2F_OK;
   }
-  // At least 64 keys a part and at most 64 parts to compose. Float32, D = 128, whole calls: 2 CTAs
-  // an SM for four heads (1 x 4096 tokens 34 us, 48 with 4); for two heads 2 (1 x 4096 tokens 34 us,
-  // 41 with 3) and, with more pairs than SMs, 6, where uneven sequences balance (16 x 200-4096 tokens
-  // 138 us, 188 with 3; 16 x 4096 218, 204); for one head 12 (16 x 200-4096 tokens 190 us, 212 with 8,
-  // 243 with 4). A counter a pair: more of them than the counters' region holds are not split.
-  const int ctas = p->head_chunk == 4 ? 2 : p->head_chunk == 2 ? (pairs <= sms ? 2 : 6) : 12;
+  // At least 64 keys a part and at most 64 parts to compose. Float32, D = 128, whole calls: with few
+  // pairs two CTAs an SM (1 x 4096 tokens, 32 heads on 8 44 us, 60 with 4; 32 on 16 34, 41 with 3);
+  // with more six, or twelve of one head, where uneven sequences balance (16 x 200-4096 tokens, 32
+  // heads on 8: 103 us, 136 with 2; on 16: 138, 188 with 3; 32 on 32: 190, 243 with 4), although
+  // sequences of one length lose (16 x 4096: 150 us, 144 with 2; 218, 204; none). A counter a pair:
+  // more of them than the counters' region holds are not split.
+  const bool few = p->head_chunk == 4 ? 2 * pairs <= sms : p->head_chunk == 2 && pairs <= sms;
+  const int ctas = few ? 2 : p->head_chunk == 1 ? 12 : 6;
   const long long most = pairs > 4LL * sms ? 1 : ctas * sms;
   p->splits = (int)max(1LL, min(min(most / pairs, (long long)cdiv(max_ctx, 64)), 64LL));
   p->off_partial = counter_bytes(0);

@@ -15,7 +15,7 @@
 //
 // A CTA has as many heads as the group, up to four, so that K and V are read once for them. float32,
 // D = 128: 16 x 4096 tokens of 32 heads 331 us, 6.5 TB/s (577 with room for four heads in every CTA
-// and a key at a time); of 32 heads on 8 143 us, 3.7 TB/s (165 with one key
+// and a key at a time); of 32 heads on 8 150 us, 3.6 TB/s (165 with one key
 // at a time): two CTAs an SM, whose registers four heads fill, wait for their loads.
 #include "attn_common.cuh"
 
