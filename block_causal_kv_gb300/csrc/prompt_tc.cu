@@ -910,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_ref = small ? m_ref + up : top;
             }
             l *= alpha;
+            tmem_wait_st();  // (the first half's weights and outputs scaled with them: a load does not wait for stores)
             if (c == 1) scale_p(ts, alpha);
             // (P V of the tile before is complete: S of this one came after it)
             if (!first) scale_o<D>(to, alpha);
