@@ -290,13 +290,15 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_simt_kernel(const PromptAr
       continue;
     }
     if (cg == 0 && a.lse_out) a.lse_out[hr] = (m[x] + __log2f(l[x])) * 0.6931471805599453f;
-    const float inv = l[x] == 0.f ? 0.f : 1.0f / l[x];  // (0: every score is -inf)
+    const float inv = 1.0f / l[x];
+    const bool none = l[x] == 0.f;  // every score is -inf (the product may be 0 * infinity)
     T *dst = static_cast<T *>(a.out) + hr * D;
     if (cols)
 #pragma unroll
       for (int j = 0; j < CJ; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) store_out<T>(dst + 4 * cg + 64 * j + c, o[x][j].f[c] * inv);
+        for (int c = 0; c < 4; ++c)
+          store_out<T>(dst + 4 * cg + 64 * j + c, none ? 0.f : o[x][j].f[c] * inv);
   }
 }
 

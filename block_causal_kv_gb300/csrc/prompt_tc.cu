@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->o_full[w], outs & 1)) break;
         ++outs;
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.0f / l;  // (0: every score is -inf)
+        const float inv = 1.0f / l;
+        const bool none = l == 0.f;  // every score is -inf (the product may be 0 * infinity)
         const bool parts = x.splits > 1;
         char *dst = parts ? reinterpret_cast<char *>(a.ws_o + x.split * n_hr * D) : static_cast<char *>(a.out);
         // 128 bytes of every row at a time: bf16 outputs of 64 columns, or float parts of 32
@@ -954,7 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32(to + c * 64 + h * 32, o);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                y[h * 16 + j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                y[h * 16 + j] =
+                    none ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
             }
           }
           stage_rows(stage, row, y, hr, dst + c * 128, row_bytes);

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import seq_ref
 import test_gpu_prompt_attention as prompts
 import test_gpu_token_attention as tokens
 from gpu_common import device
@@ -85,3 +86,33 @@ def test_single_tokens_whose_keys_move_the_reference(hq, hkv, D, dtype):
     dev = device()
     p = tokens.batch([800, 63, 700], hq=hq, hkv=hkv, D=D, B=16, dtype=dtype, seed=D, q_scale=0.1)
     check(p, *tokens.run(stairs(p, 9.0, 13), dev), {0, 1, 2})
+
+
+@pytest.mark.parametrize("path", ["", "simt"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("ctx", [0, 40, 2500])
+def test_rows_without_a_finite_score_get_zero_whatever_v_holds(ctx, value, dtype, path, monkeypatch):
+    """All of a row's scores -infinity: out 0 and lse -infinity, where V holds infinities and NaN too;
+    rows of the same tile that see a finite score from another key on keep theirs."""
+    if path:
+        monkeypatch.setenv("D2F_ATTN_PATH", path)
+    dev = device()
+    for n, mod in ((150, prompts), (1, tokens)):
+        p = problem([n], [ctx], hq=4, hkv=2, D=64, B=16, dtype=dtype, seed=ctx)
+        p["mask_block"] = 1 if mod is prompts else 0
+        p["q"][..., 0] = 1.0
+        for x in ("k", "k_pool"):
+            p[x][..., 0] = float("-inf")
+        for x in ("v", "v_pool"):
+            p[x][:, 0] = value
+        out, lse = mod.run(p, dev)
+        assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    if ctx == 0:   # a causal prompt whose rows see a finite score from row 70 on
+        p = problem([150], [0], hq=4, hkv=2, D=64, B=16, dtype=dtype, seed=1)
+        p["q"][..., 0] = 1.0
+        p["k"][:70, :, 0] = float("-inf")
+        p["v"][100:, 1] = value
+        out, lse = prompts.run(p, dev)
+        assert bool((out[:70] == 0).all()) and bool((lse[:70] == float("-inf")).all())
+        seq_ref.check(p, out, lse, rows=set(range(70, 150)))
