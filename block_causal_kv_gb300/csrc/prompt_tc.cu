@@ -69,6 +69,7 @@ constexpr int kRegLaunch = 168, kRegCtl = 104, kRegSoft = 200;
 static_assert(kRegCtl + 2 * kRegSoft <= 3 * kRegLaunch, "register split within the launch's allocation");
 constexpr float kMove = 8.f;         // the reference moves when a score is 2^kMove above it
 constexpr float kNothing = -3.402823466e38f;  // reference of a row that has seen no key: the lowest float
+constexpr float kFar = 268435456.f;  // references of 2^28 and more take the far path (far_scores)
 
 struct Item {
   int b, q0, n, C;      // request, its first row, rows, cached tokens (b < 0: no more items)
@@ -269,6 +270,23 @@ __device__ __noinline__ void scale_p(uint32_t p, float alpha) {
       x[j] = pack_bf16x2(__uint_as_float(x[j] << 16) * alpha, __uint_as_float(x[j] & 0xffff0000u) * alpha);
     tmem_st16(p + c, x);
   }
+}
+
+// 64 scores of a row whose reference m is far from 0, made relative to it: y / scale with y = x' - m,
+// the product x' = x scale rounded first as m was. (One fma a score, as for other references, would
+// give the reference's own key the rounding error of m for its exponent, which from 2^31 on is above
+// what a weight holds.) Other rows of the warp keep theirs.
+__device__ __noinline__ void far_scores(uint32_t s, float scale, float m, bool far) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(s + c, x);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (far) x[j] = __float_as_uint((__fmul_rn(__uint_as_float(x[j]), scale) - m) / scale);
+    tmem_st16(s + c, x);
+  }
+  tmem_wait_st();
 }
 
 // The product with V of one tile by the threads: each row adds the keys below its limit.
@@ -802,7 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tw = min(x.t1, x.tw[w]);
       // new rows that every row of the tile sees: the first row's
       const int first_limit = seq_limit(min(x.i0[w], x.n - 1), x.n, a.mask_block);
-      float m_ref = kNothing, l = 0.f;
+      // The reference, and what a score has to be above to move it; with a reference from kFar on the
+      // limit is -infinity, every 64 keys with a score take the rare path, and m_ref is 0.
+      float m_ref = kNothing, m_far = kNothing, limit_up = rv ? kNothing : INFINITY, l = 0.f;
       bool ok = true;
       for (int t = x.t0; t < tw; ++t) {
         const uint32_t ev = e + 2 * (t - x.t0) + 1;
@@ -848,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Weights with the reference as it is, the largest score beside them; where that is too far
           // above the reference (seldom, and not a second time), the reference moves and the weights
           // are computed again.
+          bool again = false;
           while (true) {
             uint32_t r[64];
             tmem_ld64(ts + c * 64, r);
@@ -868,11 +889,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 mx[j & 3] = fmax3(mx[j & 3], __uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-              m_ref = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2, kNothing);
+              const float m = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2, kNothing);
+              const bool far = fabsf(m) >= kFar && m != kNothing;
+              if (!far) m_ref = m;
+              if (rv) limit_up = far ? -INFINITY : m + kMove;
             }
             // (One fma a score: the reference's own key has the rounding error of m_ref for its exponent,
-            // up to 2^6 with scores of 2^30. Rounding the product first where that is large cost all
-            // calls 3 to 15 %, whichever way the choice was made.)
+            // up to 2^4 with references below kFar.)
             const float neg = -m_ref;
             constexpr int kA = 2, kB = 6;
 #pragma unroll
@@ -898,22 +921,35 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-            const bool move = rv && top > m_ref + kMove;
-            if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
+            const bool move = top > limit_up;
+            if (__builtin_expect(!__any_sync(0xffffffffu, move) || again, 1)) break;
             // By a whole number of powers of two, so that weights of this tile's first half which are
             // stored already keep their bits; the first time, and by more than 126, to the score itself.
             float alpha = 1.f;
+            bool far = limit_up == -INFINITY;
             if (move) {
-              const float up = ceilf(top - m_ref);
-              const bool small = up <= 126.f;
-              alpha = small ? __uint_as_float((uint32_t)(127 - (int)up) << 23) : 0.f;
-              m_ref = small ? m_ref + up : top;
+              far |= fabsf(top) >= kFar;
+              if (far) {
+                const float old = limit_up == -INFINITY ? m_far : m_ref;
+                m_far = fmaxf(old, top);
+                alpha = fast_exp2(old - m_far);
+                m_ref = 0.f;
+                limit_up = -INFINITY;
+              } else {
+                const float up = ceilf(top - m_ref);
+                const bool small = up <= 126.f;
+                alpha = small ? __uint_as_float((uint32_t)(127 - (int)up) << 23) : 0.f;
+                m_ref = small ? m_ref + up : top;
+                limit_up = m_ref + kMove;
+              }
             }
             l *= alpha;
             tmem_wait_st();  // (the first half's weights and outputs scaled with them: a load does not wait for stores)
             if (c == 1) scale_p(ts, alpha);
             // (P V of the tile before is complete: S of this one came after it)
             if (!first) scale_o<D>(to, alpha);
+            again = __any_sync(0xffffffffu, far);
+            if (again) far_scores(ts + c * 64, sl2, m_far, far);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st32(ts + c * 32, p);
@@ -970,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[sl]));
+      if (limit_up == -INFINITY) m_ref = m_far;
       if (rv && x.splits > 1)
         a.ws_ml[x.split * n_hr + hr] = make_float2(m_ref == kNothing ? -INFINITY : m_ref, l);
       else if (rv && a.lse_out)

@@ -796,9 +796,8 @@ int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_hea
  *   block_size  1..256 (the page; ctx_len need not be a multiple of it)
  *   head_dim    32, 64 or 128
  * A key that a row does not see never reaches it, not even with infinite or NaN K or V. A row all
- * of whose scores are -infinity gets 0, with -infinity in lse_out. Finite scores are below 5e8 in
- * magnitude (float then tells no two keys apart that differ by less than 32); with larger
- * ones bf16 results may be NaN.
+ * of whose scores are -infinity gets 0, with -infinity in lse_out. Finite scores are below 2.3e38 in
+ * magnitude (they are held as float, times log2 e).
  * Results do not depend on the order in which CTAs run. Device buffers are 16-byte aligned.
  *
  * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
@@ -848,7 +847,7 @@ int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int n
  *                0 for these reasons), or NULL
  *   max_ctx      host hint used only to split the cache's length among CTAs
  *   block_size   1..256; head_dim 32, 64 or 128
- * Slots at or past ctx_len may hold anything.
+ * Slots at or past ctx_len may hold anything. Finite scores are below 2.3e38 in magnitude.
  *
  * Errors in err_word: D2F_ERR_BAD_INDEX for a cached page whose id is out of range (its tokens
  * are left out of the softmax) and for a new token without a page (its page-table row is full or

@@ -116,3 +116,59 @@ def test_rows_without_a_finite_score_get_zero_whatever_v_holds(ctx, value, dtype
         out, lse = prompts.run(p, dev)
         assert bool((out[:70] == 0).all()) and bool((lse[:70] == float("-inf")).all())
         seq_ref.check(p, out, lse, rows=set(range(70, 150)))
+
+
+@pytest.mark.parametrize("path", ["", "simt"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("low", [3e9, 1e10, 1e20, 2e34])
+@pytest.mark.parametrize("D,n,ctx", [(64, 300, 0), (128, 300, 200), (64, 40, 2500)])
+@pytest.mark.parametrize("shape", ["low", "high", "rising", "near last", "far last"])
+def test_scores_far_from_zero(shape, D, n, ctx, low, dtype, path, monkeypatch):
+    """Scores up to 2e33 in magnitude beside rows whose scores are of unit size: a row that sees scores
+    far from 0 takes the V of its largest one (the others are further below it than float tells
+    apart), whether its reference begins there, gets there or leaves."""
+    if path:
+        monkeypatch.setenv("D2F_ATTN_PATH", path)
+    dev = device()
+    p = problem([n], [ctx], hq=4, hkv=2, D=D, B=16, dtype=dtype, seed=n)
+    at = np.arange(n)
+    far = torch.from_numpy(at % 3 != 0)     # rows that take dim 0 into account
+    p["q"][..., 0] = far[:, None].to(dtype)
+    p["k_pool"][..., 0] = -low
+    k0 = np.full(n, -low)
+    best = np.full(n, -1)                   # the key whose V the row takes; -1: none stands out
+    near = np.zeros(n, bool)                # rows whose visible scores are of unit size
+    if shape in ("low", "high"):
+        k0[:] = -low if shape == "low" else low / 4
+        k0[5] = -low / 4 if shape == "low" else low
+        best[5:] = 5
+    elif shape == "rising":                 # one key in 64 above all before it
+        for h, j in enumerate(range(5, n, 64)):
+            k0[j] = low * 2.0 ** (h - 5)
+            best[j:] = j
+    elif shape == "near last":
+        k0[5] = -low / 4
+        best[5:20] = 5
+        k0[20:] = 0
+        near[20:] = True
+    else:
+        k0[:20], k0[20] = 0, low
+        near[:20] = True
+        best[20:] = 20
+    p["k"][..., 0] = torch.from_numpy(k0).to(dtype)[:, None]
+    out, lse = prompts.run(p, dev)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    # far rows: one weight, rounded to bf16 on the tensor cores, and the output's rounding
+    rows = np.flatnonzero((best >= 0) & far.numpy())
+    want = p["v"][best[rows]].double().repeat_interleave(2, 1)
+    tol = 2.0 ** -8 * (1 + 2.0 ** -7) * 2 if dtype == BF else 2.0 ** -22
+    assert bool(((out.cpu().double()[rows] - want).abs() <= tol * want.abs()).all())
+    # (float32 products and logarithms: a few roundings of 2^-24; beside them the other dims' part of
+    # the score, below 64)
+    top = p["scale"] * p["k"][best[rows], :, 0].double().numpy().repeat(2, 1)
+    assert np.allclose(lse.cpu().double().numpy()[rows], top, rtol=1e-6, atol=64)
+    # rows that leave dim 0 out, and rows over keys of unit size: as if the others scored -250 or less
+    p["k"][..., 0] = torch.from_numpy(np.where(k0 < 0, -2000.0 * (D / 64) ** 0.5, 0.0)).to(dtype)[:, None]
+    p["k_pool"][..., 0] = -2000.0 * (D / 64) ** 0.5
+    rows = set(np.flatnonzero(near | ~far.numpy()).tolist())
+    seq_ref.check(p, out, lse, rows=rows)
