@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const PromptArgs a) {
   if (q0 < 0 || q1 > a.rows || row < q0 || row >= q1 || C < 0 ||
       (long long)C > (long long)a.max_pages_per_seq * a.block_size)
     return;
-  const int splits = a.split_count ? __ldcg(a.split_count + lo) : a.num_splits;
+  // (After a wait that ran out the counts may not have been written: no more than there are parts.)
+  const int splits = a.split_count ? min(__ldcg(a.split_count + lo), a.num_splits) : a.num_splits;
   if (splits <= 1) return;  // (written by its only item)
   float2 ml = make_float2(-INFINITY, 0.f);
   if (lane < splits) ml = __ldcg(&a.ws_ml[lane * n_hr + hr]);

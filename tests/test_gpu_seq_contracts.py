@@ -1,0 +1,61 @@
+"""What the contract of d2f_prompt_attn promises about arguments that no ordinary call has."""
+import ctypes
+
+import pytest
+import torch
+
+import test_gpu_prompt_attention as prompts
+from gpu_common import device
+from seq_ref import check, problem
+
+from block_causal_kv_gb300 import d2f
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("cycles", [1, 100, 1000, 10000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_run_out_over_a_workspace_of_large_numbers(cycles, D, monkeypatch):
+    """The composition takes no more parts than the workspace has room for, whatever the call left
+    unwritten in it; the next call over it is right."""
+    dev = device()
+    p = problem([20, 5, 33], [4000, 300, 33], hq=2, hkv=1, D=D, B=16, dtype=BF, seed=5)
+    t = prompts.to_gpu(p, dev)
+    n = d2f.prompt_attn_workspace_size(3, 58, 4000, 2, 1, D, 16)
+    assert n > 0
+    ws = torch.full((n,), 0x7f, dtype=torch.uint8, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+    monkeypatch.setenv("D2F_WAIT_CYCLES", str(cycles))
+    out, lse = prompts.call(p, t, workspace=ws, err=err)
+    torch.cuda.synchronize()
+    assert int(err) in (0, 5)
+    if int(err) == 0:
+        check(p, out, lse)
+    monkeypatch.delenv("D2F_WAIT_CYCLES")
+    check(p, *prompts.run(p, dev, workspace=ws))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("num_pages", [0, 4])
+def test_no_pages_at_all(num_pages, dtype):
+    """ctx_len of zeros over a page table without columns: there is no cache to point to."""
+    dev = device()
+    p = problem([150, 7], [0, 0], hq=4, hkv=2, D=128, B=16, dtype=dtype, seed=1)
+    t = prompts.to_gpu(p, dev)
+    want, want_lse = prompts.call(p, t)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    lib = d2f.load()
+
+    def ptr(x):
+        return ctypes.c_void_p(x.data_ptr())
+    status = lib.d2f_prompt_attn(ptr(t["q"]), ptr(t["k"]), ptr(t["v"]), ptr(t["start"]), None, None,
+                                 None, 0, ptr(t["ctx"]), ptr(out), ptr(lse), 2, 157, 0, 4, 2, 128, 16,
+                                 num_pages, d2f.BF16 if dtype == BF else d2f.F32, 1,
+                                 ctypes.c_float(p["scale"]), None, 0, ptr(err),
+                                 ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert status == 0, lib.d2f_last_error_string().decode()
+    assert int(err) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
