@@ -372,6 +372,9 @@ __device__ __noinline__ bool clean_v(const PromptArgs &a, const Item &x, uint32_
   return __any_sync(0xffffffffu, ((hit[0] | hit[1] | hit[2] | hit[3]) & 0x7fff7fffu) != 0);
 }
 
+// (Out of line and at the producer's end: inlined behind the item, it cost the long prompt 2 %.)
+__device__ __noinline__ void report_lengths(const PromptArgs &a) { seq_report(a); }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
@@ -419,19 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   grid_dependency_wait();  // (what is above reads nothing that the kernel before may write)
-  if (warp == 3 && blockIdx.x == 0) seq_report(a);
 
   if (warp < 4) {
     reg_dec<kRegCtl>();
     if (warp == 0) {
       // ============ producer ====================================================
       uint32_t e = 0, items = 0, asked = 0;
-      bool ok = true;
+      bool ok = true, had0 = false;
       int it = blockIdx.x;
       const int pages = kKeys / a.block_size;  // pages of a tile (cached keys)
       while (true) {
         Item w;
         w.splits = 1;
+        had0 |= it == 0;
         SeqTile s;
         if (a.split_count) {
           s = seq_even(a, it, a.grid, kKeys, w.splits, w.split, w.g, it == 0 ? a.split_count : nullptr);
@@ -560,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&bars->slot_full[sl]));
         }
       }
+      if (had0) report_lengths(a);  // (whichever CTA took item 0: its own may never start)
       // Drain: what was asked for has landed before the CTA ends.
       if (lane == 0) {
         volatile int no_abort = 0;

@@ -59,3 +59,29 @@ def test_no_pages_at_all(num_pages, dtype):
     torch.cuda.synchronize()
     assert status == 0, lib.d2f_last_error_string().decode()
     assert int(err) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("batch", [2, 40, 5000])
+@pytest.mark.parametrize("which", ["first", "last"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_request_without_rows_is_reported_too(dtype, which, batch):
+    """A length past the page table of a request that brings no rows, in launches of one item and of
+    many, while another stream keeps SMs busy."""
+    dev = device()
+    new = [3] * batch
+    b = 0 if which == "first" else batch - 1
+    new[b] = 0
+    p = problem(new, [0] * batch, hq=2, hkv=2, D=64, B=16, dtype=dtype, seed=batch)
+    t = prompts.to_gpu(p, dev)
+    t["ctx"][b] = 10 ** 6
+    busy = torch.randn((4096, 4096), device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            busy @ busy
+    out, lse = prompts.call(p, t, prefix=True, max_ctx=0, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 1
+    check(p, out, lse, rows=set(range(0, sum(new), max(1, sum(new) // 50))))
