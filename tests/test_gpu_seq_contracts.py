@@ -85,3 +85,40 @@ def test_a_request_without_rows_is_reported_too(dtype, which, batch):
     torch.cuda.synchronize()
     assert int(err) == 1
     check(p, out, lse, rows=set(range(0, sum(new), max(1, sum(new) // 50))))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("splits", [False, True])
+@pytest.mark.parametrize("what", ["negative", "decreasing", "past rows", "first", "ctx", "ctx < 0"])
+def test_rows_of_skipped_requests_stay(what, splits, dtype):
+    """Inconsistent lengths, with keys that are split among CTAs too: rows that only skipped requests
+    own, or none, are left as they are; where row_start is consistent the other requests are right."""
+    dev = device()
+    p = problem([20, 30, 40], [3000 if splits else 10, 20, 33], hq=2, hkv=2, D=64, B=16, dtype=dtype,
+                seed=8)
+    rows = 90
+    assert splits == (d2f.prompt_attn_workspace_size(3, rows, p["ctx"][0], 2, 2, 64, 16,
+                                                     d2f.BF16 if dtype == BF else d2f.F32) > 0)
+    t = prompts.to_gpu(p, dev)
+    if what == "negative":
+        t["start"][0], stay = -5, range(0, 20)
+    elif what == "decreasing":                      # 0, 20, 10, 10
+        t["start"][2:], stay = 10, range(20, 90)
+    elif what == "past rows":
+        t["start"][3], stay = 91, range(50, 90)
+    elif what == "first":
+        t["start"][0], stay = 5, range(0, 5)
+    else:
+        t["ctx"][1] = p["table"].shape[1] * 16 + 1 if what == "ctx" else -1
+        stay = range(20, 50)
+    out = torch.full((rows, 2, 64), 7.0, dtype=dtype, device=dev)
+    lse = torch.full((rows, 2), 7.0, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    prompts.call(p, t, err=err, out=out, lse=lse, max_ctx=p["ctx"][0])
+    torch.cuda.synchronize()
+    assert int(err) == 1
+    stay = torch.tensor(list(stay), device=dev)
+    assert bool((out[stay] == 7).all()) and bool((lse[stay] == 7).all())
+    if what.startswith("ctx"):
+        p["ctx"][1] = -1
+        check(p, out, lse)
