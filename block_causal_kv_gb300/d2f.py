@@ -820,8 +820,8 @@ def prompt_attn(q, k, v, row_start, *, mask_block=1, k_pool=None, v_pool=None, p
         checks, pages = _pools(k_pool, v_pool, qd, hkv, block_size, d)
         checks += (("page_table", page_table, i32, (batch, max_pages)),
                    ("ctx_len", ctx_len, i32, (batch,)))
-    else:
-        k_pool = v_pool = page_table = None
+    elif not (k_pool is v_pool is page_table is None):
+        raise ValueError("k_pool, v_pool and page_table go with ctx_len")
     dev = _device(("q", q, qd, q.shape), ("k", k, qd, (rows, hkv, d)), ("v", v, qd, (rows, hkv, d)),
                   ("row_start", row_start, i32, (batch + 1,)), *checks,
                   ("out", out, qd, q.shape), ("lse", lse, torch.float32, (rows, hq)),
