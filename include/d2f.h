@@ -43,12 +43,15 @@
  * - Workspace: caller-provided device memory of at least the size the matching
  *   *_workspace_size query returns, 16-byte aligned (else D2F_ERR_INVALID_ARG). It
  *   must be zero-filled before its first use (e.g. cudaMemsetAsync); every call
- *   leaves it ready for the next call on the same stream. Calls that share one workspace must not overlap in time (captured
- *   graphs that may run at the same time need one each). The attention entry points
- *   with num_splits 0 and the log probabilities leave it ready for calls of other
- *   sizes and for one another too, so one workspace of the largest size serves all
- *   of them in turn; the commit's is for one total_q and block_size, and zeroed
- *   again before a call with others.
+ *   leaves it ready for the next call on the same stream. Calls that share one workspace
+ *   must not overlap in time (captured graphs that may run at the same time need one
+ *   each). The attention entry points (of windows with num_splits 0, of the 4-bit cache,
+ *   of prompts, of single tokens) and the log probabilities leave it ready for calls of
+ *   other sizes and for one another too, so one workspace of the largest size serves all
+ *   of them in turn. The commit's is for one total_q and block_size, and that of a window
+ *   attention with num_splits given is for its sizes: their counters may lie where the
+ *   other calls keep partials, so such a workspace is zeroed again before a call with
+ *   other sizes or of another entry point.
  *
  * Size limits (a call beyond one returns D2F_ERR_UNSUPPORTED before anything is
  * enqueued):
@@ -805,8 +808,9 @@ int d2f_prompt_attn_workspace_size(int batch, int rows, int max_ctx, int num_hea
  * or passes rows, or a ctx_len out of range: requests with such lengths are skipped, and with an
  * inconsistent row_start the others' results are unspecified; D2F_ERR_TIMEOUT for a wait of the
  * kernel's that ran out. Nothing outside the buffers is touched.
- * Limits: batch and num_heads_q <= 65535, rows <= 2^30. The workspace needs no zeroing, and may
- * be any entry point's.
+ * Limits: batch and num_heads_q <= 65535, rows <= 2^30. The workspace needs no zeroing. It may be
+ * one that the entry points named at the top under "Workspace" use in turn, whose counters it leaves
+ * as they are; a commit or a window attention with num_splits given wants it zeroed afterwards.
  */
 int d2f_prompt_attn(const void *q, const void *k, const void *v, const int32_t *row_start,
                     const void *k_pool, const void *v_pool, const int32_t *page_table,
@@ -854,8 +858,8 @@ int d2f_token_attn_workspace_size(int batch, int max_ctx, int num_heads_q, int n
  * the id out of range: it takes part in the attention and is not stored); D2F_ERR_INVALID_ARG
  * for a ctx_len past the page table (the sequence is skipped).
  * Limits: batch and num_heads_q <= 65535. The workspace is the caller's, zeroed once (and again
- * after a device error); calls of any sizes may use it in turn, with those of the attention
- * entry points and the log probabilities.
+ * after a device error); calls of any sizes may use it in turn, with those of the entry points
+ * named at the top under "Workspace".
  */
 int d2f_token_attn(const void *q, const void *k_new, const void *v_new, void *k_pool, void *v_pool,
                    const int32_t *page_table, int max_pages_per_seq, const int32_t *ctx_len,

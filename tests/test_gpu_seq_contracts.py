@@ -5,10 +5,11 @@ import pytest
 import torch
 
 import test_gpu_prompt_attention as prompts
+import test_gpu_token_attention as tokens
 from gpu_common import device
 from seq_ref import check, problem
 
-from block_causal_kv_gb300 import d2f
+from block_causal_kv_gb300 import d2f, synth
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -122,3 +123,47 @@ def test_rows_of_skipped_requests_stay(what, splits, dtype):
     if what.startswith("ctx"):
         p["ctx"][1] = -1
         check(p, out, lse)
+
+
+def test_a_workspace_zeroed_between_entry_points_that_do_not_share_one():
+    """Calls whose counters pass four an SM (a commit of many blocks, a window attention with num_splits
+    given) use a prompt's or a single token's workspace once it is zeroed again, and it theirs."""
+    dev = device()
+    w = synth.Workload("m", 4, 1, 1, 8, 1, BF, [0] * 4, [640, 400, 960, 240], 96, masked_frac=0.6,
+                       taus=(0.05, 0.3, 0.6), logit_sigma=1.5, seed=3)
+    c = synth.make_problem(w)
+
+    def commit(ws):
+        g = c.to(dev)
+        res = d2f.commit(g.logits, g.tokens, g.masked, g.q_start, g.block_phase, g.tau, block_size=1,
+                         mask_id=c.mask_id, num_splits=2, workspace=ws)
+        return g.tokens, g.masked, res["conf"], res["argmax"], res["block_remaining"]
+    w = synth.Workload("w", 24, 32, 32, 128, 16, F32, [64] * 24, [1] * 24, 64, permute_pages=True,
+                       seed=4)
+    a = synth.make_problem(w)
+    g = a.to(dev)
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    assert 24 * 32 > 4 * sms and 2 * 2240 > 4 * sms
+
+    def windows(ws):
+        return d2f.block_attn(g.q, g.k_win, g.v_win, g.k_pool, g.v_pool, g.page_table, g.ctx_len,
+                              g.q_start, block_size=16, max_q_per_seq=a.max_q_per_seq,
+                              max_ctx=a.max_ctx, num_splits=2, workspace=ws)
+    p = problem([200, 9], [2200, 100], hq=2, hkv=1, D=128, B=16, dtype=F32, seed=1)
+    t = prompts.to_gpu(p, dev)
+    q = tokens.batch([3000, 5, 700], hq=8, hkv=2, D=128, B=16, dtype=BF, seed=2)
+    u = tokens.to_gpu(q, dev)
+    calls = [(commit, d2f.commit_workspace_size(2240, 96, 1, num_splits=2)),
+             (windows, d2f.attn_workspace_size(24, w.total_q, a.max_q_per_seq, a.max_ctx, 32, 32, 128,
+                                               16, d2f.F32, 2)),
+             (lambda ws: prompts.call(p, t, workspace=ws),
+              d2f.prompt_attn_workspace_size(2, 209, 2200, 2, 1, 128, 16, d2f.F32)),
+             (lambda ws: tokens.call(q, u, workspace=ws),
+              d2f.token_attn_workspace_size(3, 3000, 8, 2, 128, 16))]
+    assert all(n > 4 * 4 * sms for _, n in calls)
+    fresh = [[x.clone() for x in f(torch.zeros(n, dtype=torch.uint8, device=dev))] for f, n in calls]
+    ws = torch.zeros(max(n for _, n in calls), dtype=torch.uint8, device=dev)
+    for i in (2, 0, 3, 1, 2, 3, 0, 1, 3, 0, 2, 1):
+        ws.zero_()
+        for got, want in zip(calls[i][0](ws), fresh[i]):
+            assert torch.equal(got, want), i
