@@ -6,8 +6,8 @@
 // A copy: row r of the source is Hkv pieces of head_dim elements, one after another; each
 // piece goes to its own place, k_pool[page][g][offset]. A thread moves kBatch units of
 // 16 bytes (whole elements where head_dim does not allow that), all loads before the stores.
-// 32,646 rows of 32 heads of 128, bf16, K and V: 172 us, 6.2 TB/s read and written, 93 % of the
-// measured copy rate.
+// 32,646 rows of 32 heads of 128, K and V: bf16 180 us in a graph, L2 flushed, 5.9 TB/s read and
+// written, 89 % of the measured copy rate; float32 356 us, 6.0.
 #include "d2f_internal.cuh"
 
 namespace d2f {

@@ -10,10 +10,10 @@
 // sums and both accumulators are float. The weights enter the product with V as bf16 (2^-8 of
 // each, the type of the MMA's operands; the sum keeps the unrounded ones).
 //
-// Work. An item is a pair of row tiles of 128 rows of one (request, KV head) (neighbours, or from both
-// ends of the request: `fold`), times a split of its keys. The G = Hq / Hkv query heads of the KV head are packed into the rows (row r = query
-// r / G, head r % G, 128 / G queries a tile), so a K/V tile that is read once serves all of them.
-// A CTA keeps an SM (its two row tiles, a ring of K and V tiles of 128 keys) and takes
+// Work. An item is a pair of row tiles of 128 rows of one (request, KV head) (neighbours, or from
+// both ends of the request: `fold`), times a split of its keys. The G = Hq / Hkv query heads of the
+// KV head are packed into the rows (row r = query r / G, head r % G, 128 / G queries a tile), so a
+// K/V tile that is read once serves all of them. A CTA keeps an SM (its two row tiles, a ring of K and V tiles of 128 keys) and takes
 // further items from the launch's own grid (cluster launch control: a CTA that has loaded its
 // item's last tile cancels one that has not started and does its work), so that the next
 // item's queries and keys load while the last one computes, and unequal items even out. Items
@@ -21,14 +21,14 @@
 // prefixes uneven, the keys are cut into even pieces and a second launch composes them
 // (seq_even, prompt_merge_kernel).
 //
-// What bounds it. A pair of 128 x 128 tiles is 4 * 1024 cycles of products for D = 128 and 2 * 512
-// of exponentials a softmax warpgroup. 16,384 causal rows, 28 heads on 4: 1217 us at full clocks,
-// 1580 TFLOP/s (82 % of the measured product rate; 1300 us in a row of calls, where the power cap
-// holds the clock at some 1.6 GHz). Without the weights' arithmetic the same loop takes 1141 us: S's
-// operands, both from shared memory, fill its bandwidth. 16 requests of 251 to 4096 rows, 32 heads
-// on 8: 768 us; the short rows' tiles that the mask cuts cost the difference. D = 64: 1105 us for the
-// long case, 870 TFLOP/s, bound by the exponentials and their chain, which are the same for half
-// the products.
+// What bounds it. A pair of 128 x 128 tiles is 4 * 512 cycles of products for D = 128 (8192 operations
+// a cycle) and 2 * 512 of exponentials, half of them a softmax warpgroup's. 16,384 causal rows, 28
+// heads on 4: 1224 us at full clocks, 1570 TFLOP/s (81 % of the measured product rate; 1300 to 1320 us
+// in a row of calls, where the power cap holds the clock at some 1.6 GHz). Without the weights'
+// arithmetic the same loop takes 1141 us: S's operands, both from shared memory, fill its bandwidth.
+// 16 requests of 251 to 4096 rows, 32 heads on 8: 775 us; the short rows' tiles that the mask cuts
+// cost the difference. D = 64: 1091 us for the long case, 880 TFLOP/s, bound by the exponentials and
+// their chain, which are the same for half the products.
 //
 // Roles of a CTA's warps:
 //   0        producer: which request an item belongs to, tensor copies of the queries and of the
@@ -948,7 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             l *= alpha;
-            tmem_wait_st();  // (the first half's weights and outputs scaled with them: a load does not wait for stores)
+            // (What the tile's first half stored is loaded here: a load does not wait for a store.)
+            tmem_wait_st();
             if (c == 1) scale_p(ts, alpha);
             // (P V of the tile before is complete: S of this one came after it)
             if (!first) scale_o<D>(to, alpha);

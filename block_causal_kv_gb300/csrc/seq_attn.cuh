@@ -144,7 +144,7 @@ __device__ __forceinline__ SeqTile seq_even(const PromptArgs &a, int c, int grid
 
 // New rows that row i of a request of n rows sees: [0, seq_limit).
 __device__ __forceinline__ int seq_limit(int i, int n, int mask_block) {
-  return min(n, (i / mask_block + 1) * mask_block);  // (mask_block <= rows + 1, checked on the host)
+  return min(n, (i / mask_block + 1) * mask_block);  // (mask_block <= rows, set on the host)
 }
 
 // Whether row_start and ctx_len are consistent for every request; called by one warp of the

@@ -29,9 +29,11 @@
 // (sequence, KV head) and the composition by the CTA that came last, 16 x 251 to 4096 tokens of 32
 // heads took 130 us.)
 //
-// 4 x 32,768 tokens of 32 heads 313 us, 6.9 TB/s; 64 x 8192 of 28 heads on 4 166 us and 13 for the
-// composition, 6.0 TB/s; 16 x 251 to 4096 of 32 heads 80 us and 4, 5.4 TB/s (the places on the line
-// and the first copies take 4 us of it).
+// Both launches in a graph, L2 flushed: 4 x 32,768 tokens of 32 heads 337 us, 6.4 TB/s; 64 x 8192 of 28
+// heads on 4 200 us, 13 of them the composition, 5.4 TB/s; 16 x 251 to 4096 of 32 heads 101 us, 4.5 TB/s
+// (4 us for the places on the line and the first copies, 4 the composition). In a row of calls, which
+// overlap and find part of the cache in L2, 314, 180 and 84. head_dim 64: 255, 149 and 75 us, 4.2, 3.6
+// and 3.0 TB/s (a chunk of 16 keys has half the bytes).
 //
 // Softmax in log2 units with a reference a head and warp, which moves only when a score is more
 // than 2^8 above it. Weights enter the product with V as bf16 (2^-8 of each; the sum keeps the
