@@ -364,88 +364,88 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) token_tc_kernel(const
       }
     }
     if (done + 1 < filled && (meta[stage].keys & kFirst)) load_q(meta[stage].b, meta[stage].pair);
-      if (fresh && hc == 0 && mt.C >= 16 * mt.u && mt.C < 16 * mt.u + 16) {
-        // the new token to its slot, which no CTA reads in this call
-        const int pg = mt.C / B < a.max_pages_per_seq
-                           ? __ldg(a.page_table + (int64_t)mt.b * a.max_pages_per_seq + mt.C / B) : -1;
-        if (pg < 0 || pg >= a.num_pages) {
-          if (lane == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
-        } else if ((lane & 15) < D / 8) {
-          const int64_t from = ((int64_t)mt.b * Hk + g) * (D / 8) + (lane & 15);
-          const int64_t to = (((int64_t)pg * Hk + g) * B + mt.C % B) * (D / 8) + (lane & 15);
-          if (lane < 16)
-            static_cast<uint4 *>(a.k_pool)[to] = static_cast<const uint4 *>(a.k_new)[from];
-          else
-            static_cast<uint4 *>(a.v_pool)[to] = static_cast<const uint4 *>(a.v_new)[from];
-        }
+    if (fresh && hc == 0 && mt.C >= 16 * mt.u && mt.C < 16 * mt.u + 16) {
+      // the new token to its slot, which no CTA reads in this call
+      const int pg = mt.C / B < a.max_pages_per_seq
+                         ? __ldg(a.page_table + (int64_t)mt.b * a.max_pages_per_seq + mt.C / B) : -1;
+      if (pg < 0 || pg >= a.num_pages) {
+        if (lane == 0) set_err(a.err, D2F_ERR_BAD_INDEX);
+      } else if ((lane & 15) < D / 8) {
+        const int64_t from = ((int64_t)mt.b * Hk + g) * (D / 8) + (lane & 15);
+        const int64_t to = (((int64_t)pg * Hk + g) * B + mt.C % B) * (D / 8) + (lane & 15);
+        if (lane < 16)
+          static_cast<uint4 *>(a.k_pool)[to] = static_cast<const uint4 *>(a.k_new)[from];
+        else
+          static_cast<uint4 *>(a.v_pool)[to] = static_cast<const uint4 *>(a.v_new)[from];
       }
-      float x[NQ][4];
+    }
+    float x[NQ][4];
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    for (int i = 0; i < NQ; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const uint4 k0 = ld_shared_v4(at + (k_at ^ (k << 6))), k1 = ld_shared_v4(at + (k_at ^ (k << 6)) + 8 * L::kRow);
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          mma_bf16(x[i], k0.x, k1.x, k0.y, k1.y, q[i][k].x, q[i][k].y);
-          mma_bf16(x[i], k0.z, k1.z, k0.w, k1.w, q[i][k].z, q[i][k].w);
-        }
-      }
-      uint32_t p[NQ][2];
+    for (int k = 0; k < KB; ++k) {
+      const uint4 k0 = ld_shared_v4(at + (k_at ^ (k << 6))), k1 = ld_shared_v4(at + (k_at ^ (k << 6)) + 8 * L::kRow);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        bool move = false;
+        mma_bf16(x[i], k0.x, k1.x, k0.y, k1.y, q[i][k].x, q[i][k].y);
+        mma_bf16(x[i], k0.z, k1.z, k0.w, k1.w, q[i][k].z, q[i][k].w);
+      }
+    }
+    uint32_t p[NQ][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i][e] = (mt.keys >> (r + 8 * (e >> 1)) & 1u) ? x[i][e] * a.scale_log2 : -INFINITY;
-          move |= x[i][e] > m[i][e & 1] + kMove;
+    for (int i = 0; i < NQ; ++i) {
+      bool move = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = (mt.keys >> (r + 8 * (e >> 1)) & 1u) ? x[i][e] * a.scale_log2 : -INFINITY;
+        move |= x[i][e] > m[i][e & 1] + kMove;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(x[i][e], x[i][e + 2]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          top = fmaxf(top, m[i][e]);
+          const float alpha = fast_exp2(m[i][e] - top);
+          m[i][e] = top;
+          l[i][e] *= alpha;
+#pragma unroll
+          for (int j = 0; j < VB; ++j)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              o[i][j][w][e] *= alpha;
+              o[i][j][w][e + 2] *= alpha;
+            }
         }
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(x[i][e], x[i][e + 2]);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            top = fmaxf(top, m[i][e]);
-            const float alpha = fast_exp2(m[i][e] - top);
-            m[i][e] = top;
-            l[i][e] *= alpha;
-#pragma unroll
-            for (int j = 0; j < VB; ++j)
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                o[i][j][w][e] *= alpha;
-                o[i][j][w][e + 2] *= alpha;
-              }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i][e] = fast_exp2(x[i][e] - m[i][e & 1]);
-          l[i][e & 1] += x[i][e];
-        }
-        p[i][0] = transpose8(pack_bf16x2(x[i][0], x[i][1]));
-        p[i][1] = transpose8(pack_bf16x2(x[i][2], x[i][3]));
       }
 #pragma unroll
-      for (int j = 0; j < VB; ++j) {
-        uint32_t v[4][4];  // tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 y = ld_shared_v4(at + (v_at ^ (j << 7) ^ ((e & 1) << 6)) + ((e & 1) + 8 * (e >> 1)) * L::kRow);
-          v[e][0] = y.x;
-          v[e][1] = y.y;
-          v[e][2] = y.z;
-          v[e][3] = y.w;
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {  // dims 64 j + 8 r + 2 w and + 1
-          const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-          const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) mma_bf16(o[i][j][w], a0, a1, a2, a3, p[i][0], p[i][1]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        x[i][e] = fast_exp2(x[i][e] - m[i][e & 1]);
+        l[i][e & 1] += x[i][e];
       }
+      p[i][0] = transpose8(pack_bf16x2(x[i][0], x[i][1]));
+      p[i][1] = transpose8(pack_bf16x2(x[i][2], x[i][3]));
+    }
+#pragma unroll
+    for (int j = 0; j < VB; ++j) {
+      uint32_t v[4][4];  // tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 y = ld_shared_v4(at + (v_at ^ (j << 7) ^ ((e & 1) << 6)) + ((e & 1) + 8 * (e >> 1)) * L::kRow);
+        v[e][0] = y.x;
+        v[e][1] = y.y;
+        v[e][2] = y.z;
+        v[e][3] = y.w;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // dims 64 j + 8 r + 2 w and + 1
+        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+        const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) mma_bf16(o[i][j][w], a0, a1, a2, a3, p[i][0], p[i][1]);
+      }
+    }
     if (!(mt.keys & kLast)) continue;
 
     // ---- the segment's outputs, or its part ----

@@ -167,3 +167,15 @@ def test_a_workspace_zeroed_between_entry_points_that_do_not_share_one():
         ws.zero_()
         for got, want in zip(calls[i][0](ws), fresh[i]):
             assert torch.equal(got, want), i
+
+
+@pytest.mark.parametrize("hq", [65, 127, 128, 129])
+@pytest.mark.parametrize("D,B", [(128, 8), (64, 128)])
+@pytest.mark.parametrize("new,ctx", [([5, 1, 40], [0, 0, 0]), ([3, 0, 9], [1500, 7, 130])])
+def test_groups_about_a_row_tile_wide(new, ctx, D, B, hq):
+    """One query, or none beside another, in a tile of 128 rows; one head more than a tile has."""
+    dev = device()
+    p = problem(new, ctx, hq=hq, hkv=1, D=D, B=B, dtype=BF, seed=hq)
+    check(p, *prompts.run(p, dev))
+    p = tokens.batch([c + 1 for c in ctx], hq=hq, hkv=1, D=D, B=B, dtype=BF, seed=hq)
+    check(p, *tokens.run(p, dev))
