@@ -11,10 +11,11 @@
 // through shared memory (over K, which is done with), O += P V with R / 16 rows and D / 16 columns a
 // thread. Multiply-adds are made in pairs, which halves their issue (4096 causal rows of 32 heads on 8,
 // D = 128, float32: 3440 -> 3166 us, 43 TFLOP/s); shared memory's reads bound it, eight 16-byte loads
-// for 32 pairs. bf16 shapes run at the same rate or less: 16 x 251 to 4096 rows of 32 heads on 8 with head_dim
-// 32 10.1 ms, 25 TFLOP/s; 1024 rows of 130 heads on 1, D = 128, 1.3 ms, 28; 2 x 40-77 rows of 28 heads on 4 behind
-// 20,000 to 32,768 tokens in pages of 5 or 48 1.6 ms, 30 (0.08 in pages of 16). Operands are float in shared memory; rows are padded by four floats so that 16 keys a
-// quarter apart fall on different banks.
+// for 32 pairs. Operands are float in shared memory; rows are padded by four floats so that 16 keys a
+// quarter apart fall on different banks. bf16 shapes run at the same rate or less: 16 x 251 to 4096 rows
+// of 32 heads on 8 with head_dim 32 10.1 ms, 25 TFLOP/s; 1024 rows of 130 heads on 1, D = 128, 1.3 ms, 28;
+// 2 x 40 to 77 rows of 28 heads on 4 behind 20,000 to 32,768 tokens in pages of 5 or 48 1.6 ms, 30 (in
+// pages of 16, on the tensor cores, 80 us).
 #include "attn_common.cuh"
 #include "seq_attn.cuh"
 

@@ -13,13 +13,13 @@
 // Work. An item is a pair of row tiles of 128 rows of one (request, KV head) (neighbours, or from
 // both ends of the request: `fold`), times a split of its keys. The G = Hq / Hkv query heads of the
 // KV head are packed into the rows (row r = query r / G, head r % G, 128 / G queries a tile), so a
-// K/V tile that is read once serves all of them. A CTA keeps an SM (its two row tiles, a ring of K and V tiles of 128 keys) and takes
-// further items from the launch's own grid (cluster launch control: a CTA that has loaded its
-// item's last tile cancels one that has not started and does its work), so that the next
-// item's queries and keys load while the last one computes, and unequal items even out. Items
-// of a request's last rows, which see the most keys, come first. Where row tiles are few, or long
-// prefixes uneven, the keys are cut into even pieces and a second launch composes them
-// (seq_even, prompt_merge_kernel).
+// K/V tile that is read once serves all of them. A CTA keeps an SM (its two row tiles, a ring of K
+// and V tiles of 128 keys) and takes further items from the launch's own grid (cluster launch
+// control: a CTA that has loaded its item's last tile cancels one that has not started and does its
+// work), so that the next item's queries and keys load while the last one computes, and unequal
+// items even out. Items of a request's last rows, which see the most keys, come first. Where row
+// tiles are few, or long prefixes uneven, the keys are cut into even pieces and a second launch
+// composes them (seq_even, prompt_merge_kernel).
 //
 // What bounds it. A pair of 128 x 128 tiles is 4 * 512 cycles of products for D = 128 (8192 operations
 // a cycle) and 2 * 512 of exponentials, half of them a softmax warpgroup's. 16,384 causal rows, 28
@@ -996,8 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32(to + c * 64 + h * 32, o);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                y[h * 16 + j] =
-                    none ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                y[h * 16 + j] = none ? 0u : pack_bf16x2(__uint_as_float(o[2 * j]) * inv,
+                                                        __uint_as_float(o[2 * j + 1]) * inv);
             }
           }
           stage_rows(stage, row, y, hr, dst + c * 128, row_bytes);
